@@ -265,7 +265,8 @@ def _plain_logprobs(s):
     lse = m + torch.log(total)
     d = torch.where(e > 0, x - m, torch.zeros_like(x))
     entropy = torch.where(some, torch.log(total) - (e * d).sum(dim=1, keepdim=True) / total, torch.zeros_like(m))
-    lp = lambda v: torch.where(some & (v > -math.inf), v - lse, torch.full_like(v, -math.inf))  # noqa: E731
+    # differences from the row's maximum first: with logits of the type's lowest value lse alone loses log(total)
+    lp = lambda v: torch.where(some & (v > -math.inf), (v - m) - torch.log(total), torch.full_like(v, -math.inf))  # noqa: E731
     t = s["targets"].long()
     xt = logits.gather(1, t)
     # rank: 1 + tokens that come before in (logit descending, id ascending)
@@ -409,8 +410,10 @@ def _exact_logprobs(c, s):
     step = max(1, (1 << 26) // V)
     for t0 in range(0, T, step):
         x = s["logits"][t0:t0 + step].double() * float(torch.tensor(c["scale"], dtype=torch.float32))
-        lse = torch.logsumexp(x, dim=1, keepdim=True)
-        l = torch.where(torch.isneginf(x), torch.full_like(x, -math.inf), x - lse)
+        most = x.max(dim=1, keepdim=True).values.clamp(min=torch.finfo(torch.float64).min)
+        shifted = torch.logsumexp(x - most, dim=1, keepdim=True)
+        lse = most + shifted
+        l = torch.where(torch.isneginf(x), torch.full_like(x, -math.inf), (x - most) - shifted)
         p = torch.exp(l)
         ent = -torch.where(p > 0, p * l, torch.zeros_like(p)).sum(dim=1)
         part = [l.gather(1, s["targets"][t0:t0 + step].long()), ent, lse[:, 0]]

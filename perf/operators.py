@@ -109,9 +109,9 @@ def draw(rng):
     vocab = _log_int(rng, 500, 200000)
     kinds = kind()
     rows = _log_int(rng, 1, min(4096, (_LOGITS_MAX // 2 if kinds == "f32" else _LOGITS_MAX * 3 // 4) // vocab))
+    mask = rng.choice(("none", "none", "grammar", "lowest"))
     return _lp(None, rows, vocab, logits=kinds, top=rng.choice((0, 1, 5, 20, 32)), targets=rng.choice((1, 1, 2, 8)),
-               mask=rng.choice(("none", "none", "grammar", "lowest")), scale=rng.choice((1.0, 0.7, 1.25)),
-               pad=rng.choice((0, 0, 1, 8)))
+               mask=mask, scale=rng.choice((1.0, 0.7, 1.0 if mask == "lowest" else 1.25)), pad=rng.choice((0, 0, 1, 8)))
 
 
 def work(case):

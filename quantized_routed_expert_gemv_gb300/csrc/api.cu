@@ -674,6 +674,13 @@ extern "C" const char* moe_last_error(void) { return g_err; }
 namespace moe {
 int check_scratch(void* ws, cudaStream_t st, const char* name) { return check_workspace(ws, st, name); }
 int report_error(int code, const char* msg) { return fail(code, "%s", msg); }
+int reportf(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return code;
+}
 int report_cuda(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 int layer_device(const moe_layer* L) { return valid(L) ? L->device : -1; }
 const moe_layer_desc* layer_desc(const moe_layer* L) { return valid(L) ? &L->d : nullptr; }

@@ -23,6 +23,85 @@ def bf16_bits(t: torch.Tensor) -> np.ndarray:
     return t.detach().cpu().contiguous().view(torch.int16).numpy().view(np.uint16)
 
 
+_ELEM_TYPE = {torch.bfloat16: moe.MOE_BF16, torch.float16: moe.MOE_F16, torch.float32: moe.MOE_F32}
+
+
+def _stream(device, stream):
+    return stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Leading dimension of a matrix whose rows are contiguous."""
+    assert t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1), "rows must be contiguous"
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def block_norm(y=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=True, pre_norm=True, w_add=0.0,
+               eps=1e-6, residual_scale=1.0, h_out=None, x_out=None, x_type=torch.bfloat16, stream=None):
+    """moe_block_norm of device tensors: y and h [rows][hidden] (either may be
+    None); gate a tensor that broadcasts to [rows][hidden]; weights
+    [hidden].  Returns (h', x), allocated unless given."""
+    like = h if h is not None else y
+    rows, hidden = like.shape
+    if h_out is None:
+        h_out = torch.empty(rows, hidden, dtype=like.dtype, device=like.device)
+    if x_out is None:
+        x_out = torch.empty(rows, hidden, dtype=x_type, device=like.device)
+    a = moe.moe_block_norm_args()
+    a.rows, a.hidden, a.h_type = rows, hidden, _ELEM_TYPE[h_out.dtype]
+    if y is not None:
+        a.y, a.ld_y, a.y_type = y.data_ptr(), _ld(y), _ELEM_TYPE[y.dtype]
+    if h is not None:
+        assert h.dtype == h_out.dtype
+        a.h, a.ld_h = h.data_ptr(), _ld(h)
+    if gate is not None:
+        g = gate.expand(rows, hidden)
+        a.gate, a.gate_type = g.data_ptr(), _ELEM_TYPE[g.dtype]
+        a.ld_gate_row, a.ld_gate_col = (g.stride(0) if rows > 1 else 0), (g.stride(1) if hidden > 1 else 0)
+    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+        if w is not None:
+            assert w.shape == (hidden,) and w.is_contiguous()
+            setattr(a, name, w.data_ptr())
+            a.w_type = _ELEM_TYPE[w.dtype]
+    assert w_post is None or w_pre is None or w_post.dtype == w_pre.dtype
+    a.post_norm, a.pre_norm = int(post_norm), int(pre_norm)
+    a.w_add, a.eps, a.residual_scale = w_add, eps, residual_scale
+    a.h_out, a.ld_h_out = h_out.data_ptr(), _ld(h_out)
+    a.x_out, a.ld_x_out, a.x_type = x_out.data_ptr(), _ld(x_out), _ELEM_TYPE[x_out.dtype]
+    moe.moe_block_norm(a, _stream(like.device, stream))
+    return h_out, x_out
+
+
+def token_logprobs(logits: torch.Tensor, targets=None, top_n: int = 0, scale: float = 1.0, ranks: bool = True,
+                   stream=None) -> dict:
+    """moe_token_logprobs of device logits [rows][vocab]; targets int32 [rows]
+    or [rows][n_targets].  Returns device tensors: lse, entropy [rows];
+    logprob and rank in the targets' shape; top_ids, top_logprobs
+    [rows][top_n]."""
+    rows, vocab = logits.shape
+    dev = logits.device
+    a = moe.moe_token_logprobs_args()
+    a.logits, a.ld_logits, a.logits_type = logits.data_ptr(), _ld(logits), _ELEM_TYPE[logits.dtype]
+    a.rows, a.vocab, a.top_n, a.scale = rows, vocab, top_n, scale
+    out = {"lse": torch.empty(rows, dtype=torch.float32, device=dev),
+           "entropy": torch.empty(rows, dtype=torch.float32, device=dev)}
+    a.lse, a.entropy = out["lse"].data_ptr(), out["entropy"].data_ptr()
+    if targets is not None:
+        assert targets.dtype == torch.int32 and targets.is_contiguous() and targets.shape[0] == rows
+        a.targets, a.n_targets = targets.data_ptr(), targets.numel() // max(rows, 1)
+        out["logprob"] = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+        a.target_logprobs = out["logprob"].data_ptr()
+        if ranks:
+            out["rank"] = torch.empty(targets.shape, dtype=torch.int32, device=dev)
+            a.target_ranks = out["rank"].data_ptr()
+    if top_n:
+        out["top_ids"] = torch.empty(rows, top_n, dtype=torch.int32, device=dev)
+        out["top_logprobs"] = torch.empty(rows, top_n, dtype=torch.float32, device=dev)
+        a.top_ids, a.top_logprobs = out["top_ids"].data_ptr(), out["top_logprobs"].data_ptr()
+    moe.moe_token_logprobs(a, _stream(dev, stream))
+    return out
+
+
 class DeviceLayer:
     def __init__(self, shape: synth.Shape, weight_seed: int, layer: int = 0, beta=None,
                  max_tokens: int = 16, device="cuda:0", chunk_records: int = 32,

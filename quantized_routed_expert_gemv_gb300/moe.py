@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in ``include/moe.h`` (ctypes, marshalling only).
+"""Python binding of the C ABI in ``include/moe.h`` and ``include/moe_block.h``
+(ctypes, marshalling only).
 
 Every function keeps the C name and takes raw addresses (ints) for device and
 host buffers, exactly like the C call.  No step of the layer runs here: if
@@ -53,6 +54,27 @@ class moe_residency_stats_t(ctypes.Structure):
                 ("lookahead_hits", ctypes.c_uint64), ("lookahead_bytes", ctypes.c_uint64)]
 
 
+# element types of the operators in include/moe_block.h
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+
+
+class moe_block_norm_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("y", "h", "gate", "w_post", "w_pre", "h_out", "x_out")] +
+                [(n, ctypes.c_int64) for n in ("ld_y", "ld_h", "ld_gate_row", "ld_gate_col", "ld_h_out",
+                                               "ld_x_out")] +
+                [(n, ctypes.c_int32) for n in ("rows", "hidden", "y_type", "h_type", "gate_type", "w_type",
+                                               "x_type", "post_norm", "pre_norm")] +
+                [(n, ctypes.c_float) for n in ("w_add", "eps", "residual_scale")])
+
+
+class moe_token_logprobs_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "targets", "target_logprobs", "target_ranks", "entropy",
+                                                "lse", "top_ids", "top_logprobs")] +
+                [("ld_logits", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("rows", "vocab", "logits_type", "n_targets", "top_n")] +
+                [("scale", ctypes.c_float)])
+
+
 class MoEError(RuntimeError):
     def __init__(self, code: int, where: str, msg: str):
         super().__init__(f"{where}: {ERROR_NAMES.get(code, code)}: {msg}")
@@ -93,6 +115,8 @@ SIGNATURES = {
     "moe_crc32": (ctypes.c_uint32, [_vp, _sz]),
     "moe_residency_lookahead": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "moe_rvq_record_layout_of": (ctypes.c_int, [_i32, _i32, ctypes.POINTER(moe_record_layout)]),
+    "moe_block_norm": (ctypes.c_int, [ctypes.POINTER(moe_block_norm_args), _vp]),
+    "moe_token_logprobs": (ctypes.c_int, [ctypes.POINTER(moe_token_logprobs_args), _vp]),
 }
 
 
@@ -236,3 +260,11 @@ def moe_residency_close(res: int) -> None:
 def moe_check(layer: int, ws: int, stream: int = 0) -> int:
     """Returns the device-latched status code (MOE_OK, MOE_ERR_TIMEOUT, ...)."""
     return int(lib().moe_check(layer, ws, stream))
+
+
+def moe_block_norm(args: moe_block_norm_args, stream: int = 0) -> None:
+    check(lib().moe_block_norm(args, stream), "moe_block_norm")
+
+
+def moe_token_logprobs(args: moe_token_logprobs_args, stream: int = 0) -> None:
+    check(lib().moe_token_logprobs(args, stream), "moe_token_logprobs")

@@ -1,4 +1,4 @@
-"""Builds libmoe.so (the C ABI of include/moe.h and include/moe_block.h) in-tree with nvcc for sm_103a.
+"""Builds libmoe.so (the C ABI of include/moe*.h) in-tree with nvcc for sm_103a.
 
 Each .cu file is compiled to an object in parallel, then linked into
 ``quantized_routed_expert_gemv_gb300/libmoe.so``.  nvcc cross-compiles, so
@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 SO = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "decode.cu", "decode_b1.cu", "decode_bt.cu", "prefill.cu", "residency.cu", "noalloc.cu",
-           "rvq.cu", "block_norm.cu", "token_logprobs.cu"]
+           "rvq.cu", "block_norm.cu", "token_logprobs.cu", "fp8.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tcgen05.cuh", "tma.cuh", "gemv.cuh", "fused.cuh", "elem.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
@@ -30,7 +30,7 @@ def _nvcc():
 
 def _deps():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files += [os.path.join(ROOT, "include", h) for h in ("moe.h", "moe_block.h")]
+    files += [os.path.join(ROOT, "include", h) for h in ("moe.h", "moe_block.h", "moe_fp8.h")]
     return [f for f in files if os.path.exists(f)]
 
 

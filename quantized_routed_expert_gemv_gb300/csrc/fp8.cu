@@ -1,0 +1,651 @@
+// fp8.cu -- linear layers in 8-bit floating point (include/moe_fp8.h).
+//
+// Mathematics: with 128 inputs to a block b,
+//     out[t][n] = sum_b (xs[t][b] ws[n/128][b]) sum_{k in b} xq[t][k] w[n][k].
+// The inner sums are products of e4m3 codes on the tensor cores
+// (tcgen05.mma kind::f8f6f4, fp32 accumulators in tensor memory, one fresh
+// accumulator per block); the outer sum adds the scaled block sums in fp32
+// registers.
+//
+// Layout: 128 outputs (weight rows) are the MMA's M, so a tile's weight scale
+// is one number per block; BN rows of x are its N.  Few rows of x thus leave
+// no tensor-core row idle, and the weights, which bound that case, are read
+// once.  Roles: one warp loads (TMA tiles of w, bulk copies of x), one issues
+// the MMAs, one multiplies the scales of each block into shared memory, four
+// or eight read the accumulators.  Accumulators are double or quadruple
+// buffered in tensor memory, so the MMAs of the next blocks run while a block
+// is scaled.
+//
+// Bound: reading w for few rows, the tensor cores for many.  With fewer tiles
+// than SMs a cluster of 2, 4 or 8 CTAs splits the blocks of a tile and joins
+// its partial sums through distributed shared memory in rank order.
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe_fp8.h"
+#include "common.cuh"
+#include "elem.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+int reportf(int code, const char* fmt, ...);
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kBlk = 128;              // inputs per scale block, and outputs per tile
+constexpr int kTileW = kBlk * kBlk;    // bytes of a weight tile
+constexpr int kScaleRing = 8;          // blocks of prepared scales
+constexpr size_t kCtlBytes = 256;      // control words at the workspace's start ([0] error bits)
+constexpr int kMaxRows = 1 << 20;
+constexpr uint32_t kMagic = 0x4D6F4638u;
+
+// Workspace: control words, xs [blocks][rows_pad] floats, then the codes of x
+// as tiles [row tile of bn][block][bn rows x 128 bytes], each in the 128-byte
+// swizzled order the tensor core reads (16-byte piece p of row r at
+// r * 128 + ((p ^ (r & 7)) << 4)), so a plain bulk copy loads a tile.
+struct Layout {
+  int bn, row_tiles, rows_pad, blocks;
+  size_t xs, codes, bytes;
+};
+
+int tile_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+
+Layout layout_of(int rows, int k) {
+  Layout l;
+  l.bn = tile_rows(rows);
+  l.row_tiles = (rows + l.bn - 1) / l.bn;
+  l.rows_pad = l.row_tiles * l.bn;
+  l.blocks = (k + kBlk - 1) / kBlk;
+  l.xs = kCtlBytes;
+  l.codes = (l.xs + sizeof(float) * static_cast<size_t>(l.blocks) * l.rows_pad + 1023) / 1024 * 1024;
+  l.bytes = l.codes + static_cast<size_t>(l.blocks) * l.rows_pad * kBlk;
+  return l;
+}
+
+// ---- quantisation of x -----------------------------------------------------------
+
+struct QuantArgs {
+  const void* x;
+  int64_t ld;
+  int type, rows, k, blocks, rows_pad, bn, vec;
+  float* xs;
+  uint8_t* codes;
+};
+
+// The scale of a block whose largest |x| has these bits: the smallest power
+// of two s >= 2^-126 with max <= 448 s (448 = 1.75 * 2^8), 1 for zeros, NaN
+// if there is an infinity or a NaN.  `inv` is 1 / s (0 for NaN).
+__device__ __forceinline__ float block_scale(uint32_t max_bits, float& inv) {
+  if (max_bits == 0) return inv = 1.0f;
+  if (max_bits >= 0x7F800000u) {
+    inv = 0.0f;
+    return __uint_as_float(0x7FC00000u);
+  }
+  int p = static_cast<int>(max_bits >> 23) - 127 - ((max_bits & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
+  p = max(p, -126);
+  inv = __uint_as_float(static_cast<uint32_t>(127 - p) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + p) << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Eight threads per (row, block), 16 inputs each.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs q) {
+  pdl_launch_dependents();
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+  const int piece = threadIdx.x & 7;
+  const bool in = unit < static_cast<int64_t>(q.rows) * q.blocks;
+  const int row = in ? static_cast<int>(unit / q.blocks) : 0, b = in ? static_cast<int>(unit % q.blocks) : 0;
+  const int j = b * kBlk + piece * 16;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  if (in) {
+    const int64_t at = static_cast<int64_t>(row) * q.ld;
+    if (q.vec && j + 16 <= q.k) {
+      float a[8], c[8];
+      load8(q.x, q.type, at + j, a);
+      load8(q.x, q.type, at + j + 8, c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = a[i], v[8 + i] = c[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (j + i < q.k) v[i] = load_elem(q.x, q.type, at + j + i);
+    }
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float inv;
+  const float s = block_scale(m, inv);
+  if (!in) return;
+  uint4 w;
+  w.x = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  w.y = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  w.z = e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv);
+  w.w = e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv);
+  const int tile = row / q.bn, r = row % q.bn;
+  uint8_t* t = q.codes + (static_cast<size_t>(tile) * q.blocks + b) * (static_cast<size_t>(q.bn) * kBlk);
+  *reinterpret_cast<uint4*>(t + r * kBlk + ((piece ^ (r & 7)) << 4)) = w;
+  if (piece == 0) q.xs[static_cast<size_t>(b) * q.rows_pad + row] = s;
+}
+
+// One 128 x 128 block of weights per thread block.
+__global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, int type, int64_t ld, int n, int k,
+                                                               uint8_t* codes, int64_t ldc, float* scales) {
+  __shared__ uint32_t wmax[8];
+  const int nb = blockIdx.y, kb = blockIdx.x;
+  uint32_t m = 0;
+  for (int i = threadIdx.x; i < kBlk * kBlk; i += 256) {
+    const int r = nb * kBlk + i / kBlk, c = kb * kBlk + i % kBlk;
+    if (r < n && c < k) m = max(m, __float_as_uint(load_elem(w, type, r * ld + c)) & 0x7FFFFFFFu);
+  }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, wmax[i]);
+  const float s = m ? __uint_as_float(m) / 448.0f : 1.0f;
+  if (threadIdx.x == 0) scales[static_cast<size_t>(nb) * gridDim.x + kb] = s;
+  for (int i = threadIdx.x; i < kBlk * kBlk; i += 256) {
+    const int r = nb * kBlk + i / kBlk;
+    const int64_t c = static_cast<int64_t>(kb) * kBlk + i % kBlk;
+    if (r >= n || c >= ldc) continue;
+    const float v = c < k ? load_elem(w, type, r * ld + c) / s : 0.0f;
+    codes[r * ldc + c] = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
+// ---- tensor-core helpers -------------------------------------------------------------
+
+// 128-byte swizzled K-major operand: rows of 128 bytes, groups of 8 rows
+// 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= 1ull << 16;                                   // leading offset: unused with a swizzle
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // stride offset
+  d |= 1ull << 46;                                   // descriptor version
+  d |= 2ull << 61;                                   // 128-byte swizzle
+  return d;
+}
+
+// kind::f8f6f4: fp32 accumulator, e4m3 A and B, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Sixteen consecutive columns of this warp's 32 lanes; asynchronous until tmem_wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// ---- the product -----------------------------------------------------------------------
+
+struct GemmArgs {
+  const float* ws;       // [row block of w][blocks]
+  const float* xs;       // [blocks][rows_pad]
+  const uint8_t* codes;  // tiles of x
+  void* out;
+  int64_t ld_out;
+  int out_type;
+  int n, rows, rows_pad, blocks;
+  int tiles_n, tiles_m, split;
+  unsigned* ctl;
+};
+
+template <int BN>
+struct Cfg {
+  static constexpr int kEpi = BN >= 128 ? 8 : 4;               // warps that read accumulators
+  static constexpr int kThreads = 128 + 32 * kEpi;
+  static constexpr int kCols = BN / (kEpi / 4);                // columns per thread
+  static constexpr int kBuf = BN == 256 ? 2 : 4;               // accumulators in tensor memory
+  static constexpr uint32_t kTmem = BN * kBuf < 32 ? 32 : BN * kBuf;
+  static constexpr int kStage = kTileW + BN * kBlk;
+  static constexpr int kStages = (200 * 1024) / kStage < 8 ? (200 * 1024) / kStage : 8;
+  static constexpr int kScaleOff = kStages * kStage;           // [kScaleRing][BN] floats
+  static constexpr int kBarOff = kScaleOff + kScaleRing * BN * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kBuf + 2 * kScaleRing + 1;
+  static constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;  // + alignment of the base
+};
+
+template <int BN>
+__global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
+    fp8_gemm_kernel(const GemmArgs g, const __grid_constant__ CUtensorMap wmap) {
+  using C = Cfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  float* scale_ring = reinterpret_cast<float*>(sm + C::kScaleOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kBarOff);
+  uint64_t *full = bars, *empty = full + C::kStages, *tfull = empty + C::kStages, *tempty = tfull + C::kBuf,
+           *sfull = tempty + C::kBuf, *sempty = sfull + kScaleRing, *done = sempty + kScaleRing;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = g.split;
+  const int part = split > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  const int worker = blockIdx.x / split, workers = gridDim.x / split;
+  const int tiles = g.tiles_n * g.tiles_m;
+  const int b0 = static_cast<int>(static_cast<int64_t>(g.blocks) * part / split);
+  const int b1 = static_cast<int>(static_cast<int64_t>(g.blocks) * (part + 1) / split);
+  const int nb = b1 - b0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+    for (int i = 0; i < C::kBuf; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, C::kEpi);
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(sfull + i, 1), mbar_init(sempty + i, C::kEpi);
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_u32(slot), C::kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  bool ok = true;
+
+  if (warp == 0) {
+    // loads: the weight tiles of the first stages do not depend on the
+    // quantisation kernel before this one
+    if (lane == 0) {
+      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
+      const uint64_t wpol = g.tiles_m == 1 ? once : keep;
+      const int total = ((tiles - worker + workers - 1) / workers) * nb;
+      const int ahead = min(total, C::kStages);
+      auto load_w = [&](int s, int tile, int b) {
+        uint8_t* st = sm + s * C::kStage;
+        const int rows = min(BN, g.rows - (tile % g.tiles_m) * BN);
+        const uint32_t xbytes = (rows + 7) / 8 * 1024;
+        mbar_arrive_expect_tx(full + s, kTileW + xbytes);
+        tma_load_2d(st, &wmap, b * kBlk, (tile / g.tiles_m) * kBlk, full + s, wpol);
+      };
+      auto load_x = [&](int s, int tile, int b) {
+        const int mt = tile % g.tiles_m, rows = min(BN, g.rows - mt * BN);
+        bulk_g2s(sm + s * C::kStage + kTileW,
+                 g.codes + (static_cast<size_t>(mt) * g.blocks + b) * (static_cast<size_t>(BN) * kBlk),
+                 (rows + 7) / 8 * 1024, full + s);
+      };
+      for (int i = 0; i < ahead; ++i) load_w(i, worker + (i / nb) * workers, b0 + i % nb);
+      pdl_wait();
+      for (int i = 0; i < ahead; ++i) load_x(i, worker + (i / nb) * workers, b0 + i % nb);
+      RingPos p;
+      int issued = ahead;
+      if (ahead == C::kStages) p.ph = 1;
+      else p.s = ahead;
+      int tile = worker + (ahead / nb) * workers, b = ahead % nb;
+      for (; issued < total; ++issued) {
+        if (!mbar_wait(empty + p.s, p.ph ^ 1u)) {
+          ok = false;
+          break;
+        }
+        load_w(p.s, tile, b0 + b);
+        load_x(p.s, tile, b0 + b);
+        p.next(C::kStages);
+        if (++b == nb) b = 0, tile += workers;
+      }
+      // a run that gave up leaves no copy in flight
+      if (!ok) {
+        latch_error(g.ctl, kErrTimeout);
+        for (int i = max(0, issued - C::kStages); i < issued; ++i)
+          mbar_wait(full + i % C::kStages, static_cast<uint32_t>(i / C::kStages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(kBlk, BN);
+      RingPos p, t;
+      for (int tile = worker; ok && tile < tiles; tile += workers) {
+        for (int b = 0; b < nb; ++b) {
+          ok = mbar_wait(tempty + t.s, t.ph ^ 1u) && mbar_wait(full + p.s, p.ph);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t wd = desc_sw128(smem_u32(sm + p.s * C::kStage));
+          const uint64_t xd = desc_sw128(smem_u32(sm + p.s * C::kStage + kTileW));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3(tmem + t.s * BN, wd + 2 * k, xd + 2 * k, idesc, k > 0);
+          mma_commit(smem_u32(empty + p.s));
+          mma_commit(smem_u32(tfull + t.s));
+          p.next(C::kStages);
+          t.next(C::kBuf);
+        }
+      }
+      mma_commit(smem_u32(done));
+      if (!mbar_wait(done, 0)) ok = false;
+      if (!ok) latch_error(g.ctl, kErrTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // scales: xs[b][rows of the tile] * ws[tile][b], kScaleRing blocks ahead
+    pdl_wait();
+    RingPos p;
+    for (int tile = worker; ok && tile < tiles; tile += workers) {
+      const float* ws = g.ws + static_cast<size_t>(tile / g.tiles_m) * g.blocks;
+      const float* xs = g.xs + (tile % g.tiles_m) * BN;
+      for (int b = b0; b < b1; ++b) {
+        const float w = ws[b];
+        float v[(BN + 31) / 32];
+#pragma unroll
+        for (int i = 0; i < (BN + 31) / 32; ++i)
+          v[i] = 32 * i + lane < BN ? xs[static_cast<size_t>(b) * g.rows_pad + 32 * i + lane] * w : 0.0f;
+        if (!mbar_wait_warp(sempty + p.s, p.ph ^ 1u)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int i = 0; i < (BN + 31) / 32; ++i)
+          if (32 * i + lane < BN) scale_ring[p.s * BN + 32 * i + lane] = v[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull + p.s);
+        p.next(kScaleRing);
+      }
+    }
+    if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
+  } else if (warp >= 4) {
+    const int quad = warp & 3, col0 = ((warp - 4) >> 2) * C::kCols;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    RingPos t, p;
+    for (int tile = worker; ok && tile < tiles; tile += workers) {
+      float acc[C::kCols];
+#pragma unroll
+      for (int c = 0; c < C::kCols; ++c) acc[c] = 0.0f;
+      for (int b = 0; b < nb; ++b) {
+        ok = mbar_wait_warp(sfull + p.s, p.ph) && mbar_wait_warp(tfull + t.s, t.ph);
+        if (!ok) break;
+        tc_fence_after();
+        const float4* sc = reinterpret_cast<const float4*>(scale_ring + p.s * BN + col0);
+#pragma unroll
+        for (int c = 0; c < C::kCols; c += 16) {
+          uint32_t d[16];
+          tmem_ld16(tmem + lane_base + t.s * BN + col0 + c, d);
+          tmem_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 s = sc[c / 4 + i];
+            acc[c + 4 * i] = fmaf(__uint_as_float(d[4 * i]), s.x, acc[c + 4 * i]);
+            acc[c + 4 * i + 1] = fmaf(__uint_as_float(d[4 * i + 1]), s.y, acc[c + 4 * i + 1]);
+            acc[c + 4 * i + 2] = fmaf(__uint_as_float(d[4 * i + 2]), s.z, acc[c + 4 * i + 2]);
+            acc[c + 4 * i + 3] = fmaf(__uint_as_float(d[4 * i + 3]), s.w, acc[c + 4 * i + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty + t.s), mbar_arrive(sempty + p.s);
+        t.next(C::kBuf);
+        p.next(kScaleRing);
+      }
+      if (!ok) break;
+      const int n = (tile / g.tiles_m) * kBlk + quad * 32 + lane;
+      if (split == 1) {
+        const int t0 = (tile % g.tiles_m) * BN + col0;
+#pragma unroll
+        for (int c = 0; c < C::kCols; ++c)
+          if (n < g.n && t0 + c < g.rows) store_elem(g.out, g.out_type, (t0 + c) * g.ld_out + n, acc[c]);
+      } else {
+        // the ring is idle now: every copy and MMA of this CTA's one tile is done
+        float* partial = reinterpret_cast<float*>(sm);
+#pragma unroll
+        for (int c = 0; c < C::kCols; ++c) partial[(col0 + c) * kBlk + quad * 32 + lane] = acc[c];
+      }
+    }
+    if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
+  }
+
+  if (split > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const int tile = worker;
+    const int mt = tile % g.tiles_m, rows = min(BN, g.rows - mt * BN);
+    if (threadIdx.x >= 128) {
+      const int r = threadIdx.x & 127, n = (tile / g.tiles_m) * kBlk + r;
+      for (int c = part + split * ((threadIdx.x >> 7) - 1); c < rows; c += split * (C::kEpi / 4)) {
+        float s = 0.0f;
+        for (int q = 0; q < split; ++q)
+          s += cluster.map_shared_rank(reinterpret_cast<float*>(sm), q)[c * kBlk + r];
+        if (n < g.n) store_elem(g.out, g.out_type, static_cast<int64_t>(mt * BN + c) * g.ld_out + n, s);
+      }
+    }
+    cluster.sync();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmem);
+}
+
+template <int BN>
+cudaError_t launch_gemm(const GemmArgs& g, const CUtensorMap& map, int grid, cudaStream_t st) {
+  static_assert(Cfg<BN>::kStages >= 2 && Cfg<BN>::kStages * Cfg<BN>::kStage >= BN * kBlk * 4, "ring");
+  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
+  if (e) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Cfg<BN>::kThreads);
+  cfg.dynamicSmemBytes = Cfg<BN>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = g.split;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN>, g, map);
+}
+
+}  // namespace
+}  // namespace moe
+
+struct moe_fp8 {
+  uint32_t magic;
+  int n, k, device, num_sms;
+  const float* scales;
+  CUtensorMap map;
+};
+
+using namespace moe;
+
+static bool handle_ok(const moe_fp8* w) { return w && w->magic == kMagic; }
+
+extern "C" int moe_fp8_open(int32_t n, int32_t k, const uint8_t* codes, int64_t ld_codes, const float* scales,
+                            moe_fp8** out) {
+  if (!out) return reportf(MOE_ERR_ARG, "moe_fp8_open: out is NULL");
+  *out = nullptr;
+  if (n < 1 || n > (1 << 24) || k < 1 || k > 65536)
+    return reportf(MOE_ERR_ARG, "moe_fp8_open: n=%d must be in [1, 2^24], k=%d in [1, 65536]", n, k);
+  if (!codes || !scales) return reportf(MOE_ERR_ARG, "moe_fp8_open: codes or scales is NULL");
+  if (ld_codes < k || ld_codes % 16 || ld_codes > (1ll << 32))
+    return reportf(MOE_ERR_ARG, "moe_fp8_open: ld_codes=%lld must be a multiple of 16 and at least k=%d",
+                   static_cast<long long>(ld_codes), k);
+  if (reinterpret_cast<uintptr_t>(codes) % 16 || reinterpret_cast<uintptr_t>(scales) % 4)
+    return reportf(MOE_ERR_ALIGN, "moe_fp8_open: codes must be 16-byte aligned, scales 4-byte");
+  int dev = 0, major = 0, minor = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (!e) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (!e) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (!e) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e) return reportf(MOE_ERR_CUDA, "moe_fp8_open: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  if (major != 10 || minor != 3)
+    return reportf(MOE_ERR_UNSUPPORTED, "moe_fp8_open: device %d is sm_%d%d; this library is built for sm_103a", dev,
+                   major, minor);
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
+    return reportf(MOE_ERR_CUDA, "moe_fp8_open: no cuTensorMapEncodeTiled in this driver");
+  moe_fp8* w = new (std::nothrow) moe_fp8;
+  if (!w) return reportf(MOE_ERR_NOMEM, "moe_fp8_open: out of host memory");
+  w->magic = kMagic, w->n = n, w->k = k, w->device = dev, w->num_sms = sms, w->scales = scales;
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(n)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld_codes)};
+  const cuuint32_t box[2] = {kBlk, kBlk}, es[2] = {1, 1};
+  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  if (reinterpret_cast<EncodeFn>(fn)(&w->map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dim, stride,
+                                     box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+      CUDA_SUCCESS) {
+    delete w;
+    return reportf(MOE_ERR_CUDA, "moe_fp8_open: cuTensorMapEncodeTiled refused n=%d k=%d ld_codes=%lld", n, k,
+                   static_cast<long long>(ld_codes));
+  }
+  *out = w;
+  return MOE_OK;
+}
+
+extern "C" void moe_fp8_close(moe_fp8* w) {
+  if (!handle_ok(w)) return;
+  w->magic = 0;
+  delete w;
+}
+
+extern "C" size_t moe_fp8_workspace_bytes(const moe_fp8* w, int32_t max_rows) {
+  if (!handle_ok(w) || max_rows < 1 || max_rows > kMaxRows) return 0;
+  // the tile height grows with the rows, so fewer rows never need more: the
+  // padded rows of any smaller count stay within 16, 32, ... or a multiple of 256
+  return layout_of(max_rows, w->k).bytes;
+}
+
+extern "C" int moe_fp8_workspace_init(const moe_fp8* w, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!handle_ok(w)) return reportf(MOE_ERR_ARG, "moe_fp8_workspace_init: invalid handle");
+  if (!workspace || workspace_bytes < kCtlBytes)
+    return reportf(MOE_ERR_ARG, "moe_fp8_workspace_init: workspace is NULL or has %zu bytes", workspace_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return reportf(MOE_ERR_ALIGN, "moe_fp8_workspace_init: workspace must be 256-byte aligned");
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, kCtlBytes, static_cast<cudaStream_t>(stream));
+  if (e) return reportf(MOE_ERR_CUDA, "moe_fp8_workspace_init: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  return MOE_OK;
+}
+
+extern "C" int moe_fp8_linear(moe_fp8* w, const void* x, int32_t x_type, int64_t ld_x, int32_t rows, void* out,
+                              int32_t out_type, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!handle_ok(w)) return reportf(MOE_ERR_ARG, "moe_fp8_linear: invalid handle");
+  if (rows < 0 || rows > kMaxRows) return reportf(MOE_ERR_ARG, "moe_fp8_linear: rows=%d must be in [0, %d]", rows, kMaxRows);
+  if (rows == 0) return MOE_OK;
+  if (!x || !out || !workspace) return reportf(MOE_ERR_ARG, "moe_fp8_linear: x, out or workspace is NULL");
+  if (!elem_type_ok(x_type) || !elem_type_ok(out_type))
+    return reportf(MOE_ERR_ARG, "moe_fp8_linear: unknown type (x %d, out %d)", x_type, out_type);
+  if (ld_x < w->k || ld_out < w->n)
+    return reportf(MOE_ERR_ARG, "moe_fp8_linear: ld_x=%lld is below k=%d or ld_out=%lld below n=%d",
+                   static_cast<long long>(ld_x), w->k, static_cast<long long>(ld_out), w->n);
+  if (reinterpret_cast<uintptr_t>(x) % elem_size(x_type) || reinterpret_cast<uintptr_t>(out) % elem_size(out_type) ||
+      reinterpret_cast<uintptr_t>(workspace) % 256)
+    return reportf(MOE_ERR_ALIGN, "moe_fp8_linear: x or out is not aligned to its elements, or workspace to 256 bytes");
+  const Layout l = layout_of(rows, w->k);
+  if (workspace_bytes < l.bytes)
+    return reportf(MOE_ERR_ARG, "moe_fp8_linear: %d rows need %zu bytes of workspace, got %zu", rows, l.bytes,
+                   workspace_bytes);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+
+  QuantArgs q;
+  q.x = x, q.ld = ld_x, q.type = x_type, q.rows = rows, q.k = w->k;
+  q.blocks = l.blocks, q.rows_pad = l.rows_pad, q.bn = l.bn;
+  q.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld_x * elem_size(x_type) % 16 == 0;
+  q.xs = reinterpret_cast<float*>(base + l.xs), q.codes = base + l.codes;
+  const int64_t units = static_cast<int64_t>(rows) * l.blocks;
+  quantize_rows_kernel<<<static_cast<unsigned>((units + 31) / 32), 256, 0, st>>>(q);
+  cudaError_t e = cudaGetLastError();
+  if (!e) {
+    GemmArgs g;
+    g.ws = w->scales, g.xs = q.xs, g.codes = q.codes;
+    g.out = out, g.ld_out = ld_out, g.out_type = out_type;
+    g.n = w->n, g.rows = rows, g.rows_pad = l.rows_pad, g.blocks = l.blocks;
+    g.tiles_n = (w->n + kBlk - 1) / kBlk, g.tiles_m = l.row_tiles;
+    g.ctl = reinterpret_cast<unsigned*>(base);
+    const int64_t tiles = static_cast<int64_t>(g.tiles_n) * g.tiles_m;
+    if (tiles > 0x3FFFFFFF) return reportf(MOE_ERR_ARG, "moe_fp8_linear: %d rows x %d outputs are too many tiles", rows, w->n);
+    g.split = 1;
+    while (g.split < 8 && tiles * g.split * 2 <= w->num_sms && g.split * 2 <= l.blocks) g.split *= 2;
+    const int grid = g.split > 1 ? static_cast<int>(tiles) * g.split
+                                 : static_cast<int>(tiles < w->num_sms ? tiles : w->num_sms);
+    switch (l.bn) {
+      case 16: e = launch_gemm<16>(g, w->map, grid, st); break;
+      case 32: e = launch_gemm<32>(g, w->map, grid, st); break;
+      case 64: e = launch_gemm<64>(g, w->map, grid, st); break;
+      case 128: e = launch_gemm<128>(g, w->map, grid, st); break;
+      default: e = launch_gemm<256>(g, w->map, grid, st); break;
+    }
+  }
+  if (e) return reportf(MOE_ERR_CUDA, "moe_fp8_linear: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  return MOE_OK;
+}
+
+extern "C" int moe_fp8_check(const moe_fp8* w, void* workspace, void* stream) {
+  if (!handle_ok(w)) return reportf(MOE_ERR_ARG, "moe_fp8_check: invalid handle");
+  if (!workspace) return reportf(MOE_ERR_ARG, "moe_fp8_check: workspace is NULL");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned bits = 0;
+  cudaError_t e = cudaMemcpyAsync(&bits, workspace, sizeof bits, cudaMemcpyDeviceToHost, st);
+  if (!e) e = cudaStreamSynchronize(st);
+  if (!e && bits) {
+    e = cudaMemsetAsync(workspace, 0, kCtlBytes, st);
+    if (!e) e = cudaStreamSynchronize(st);
+  }
+  if (e) return reportf(MOE_ERR_CUDA, "moe_fp8_check: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  if (bits) return reportf(MOE_ERR_TIMEOUT, "moe_fp8_check: a bounded device-side wait ran out (bits 0x%x)", bits);
+  return MOE_OK;
+}
+
+extern "C" int moe_fp8_quantize_weights(const void* weights, int32_t w_type, int64_t ld_w, int32_t n, int32_t k,
+                                        uint8_t* codes, int64_t ld_codes, float* scales, void* stream) {
+  if (n < 1 || n > (1 << 24) || k < 1 || k > 65536)
+    return reportf(MOE_ERR_ARG, "moe_fp8_quantize_weights: n=%d must be in [1, 2^24], k=%d in [1, 65536]", n, k);
+  if (!weights || !codes || !scales) return reportf(MOE_ERR_ARG, "moe_fp8_quantize_weights: a pointer is NULL");
+  if (!elem_type_ok(w_type)) return reportf(MOE_ERR_ARG, "moe_fp8_quantize_weights: unknown type %d", w_type);
+  if (ld_w < k || ld_codes < k || ld_codes % 16)
+    return reportf(MOE_ERR_ARG, "moe_fp8_quantize_weights: ld_w=%lld and ld_codes=%lld must be at least k=%d, ld_codes a multiple of 16",
+                   static_cast<long long>(ld_w), static_cast<long long>(ld_codes), k);
+  if (reinterpret_cast<uintptr_t>(weights) % elem_size(w_type) || reinterpret_cast<uintptr_t>(codes) % 16 ||
+      reinterpret_cast<uintptr_t>(scales) % 4)
+    return reportf(MOE_ERR_ALIGN, "moe_fp8_quantize_weights: a pointer is misaligned");
+  const int nblocks = (n + kBlk - 1) / kBlk;
+  // row blocks in the grid's y, which is limited to 65535
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int kblocks = (k + kBlk - 1) / kBlk;
+  for (int r0 = 0; r0 < nblocks; r0 += 65535) {
+    const int cnt = nblocks - r0 < 65535 ? nblocks - r0 : 65535;
+    const int64_t row = static_cast<int64_t>(r0) * kBlk;
+    quantize_weights_kernel<<<dim3(kblocks, cnt), 256, 0, st>>>(
+        static_cast<const char*>(weights) + row * ld_w * elem_size(w_type), w_type, ld_w, n - static_cast<int>(row), k,
+        codes + row * ld_codes, ld_codes, scales + static_cast<size_t>(r0) * kblocks);
+    const cudaError_t e = cudaGetLastError();
+    if (e) return reportf(MOE_ERR_CUDA, "moe_fp8_quantize_weights: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  }
+  return MOE_OK;
+}

@@ -102,6 +102,59 @@ def token_logprobs(logits: torch.Tensor, targets=None, top_n: int = 0, scale: fl
     return out
 
 
+class Fp8Linear:
+    """A linear layer in 8-bit floating point (moe_fp8_*): codes uint8
+    [n][ld] with ld a multiple of 16 (e4m3, k of each row used), scales float
+    [ceil(n/128)][ceil(k/128)].  Owns the handle and a workspace for up to
+    max_rows rows."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, k: int, max_rows: int, stream=None):
+        self.codes, self.scales, self.k, self.n = codes, scales, k, codes.shape[0]
+        self.max_rows = max_rows
+        assert scales.is_contiguous() and scales.dtype == torch.float32
+        assert scales.shape == (-(-self.n // 128), -(-k // 128))
+        self.handle = moe.moe_fp8_open(self.n, k, codes.data_ptr(), _ld(codes), scales.data_ptr())
+        self.ws_bytes = moe.moe_fp8_workspace_bytes(self.handle, max_rows)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=codes.device)
+        self.ws_ptr = self.ws.data_ptr()
+        moe.moe_fp8_workspace_init(self.handle, self.ws_ptr, self.ws_bytes, _stream(codes.device, stream))
+
+    @classmethod
+    def from_weights(cls, weights: torch.Tensor, max_rows: int, stream=None):
+        """Quantises device weights [n][k] (moe_fp8_quantize_weights)."""
+        n, k = weights.shape
+        ld = -(-k // 16) * 16
+        codes = torch.empty(n, ld, dtype=torch.uint8, device=weights.device)
+        scales = torch.empty(-(-n // 128), -(-k // 128), dtype=torch.float32, device=weights.device)
+        moe.moe_fp8_quantize_weights(weights.data_ptr(), _ELEM_TYPE[weights.dtype], _ld(weights), n, k,
+                                     codes.data_ptr(), ld, scales.data_ptr(), _stream(weights.device, stream))
+        return cls(codes, scales, k, max_rows, stream)
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, out_type=torch.bfloat16, stream=None):
+        """x [rows][k] -> [rows][n]."""
+        rows = x.shape[0]
+        assert x.shape[1] == self.k
+        if out is None:
+            out = torch.empty(rows, self.n, dtype=out_type, device=x.device)
+        moe.moe_fp8_linear(self.handle, x.data_ptr(), _ELEM_TYPE[x.dtype], _ld(x), rows, out.data_ptr(),
+                           _ELEM_TYPE[out.dtype], _ld(out), self.ws_ptr, self.ws_bytes, _stream(x.device, stream))
+        return out
+
+    def check(self, stream=None) -> int:
+        return moe.moe_fp8_check(self.handle, self.ws_ptr, _stream(self.codes.device, stream))
+
+    def close(self):
+        if self.handle:
+            moe.moe_fp8_close(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
 class DeviceLayer:
     def __init__(self, shape: synth.Shape, weight_seed: int, layer: int = 0, beta=None,
                  max_tokens: int = 16, device="cuda:0", chunk_records: int = 32,

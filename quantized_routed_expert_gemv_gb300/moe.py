@@ -1,5 +1,5 @@
-"""Python binding of the C ABI in ``include/moe.h`` and ``include/moe_block.h``
-(ctypes, marshalling only).
+"""Python binding of the C ABI in ``include/moe.h``, ``include/moe_block.h`` and
+``include/moe_fp8.h`` (ctypes, marshalling only).
 
 Every function keeps the C name and takes raw addresses (ints) for device and
 host buffers, exactly like the C call.  No step of the layer runs here: if
@@ -117,6 +117,15 @@ SIGNATURES = {
     "moe_rvq_record_layout_of": (ctypes.c_int, [_i32, _i32, ctypes.POINTER(moe_record_layout)]),
     "moe_block_norm": (ctypes.c_int, [ctypes.POINTER(moe_block_norm_args), _vp]),
     "moe_token_logprobs": (ctypes.c_int, [ctypes.POINTER(moe_token_logprobs_args), _vp]),
+    "moe_fp8_open": (ctypes.c_int, [_i32, _i32, _vp, ctypes.c_int64, _vp, ctypes.POINTER(_vp)]),
+    "moe_fp8_close": (None, [_vp]),
+    "moe_fp8_workspace_bytes": (_sz, [_vp, _i32]),
+    "moe_fp8_workspace_init": (ctypes.c_int, [_vp, _vp, _sz, _vp]),
+    "moe_fp8_linear": (ctypes.c_int, [_vp, _vp, _i32, ctypes.c_int64, _i32, _vp, _i32, ctypes.c_int64, _vp, _sz,
+                                      _vp]),
+    "moe_fp8_check": (ctypes.c_int, [_vp, _vp, _vp]),
+    "moe_fp8_quantize_weights": (ctypes.c_int, [_vp, _i32, ctypes.c_int64, _i32, _i32, _vp, ctypes.c_int64, _vp,
+                                                _vp]),
 }
 
 
@@ -268,3 +277,36 @@ def moe_block_norm(args: moe_block_norm_args, stream: int = 0) -> None:
 
 def moe_token_logprobs(args: moe_token_logprobs_args, stream: int = 0) -> None:
     check(lib().moe_token_logprobs(args, stream), "moe_token_logprobs")
+
+
+def moe_fp8_open(n: int, k: int, codes: int, ld_codes: int, scales: int) -> int:
+    h = _vp()
+    check(lib().moe_fp8_open(n, k, codes, ld_codes, scales, ctypes.byref(h)), "moe_fp8_open")
+    return h.value
+
+
+def moe_fp8_close(w: int) -> None:
+    lib().moe_fp8_close(w)
+
+
+def moe_fp8_workspace_bytes(w: int, max_rows: int) -> int:
+    return int(lib().moe_fp8_workspace_bytes(w, max_rows))
+
+
+def moe_fp8_workspace_init(w: int, ws: int, nbytes: int, stream: int = 0) -> None:
+    check(lib().moe_fp8_workspace_init(w, ws, nbytes, stream), "moe_fp8_workspace_init")
+
+
+def moe_fp8_linear(w, x, x_type, ld_x, rows, out, out_type, ld_out, ws, ws_bytes, stream=0) -> None:
+    check(lib().moe_fp8_linear(w, x, x_type, ld_x, rows, out, out_type, ld_out, ws, ws_bytes, stream),
+          "moe_fp8_linear")
+
+
+def moe_fp8_check(w: int, ws: int, stream: int = 0) -> int:
+    """Returns the device-latched status code (MOE_OK or MOE_ERR_TIMEOUT)."""
+    return int(lib().moe_fp8_check(w, ws, stream))
+
+
+def moe_fp8_quantize_weights(weights, w_type, ld_w, n, k, codes, ld_codes, scales, stream=0) -> None:
+    check(lib().moe_fp8_quantize_weights(weights, w_type, ld_w, n, k, codes, ld_codes, scales, stream),
+          "moe_fp8_quantize_weights")

@@ -69,3 +69,28 @@ def test_token_logprobs_refuses(L, kw, rc):
     if rc:
         assert "moe_token_logprobs" in moe.last_error()
     assert L.moe_token_logprobs(None, None) == moe.MOE_ERR_ARG
+
+
+def test_fp8_refuses(L):
+    h = ctypes.c_void_p()
+    ref = ctypes.byref(h)
+    for n, k, codes, ld, scales, rc in [(0, 64, P, 64, P, moe.MOE_ERR_ARG), (64, 0, P, 64, P, moe.MOE_ERR_ARG),
+                                        (64, 65537, P, 65552, P, moe.MOE_ERR_ARG), (64, 64, None, 64, P, moe.MOE_ERR_ARG),
+                                        (64, 64, P, 64, None, moe.MOE_ERR_ARG), (64, 64, P, 63, P, moe.MOE_ERR_ARG),
+                                        (64, 64, P, 72, P, moe.MOE_ERR_ARG), (64, 64, P + 8, 64, P, moe.MOE_ERR_ALIGN),
+                                        (64, 64, P, 64, P + 2, moe.MOE_ERR_ALIGN)]:
+        assert L.moe_fp8_open(n, k, codes, ld, scales, ref) == rc
+        assert h.value is None and "moe_fp8_open" in moe.last_error()
+    assert L.moe_fp8_open(64, 64, P, 64, P, None) == moe.MOE_ERR_ARG
+    fake = (ctypes.c_uint8 * 4096)()   # zeroed host memory: wrong magic
+    for w in (None, ctypes.addressof(fake)):
+        assert L.moe_fp8_workspace_bytes(w, 1) == 0
+        assert L.moe_fp8_workspace_init(w, P, 1 << 20, None) == moe.MOE_ERR_ARG
+        assert L.moe_fp8_linear(w, P, 0, 64, 1, P, 0, 64, P, 1 << 20, None) == moe.MOE_ERR_ARG
+        assert L.moe_fp8_check(w, P, None) == moe.MOE_ERR_ARG
+        L.moe_fp8_close(w)             # ignored
+    for args, rc in [((P, 0, 64, 0, 64, P, 64, P), moe.MOE_ERR_ARG), ((P, 3, 64, 64, 64, P, 64, P), moe.MOE_ERR_ARG),
+                     ((None, 0, 64, 64, 64, P, 64, P), moe.MOE_ERR_ARG), ((P, 0, 63, 64, 64, P, 64, P), moe.MOE_ERR_ARG),
+                     ((P, 0, 64, 64, 64, P, 72, P), moe.MOE_ERR_ARG), ((P + 1, 0, 64, 64, 64, P, 64, P), moe.MOE_ERR_ALIGN),
+                     ((P, 0, 64, 64, 64, P + 4, 64, P), moe.MOE_ERR_ALIGN)]:
+        assert L.moe_fp8_quantize_weights(*args, None) == rc, args

@@ -81,7 +81,7 @@ int moe_block_norm(const moe_block_norm_args *args, void *stream);
  * in one pass over the logits, in 32 bits.
  *
  *   rows >= 0 (0: no work); vocab >= 1; n_targets in [0, 8]; top_n in [0, 32].
- *   scale:   positive and finite.
+ *   scale:   in [2^-64, 2^64].
  *   targets: device int32 [rows][n_targets].
  *   target_logprobs: device float [rows][n_targets]; target_ranks: device
  *            int32 [rows][n_targets]; lse, entropy: device float [rows];
@@ -92,9 +92,9 @@ int moe_block_norm(const moe_block_norm_args *args, void *stream);
  * log probability is -inf and it is never listed among the top tokens; places
  * left over hold id -1 and -inf.  A row with no other logits gives lse -inf
  * and entropy 0.  A target outside [0, vocab) gives log probability -inf and
- * rank 0.  A row with a NaN or +inf gives NaN for lse, entropy and every log
- * probability (-inf for the places left over); NaNs are never listed and come
- * before no target. */
+ * rank 0.  A row with a NaN or a z of +inf gives NaN for lse, entropy and the
+ * log probabilities of its tokens; NaNs are never listed and come before no
+ * target. */
 typedef struct moe_token_logprobs_args {
     const void *logits;
     const int32_t *targets;

@@ -7,11 +7,15 @@
 // once, h' and x written once, nothing in between goes to memory.
 //
 // Bound: memory traffic for many rows (about 11 operations per value against
-// 8 to 12 bytes), the latency of one load and two reductions for few.
+// 8 to 12 bytes), the latency of one load and two reductions for few.  Two
+// kernels: block_norm_kernel takes one row per block (or per warp);
+// block_norm_stream_kernel keeps one block on each SM whose teams of threads
+// load their next rows while they work on one, with the weights at hand.
 #include <cstdint>
 
 #include <cuda_runtime.h>
 
+#include "common.cuh"
 #include "elem.cuh"
 
 namespace moe {
@@ -20,6 +24,10 @@ int reportf(int code, const char* fmt, ...);
 namespace {
 
 constexpr int kMaxHidden = 16384;
+constexpr int kStreamRows = 8;       // rows per SM from which streaming pays
+constexpr int kStreamThreads = 896;  // of a streaming block: 72 registers each
+constexpr int kStreamHidden = 8192;  // widest row of a team (512 threads of 16 values)
+constexpr int kMaxTeams = 14;        // one named barrier each
 
 // Sum over the row's threads, the same value in all of them.  A block of 32
 // threads per row needs no barrier.  `red` has one slot per warp.
@@ -36,19 +44,55 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return s;
 }
 
+// VEC values as loaded, converted only when they are used, so that loads are
+// issued together whatever their types.
 template <int VEC>
-__device__ __forceinline__ void load_chunk(const void* p, int type, int64_t row, int j, int H, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    if (j + 8 <= H) {
-      load8(p, type, row + j, v);
-    } else {
+struct Raw {
+  uint32_t w[VEC];  // 16-bit types: two values a word (VEC = 8), or one
+
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = j + i < H ? load_elem(p, type, row + j + i) : 0.0f;
-    }
-  } else {
-    v[0] = j < H ? load_elem(p, type, row + j) : 0.0f;
+    for (int i = 0; i < VEC; ++i) w[i] = 0;
   }
-}
+  // Elements [j, j + VEC) of the row that starts at element `row`, zeros past H.
+  __device__ __forceinline__ void load(const void* p, bool wide, int64_t row, int j, int H) {
+    if constexpr (VEC == 8) {
+      if (j + 8 <= H) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (row + j) * (wide ? 4 : 2));
+        const uint4 a = q[0];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        if (wide) {
+          const uint4 b = q[1];
+          w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        }
+      } else {
+        zero();
+        if (wide) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (j + i < H) w[i] = static_cast<const uint32_t*>(p)[row + j + i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (j + i < H) w[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[row + j + i]) << (16 * (i & 1));
+        }
+      }
+    } else {
+      w[0] = 0;
+      if (j < H) w[0] = wide ? static_cast<const uint32_t*>(p)[row + j] : static_cast<const uint16_t*>(p)[row + j];
+    }
+  }
+  __device__ __forceinline__ void get(int type, float (&v)[VEC]) const {
+    if (type == MOE_F32) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (VEC == 8) {
+      unpack8(make_uint4(w[0], w[1], w[2], w[3]), type, v);
+    } else {
+      v[0] = half_bits_to_f32(w[0], type);
+    }
+  }
+};
 
 template <int VEC>
 __device__ __forceinline__ void store_chunk(void* p, int type, int64_t row, int j, int H, const float (&v)[VEC]) {
@@ -65,90 +109,272 @@ __device__ __forceinline__ void store_chunk(void* p, int type, int64_t row, int 
   }
 }
 
+template <int VEC>
+__device__ __forceinline__ void scale_by(float (&v)[VEC], float s, float add, const Raw<VEC>& raw, int type) {
+  float w[VEC];
+  raw.get(type, w);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] *= s * (add + w[i]);
+}
+
 // blockDim = (threads per row, rows per block); more than one row per block
 // only with 32 threads per row.  A thread holds NC chunks of VEC values.
-template <int VEC, int NC>
+// Y32, H32: y and h are 32-bit.
+template <int VEC, int NC, bool Y32, bool H32>
 __global__ void __launch_bounds__(VEC == 8 ? 512 : 1024) block_norm_kernel(const moe_block_norm_args a) {
   __shared__ float red[2][32];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= a.rows) return;
   const int H = a.hidden;
-  float v[NC][VEC], h[NC][VEC];
+  const int yt = Y32 ? MOE_F32 : a.y_type, ht = H32 ? MOE_F32 : a.h_type;
+  auto at = [&](int c) { return static_cast<int>(c * blockDim.x + threadIdx.x) * VEC; };
+  Raw<VEC> y[NC], h[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (a.y) y[c].load(a.y, Y32, t * a.ld_y, at(c), H);
+    else y[c].zero();
+    if (a.h) h[c].load(a.h, H32, t * a.ld_h, at(c), H);
+    else h[c].zero();
+  }
+  // few rows: the weights come with the row; many: from L1 when they are used
+  Raw<VEC> wp[NC], wn[NC], gt[NC];
+  const bool w32 = a.w_type == MOE_F32, g32 = a.gate_type == MOE_F32;
+  auto load_w = [&](int c) {
+    wp[c].zero();
+    if (a.post_norm && a.w_post) wp[c].load(a.w_post, w32, 0, at(c), H);
+    if (a.y && a.gate && a.ld_gate_col) gt[c].load(a.gate, g32, t * a.ld_gate_row, at(c), H);
+  };
+  auto load_wn = [&](int c) {
+    wn[c].zero();
+    if (a.pre_norm && a.w_pre) wn[c].load(a.w_pre, w32, 0, at(c), H);
+  };
+  if constexpr (NC == 1) load_w(0), load_wn(0);
+  float g1 = 1.0f;
+  if (a.y && a.gate && !a.ld_gate_col) g1 = load_elem(a.gate, a.gate_type, t * a.ld_gate_row);
+  float v[NC][VEC];
   float ss = 0.0f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int j = (c * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[c][i] = h[c][i] = 0.0f;
-    if (a.y) load_chunk<VEC>(a.y, a.y_type, t * a.ld_y, j, H, v[c]);
-    if (a.h) load_chunk<VEC>(a.h, a.h_type, t * a.ld_h, j, H, h[c]);
-  }
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
+    y[c].get(yt, v[c]);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+  }
   const float inv_h = 1.0f / static_cast<float>(H);
   float rs = 1.0f;
   if (a.post_norm) rs = rsqrtf(row_sum(ss, red[0]) * inv_h + a.eps);
   ss = 0.0f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int j = (c * blockDim.x + threadIdx.x) * VEC;
+    if constexpr (NC > 1) load_w(c);
     if (a.y) {
-      float w[VEC];
-      if (a.post_norm) {
+      if (a.post_norm) scale_by<VEC>(v[c], rs, a.w_add, wp[c], a.w_type);
+      if (a.gate && a.ld_gate_col) {
+        scale_by<VEC>(v[c], 1.0f, 0.0f, gt[c], a.gate_type);
+      } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = 0.0f;
-        if (a.w_post) load_chunk<VEC>(a.w_post, a.w_type, 0, j, H, w);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[c][i] *= rs * (a.w_add + w[i]);
-      }
-      if (a.gate) {
-        if (a.ld_gate_col) {
-          load_chunk<VEC>(a.gate, a.gate_type, t * a.ld_gate_row, j, H, w);
-        } else {
-          const float g = load_elem(a.gate, a.gate_type, t * a.ld_gate_row);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) w[i] = g;
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[c][i] *= w[i];
+        for (int i = 0; i < VEC; ++i) v[c][i] *= g1;
       }
     }
+    if (a.h) {
+      float hv[VEC];
+      h[c].get(ht, hv);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      if (a.h) v[c][i] = fmaf(a.residual_scale, h[c][i], v[c][i]);
-      if (j + i < H) ss = fmaf(v[c][i], v[c][i], ss);
+      for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(a.residual_scale, hv[i], v[c][i]);
     }
-    if (a.h_out) store_chunk<VEC>(a.h_out, a.h_type, t * a.ld_h_out, j, H, v[c]);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (at(c) + i < H) ss = fmaf(v[c][i], v[c][i], ss);
+    if (a.h_out) store_chunk<VEC>(a.h_out, a.h_type, t * a.ld_h_out, at(c), H, v[c]);
   }
   if (!a.x_out) return;
   rs = 1.0f;
   if (a.pre_norm) rs = rsqrtf(row_sum(ss, red[1]) * inv_h + a.eps);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int j = (c * blockDim.x + threadIdx.x) * VEC;
     if (a.pre_norm) {
-      float w[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) w[i] = 0.0f;
-      if (a.w_pre) load_chunk<VEC>(a.w_pre, a.w_type, 0, j, H, w);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[c][i] *= rs * (a.w_add + w[i]);
+      if constexpr (NC > 1) load_wn(c);
+      scale_by<VEC>(v[c], rs, a.w_add, wn[c], a.w_type);
     }
-    store_chunk<VEC>(a.x_out, a.x_type, t * a.ld_x_out, j, H, v[c]);
+    store_chunk<VEC>(a.x_out, a.x_type, t * a.ld_x_out, at(c), H, v[c]);
   }
+}
+
+// The whole boundary (y and h, both norms, both outputs, at most a gate of
+// every channel) of rows of a multiple of 8 values, for many rows.  One block
+// of several teams per SM; a team takes rows by itself, 16 values a thread in
+// two chunks of 8, and loads its next row while it works on one.  The weights
+// lie in shared memory as fp32, the gate in the post-norm's, in two planes of
+// 16 bytes a chunk; the arithmetic goes in pairs.  With the other kernel's
+// some 60 instructions a value and weights read from L1 between the sums,
+// issue and latency were the bound, not memory.
+template <bool Y32, bool H32>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    block_norm_stream_kernel(const moe_block_norm_args a, int team_threads) {
+  extern __shared__ __align__(16) float4 w4[];  // [post, pre][plane][chunk]
+  __shared__ float red[kMaxTeams][4][16];       // by row parity and sum: a barrier lies between two uses of one
+  const int H = a.hidden, chunks = 2 * team_threads;
+  const int team = threadIdx.x / team_threads, tt = threadIdx.x - team * team_threads, teams = blockDim.x / team_threads;
+  for (int c = threadIdx.x; c < 2 * chunks; c += blockDim.x) {
+    // half-chunk c: elements [4 c, 4 c + 4) in plane c % 2 at chunk c / 2
+    float p[4], n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 4 * c + i;
+      p[i] = n[i] = 0.0f;
+      if (k < H) {
+        p[i] = a.w_add + (a.w_post ? load_elem(a.w_post, a.w_type, k) : 0.0f);
+        if (a.gate) p[i] *= load_elem(a.gate, a.gate_type, k);
+        n[i] = a.w_add + (a.w_pre ? load_elem(a.w_pre, a.w_type, k) : 0.0f);
+      }
+    }
+    const int at = (c & 1) * chunks + (c >> 1);
+    w4[at] = make_float4(p[0], p[1], p[2], p[3]);
+    w4[2 * chunks + at] = make_float4(n[0], n[1], n[2], n[3]);
+  }
+  __syncthreads();
+
+  const float inv_h = 1.0f / static_cast<float>(H), eps = a.eps;
+  const int warp = tt >> 5, warps = team_threads >> 5, lane = tt & 31;
+  float* const mine = &red[team][0][0];
+  auto sum_row = [&](float v, int which) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane == 0) mine[which * 16 + warp] = v;
+    named_bar(1 + team, team_threads);
+    v = (lane & 15) < warps ? mine[which * 16 + (lane & 15)] : 0.0f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  };
+  auto pairs = [](const uint4& lo, const uint4& hi, bool wide, int type, float2 (&v)[4]) {
+    if (wide) {
+      v[0] = make_float2(__uint_as_float(lo.x), __uint_as_float(lo.y));
+      v[1] = make_float2(__uint_as_float(lo.z), __uint_as_float(lo.w));
+      v[2] = make_float2(__uint_as_float(hi.x), __uint_as_float(hi.y));
+      v[3] = make_float2(__uint_as_float(hi.z), __uint_as_float(hi.w));
+    } else {
+      float f[8];
+      unpack8(lo, type, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    }
+  };
+  auto scaled = [&](float2 (&v)[4], float rs, const float4* w) {
+    const float4 lo = w[0], hi = w[chunks];
+    const float2 q = make_float2(rs, rs);
+    v[0] = __fmul2_rn(__fmul2_rn(v[0], q), make_float2(lo.x, lo.y));
+    v[1] = __fmul2_rn(__fmul2_rn(v[1], q), make_float2(lo.z, lo.w));
+    v[2] = __fmul2_rn(__fmul2_rn(v[2], q), make_float2(hi.x, hi.y));
+    v[3] = __fmul2_rn(__fmul2_rn(v[3], q), make_float2(hi.z, hi.w));
+  };
+  auto squares = [](const float2 (&v)[2][4]) {
+    float2 q = __fmul2_rn(v[0][0], v[0][0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) q = __ffma2_rn(v[i >> 2][i & 3], v[i >> 2][i & 3], q);
+    return q.x + q.y;
+  };
+  auto store = [&](char* p, bool wide, int type, const float2 (&v)[4]) {
+    uint4* q = reinterpret_cast<uint4*>(p);
+    if (wide) {
+      q[0] = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+      q[1] = make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y), __float_as_uint(v[3].x), __float_as_uint(v[3].y));
+    } else {
+      q[0] = make_uint4(pack2(v[0].x, v[0].y, type), pack2(v[1].x, v[1].y, type), pack2(v[2].x, v[2].y, type),
+                        pack2(v[3].x, v[3].y, type));
+    }
+  };
+
+  // a team's threads cover chunk 0 wholly (H > 8 * team_threads), chunk 1 in part
+  constexpr int YE = Y32 ? 4 : 2, HE = H32 ? 4 : 2;
+  const int xe = elem_size(a.x_type), apart = team_threads * 8;
+  const bool two = tt * 8 + apart < H;
+  const int stride = static_cast<int>(gridDim.x) * teams;
+  int t = static_cast<int>(blockIdx.x) * teams + team;
+  if (t >= a.rows) return;
+  const char* py = static_cast<const char*>(a.y) + (t * a.ld_y + tt * 8) * YE;
+  const char* ph = static_cast<const char*>(a.h) + (t * a.ld_h + tt * 8) * HE;
+  char* po = static_cast<char*>(a.h_out) + (t * a.ld_h_out + tt * 8) * HE;
+  char* px = static_cast<char*>(a.x_out) + (t * a.ld_x_out + tt * 8) * xe;
+  const float4* const wp = w4 + tt;
+  const float4* const wn = w4 + 2 * chunks + tt;
+  uint4 y[2][2], h[2][2];
+  auto fetch = [&]() {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    y[0][0] = *reinterpret_cast<const uint4*>(py);
+    if (Y32) y[0][1] = *reinterpret_cast<const uint4*>(py + 16);
+    h[0][0] = *reinterpret_cast<const uint4*>(ph);
+    if (H32) h[0][1] = *reinterpret_cast<const uint4*>(ph + 16);
+    y[1][0] = two ? *reinterpret_cast<const uint4*>(py + apart * YE) : zero;
+    if (Y32) y[1][1] = two ? *reinterpret_cast<const uint4*>(py + apart * YE + 16) : zero;
+    h[1][0] = two ? *reinterpret_cast<const uint4*>(ph + apart * HE) : zero;
+    if (H32) h[1][1] = two ? *reinterpret_cast<const uint4*>(ph + apart * HE + 16) : zero;
+  };
+  fetch();
+  const float2 rscale = make_float2(a.residual_scale, a.residual_scale);
+  for (int odd = 0;; odd ^= 2) {
+    // places past the row hold zeros, so they add nothing to the sums
+    float2 v[2][4];
+    pairs(y[0][0], y[0][1], Y32, a.y_type, v[0]);
+    pairs(y[1][0], y[1][1], Y32, a.y_type, v[1]);
+    const float rs = rsqrtf(sum_row(squares(v), odd) * inv_h + eps);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float2 hv[4];
+      scaled(v[c], rs, wp + c * team_threads);
+      pairs(h[c][0], h[c][1], H32, a.h_type, hv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[c][i] = __ffma2_rn(rscale, hv[i], v[c][i]);
+    }
+    t += stride;
+    const bool more = t < a.rows;
+    if (more) {
+      py += stride * a.ld_y * YE;
+      ph += stride * a.ld_h * HE;
+      fetch();
+    }
+    store(po, H32, a.h_type, v[0]);
+    if (two) store(po + apart * HE, H32, a.h_type, v[1]);
+    const float rx = rsqrtf(sum_row(squares(v), odd + 1) * inv_h + eps);
+    scaled(v[0], rx, wn);
+    scaled(v[1], rx, wn + team_threads);
+    store(px, a.x_type == MOE_F32, a.x_type, v[0]);
+    if (two) store(px + apart * xe, a.x_type == MOE_F32, a.x_type, v[1]);
+    if (!more) return;
+    po += stride * a.ld_h_out * HE;
+    px += stride * a.ld_x_out * xe;
+  }
+}
+
+template <int VEC, int NC>
+cudaError_t launch_nc(const moe_block_norm_args& a, dim3 grid, dim3 block, cudaStream_t st) {
+  const bool y32 = a.y_type == MOE_F32, h32 = a.h_type == MOE_F32;
+  if (y32 && h32) block_norm_kernel<VEC, NC, true, true><<<grid, block, 0, st>>>(a);
+  else if (y32) block_norm_kernel<VEC, NC, true, false><<<grid, block, 0, st>>>(a);
+  else if (h32) block_norm_kernel<VEC, NC, false, true><<<grid, block, 0, st>>>(a);
+  else block_norm_kernel<VEC, NC, false, false><<<grid, block, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <int VEC>
 cudaError_t launch_vec(const moe_block_norm_args& a, int nc, dim3 grid, dim3 block, cudaStream_t st) {
-  switch (nc) {
-    case 1: block_norm_kernel<VEC, 1><<<grid, block, 0, st>>>(a); break;
-    case 2: block_norm_kernel<VEC, 2><<<grid, block, 0, st>>>(a); break;
-    case 4: block_norm_kernel<VEC, 4><<<grid, block, 0, st>>>(a); break;
-    default:
-      if constexpr (VEC == 1) block_norm_kernel<VEC, 16><<<grid, block, 0, st>>>(a);
-  }
+  if (nc == 1) return launch_nc<VEC, 1>(a, grid, block, st);
+  if (nc == 2) return launch_nc<VEC, 2>(a, grid, block, st);
+  if (nc == 4) return launch_nc<VEC, 4>(a, grid, block, st);
+  if constexpr (VEC == 1) return launch_nc<1, 16>(a, grid, block, st);
+  return cudaErrorInvalidValue;
+}
+
+template <bool Y32, bool H32>
+cudaError_t launch_stream(const moe_block_norm_args& a, int num_sms, cudaStream_t st) {
+  const int threads = (a.hidden + 511) / 512 * 32;  // of a team: 16 values each
+  const int fit = kStreamThreads / threads, teams = fit < kMaxTeams ? fit : kMaxTeams;
+  const int smem = 2 * threads * 16 * static_cast<int>(sizeof(float));
+  auto kernel = block_norm_stream_kernel<Y32, H32>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e) return e;
+  const int64_t blocks = (static_cast<int64_t>(a.rows) + teams - 1) / teams;
+  kernel<<<static_cast<unsigned>(blocks < num_sms ? blocks : num_sms), threads * teams, smem, st>>>(
+      a, threads);
   return cudaGetLastError();
 }
 
@@ -202,18 +428,32 @@ extern "C" int moe_block_norm(const moe_block_norm_args* args, void* stream) {
                    vec_ok(a.w_post, a.w_type, 0) && vec_ok(a.w_pre, a.w_type, 0) &&
                    (!a.ld_gate_col || vec_ok(a.gate, a.gate_type, a.ld_gate_row));
   const int chunks = vec ? (a.hidden + 7) / 8 : a.hidden;
-  const int max_nc = vec ? 4 : 16;
-  int nc = 1;
-  dim3 block(32, 1);
-  if (chunks <= 32) {
-    block.y = 4;
-  } else {
-    while (nc < max_nc && chunks > 512 * nc) nc = nc == 4 ? 16 : nc * 2;
-    block.x = ((chunks + nc - 1) / nc + 31) / 32 * 32;
-  }
-  const dim3 grid((static_cast<unsigned>(a.rows) + block.y - 1) / block.y);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = vec ? launch_vec<8>(a, nc, grid, block, st) : launch_vec<1>(a, nc, grid, block, st);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (!e) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e) return reportf(MOE_ERR_CUDA, "moe_block_norm: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  if (vec && a.hidden % 8 == 0 && a.hidden > 256 && a.hidden <= kStreamHidden && a.y && a.h && a.h_out && a.x_out &&
+      a.post_norm && a.pre_norm && (!a.gate || (a.ld_gate_col && !a.ld_gate_row)) &&
+      a.rows >= static_cast<int64_t>(kStreamRows) * sms) {
+    const bool y32 = a.y_type == MOE_F32, h32 = a.h_type == MOE_F32;
+    e = y32 && h32 ? launch_stream<true, true>(a, sms, st)
+        : y32      ? launch_stream<true, false>(a, sms, st)
+        : h32      ? launch_stream<false, true>(a, sms, st)
+                   : launch_stream<false, false>(a, sms, st);
+  } else {
+    const int max_nc = vec ? 4 : 16;
+    int nc = 1;
+    dim3 block(32, 1);
+    if (chunks <= 32) {
+      block.y = 4;
+    } else {
+      while (nc < max_nc && chunks > 512 * nc) nc = nc == 4 ? 16 : nc * 2;
+      block.x = ((chunks + nc - 1) / nc + 31) / 32 * 32;
+    }
+    const dim3 grid((static_cast<unsigned>(a.rows) + block.y - 1) / block.y);
+    e = vec ? launch_vec<8>(a, nc, grid, block, st) : launch_vec<1>(a, nc, grid, block, st);
+  }
   if (e != cudaSuccess) return reportf(MOE_ERR_CUDA, "moe_block_norm: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
   return MOE_OK;
 }

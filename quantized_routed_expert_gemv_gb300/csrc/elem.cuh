@@ -55,12 +55,19 @@ __device__ __forceinline__ void unpack8(uint4 r, int type, float (&v)[8]) {
   }
 }
 
+// Two values to a word of 16-bit ones, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+  if (type == MOE_BF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ uint4 pack8(const float (&v)[8], int type) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = f32_to_half_bits(v[2 * i], type) | (f32_to_half_bits(v[2 * i + 1], type) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type),
+                    pack2(v[6], v[7], type));
 }
 
 // Eight values at element i (i a multiple of 8 of a 16-byte aligned row).

@@ -1,33 +1,36 @@
 // token_logprobs.cu -- log probabilities, ranks, entropy and top tokens of
 // rows of logits (moe_token_logprobs), in one pass over the logits.
 //
-// Mathematics, with u = scale * log2(e) and a reference R near the row's
-// maximum:
-//     S = sum_v 2^(u (l_v - R)),  A = sum_v u (l_v - R) 2^(u (l_v - R))
-//     lse = scale R + ln S,  entropy = ln S - ln 2 * A / S,
-//     logprob_t = scale (l_t - R) - ln S.
-// Every thread keeps its own (R, S, A) and moves R only when a logit lies
-// more than 2^kRefSlack above it, so the usual step has no rescaling; S, A
-// and the differences stay in fp32.  Differences are clamped at -200 (in
-// powers of two), where 2^d is 0, so -inf and the type's lowest value add 0
-// to A instead of 0 * -inf.
+// Mathematics, in powers of two: with u = scale * log2(e) and a reference r
+// near the row's largest u l,
+//     S = sum_v 2^(u l_v - r),  A = sum_v (u l_v - r) 2^(u l_v - r)
+//     lse = ln 2 (r + log2 S),  entropy = ln 2 (log2 S - A / S),
+//     logprob_t = ln 2 (u l_t - r - log2 S).
+// One fma gives u l - r with a single rounding.  Every thread keeps its own
+// (r, S, A) in fp32 and moves r only when a logit lies more than kRefSlack
+// powers of two above it, so the usual step has no rescaling.  Values whose
+// u l is below -2^99 (masks of the type's lowest value) add 0; a row that
+// has nothing else, or whose u l overflows upwards, has all of its
+// probability on the logits equal to its largest (neighbouring values are
+// more than 2^75 powers of two apart there), which are counted instead.
 //
-// Top tokens: a thread's running maximum (and the chunk it was first seen
-// in) is the best of the group of tokens that thread visited.  Any token of
-// the row's top n lies in one of the n groups whose best come first, since
-// the best of every group that precedes its own group's precedes it too.  So
-// the pass keeps one value per thread, and afterwards only the n winning
-// groups are read again (from cache) for tokens that do not come after the
-// n-th best.
+// Top tokens: a thread's running maximum is the best of the group of tokens
+// that thread visited.  Any token of the row's top n lies in one of the n
+// groups whose best tokens come first: the best of each group before its own
+// comes before it too.  So the pass keeps one value per thread, and afterwards
+// only the n winning groups are read again (from cache), for the tokens that
+// do not come after the n-th group's best.
 //
 // A row is read by one block, or by a cluster of up to 8 blocks, each a
-// contiguous part, when there are too few rows for the SMs; the parts are
-// joined through distributed shared memory in rank order, so results do not
-// depend on timing.
+// contiguous part, when there are too few rows for the SMs; the parts meet in
+// the first block's shared memory and are joined in rank order, so results do
+// not depend on timing.
 #include <cmath>
 #include <cstdint>
 
 #include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "elem.cuh"
@@ -41,11 +44,15 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+// chunks of 8 logits a thread loads at once
+__host__ __device__ constexpr int batch_of(int type) { return type == MOE_F32 ? 2 : 4; }
 constexpr int kMaxTop = 32;
 constexpr int kMaxTargets = 8;
 constexpr int kMaxSplit = 8;
 constexpr int kCand = 1024;            // candidate buffer of the top selection
 constexpr float kRefSlack = 80.0f;     // powers of two a logit may lie above the reference
+constexpr float kUnset = 3.402823466e38f;
+constexpr float kFloor = -6.338253e29f;  // -2^99: what lies below adds no probability
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Key {  // order: value descending, id ascending; id < 0: none
@@ -53,14 +60,11 @@ struct Key {  // order: value descending, id ascending; id < 0: none
   int id;
 };
 
-__device__ __forceinline__ bool before(float av, int ai, float bv, int bi) {
-  return av > bv || (av == bv && ai < bi);
-}
+__device__ __forceinline__ bool before(const Key& a, const Key& b) { return a.v > b.v || (a.v == b.v && a.id < b.id); }
 
-// What one block knows of its part of a row, read by the cluster's first
-// block.
+// What a block knows of its part of a row.
 struct Part {
-  float R, S, A;
+  float r, S, A, best;
   int cnt[kMaxTargets];
   Key top[kMaxTop];
 };
@@ -78,164 +82,435 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
-// Smallest float above v (v itself for NaN and +inf -> NaN): x > v iff x >= next_up(v).
+// Smallest value above v: x > v iff x >= next_up(v) (NaN for NaN and +inf).
 __device__ __forceinline__ float next_up(float v) {
   const uint32_t u = __float_as_uint(v);
   if (v == 0.0f) return __uint_as_float(1u);
   return __uint_as_float(v > 0.0f ? u + 1 : u - 1);
 }
+__device__ __forceinline__ uint32_t next_up16(uint32_t bits, uint32_t inf) {
+  if ((bits & 0x7FFFu) == 0) return 1u;
+  if ((bits & 0x7FFFu) > inf) return bits;  // NaN stays NaN
+  return bits & 0x8000u ? bits - 1 : bits + 1;
+}
 
-// The row's logits as chunks of 8 on a grid of 16-byte aligned addresses:
-// chunk c holds elements [8 c - off, 8 c - off + 8) of the row.  Elements
-// outside the row read as -inf.
+// A thread's running sums.
+struct Sums {
+  float r = kUnset;
+  float2 S = {0.0f, 0.0f}, A = {0.0f, 0.0f};
+
+  // Makes room for values up to m (in powers of two).
+  __device__ __forceinline__ void reach(float m) {
+    if (m > kFloor && (r == kUnset || m - r > kRefSlack)) {
+      const float d = r == kUnset ? -1e4f : max_nan(r - m, -1e4f);
+      const float e = ex2(d);
+      A.x = fmaf(S.x, d, A.x) * e, A.y = fmaf(S.y, d, A.y) * e;
+      S.x *= e, S.y *= e;
+      r = m;
+    }
+  }
+  // Two logits (already bounded below unless CLAMP).
+  template <bool CLAMP>
+  __device__ __forceinline__ void add(float2 l, float u) {
+    float2 d = __ffma2_rn(l, make_float2(u, u), make_float2(-r, -r));
+    if (CLAMP) d.x = max_nan(d.x, -200.0f), d.y = max_nan(d.y, -200.0f);
+    const float2 e = make_float2(ex2(d.x), ex2(d.y));
+    S = __fadd2_rn(S, e);
+    A = __ffma2_rn(e, d, A);
+  }
+};
+
+// Joins the (r, S, A) of a warp's lanes in every lane: moved to the largest
+// reference, then summed in a fixed order.  Lanes without a sum have r unset
+// and S = 0.
+__device__ __forceinline__ void join_warp(float& r, float& S, float& A) {
+  const int b = __float_as_int(r == kUnset ? -INFINITY : r);
+  const int key = __reduce_max_sync(0xFFFFFFFFu, b ^ ((b >> 31) & 0x7FFFFFFF));
+  const float top = __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF));
+  const float d = r == kUnset ? -1e4f : max_nan(r - top, -1e4f), e = exp2f(d);
+  A = fmaf(S, d, A) * e;
+  S *= e;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
+    A += __shfl_xor_sync(0xFFFFFFFFu, A, o);
+  }
+  r = top == -INFINITY ? kUnset : top;
+}
+
+__device__ __forceinline__ float max_warp(float v) {
+  const int b = __float_as_int(v);
+  const int key = __reduce_max_sync(0xFFFFFFFFu, b ^ ((b >> 31) & 0x7FFFFFFF));
+  return __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF));
+}
+
+// Calls emit(place, i) for the keys among the first n of keys[0..m): a key's
+// place is the number of keys before it.  A warp takes a key at a time.
+template <class Emit>
+__device__ __forceinline__ void place_keys(const Key* keys, int m, int n, Emit emit) {
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < m; i += kWarps) {
+    const Key k = keys[i];
+    int c = 0;
+    for (int q = lane; q < m; q += 32) c += before(keys[q], k);
+    c = __reduce_add_sync(0xFFFFFFFFu, c);
+    if (lane == 0 && c < n) emit(c, i);
+  }
+}
+
+// The row's logits on a grid of 16-byte aligned addresses: chunk c holds
+// elements [8 c - off, 8 c - off + 8).  Chunks [w0, w1) lie wholly in the row;
+// the elements before and after them, at most 14, are its edges.
 template <int TYPE>
 struct Row {
-  const void* p;
-  int off, vocab, chunks;
+  static constexpr int ES = TYPE == MOE_F32 ? 4 : 2;
+  const char* p;
+  int off, vocab, w0, w1;
   __device__ __forceinline__ Row(const moe_token_logprobs_args& a, int64_t t) {
-    constexpr int ES = TYPE == MOE_F32 ? 4 : 2;
     p = static_cast<const char*>(a.logits) + t * a.ld_logits * ES;
     off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / ES);
     vocab = a.vocab;
-    chunks = static_cast<int>((static_cast<int64_t>(vocab) + off + 7) / 8);
+    w0 = off ? 1 : 0;
+    w1 = max(w0, (vocab + off) / 8);
   }
-  __device__ __forceinline__ bool whole(int c) const { return 8 * c >= off && vocab - 8 >= 8 * c - off; }
-  __device__ __forceinline__ void load(int c, float (&v)[8]) const {
-    const int j = 8 * c - off;
-    if (whole(c)) {
-      load8(p, TYPE, j, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = j + i >= 0 && j + i < vocab ? load_elem(p, TYPE, j + i) : -INFINITY;
-    }
+  __device__ __forceinline__ const uint4* chunk(int c) const {
+    return reinterpret_cast<const uint4*>(p + (static_cast<int64_t>(c) * 8 - off) * ES);
+  }
+  __device__ __forceinline__ void load(int c, float (&v)[8]) const { load8(chunk(c), TYPE, 0, v); }
+  __device__ __forceinline__ float at(int j) const { return load_elem(p, TYPE, j); }
+  // The i-th edge element's index, or -1.
+  __device__ __forceinline__ int edge(int i) const {
+    const int head = min(vocab, 8 * w0 - off);
+    if (i < head) return i;
+    const int j = i - head + max(head, 8 * w1 - off);
+    return j < vocab ? j : -1;
   }
 };
-
-__device__ __forceinline__ void merge(float& R, float& S, float& A, float r, float s, float a, float u) {
-  if (s == 0.0f) return;
-  if (S == 0.0f) {
-    R = r, S = s, A = a;
-    return;
-  }
-  const float m = fmaxf(R, r);
-  const float d0 = max_nan((R - m) * u, -1e4f), d1 = max_nan((r - m) * u, -1e4f);
-  const float e0 = exp2f(d0), e1 = exp2f(d1);
-  A = (A + S * d0) * e0 + (a + s * d1) * e1;
-  S = S * e0 + s * e1;
-  R = m;
-}
-
-// One warp: the n first keys of the 32 * PER keys its lanes hold, in order,
-// to out[0..n).
-template <int PER>
-__device__ __forceinline__ void warp_select(Key (&k)[PER], int n, Key* out) {
-  const int lane = threadIdx.x & 31;
-  for (int r = 0; r < n; ++r) {
-    Key b = {-INFINITY, -1};
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (k[i].id >= 0 && (b.id < 0 || before(k[i].v, k[i].id, b.v, b.id))) b = k[i];
-    Key w = b;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float v = __shfl_xor_sync(0xFFFFFFFFu, w.v, o);
-      const int id = __shfl_xor_sync(0xFFFFFFFFu, w.id, o);
-      if (id >= 0 && (w.id < 0 || before(v, id, w.v, w.id))) w.v = v, w.id = id;
-    }
-    if (lane == 0) out[r] = w;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (w.id >= 0 && k[i].id == w.id) k[i].id = -1;
-  }
-}
 
 struct Smem {
-  Key group[kThreads];   // each thread's first-ranked token
-  int owner[kMaxTop];    // threads whose groups win
-  Key sel[kMaxTop];
+  Part parts[kMaxSplit];       // the cluster's first block: one per part
+  Part mine;
+  float team[32];              // best value of each team of kThreads / 32 threads
+  float cut;                   // value no group of the top n lies below
+  int ngroup, ncand;
+  Key group[kThreads];         // groups at or above it: best token ...
+  int owner[kThreads];         // ... and thread
+  Key sel[kMaxTop];            // the n first groups
+  int sel_owner[kMaxTop];
   Key cand[kCand];
-  int ncand;
   Key last, best[kWarps];
-  float R[kWarps], S[kWarps], A[kWarps];
+  float r[kWarps], S[kWarps], A[kWarps];
   int cnt[kWarps][kMaxTargets];
-  Part part;
 };
 
-// NT: number of targets whose ranks are counted, rounded up to 0, 1 or 8.
+// The first n tokens of this block's part to part.top.
+template <int TYPE>
+__device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n, int c0, int c1, float best, int best_b,
+                                           float edge_v, int edge_j) {
+  constexpr int kBatch = batch_of(TYPE);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // a value that n groups reach: the n-th largest of 32 teams' best
+  constexpr int kTeam = kThreads / 32;
+  float h = best;
+#pragma unroll
+  for (int o = kTeam / 2; o; o >>= 1) h = fmaxf(h, __shfl_xor_sync(0xFFFFFFFFu, h, o));
+  if (tid % kTeam == 0) sm.team[tid / kTeam] = h;
+  if (tid == 0) sm.ngroup = sm.ncand = 0, sm.cut = -INFINITY;
+  if (tid < kMaxTop) sm.sel[tid].v = -INFINITY, sm.sel[tid].id = -1, sm.mine.top[tid].v = -INFINITY, sm.mine.top[tid].id = -1;
+  __syncthreads();
+  if (warp == 0) {
+    const float v = sm.team[lane];
+    int place = 0;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      const float w = __shfl_sync(0xFFFFFFFFu, v, q);
+      place += w > v || (w == v && q < lane);
+    }
+    if (place == n - 1) sm.cut = v;
+  }
+  __syncthreads();
+  if (best > -INFINITY && best >= sm.cut) {
+    // the token: the first place of that value in the batch it was seen in
+    int id = -1;
+#pragma unroll
+    for (int i = kBatch - 1; i >= 0; --i) {
+      const int c = best_b + i * kThreads + tid;
+      if (c < c1) {
+        float v[8];
+        row.load(c, v);
+#pragma unroll
+        for (int k = 7; k >= 0; --k)
+          if (v[k] == best) id = 8 * c - row.off + k;
+      }
+    }
+    const int s = atomicAdd(&sm.ngroup, 1);
+    sm.group[s].v = best, sm.group[s].id = id, sm.owner[s] = tid;
+  }
+  __syncthreads();
+  const int m = sm.ngroup;
+  place_keys(sm.group, m, n, [&](int place, int i) { sm.sel[place] = sm.group[i], sm.sel_owner[place] = sm.owner[i]; });
+  __syncthreads();
+  const Key cut = sm.sel[n - 1];
+  auto push = [&](float v, int id) {
+    const Key k = {v, id};
+    if (v > -INFINITY && (cut.id < 0 || !before(cut, k))) {
+      const int s = atomicAdd(&sm.ncand, 1);
+      if (s < kCand) sm.cand[s] = k;
+    }
+  };
+  if (edge_j >= 0) push(edge_v, edge_j);
+  // chunk k of winner g is item g * chunks + k, one thread each
+  const int chunks = (c1 - c0 + kThreads - 1) / kThreads, items = min(n, m) * chunks;
+  for (int e = tid; e < items; e += kThreads) {
+    const int g = e / chunks, c = c0 + sm.sel_owner[g] + (e - g * chunks) * kThreads;
+    if (c < c1) {
+      float v[8];
+      row.load(c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) push(v[i], 8 * c - row.off + i);
+    }
+  }
+  __syncthreads();
+  const int nc = sm.ncand;
+  if (nc <= kCand) {
+    place_keys(sm.cand, nc, n, [&](int place, int i) { sm.mine.top[place] = sm.cand[i]; });
+    return;
+  }
+  // many tokens in few groups: one round over the winning groups per place
+  if (tid == 0) sm.last.v = INFINITY, sm.last.id = -1;
+  __syncthreads();
+  for (int r = 0; r < n; ++r) {
+    const Key last = sm.last;
+    Key b = {-INFINITY, -1};
+    auto look = [&](float v, int id) {
+      const Key k = {v, id};
+      if (v > -INFINITY && before(last, k) && (b.id < 0 || before(k, b))) b = k;
+    };
+    if (edge_j >= 0) look(edge_v, edge_j);
+    for (int e = tid; e < items; e += kThreads) {
+      const int g = e / chunks, c = c0 + sm.sel_owner[g] + (e - g * chunks) * kThreads;
+      if (c < c1) {
+        float v[8];
+        row.load(c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) look(v[i], 8 * c - row.off + i);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const Key k = {__shfl_xor_sync(0xFFFFFFFFu, b.v, o), __shfl_xor_sync(0xFFFFFFFFu, b.id, o)};
+      if (k.id >= 0 && (b.id < 0 || before(k, b))) b = k;
+    }
+    if (lane == 0) sm.best[warp] = b;
+    __syncthreads();
+    if (tid == 0) {
+      Key w = {-INFINITY, -1};
+      for (int q = 0; q < kWarps; ++q)
+        if (sm.best[q].id >= 0 && (w.id < 0 || before(sm.best[q], w))) w = sm.best[q];
+      sm.mine.top[r] = w;
+      if (w.id >= 0) sm.last = w;
+    }
+    __syncthreads();
+  }
+}
+
+// NT: targets whose ranks are counted, rounded up to 0, 1 or 8.
 template <int TYPE, int NT>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const moe_token_logprobs_args a, int split) {
+__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_token_logprobs_args a, int split) {
   __shared__ Smem sm;
+  constexpr bool F32 = TYPE == MOE_F32;
+  constexpr int kBatch = batch_of(TYPE);
+  constexpr int NG = NT > 0 ? NT : 1;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = split > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+  if (split > 1) cluster.barrier_arrive();  // paired with the wait before the parts meet
   const int64_t t = blockIdx.x / split;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Row<TYPE> row(a, t);
   const float u = a.scale * 1.4426950408889634f;
-  const int per = (row.chunks + split - 1) / split;
-  const int c0 = rank * per, c1 = min(row.chunks, c0 + per);
+  const int per = (row.w1 - row.w0 + split - 1) / split;
+  const int c0 = min(row.w1, row.w0 + rank * per), c1 = min(row.w1, c0 + per);
 
-  float xt[NT > 0 ? NT : 1];
-  int ct[NT > 0 ? NT : 1], it[NT > 0 ? NT : 1], cnt[NT > 0 ? NT : 1];
+  // raw logits of a batch: chunk i at c + i * kThreads, -inf outside the part
+  uint4 raw[kBatch][F32 ? 2 : 1];
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = c + i * kThreads;
+      constexpr uint32_t fill = F32 ? 0xFF800000u : TYPE == MOE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+#pragma unroll
+      for (int q = 0; q < (F32 ? 2 : 1); ++q)
+        raw[i][q] = k < c1 ? __ldg(row.chunk(k) + q) : make_uint4(fill, fill, fill, fill);
+    }
+  };
+  fetch(c0 + tid);
+
+  // ranks: chunk c counts logits >= lo if it lies before the target's chunk,
+  // else >= hi (the next value); the target's own chunk is completed below
+  int tj[NG], tc[NG], cnt[NG];
+  float xt[NG];
+  uint32_t lo[NG], hi[NG];
+  uint32_t cnt2[NG];
   if constexpr (NT > 0) {
 #pragma unroll
     for (int g = 0; g < NT; ++g) {
-      it[g] = g < a.n_targets ? a.targets[t * a.n_targets + g] : -1;
-      const bool in = it[g] >= 0 && it[g] < a.vocab;
-      xt[g] = in ? load_elem(row.p, TYPE, it[g]) : NAN;
-      ct[g] = in ? (it[g] + row.off) / 8 : -1;
+      tj[g] = g < a.n_targets ? a.targets[t * a.n_targets + g] : -1;
+      const bool in = tj[g] >= 0 && tj[g] < a.vocab;
+      if (!in) tj[g] = -1;
+      xt[g] = in ? row.at(tj[g]) : NAN;
+      tc[g] = in ? (tj[g] + row.off) / 8 : -1;
       cnt[g] = 0;
+      cnt2[g] = 0;
+      if constexpr (F32) {
+        lo[g] = __float_as_uint(xt[g]);
+        hi[g] = __float_as_uint(next_up(xt[g]));
+      } else {
+        const uint32_t nan = TYPE == MOE_BF16 ? 0x7FC0u : 0x7E00u;
+        const uint32_t b = in ? reinterpret_cast<const uint16_t*>(row.p)[tj[g]] : nan;
+        const uint32_t n = next_up16(b, TYPE == MOE_BF16 ? 0x7F80u : 0x7C00u);
+        lo[g] = b * 0x10001u;
+        hi[g] = n * 0x10001u;
+      }
     }
   }
 
-  // the pass
-  float R = -3.402823466e38f, S = 0.0f, A = 0.0f, best = -INFINITY;
-  int best_c = -1;
-  for (int c = c0 + tid; c < c1; c += kThreads) {
-    float v[8];
-    row.load(c, v);
-    float m = v[0];
+  Sums sums;
+  float best = -INFINITY;
+  int best_b = -1;
+  // bf16 logits are bounded below before they are widened, so that a value
+  // under the floor gives 0 * finite in A
+  const float bound = __bfloat162float(__float2bfloat16_rn(fmaxf(-1.2676506e30f / u, -3.3895314e38f)));
+  const __nv_bfloat162 bound2 = __float2bfloat162_rn(bound);
+  int batches = 0;
+  for (int c = c0 + tid; c - tid < c1; c += kBatch * kThreads) {
+    uint4 cur[kBatch][F32 ? 2 : 1];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, v[i]);
-    if (m > best) best = m, best_c = c;
-    if ((m - R) * u > kRefSlack) {
-      const float d = max_nan((R - m) * u, -1e4f), e = exp2f(d);
-      A = (A + S * d) * e;
-      S *= e;
-      R = m;
-    }
+    for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = max_nan((v[i] - R) * u, -200.0f);
-      const float e = ex2(d);
-      S += e;
-      A = fmaf(e, d, A);
+      for (int q = 0; q < (F32 ? 2 : 1); ++q) cur[i][q] = raw[i][q];
+    if (c - tid + kBatch * kThreads < c1) fetch(c + kBatch * kThreads);
+
+    float m;
+    if constexpr (F32) {
+      m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          m = fmaxf(m, fmaxf(__uint_as_float(cur[i][q].x), __uint_as_float(cur[i][q].y)));
+          m = fmaxf(m, fmaxf(__uint_as_float(cur[i][q].z), __uint_as_float(cur[i][q].w)));
+        }
+    } else if constexpr (TYPE == MOE_BF16) {
+      __nv_bfloat162 w = *reinterpret_cast<const __nv_bfloat162*>(&cur[0][0].x);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&cur[i][0]);
+        w = __hmax2(w, __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3])));
+      }
+      m = fmaxf(__low2float(w), __high2float(w));
+    } else {
+      __half2 w = *reinterpret_cast<const __half2*>(&cur[0][0].x);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const __half2* v = reinterpret_cast<const __half2*>(&cur[i][0]);
+        w = __hmax2(w, __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3])));
+      }
+      m = fmaxf(__low2float(w), __high2float(w));
     }
-    if constexpr (NT > 0) {
-      const bool whole = row.whole(c);
+    if (m > best) best = m, best_b = c - tid;
+    sums.reach(m * u);
+
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = c + i * kThreads;
 #pragma unroll
       for (int g = 0; g < NT; ++g) {
-        if (whole && c != ct[g]) {
-          const float thr = c < ct[g] ? xt[g] : next_up(xt[g]);
+        // outside the part nothing counts
+        const uint32_t none = F32 ? 0x7FC00000u : TYPE == MOE_BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+        const uint32_t thr = k >= c1 ? none : k < tc[g] ? lo[g] : hi[g];
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&cur[i][0]);
+        if constexpr (F32) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) cnt[g] += v[i] >= thr;
+          for (int q = 0; q < 8; ++q) cnt[g] += __uint_as_float(w[q]) >= __uint_as_float(thr);
+        } else if constexpr (TYPE == MOE_BF16) {
+          __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&cnt2[g]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            s = __hadd2(s, __hge2(*reinterpret_cast<const __nv_bfloat162*>(w + q), *reinterpret_cast<const __nv_bfloat162*>(&thr)));
+          cnt2[g] = *reinterpret_cast<const uint32_t*>(&s);
         } else {
-          const int j = 8 * c - row.off;
+          __half2 s = *reinterpret_cast<const __half2*>(&cnt2[g]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            cnt[g] += j + i >= 0 && j + i < a.vocab && (v[i] > xt[g] || (v[i] == xt[g] && j + i < it[g]));
+          for (int q = 0; q < 4; ++q)
+            s = __hadd2(s, __hge2(*reinterpret_cast<const __half2*>(w + q), *reinterpret_cast<const __half2*>(&thr)));
+          cnt2[g] = *reinterpret_cast<const uint32_t*>(&s);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < (F32 ? 2 : 1); ++q) {
+        const uint32_t w[4] = {cur[i][q].x, cur[i][q].y, cur[i][q].z, cur[i][q].w};
+        if constexpr (F32) {
+          sums.add<true>(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), u);
+          sums.add<true>(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), u);
+        } else {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            if constexpr (TYPE == MOE_BF16) {
+              const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[z]), bound2);
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(&b);
+              sums.add<false>(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)), u);
+            } else {
+              sums.add<true>(__half22float2(*reinterpret_cast<const __half2*>(&w[z])), u);
+            }
+          }
+        }
+      }
+    }
+    if constexpr (!F32 && NT > 0) {
+      // a half counts 16 a batch and is exact to 256
+      if (++batches == 16 || c - tid + kBatch * kThreads >= c1) {
+        batches = 0;
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
+          float2 f;
+          if constexpr (TYPE == MOE_BF16)
+            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&cnt2[g]));
+          else
+            f = __half22float2(*reinterpret_cast<const __half2*>(&cnt2[g]));
+          cnt[g] += static_cast<int>(f.x) + static_cast<int>(f.y);
+          cnt2[g] = 0;
         }
       }
     }
   }
 
-  // join the block's sums in a fixed order
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float r = __shfl_down_sync(0xFFFFFFFFu, R, o), s = __shfl_down_sync(0xFFFFFFFFu, S, o),
-                b = __shfl_down_sync(0xFFFFFFFFu, A, o);
-    merge(R, S, A, r, s, b, u);
+  // the row's edges, by the first part; the places of the targets' own chunks
+  // that come before them in a tie
+  int edge_j = -1;
+  float edge_v = -INFINITY;
+  if (rank == 0 && tid < 16) {
+    edge_j = row.edge(tid);
+    if (edge_j >= 0) {
+      edge_v = row.at(edge_j);
+      sums.reach(edge_v * u);
+      sums.add<true>(make_float2(edge_v, -INFINITY), u);
+    }
   }
-  if (lane == 0) sm.R[warp] = R, sm.S[warp] = S, sm.A[warp] = A;
+  if constexpr (NT > 0) {
+#pragma unroll
+    for (int g = 0; g < NT; ++g) {
+      if (edge_j >= 0) cnt[g] += edge_v > xt[g] || (edge_v == xt[g] && edge_j < tj[g]);
+      if (rank == 0 && tid < 8 && tc[g] >= row.w0 && tc[g] < row.w1) {
+        const int j = 8 * tc[g] - row.off + tid;
+        cnt[g] += j < tj[g] && row.at(j) == xt[g];
+      }
+    }
+  }
+
+  // join the block's sums in a fixed order
+  float r = sums.r, S = sums.S.x + sums.S.y, A = sums.A.x + sums.A.y;
+  join_warp(r, S, A);
+  if (lane == 0) sm.r[warp] = r, sm.S[warp] = S, sm.A[warp] = A;
   if constexpr (NT > 0) {
 #pragma unroll
     for (int g = 0; g < NT; ++g) {
@@ -244,179 +519,101 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const moe_toke
     }
   }
   const int n = a.top_n;
-  if (n > 0) {
-    // the id of the thread's best: the first place of that value in its chunk
-    int id = -1;
-    if (best_c >= 0) {
-      float v[8];
-      row.load(best_c, v);
-      const int j = 8 * best_c - row.off;
-#pragma unroll
-      for (int i = 7; i >= 0; --i)
-        if (v[i] == best) id = j + i;
-    }
-    sm.group[tid].v = best, sm.group[tid].id = id;
-  }
-  if (tid == 0) sm.ncand = 0;
+  float top_v = max_warp(fmaxf(best, edge_v));
+  if (lane == 0) sm.best[warp].v = top_v;
   __syncthreads();
-  if (warp == 0) {
-    float r = -3.402823466e38f, s = 0.0f, b = 0.0f;
-    if (lane < kWarps) r = sm.R[lane], s = sm.S[lane], b = sm.A[lane];
-#pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) {
-      const float r2 = __shfl_down_sync(0xFFFFFFFFu, r, o), s2 = __shfl_down_sync(0xFFFFFFFFu, s, o),
-                  b2 = __shfl_down_sync(0xFFFFFFFFu, b, o);
-      merge(r, s, b, r2, s2, b2, u);
-    }
-    if (lane == 0) sm.part.R = r, sm.part.S = s, sm.part.A = b;
+  if (warp == kWarps - 1) {
+    // while the other warps begin the selection
+    r = kUnset, S = 0.0f, A = 0.0f, top_v = -INFINITY;
+    if (lane < kWarps) r = sm.r[lane], S = sm.S[lane], A = sm.A[lane], top_v = sm.best[lane].v;
+    join_warp(r, S, A);
+    top_v = max_warp(top_v);
+    if (lane == 0) sm.mine.r = r, sm.mine.S = S, sm.mine.A = A, sm.mine.best = top_v;
     if (lane < NT) {
       int q = 0;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) q += sm.cnt[w][lane];
-      sm.part.cnt[lane] = q;
+      sm.mine.cnt[lane] = q;
     }
   }
-  if (n > 0) {
-    if (warp == 0) {
-      Key k[kWarps];
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) k[i] = sm.group[32 * i + lane];
-      warp_select<kWarps>(k, n, sm.sel);
-    }
-    __syncthreads();
-    if (tid < n) sm.owner[tid] = -1;
-    __syncthreads();
-    {
-      const Key mine = sm.group[tid];
-      if (mine.id >= 0)
-        for (int r = 0; r < n; ++r)
-          if (sm.sel[r].id == mine.id) sm.owner[r] = tid;
-    }
-    __syncthreads();
-    // the winning groups' tokens that do not come after the n-th group's best
-    const Key thr = sm.sel[n - 1];
-    for (int r = warp; r < n; r += kWarps) {
-      const int o = sm.owner[r];
-      if (o < 0) continue;
-      for (int c = c0 + o + lane * kThreads; c < c1; c += 32 * kThreads) {
-        float v[8];
-        row.load(c, v);
-        const int j = 8 * c - row.off;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (v[i] > -INFINITY && (thr.id < 0 || !before(thr.v, thr.id, v[i], j + i))) {
-            const int s = atomicAdd(&sm.ncand, 1);
-            if (s < kCand) sm.cand[s].v = v[i], sm.cand[s].id = j + i;
-          }
-        }
-      }
-    }
-    __syncthreads();
-    const int m = sm.ncand;
-    if (m <= kCand) {
-      // a candidate's place is the number of candidates before it
-      for (int i = tid; i < n; i += kThreads) sm.part.top[i].v = -INFINITY, sm.part.top[i].id = -1;
-      __syncthreads();
-      for (int i = tid; i < m; i += kThreads) {
-        const Key k = sm.cand[i];
-        int place = 0;
-        for (int q = 0; q < m; ++q) place += before(sm.cand[q].v, sm.cand[q].id, k.v, k.id);
-        if (place < n) sm.part.top[place] = k;
-      }
-    } else {
-      // many tokens of few groups: one round over the winning groups per place
-      if (tid == 0) sm.last.v = INFINITY, sm.last.id = -1;
-      __syncthreads();
-      for (int r = 0; r < n; ++r) {
-        const Key last = sm.last;
-        Key b = {-INFINITY, -1};
-        for (int q = warp; q < n; q += kWarps) {
-          const int o = sm.owner[q];
-          if (o < 0) continue;
-          for (int c = c0 + o + lane * kThreads; c < c1; c += 32 * kThreads) {
-            float v[8];
-            row.load(c, v);
-            const int j = 8 * c - row.off;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (v[i] > -INFINITY && before(last.v, last.id, v[i], j + i) &&
-                  (b.id < 0 || before(v[i], j + i, b.v, b.id)))
-                b.v = v[i], b.id = j + i;
-          }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          const float v = __shfl_xor_sync(0xFFFFFFFFu, b.v, o);
-          const int id = __shfl_xor_sync(0xFFFFFFFFu, b.id, o);
-          if (id >= 0 && (b.id < 0 || before(v, id, b.v, b.id))) b.v = v, b.id = id;
-        }
-        if (lane == 0) sm.best[warp] = b;
-        __syncthreads();
-        if (tid == 0) {
-          Key w = {-INFINITY, -1};
-          for (int q = 0; q < kWarps; ++q)
-            if (sm.best[q].id >= 0 && (w.id < 0 || before(sm.best[q].v, sm.best[q].id, w.v, w.id))) w = sm.best[q];
-          sm.part.top[r] = w;
-          if (w.id >= 0) sm.last = w;
-        }
-        __syncthreads();
-      }
-    }
-  }
+  if (n > 0) select_top<TYPE>(row, sm, n, c0, c1, best, best_b, edge_v, edge_j);
   __syncthreads();
 
-  // join the parts of the row
+  // the parts meet in the first block
+  Part* all = &sm.mine;
   if (split > 1) {
-    cluster.sync();
-    if (rank == 0 && warp == 0) {
-      float r = sm.part.R, s = sm.part.S, b = sm.part.A;
-      for (int q = 1; q < split; ++q) {
-        const Part* o = cluster.map_shared_rank(&sm.part, q);
-        merge(r, s, b, o->R, o->S, o->A, u);
-      }
-      int q_cnt = 0;
-      if (lane < NT)
-        for (int q = 0; q < split; ++q) q_cnt += cluster.map_shared_rank(&sm.part, q)->cnt[lane];
-      Key k[kMaxSplit];
-#pragma unroll
-      for (int q = 0; q < kMaxSplit; ++q) {
-        k[q].v = -INFINITY, k[q].id = -1;
-        if (q < split && lane < n) k[q] = cluster.map_shared_rank(&sm.part, q)->top[lane];
-      }
-      __syncwarp();
-      if (lane == 0) sm.part.R = r, sm.part.S = s, sm.part.A = b;
-      if (lane < NT) sm.part.cnt[lane] = q_cnt;
-      warp_select<kMaxSplit>(k, n, sm.part.top);
-      __syncwarp();
-    }
+    constexpr int words = sizeof(Part) / 4;
+    static_assert(words <= kThreads, "one word a thread");
+    uint32_t* to = reinterpret_cast<uint32_t*>(cluster.map_shared_rank(&sm.parts[rank], 0));
+    cluster.barrier_wait();  // the first block has started
+    if (tid < words) to[tid] = reinterpret_cast<const uint32_t*>(&sm.mine)[tid];
     cluster.sync();
     if (rank != 0) return;
+    all = sm.parts;
+    if (n > 0) {
+      if (tid < kMaxTop) sm.mine.top[tid].v = -INFINITY, sm.mine.top[tid].id = -1;
+      for (int i = tid; i < split * n; i += kThreads) sm.cand[i] = all[i / n].top[i % n];
+      __syncthreads();
+      place_keys(sm.cand, split * n, n, [&](int place, int i) {
+        if (sm.cand[i].id >= 0) sm.mine.top[place] = sm.cand[i];
+      });
+    }
   }
-
+  r = kUnset, S = 0.0f, A = 0.0f, top_v = -INFINITY;
+  if (lane < split) r = all[lane].r, S = all[lane].S, A = all[lane].A, top_v = all[lane].best;
+  join_warp(r, S, A);
+  top_v = max_warp(top_v);
+  const bool empty = (S == 0.0f && top_v == -INFINITY) || top_v * a.scale == -INFINITY;
+  // all probability on the largest logits: count them
+  const bool flat = !empty && top_v > -INFINITY && top_v < INFINITY &&
+                    (S == 0.0f || fabsf(top_v * u) > 1e38f || (TYPE == MOE_BF16 && top_v <= bound));
+  bool bad = top_v == INFINITY || top_v * a.scale == INFINITY || (!flat && S != S);
+  __syncthreads();
+  if (flat) {
+    int eq = 0, nan = 0;
+    for (int j = tid; j < a.vocab; j += kThreads) {
+      const float v = row.at(j);
+      eq += v == top_v;
+      nan |= v != v;
+    }
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+    nan = __reduce_add_sync(0xFFFFFFFFu, nan);
+    if (lane == 0) sm.cnt[warp][0] = eq, sm.cnt[warp][1] = nan;
+    __syncthreads();
+    eq = nan = 0;
+    for (int w = 0; w < kWarps; ++w) eq += sm.cnt[w][0], nan += sm.cnt[w][1];
+    S = static_cast<float>(eq);
+    A = 0.0f;
+    bad = bad || nan;
+  }
   if (warp != 0) return;
-  R = sm.part.R, S = sm.part.S, A = sm.part.A;
-  const float ln_s = logf(S);
-  // no probability anywhere: only -inf, or logits that overflow to it
-  const bool empty = S == 0.0f || R * a.scale == -INFINITY;
-  const bool bad = S != S || R == INFINITY;
+
+  const float log2_s = log2f(S);
+  const float lse = flat ? fmaf(top_v, a.scale, kLn2 * log2_s) : kLn2 * (r + log2_s);
   auto logprob = [&](float x) {
     if (bad) return NAN;
-    return empty || x * a.scale == -INFINITY ? -INFINITY : (x - R) * a.scale - ln_s;
+    if (empty || x * a.scale == -INFINITY) return -INFINITY;
+    if (flat) return x == top_v ? -kLn2 * log2_s : (x - top_v) * a.scale - kLn2 * log2_s;
+    const float d = fmaf(x, u, -r);
+    return d == -INFINITY ? x * a.scale - lse : kLn2 * (d - log2_s);
   };
   if (lane == 0) {
-    if (a.lse) a.lse[t] = bad ? NAN : empty ? -INFINITY : fmaf(R, a.scale, ln_s);
-    if (a.entropy) a.entropy[t] = bad ? NAN : empty ? 0.0f : ln_s - kLn2 * (A / S);
+    if (a.lse) a.lse[t] = bad ? NAN : empty ? -INFINITY : lse;
+    if (a.entropy) a.entropy[t] = bad ? NAN : empty ? 0.0f : kLn2 * (log2_s - A / S);
   }
   if (lane < a.n_targets) {
     const int64_t i = t * a.n_targets + lane;
     const int id = a.targets[i];
     const bool in = id >= 0 && id < a.vocab;
-    if (a.target_logprobs) a.target_logprobs[i] = in ? logprob(load_elem(row.p, TYPE, id)) : -INFINITY;
+    if (a.target_logprobs) a.target_logprobs[i] = in ? logprob(row.at(id)) : -INFINITY;
     if constexpr (NT > 0) {
-      if (a.target_ranks) a.target_ranks[i] = in ? sm.part.cnt[lane] + 1 : 0;
+      int q = 0;
+      for (int w = 0; w < split; ++w) q += all[w].cnt[lane];
+      if (a.target_ranks) a.target_ranks[i] = in ? q + 1 : 0;
     }
   }
   if (lane < n) {
-    Key k = sm.part.top[lane];
+    Key k = sm.mine.top[lane];
     if (k.id >= 0 && k.v * a.scale == -INFINITY) k.id = -1;
     if (a.top_ids) a.top_ids[t * n + lane] = k.id;
     if (a.top_logprobs) a.top_logprobs[t * n + lane] = k.id >= 0 ? logprob(k.v) : -INFINITY;
@@ -464,8 +661,8 @@ extern "C" int moe_token_logprobs(const moe_token_logprobs_args* args, void* str
   if (a.top_n < 0 || a.top_n > kMaxTop)
     return reportf(MOE_ERR_ARG, "moe_token_logprobs: top_n=%d must be in [0, %d]", a.top_n, kMaxTop);
   if (a.n_targets > 0 && !a.targets) return reportf(MOE_ERR_ARG, "moe_token_logprobs: targets is NULL");
-  if (!(a.scale > 0.0f) || std::isinf(a.scale))
-    return reportf(MOE_ERR_ARG, "moe_token_logprobs: scale must be positive and finite");
+  if (!(a.scale >= 5.4210109e-20f && a.scale <= 1.8446744e19f))
+    return reportf(MOE_ERR_ARG, "moe_token_logprobs: scale must be in [2^-64, 2^64]");
   const uintptr_t words = reinterpret_cast<uintptr_t>(a.targets) | reinterpret_cast<uintptr_t>(a.target_logprobs) |
                           reinterpret_cast<uintptr_t>(a.target_ranks) | reinterpret_cast<uintptr_t>(a.entropy) |
                           reinterpret_cast<uintptr_t>(a.lse) | reinterpret_cast<uintptr_t>(a.top_ids) |

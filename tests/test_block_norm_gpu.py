@@ -115,6 +115,33 @@ def test_parts(kw):
     check(None, h, w_pre=rnd(H, seed=4), **kw)
 
 
+@pytest.mark.parametrize("H", [257, 264, 1000, 2048, 4100, 7168, 8192, 9000])
+@pytest.mark.parametrize("T", [1216, 2500])
+def test_many_rows(T, H):
+    """Enough rows for the streaming kernel, all in one pass and several per block."""
+    pad = -H % 8
+    y, h = rnd(T, H + pad, dtype=F32, seed=1)[:, :H], rnd(T, H + pad, seed=2)[:, :H]
+    ho, xo = (torch.empty(T, H + pad, dtype=BF, device=DEV)[:, :H] for _ in range(2))
+    check(y, h, gate=rnd(H, seed=3), w_post=rnd(H, seed=4), w_pre=rnd(H, seed=5), w_add=1.0, s=0.75, h_out=ho, x_out=xo)
+
+
+@pytest.mark.parametrize("yt,ht,xt,wt", [(BF, BF, BF, F32), (F32, F32, F32, BF), (HF, BF, HF, HF), (BF, F32, BF, F32)])
+@pytest.mark.parametrize("shape", [(1, 640), (1300, 1), (1300, 640)])
+def test_many_rows_types_gates_and_parts(yt, ht, xt, wt, shape):
+    T, H = 1300, 640
+    y, h = rnd(T, H, dtype=yt, seed=1), rnd(T, H, dtype=ht, seed=2)
+    w, v, g = rnd(H, dtype=wt, seed=4), rnd(H, dtype=wt, seed=5), rnd(*shape, dtype=xt, seed=3)
+    for kw in (dict(), dict(post_norm=False), dict(pre_norm=False), dict(post_norm=False, pre_norm=False)):
+        check(y, h, x_type=xt, gate=g, w_post=w, w_pre=v, **kw)
+    check(y, None, x_type=xt, gate=g, w_post=w, w_pre=v)
+    check(None, h, x_type=xt, w_pre=v)
+    keep = h.clone()
+    want = block_norm(y, h, gate=g, w_post=w, w_pre=v)
+    _, x2 = block_norm(y, keep, gate=g, w_post=w, w_pre=v, h_out=keep)
+    torch.cuda.synchronize()
+    assert torch.equal(keep, want[0]) and torch.equal(x2, want[1])
+
+
 def test_in_place_residual_and_repeat():
     T, H = 70, 7168
     y, h = rnd(T, H, dtype=F32, seed=1), rnd(T, H, seed=2)

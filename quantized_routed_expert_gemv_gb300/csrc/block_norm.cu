@@ -44,19 +44,24 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return s;
 }
 
-// VEC values as loaded, converted only when they are used, so that loads are
-// issued together whatever their types.
-template <int VEC>
+// Operands whose rows start on 16-byte boundaries, by bit.
+enum : int { kY = 1, kH = 2, kGate = 4, kWPost = 8, kWPre = 16, kHOut = 32, kXOut = 64, kAll = 127 };
+
+// Eight values as loaded, converted only when they are used, so that loads
+// are issued together whatever their types.  Of an operand whose rows do not
+// start on 16 bytes a warp loads its 256 values one by one, neighbouring
+// lanes neighbouring values (w[i] = value 32 i + lane), and exchanges them
+// through shared memory afterwards (settle).
 struct Raw {
-  uint32_t w[VEC];  // 16-bit types: two values a word (VEC = 8), or one
+  uint32_t w[8];  // 16-bit types: two values a word once settled
 
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = 0;
+    for (int i = 0; i < 8; ++i) w[i] = 0;
   }
-  // Elements [j, j + VEC) of the row that starts at element `row`, zeros past H.
-  __device__ __forceinline__ void load(const void* p, bool wide, int64_t row, int j, int H) {
-    if constexpr (VEC == 8) {
+  // Elements [j, j + 8) of the row that starts at element `row`, zeros past H.
+  __device__ __forceinline__ void load(const void* p, bool wide, bool aligned, int64_t row, int j, int H) {
+    if (aligned) {
       if (j + 8 <= H) {
         const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (row + j) * (wide ? 4 : 2));
         const uint4 a = q[0];
@@ -78,25 +83,42 @@ struct Raw {
         }
       }
     } else {
-      w[0] = 0;
-      if (j < H) w[0] = wide ? static_cast<const uint32_t*>(p)[row + j] : static_cast<const uint16_t*>(p)[row + j];
+      const int k = j - 7 * static_cast<int>(threadIdx.x & 31);  // the warp's first value + lane
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = 0;
+        if (k + 32 * i < H)
+          w[i] = wide ? static_cast<const uint32_t*>(p)[row + k + 32 * i] : static_cast<const uint16_t*>(p)[row + k + 32 * i];
+      }
     }
   }
-  __device__ __forceinline__ void get(int type, float (&v)[VEC]) const {
+  __device__ __forceinline__ void settle(uint32_t* buf, bool wide, bool aligned) {
+    if (aligned) return;
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) buf[32 * i + lane] = w[i];
+    __syncwarp();
+    const uint4 a = reinterpret_cast<const uint4*>(buf)[2 * lane], b = reinterpret_cast<const uint4*>(buf)[2 * lane + 1];
+    if (wide) {
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+      w[0] = a.x | a.y << 16, w[1] = a.z | a.w << 16, w[2] = b.x | b.y << 16, w[3] = b.z | b.w << 16;
+    }
+  }
+  __device__ __forceinline__ void get(int type, float (&v)[8]) const {
     if (type == MOE_F32) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(w[i]);
-    } else if constexpr (VEC == 8) {
-      unpack8(make_uint4(w[0], w[1], w[2], w[3]), type, v);
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
     } else {
-      v[0] = half_bits_to_f32(w[0], type);
+      unpack8(make_uint4(w[0], w[1], w[2], w[3]), type, v);
     }
   }
 };
 
-template <int VEC>
-__device__ __forceinline__ void store_chunk(void* p, int type, int64_t row, int j, int H, const float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
+__device__ __forceinline__ void store_chunk(void* p, int type, bool aligned, int64_t row, int j, int H, const float (&v)[8],
+                                            uint32_t* buf) {
+  if (aligned) {
     if (j + 8 <= H) {
       store8(p, type, row + j, v);
     } else {
@@ -105,59 +127,73 @@ __device__ __forceinline__ void store_chunk(void* p, int type, int64_t row, int 
         if (j + i < H) store_elem(p, type, row + j + i, v[i]);
     }
   } else {
-    if (j < H) store_elem(p, type, row + j, v[0]);
+    const int lane = threadIdx.x & 31, k = j - 7 * lane;
+    __syncwarp();
+    float4* to = reinterpret_cast<float4*>(buf) + 2 * lane;
+    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+    to[1] = make_float4(v[4], v[5], v[6], v[7]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + 32 * i < H) store_elem(p, type, row + k + 32 * i, __uint_as_float(buf[32 * i + lane]));
   }
 }
 
-template <int VEC>
-__device__ __forceinline__ void scale_by(float (&v)[VEC], float s, float add, const Raw<VEC>& raw, int type) {
-  float w[VEC];
+__device__ __forceinline__ void scale_by(float (&v)[8], float s, float add, const Raw& raw, int type) {
+  float w[8];
   raw.get(type, w);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] *= s * (add + w[i]);
+  for (int i = 0; i < 8; ++i) v[i] *= s * (add + w[i]);
 }
 
 // blockDim = (threads per row, rows per block); more than one row per block
-// only with 32 threads per row.  A thread holds NC chunks of VEC values.
-// Y32, H32: y and h are 32-bit.
-template <int VEC, int NC, bool Y32, bool H32>
-__global__ void __launch_bounds__(VEC == 8 ? 512 : 1024) block_norm_kernel(const moe_block_norm_args a) {
+// only with 32 threads per row.  A thread holds NC chunks of 8 values.
+// Y32, H32: y and h are 32-bit.  MIXED: the operands' types and alignments
+// (`aligned`) are looked at one by one.
+template <int NC, bool Y32, bool H32, bool MIXED>
+__global__ void __launch_bounds__(512) block_norm_kernel(const moe_block_norm_args a, int aligned) {
   __shared__ float red[2][32];
+  __shared__ __align__(16) uint32_t exchange[MIXED ? 16 : 1][256];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= a.rows) return;
   const int H = a.hidden;
+  const bool y32 = MIXED ? a.y_type == MOE_F32 : Y32, h32 = MIXED ? a.h_type == MOE_F32 : H32;
   const int yt = Y32 ? MOE_F32 : a.y_type, ht = H32 ? MOE_F32 : a.h_type;
-  auto at = [&](int c) { return static_cast<int>(c * blockDim.x + threadIdx.x) * VEC; };
-  Raw<VEC> y[NC], h[NC];
+  auto ok = [&](int bit) { return !MIXED || (aligned & bit); };
+  uint32_t* buf = MIXED ? exchange[(threadIdx.y * blockDim.x + threadIdx.x) >> 5] : nullptr;
+  auto at = [&](int c) { return static_cast<int>(c * blockDim.x + threadIdx.x) * 8; };
+  Raw y[NC], h[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    if (a.y) y[c].load(a.y, Y32, t * a.ld_y, at(c), H);
+    if (a.y) y[c].load(a.y, y32, ok(kY), t * a.ld_y, at(c), H);
     else y[c].zero();
-    if (a.h) h[c].load(a.h, H32, t * a.ld_h, at(c), H);
+    if (a.h) h[c].load(a.h, h32, ok(kH), t * a.ld_h, at(c), H);
     else h[c].zero();
   }
-  // few rows: the weights come with the row; many: from L1 when they are used
-  Raw<VEC> wp[NC], wn[NC], gt[NC];
+  // narrow rows: the weights come with the row; wide ones: from L1 when they are used
+  Raw wp[NC], wn[NC], gt[NC];
   const bool w32 = a.w_type == MOE_F32, g32 = a.gate_type == MOE_F32;
+  const bool has_wp = a.post_norm && a.w_post, has_wn = a.pre_norm && a.w_pre, has_g = a.y && a.gate && a.ld_gate_col;
   auto load_w = [&](int c) {
     wp[c].zero();
-    if (a.post_norm && a.w_post) wp[c].load(a.w_post, w32, 0, at(c), H);
-    if (a.y && a.gate && a.ld_gate_col) gt[c].load(a.gate, g32, t * a.ld_gate_row, at(c), H);
+    if (has_wp) wp[c].load(a.w_post, w32, ok(kWPost), 0, at(c), H);
+    if (has_g) gt[c].load(a.gate, g32, ok(kGate), t * a.ld_gate_row, at(c), H);
   };
   auto load_wn = [&](int c) {
     wn[c].zero();
-    if (a.pre_norm && a.w_pre) wn[c].load(a.w_pre, w32, 0, at(c), H);
+    if (has_wn) wn[c].load(a.w_pre, w32, ok(kWPre), 0, at(c), H);
   };
   if constexpr (NC == 1) load_w(0), load_wn(0);
   float g1 = 1.0f;
   if (a.y && a.gate && !a.ld_gate_col) g1 = load_elem(a.gate, a.gate_type, t * a.ld_gate_row);
-  float v[NC][VEC];
+  float v[NC][8];
   float ss = 0.0f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
+    if (a.y) y[c].settle(buf, y32, ok(kY));
     y[c].get(yt, v[c]);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+    for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
   }
   const float inv_h = 1.0f / static_cast<float>(H);
   float rs = 1.0f;
@@ -167,24 +203,29 @@ __global__ void __launch_bounds__(VEC == 8 ? 512 : 1024) block_norm_kernel(const
   for (int c = 0; c < NC; ++c) {
     if constexpr (NC > 1) load_w(c);
     if (a.y) {
-      if (a.post_norm) scale_by<VEC>(v[c], rs, a.w_add, wp[c], a.w_type);
-      if (a.gate && a.ld_gate_col) {
-        scale_by<VEC>(v[c], 1.0f, 0.0f, gt[c], a.gate_type);
+      if (a.post_norm) {
+        if (has_wp) wp[c].settle(buf, w32, ok(kWPost));
+        scale_by(v[c], rs, a.w_add, wp[c], a.w_type);
+      }
+      if (has_g) {
+        gt[c].settle(buf, g32, ok(kGate));
+        scale_by(v[c], 1.0f, 0.0f, gt[c], a.gate_type);
       } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[c][i] *= g1;
+        for (int i = 0; i < 8; ++i) v[c][i] *= g1;
       }
     }
     if (a.h) {
-      float hv[VEC];
+      float hv[8];
+      h[c].settle(buf, h32, ok(kH));
       h[c].get(ht, hv);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(a.residual_scale, hv[i], v[c][i]);
+      for (int i = 0; i < 8; ++i) v[c][i] = fmaf(a.residual_scale, hv[i], v[c][i]);
     }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
+    for (int i = 0; i < 8; ++i)
       if (at(c) + i < H) ss = fmaf(v[c][i], v[c][i], ss);
-    if (a.h_out) store_chunk<VEC>(a.h_out, a.h_type, t * a.ld_h_out, at(c), H, v[c]);
+    if (a.h_out) store_chunk(a.h_out, a.h_type, ok(kHOut), t * a.ld_h_out, at(c), H, v[c], buf);
   }
   if (!a.x_out) return;
   rs = 1.0f;
@@ -193,9 +234,10 @@ __global__ void __launch_bounds__(VEC == 8 ? 512 : 1024) block_norm_kernel(const
   for (int c = 0; c < NC; ++c) {
     if (a.pre_norm) {
       if constexpr (NC > 1) load_wn(c);
-      scale_by<VEC>(v[c], rs, a.w_add, wn[c], a.w_type);
+      if (has_wn) wn[c].settle(buf, w32, ok(kWPre));
+      scale_by(v[c], rs, a.w_add, wn[c], a.w_type);
     }
-    store_chunk<VEC>(a.x_out, a.x_type, t * a.ld_x_out, at(c), H, v[c]);
+    store_chunk(a.x_out, a.x_type, ok(kXOut), t * a.ld_x_out, at(c), H, v[c], buf);
   }
 }
 
@@ -289,7 +331,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int xe = elem_size(a.x_type), apart = team_threads * 8;
   const bool two = tt * 8 + apart < H;
   const int stride = static_cast<int>(gridDim.x) * teams;
-  int t = static_cast<int>(blockIdx.x) * teams + team;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * teams + team;
   if (t >= a.rows) return;
   const char* py = static_cast<const char*>(a.y) + (t * a.ld_y + tt * 8) * YE;
   const char* ph = static_cast<const char*>(a.h) + (t * a.ld_h + tt * 8) * HE;
@@ -345,23 +387,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
 }
 
-template <int VEC, int NC>
-cudaError_t launch_nc(const moe_block_norm_args& a, dim3 grid, dim3 block, cudaStream_t st) {
+template <int NC>
+cudaError_t launch_rows(const moe_block_norm_args& a, int aligned, dim3 grid, dim3 block, cudaStream_t st) {
   const bool y32 = a.y_type == MOE_F32, h32 = a.h_type == MOE_F32;
-  if (y32 && h32) block_norm_kernel<VEC, NC, true, true><<<grid, block, 0, st>>>(a);
-  else if (y32) block_norm_kernel<VEC, NC, true, false><<<grid, block, 0, st>>>(a);
-  else if (h32) block_norm_kernel<VEC, NC, false, true><<<grid, block, 0, st>>>(a);
-  else block_norm_kernel<VEC, NC, false, false><<<grid, block, 0, st>>>(a);
+  if (aligned != kAll) block_norm_kernel<NC, false, false, true><<<grid, block, 0, st>>>(a, aligned);
+  else if (y32 && h32) block_norm_kernel<NC, true, true, false><<<grid, block, 0, st>>>(a, aligned);
+  else if (y32) block_norm_kernel<NC, true, false, false><<<grid, block, 0, st>>>(a, aligned);
+  else if (h32) block_norm_kernel<NC, false, true, false><<<grid, block, 0, st>>>(a, aligned);
+  else block_norm_kernel<NC, false, false, false><<<grid, block, 0, st>>>(a, aligned);
   return cudaGetLastError();
-}
-
-template <int VEC>
-cudaError_t launch_vec(const moe_block_norm_args& a, int nc, dim3 grid, dim3 block, cudaStream_t st) {
-  if (nc == 1) return launch_nc<VEC, 1>(a, grid, block, st);
-  if (nc == 2) return launch_nc<VEC, 2>(a, grid, block, st);
-  if (nc == 4) return launch_nc<VEC, 4>(a, grid, block, st);
-  if constexpr (VEC == 1) return launch_nc<1, 16>(a, grid, block, st);
-  return cudaErrorInvalidValue;
 }
 
 template <bool Y32, bool H32>
@@ -423,17 +457,18 @@ extern "C" int moe_block_norm(const moe_block_norm_args* args, void* stream) {
                      static_cast<long long>(a.ld_gate_col), static_cast<long long>(a.ld_gate_row));
   }
 
-  const bool vec = vec_ok(a.y, a.y_type, a.ld_y) && vec_ok(a.h, a.h_type, a.ld_h) &&
-                   vec_ok(a.h_out, a.h_type, a.ld_h_out) && vec_ok(a.x_out, a.x_type, a.ld_x_out) &&
-                   vec_ok(a.w_post, a.w_type, 0) && vec_ok(a.w_pre, a.w_type, 0) &&
-                   (!a.ld_gate_col || vec_ok(a.gate, a.gate_type, a.ld_gate_row));
-  const int chunks = vec ? (a.hidden + 7) / 8 : a.hidden;
+  const int aligned = kAll & ~((vec_ok(a.y, a.y_type, a.ld_y) ? 0 : kY) | (vec_ok(a.h, a.h_type, a.ld_h) ? 0 : kH) |
+                               (vec_ok(a.h_out, a.h_type, a.ld_h_out) ? 0 : kHOut) |
+                               (vec_ok(a.x_out, a.x_type, a.ld_x_out) ? 0 : kXOut) |
+                               (vec_ok(a.w_post, a.w_type, 0) ? 0 : kWPost) | (vec_ok(a.w_pre, a.w_type, 0) ? 0 : kWPre) |
+                               (!a.ld_gate_col || vec_ok(a.gate, a.gate_type, a.ld_gate_row) ? 0 : kGate));
+  const int chunks = (a.hidden + 7) / 8;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (!e) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e) return reportf(MOE_ERR_CUDA, "moe_block_norm: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
-  if (vec && a.hidden % 8 == 0 && a.hidden > 256 && a.hidden <= kStreamHidden && a.y && a.h && a.h_out && a.x_out &&
+  if (aligned == kAll && a.hidden % 8 == 0 && a.hidden > 256 && a.hidden <= kStreamHidden && a.y && a.h && a.h_out && a.x_out &&
       a.post_norm && a.pre_norm && (!a.gate || (a.ld_gate_col && !a.ld_gate_row)) &&
       a.rows >= static_cast<int64_t>(kStreamRows) * sms) {
     const bool y32 = a.y_type == MOE_F32, h32 = a.h_type == MOE_F32;
@@ -442,17 +477,13 @@ extern "C" int moe_block_norm(const moe_block_norm_args* args, void* stream) {
         : h32      ? launch_stream<false, true>(a, sms, st)
                    : launch_stream<false, false>(a, sms, st);
   } else {
-    const int max_nc = vec ? 4 : 16;
-    int nc = 1;
-    dim3 block(32, 1);
-    if (chunks <= 32) {
-      block.y = 4;
-    } else {
-      while (nc < max_nc && chunks > 512 * nc) nc = nc == 4 ? 16 : nc * 2;
-      block.x = ((chunks + nc - 1) / nc + 31) / 32 * 32;
-    }
+    // a warp a row up to 256 values, else a block with up to 512 threads
+    const int nc = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
+    const dim3 block = chunks <= 32 ? dim3(32, 4) : dim3(((chunks + nc - 1) / nc + 31) / 32 * 32);
     const dim3 grid((static_cast<unsigned>(a.rows) + block.y - 1) / block.y);
-    e = vec ? launch_vec<8>(a, nc, grid, block, st) : launch_vec<1>(a, nc, grid, block, st);
+    e = nc == 1   ? launch_rows<1>(a, aligned, grid, block, st)
+        : nc == 2 ? launch_rows<2>(a, aligned, grid, block, st)
+                  : launch_rows<4>(a, aligned, grid, block, st);
   }
   if (e != cudaSuccess) return reportf(MOE_ERR_CUDA, "moe_block_norm: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
   return MOE_OK;

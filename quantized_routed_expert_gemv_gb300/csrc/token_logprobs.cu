@@ -149,9 +149,11 @@ __device__ __forceinline__ float max_warp(float v) {
 template <class Emit>
 __device__ __forceinline__ void place_keys(const Key* keys, int m, int n, Emit emit) {
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int i = threadIdx.x >> 5; i < m; i += kWarps) {
     const Key k = keys[i];
     int c = 0;
+#pragma unroll 1
     for (int q = lane; q < m; q += 32) c += before(keys[q], k);
     c = __reduce_add_sync(0xFFFFFFFFu, c);
     if (lane == 0 && c < n) emit(c, i);
@@ -221,7 +223,7 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n
   if (warp == 0) {
     const float v = sm.team[lane];
     int place = 0;
-#pragma unroll
+#pragma unroll 8
     for (int q = 0; q < 32; ++q) {
       const float w = __shfl_sync(0xFFFFFFFFu, v, q);
       place += w > v || (w == v && q < lane);
@@ -261,6 +263,7 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n
   if (edge_j >= 0) push(edge_v, edge_j);
   // chunk k of winner g is item g * chunks + k, one thread each
   const int chunks = (c1 - c0 + kThreads - 1) / kThreads, items = min(n, m) * chunks;
+#pragma unroll 1
   for (int e = tid; e < items; e += kThreads) {
     const int g = e / chunks, c = c0 + sm.sel_owner[g] + (e - g * chunks) * kThreads;
     if (c < c1) {
@@ -314,7 +317,7 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n
   }
 }
 
-// NT: targets whose ranks are counted, rounded up to 0, 1 or 8.
+// NT: targets whose ranks are counted, rounded up to 0, 1, 2, 4 or 8.
 template <int TYPE, int NT>
 __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_token_logprobs_args a, int split) {
   __shared__ Smem sm;
@@ -345,6 +348,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
   };
   fetch(c0 + tid);
 
+  // the first block's first warp writes the row's answers: its targets' logits
+  int my_target = -1;
+  float my_logit = 0.0f;
+  if (rank == 0 && tid < a.n_targets) {
+    my_target = a.targets[t * a.n_targets + tid];
+    if (my_target >= a.vocab) my_target = -1;
+    if (my_target >= 0) my_logit = row.at(my_target);
+  }
   // ranks: chunk c counts logits >= lo if it lies before the target's chunk,
   // else >= hi (the next value); the target's own chunk is completed below
   int tj[NG], tc[NG], cnt[NG];
@@ -370,6 +381,23 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
         const uint32_t n = next_up16(b, TYPE == MOE_BF16 ? 0x7F80u : 0x7C00u);
         lo[g] = b * 0x10001u;
         hi[g] = n * 0x10001u;
+      }
+    }
+  }
+
+  // Read early, used after the pass, in the first part: the row's edges, one
+  // thread each, and the logits before a target in its own chunk, a warp's
+  // first eight threads each.
+  int edge_j = -1, fix_g = -1;
+  float edge_v = -INFINITY, fix_v = NAN;
+  if (rank == 0) {
+    if (tid < 16) edge_j = row.edge(tid);
+    if (edge_j >= 0) edge_v = row.at(edge_j);
+    if constexpr (NT > 0) {
+#pragma unroll
+      for (int g = 0; g < NT; ++g) {
+        const int j = 8 * tc[g] - row.off + lane;
+        if (warp == g && lane < 8 && tc[g] >= row.w0 && tc[g] < row.w1 && j < tj[g]) fix_g = g, fix_v = row.at(j);
       }
     }
   }
@@ -484,26 +512,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
     }
   }
 
-  // the row's edges, by the first part; the places of the targets' own chunks
-  // that come before them in a tie
-  int edge_j = -1;
-  float edge_v = -INFINITY;
-  if (rank == 0 && tid < 16) {
-    edge_j = row.edge(tid);
-    if (edge_j >= 0) {
-      edge_v = row.at(edge_j);
-      sums.reach(edge_v * u);
-      sums.add<true>(make_float2(edge_v, -INFINITY), u);
-    }
+  if (edge_j >= 0) {
+    sums.reach(edge_v * u);
+    sums.add<true>(make_float2(edge_v, -INFINITY), u);
   }
   if constexpr (NT > 0) {
 #pragma unroll
     for (int g = 0; g < NT; ++g) {
       if (edge_j >= 0) cnt[g] += edge_v > xt[g] || (edge_v == xt[g] && edge_j < tj[g]);
-      if (rank == 0 && tid < 8 && tc[g] >= row.w0 && tc[g] < row.w1) {
-        const int j = 8 * tc[g] - row.off + tid;
-        cnt[g] += j < tj[g] && row.at(j) == xt[g];
-      }
+      cnt[g] += fix_g == g && fix_v == xt[g];
     }
   }
 
@@ -552,11 +569,32 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
     all = sm.parts;
     if (n > 0) {
       if (tid < kMaxTop) sm.mine.top[tid].v = -INFINITY, sm.mine.top[tid].id = -1;
-      for (int i = tid; i < split * n; i += kThreads) sm.cand[i] = all[i / n].top[i % n];
       __syncthreads();
-      place_keys(sm.cand, split * n, n, [&](int place, int i) {
-        if (sm.cand[i].id >= 0) sm.mine.top[place] = sm.cand[i];
-      });
+      if (tid < split * kMaxTop && tid % kMaxTop < n) {
+        // a token's place: its own in its part's list, and in every other
+        // list (sorted, at most 32 long) the number of tokens before it
+        const int own = tid / kMaxTop;
+        const Key k = all[own].top[tid % kMaxTop];
+        int at[kMaxSplit] = {};
+#pragma unroll 1
+        for (int step = 32; step; step >>= 1) {
+          // no branch around the loads, so that the lists' go out together
+          // (entries of absent lists are read and not used)
+          Key o[kMaxSplit];
+#pragma unroll
+          for (int q = 0; q < kMaxSplit; ++q) o[q] = all[q].top[min(at[q] + step, kMaxTop) - 1];
+#pragma unroll
+          for (int q = 0; q < kMaxSplit; ++q) {
+            const bool first = (o[q].v > k.v) | ((o[q].v == k.v) & (o[q].id < k.id));
+            at[q] += (first & (q < split) & (at[q] + step <= n)) ? step : 0;
+          }
+        }
+        int place = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q) place += at[q];
+        if (k.id >= 0 && place < n) sm.mine.top[place] = k;
+      }
+      __syncthreads();
     }
   }
   r = kUnset, S = 0.0f, A = 0.0f, top_v = -INFINITY;
@@ -603,9 +641,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
   }
   if (lane < a.n_targets) {
     const int64_t i = t * a.n_targets + lane;
-    const int id = a.targets[i];
-    const bool in = id >= 0 && id < a.vocab;
-    if (a.target_logprobs) a.target_logprobs[i] = in ? logprob(row.at(id)) : -INFINITY;
+    const bool in = my_target >= 0;
+    if (a.target_logprobs) a.target_logprobs[i] = in ? logprob(my_logit) : -INFINITY;
     if constexpr (NT > 0) {
       int q = 0;
       for (int w = 0; w < split; ++w) q += all[w].cnt[lane];
@@ -635,6 +672,8 @@ cudaError_t launch_type(const moe_token_logprobs_args& a, int split, cudaStream_
   const int nt = a.target_ranks ? a.n_targets : 0;
   if (nt == 0) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 0>, a, split);
   if (nt == 1) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 1>, a, split);
+  if (nt == 2) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 2>, a, split);
+  if (nt <= 4) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 4>, a, split);
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, kMaxTargets>, a, split);
 }
 

@@ -27,13 +27,19 @@ _ELEM_TYPE = {torch.bfloat16: moe.MOE_BF16, torch.float16: moe.MOE_F16, torch.fl
 
 
 def _stream(device, stream):
-    return stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
+    """`stream`, or the device's current one (the raw handle: building a
+    torch.cuda.Stream takes as long as the call itself)."""
+    if stream is not None:
+        return stream
+    return torch._C._cuda_getCurrentRawStream(device.index if device.index is not None else torch.cuda.current_device())
 
 
 def _ld(t: torch.Tensor) -> int:
     """Leading dimension of a matrix whose rows are contiguous."""
-    assert t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1), "rows must be contiguous"
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    ld, step = t.stride()
+    rows, cols = t.shape
+    assert step == 1 or cols == 1, "rows must be contiguous"
+    return ld if rows > 1 else max(ld, cols)
 
 
 def block_norm(y=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=True, pre_norm=True, w_add=0.0,
@@ -132,8 +138,8 @@ class Fp8Linear:
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, out_type=torch.bfloat16, stream=None):
         """x [rows][k] -> [rows][n]."""
-        rows = x.shape[0]
-        assert x.shape[1] == self.k
+        rows, k = x.shape
+        assert k == self.k
         if out is None:
             out = torch.empty(rows, self.n, dtype=out_type, device=x.device)
         moe.moe_fp8_linear(self.handle, x.data_ptr(), _ELEM_TYPE[x.dtype], _ld(x), rows, out.data_ptr(),

@@ -80,7 +80,7 @@ int moe_block_norm(const moe_block_norm_args *args, void *stream);
  *     log probabilities
  * in one pass over the logits, in 32 bits.
  *
- *   rows >= 0 (0: no work); vocab >= 1; n_targets in [0, 8]; top_n in [0, 32].
+ *   rows in [0, 2^27] (0: no work); vocab in [1, 2^24]; n_targets in [0, 8]; top_n in [0, 32].
  *   scale:   in [2^-64, 2^64].
  *   targets: device int32 [rows][n_targets].
  *   target_logprobs: device float [rows][n_targets]; target_ranks: device

@@ -42,7 +42,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // chunks of 8 logits a thread loads at once
 __host__ __device__ constexpr int batch_of(int type) { return type == MOE_F32 ? 2 : 4; }
@@ -94,31 +94,44 @@ __device__ __forceinline__ uint32_t next_up16(uint32_t bits, uint32_t inf) {
   return bits & 0x8000u ? bits - 1 : bits + 1;
 }
 
-// A thread's running sums.
+// A thread's running sums; nr is minus the reference, twice, and `limit` the
+// logit above which the reference has to move (nr unset: what adds at all).
 struct Sums {
-  float r = kUnset;
-  float2 S = {0.0f, 0.0f}, A = {0.0f, 0.0f};
+  float2 nr = {-kUnset, -kUnset}, S = {0.0f, 0.0f}, A = {0.0f, 0.0f};
+  float limit;
+  __device__ __forceinline__ explicit Sums(float u) : limit(kFloor / u) {}
 
-  // Makes room for values up to m (in powers of two).
-  __device__ __forceinline__ void reach(float m) {
-    if (m > kFloor && (r == kUnset || m - r > kRefSlack)) {
-      const float d = r == kUnset ? -1e4f : max_nan(r - m, -1e4f);
+  // Makes room for logits up to m.
+  __device__ __forceinline__ void reach(float m, float u) {
+    if (m > limit) {
+      const float z = m * u;
+      const float d = nr.x == -kUnset ? -1e4f : max_nan(-nr.x - z, -1e4f);
       const float e = ex2(d);
       A.x = fmaf(S.x, d, A.x) * e, A.y = fmaf(S.y, d, A.y) * e;
       S.x *= e, S.y *= e;
-      r = m;
+      nr = make_float2(-z, -z);
+      limit = m + kRefSlack / u;
     }
   }
-  // Two logits (already bounded below unless CLAMP).
+  // Two logits (already bounded below unless CLAMP); uu is u twice.
   template <bool CLAMP>
-  __device__ __forceinline__ void add(float2 l, float u) {
-    float2 d = __ffma2_rn(l, make_float2(u, u), make_float2(-r, -r));
+  __device__ __forceinline__ void add(float2 l, float2 uu) {
+    float2 d = __ffma2_rn(l, uu, nr);
     if (CLAMP) d.x = max_nan(d.x, -200.0f), d.y = max_nan(d.y, -200.0f);
     const float2 e = make_float2(ex2(d.x), ex2(d.y));
     S = __fadd2_rn(S, e);
     A = __ffma2_rn(e, d, A);
   }
 };
+
+// Masks of two 16-bit halves that are not below thr's, and the equal ones.
+template <int TYPE>
+__device__ __forceinline__ uint32_t ge_mask(uint32_t w, uint32_t thr) {
+  if constexpr (TYPE == MOE_BF16)
+    return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&thr));
+  else
+    return __hge2_mask(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&thr));
+}
 
 // Joins the (r, S, A) of a warp's lanes in every lane: moved to the largest
 // reference, then summed in a fixed order.  Lanes without a sum have r unset
@@ -319,7 +332,7 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n
 
 // NT: targets whose ranks are counted, rounded up to 0, 1, 2, 4 or 8.
 template <int TYPE, int NT>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_token_logprobs_args a, int split) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kernel(const moe_token_logprobs_args a, int split) {
   __shared__ Smem sm;
   constexpr bool F32 = TYPE == MOE_F32;
   constexpr int kBatch = batch_of(TYPE);
@@ -334,19 +347,29 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
   const int per = (row.w1 - row.w0 + split - 1) / split;
   const int c0 = min(row.w1, row.w0 + rank * per), c1 = min(row.w1, c0 + per);
 
-  // raw logits of a batch: chunk i at c + i * kThreads, -inf outside the part
-  uint4 raw[kBatch][F32 ? 2 : 1];
-  auto fetch = [&](int c) {
+  // Raw logits of a batch: chunk i at c + i * kThreads, -inf outside the part.
+  // The batches before the last are whole for every thread.
+  constexpr int Q = F32 ? 2 : 1, kStep = kBatch * kThreads;
+  using Batch = uint4[kBatch][Q];
+  auto fetch = [&](Batch& raw, int cb) {
+    const uint4* p = row.chunk(cb + tid);
+    if (cb + kStep <= c1) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = c + i * kThreads;
-      constexpr uint32_t fill = F32 ? 0xFF800000u : TYPE == MOE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+      for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-      for (int q = 0; q < (F32 ? 2 : 1); ++q)
-        raw[i][q] = k < c1 ? __ldg(row.chunk(k) + q) : make_uint4(fill, fill, fill, fill);
+        for (int q = 0; q < Q; ++q) raw[i][q] = __ldg(p + i * kThreads * Q + q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        constexpr uint32_t fill = F32 ? 0xFF800000u : TYPE == MOE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          raw[i][q] = cb + tid + i * kThreads < c1 ? __ldg(p + i * kThreads * Q + q) : make_uint4(fill, fill, fill, fill);
+      }
     }
   };
-  fetch(c0 + tid);
+  Batch even, odd;
+  fetch(even, c0);
 
   // the first block's first warp writes the row's answers: its targets' logits
   int my_target = -1;
@@ -358,10 +381,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
   }
   // ranks: chunk c counts logits >= lo if it lies before the target's chunk,
   // else >= hi (the next value); the target's own chunk is completed below
-  int tj[NG], tc[NG], cnt[NG];
+  int tj[NG], tc[NG];
   float xt[NG];
-  uint32_t lo[NG], hi[NG];
-  uint32_t cnt2[NG];
+  uint32_t lo[NG], hi[NG], cnt[NG];
   if constexpr (NT > 0) {
 #pragma unroll
     for (int g = 0; g < NT; ++g) {
@@ -371,7 +393,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
       xt[g] = in ? row.at(tj[g]) : NAN;
       tc[g] = in ? (tj[g] + row.off) / 8 : -1;
       cnt[g] = 0;
-      cnt2[g] = 0;
       if constexpr (F32) {
         lo[g] = __float_as_uint(xt[g]);
         hi[g] = __float_as_uint(next_up(xt[g]));
@@ -402,22 +423,16 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
     }
   }
 
-  Sums sums;
+  Sums sums(u);
   float best = -INFINITY;
-  int best_b = -1;
+  int best_c = -1;
   // bf16 logits are bounded below before they are widened, so that a value
   // under the floor gives 0 * finite in A
   const float bound = __bfloat162float(__float2bfloat16_rn(fmaxf(-1.2676506e30f / u, -3.3895314e38f)));
   const __nv_bfloat162 bound2 = __float2bfloat162_rn(bound);
-  int batches = 0;
-  for (int c = c0 + tid; c - tid < c1; c += kBatch * kThreads) {
-    uint4 cur[kBatch][F32 ? 2 : 1];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-      for (int q = 0; q < (F32 ? 2 : 1); ++q) cur[i][q] = raw[i][q];
-    if (c - tid + kBatch * kThreads < c1) fetch(c + kBatch * kThreads);
-
+  const float2 uu = make_float2(u, u);
+  // a batch whose first chunk is cb; this thread's are cb + tid + i * kThreads
+  auto process = [&](const Batch& cur, int cb) {
     float m;
     if constexpr (F32) {
       m = -INFINITY;
@@ -445,94 +460,102 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
       }
       m = fmaxf(__low2float(w), __high2float(w));
     }
-    if (m > best) best = m, best_b = c - tid;
-    sums.reach(m * u);
-
+    best_c = m > best ? cb : best_c;
+    best = fmaxf(best, m);
+    sums.reach(m, u);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = c + i * kThreads;
+    for (int g = 0; g < NT; ++g) {
+      // logits not below the target's in a batch before its chunk, above
+      // it in one after; the batch of its chunk counts as one after, and
+      // its equals in the chunks before are added
+      const uint32_t thr = cb + kStep <= tc[g] ? lo[g] : hi[g];
+      uint32_t q = 0;
 #pragma unroll
-      for (int g = 0; g < NT; ++g) {
-        // outside the part nothing counts
-        const uint32_t none = F32 ? 0x7FC00000u : TYPE == MOE_BF16 ? 0x7FC07FC0u : 0x7E007E00u;
-        const uint32_t thr = k >= c1 ? none : k < tc[g] ? lo[g] : hi[g];
+      for (int i = 0; i < kBatch; ++i) {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&cur[i][0]);
-        if constexpr (F32) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) cnt[g] += __uint_as_float(w[q]) >= __uint_as_float(thr);
-        } else if constexpr (TYPE == MOE_BF16) {
-          __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&cnt2[g]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            s = __hadd2(s, __hge2(*reinterpret_cast<const __nv_bfloat162*>(w + q), *reinterpret_cast<const __nv_bfloat162*>(&thr)));
-          cnt2[g] = *reinterpret_cast<const uint32_t*>(&s);
-        } else {
-          __half2 s = *reinterpret_cast<const __half2*>(&cnt2[g]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            s = __hadd2(s, __hge2(*reinterpret_cast<const __half2*>(w + q), *reinterpret_cast<const __half2*>(&thr)));
-          cnt2[g] = *reinterpret_cast<const uint32_t*>(&s);
+        for (int z = 0; z < 4 * Q; ++z) {
+          if constexpr (F32) q += __uint_as_float(w[z]) >= __uint_as_float(thr);
+          else q += ge_mask<TYPE>(w[z], thr);
         }
       }
+      if (cb <= tc[g] && tc[g] < cb + kStep) {
 #pragma unroll
-      for (int q = 0; q < (F32 ? 2 : 1); ++q) {
-        const uint32_t w[4] = {cur[i][q].x, cur[i][q].y, cur[i][q].z, cur[i][q].w};
-        if constexpr (F32) {
-          sums.add<true>(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), u);
-          sums.add<true>(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), u);
-        } else {
+        for (int i = 0; i < kBatch; ++i) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&cur[i][0]);
+          if (cb + tid + i * kThreads < min(tc[g], c1)) {
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            if constexpr (TYPE == MOE_BF16) {
-              const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[z]), bound2);
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(&b);
-              sums.add<false>(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)), u);
-            } else {
-              sums.add<true>(__half22float2(*reinterpret_cast<const __half2*>(&w[z])), u);
+            for (int z = 0; z < 4 * Q; ++z) {
+              if constexpr (F32) q += __uint_as_float(w[z]) == xt[g];
+              else q += ge_mask<TYPE>(w[z], lo[g]) & ~ge_mask<TYPE>(w[z], hi[g]);
             }
           }
         }
       }
+      cnt[g] += q;
     }
-    if constexpr (!F32 && NT > 0) {
-      // a half counts 16 a batch and is exact to 256
-      if (++batches == 16 || c - tid + kBatch * kThreads >= c1) {
-        batches = 0;
 #pragma unroll
-        for (int g = 0; g < NT; ++g) {
-          float2 f;
-          if constexpr (TYPE == MOE_BF16)
-            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&cnt2[g]));
-          else
-            f = __half22float2(*reinterpret_cast<const __half2*>(&cnt2[g]));
-          cnt[g] += static_cast<int>(f.x) + static_cast<int>(f.y);
-          cnt2[g] = 0;
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const uint32_t w[4] = {cur[i][q].x, cur[i][q].y, cur[i][q].z, cur[i][q].w};
+        if constexpr (F32) {
+          sums.add<true>(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), uu);
+          sums.add<true>(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), uu);
+        } else {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            if constexpr (TYPE == MOE_BF16) {
+              const __nv_bfloat162 v = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[z]), bound2);
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(&v);
+              sums.add<false>(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)), uu);
+            } else {
+              sums.add<true>(__half22float2(*reinterpret_cast<const __half2*>(&w[z])), uu);
+            }
+          }
         }
       }
-    }
+  };
+  int cb = c0;
+#pragma unroll 1
+  while (cb < c1) {
+    if (cb + kStep < c1) fetch(odd, cb + kStep);
+    process(even, cb);
+    cb += kStep;
+    if (cb >= c1) break;
+    if (cb + kStep < c1) fetch(even, cb + kStep);
+    process(odd, cb);
+    cb += kStep;
   }
 
   if (edge_j >= 0) {
-    sums.reach(edge_v * u);
-    sums.add<true>(make_float2(edge_v, -INFINITY), u);
+    sums.reach(edge_v, u);
+    sums.add<true>(make_float2(edge_v, -INFINITY), uu);
   }
-  if constexpr (NT > 0) {
 #pragma unroll
-    for (int g = 0; g < NT; ++g) {
-      if (edge_j >= 0) cnt[g] += edge_v > xt[g] || (edge_v == xt[g] && edge_j < tj[g]);
-      cnt[g] += fix_g == g && fix_v == xt[g];
+  for (int g = 0; g < NT; ++g) {
+    if constexpr (!F32) {
+      // cnt is the sum of masks: 65535 low - 65536 high counts, modulo 2^32
+      const uint32_t low = (0u - cnt[g]) & 0xFFFFu;
+      cnt[g] = low + (((65535u * low - cnt[g]) >> 16) & 0xFFFFu);
     }
+    // the last batch's places outside the part hold -inf, which counts
+    // before a target that is -inf itself
+    if (xt[g] == -INFINITY && c0 < c1 && cb <= tc[g])
+      for (int k = cb - kStep + tid; k < cb; k += kThreads) cnt[g] -= k >= c1 ? 8 : 0;
+    if (edge_j >= 0) cnt[g] += edge_v > xt[g] || (edge_v == xt[g] && edge_j < tj[g]);
+    cnt[g] += fix_g == g && fix_v == xt[g];
   }
 
   // join the block's sums in a fixed order
-  float r = sums.r, S = sums.S.x + sums.S.y, A = sums.A.x + sums.A.y;
+  float r = -sums.nr.x, S = sums.S.x + sums.S.y, A = sums.A.x + sums.A.y;
   join_warp(r, S, A);
   if (lane == 0) sm.r[warp] = r, sm.S[warp] = S, sm.A[warp] = A;
   if constexpr (NT > 0) {
 #pragma unroll
     for (int g = 0; g < NT; ++g) {
-      const int s = __reduce_add_sync(0xFFFFFFFFu, cnt[g]);
-      if (lane == 0) sm.cnt[warp][g] = s;
+      const uint32_t s = __reduce_add_sync(0xFFFFFFFFu, cnt[g]);
+      if (lane == 0) sm.cnt[warp][g] = static_cast<int>(s);
     }
   }
   const int n = a.top_n;
@@ -553,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const moe_t
       sm.mine.cnt[lane] = q;
     }
   }
-  if (n > 0) select_top<TYPE>(row, sm, n, c0, c1, best, best_b, edge_v, edge_j);
+  if (n > 0) select_top<TYPE>(row, sm, n, c0, c1, best, best_c, edge_v, edge_j);
   __syncthreads();
 
   // the parts meet in the first block
@@ -687,8 +710,8 @@ extern "C" int moe_token_logprobs(const moe_token_logprobs_args* args, void* str
   if (a.rows < 0) return reportf(MOE_ERR_ARG, "moe_token_logprobs: rows=%d is negative", a.rows);
   if (a.rows == 0) return MOE_OK;  // whatever the buffers: empty ones may be NULL
   if (a.rows > (1 << 27)) return reportf(MOE_ERR_ARG, "moe_token_logprobs: rows=%d is above 2^27", a.rows);
-  if (a.vocab < 1 || a.vocab > (1 << 30))
-    return reportf(MOE_ERR_ARG, "moe_token_logprobs: vocab=%d must be in [1, 2^30]", a.vocab);
+  if (a.vocab < 1 || a.vocab > (1 << 24))  // a thread's counts of a row fit 16 bits
+    return reportf(MOE_ERR_ARG, "moe_token_logprobs: vocab=%d must be in [1, 2^24]", a.vocab);
   if (!elem_type_ok(a.logits_type))
     return reportf(MOE_ERR_ARG, "moe_token_logprobs: logits have an unknown type %d", a.logits_type);
   if (!a.logits) return reportf(MOE_ERR_ARG, "moe_token_logprobs: logits is NULL");

@@ -43,6 +43,7 @@ namespace cg = cooperative_groups;
 constexpr int kBlk = 128;              // inputs per scale block, and outputs per tile
 constexpr int kTileW = kBlk * kBlk;    // bytes of a weight tile
 constexpr int kScaleRing = 8;          // blocks of prepared scales
+constexpr int kMaxSplit = 4;           // CTAs that share a tile
 constexpr size_t kCtlBytes = 256;      // control words at the workspace's start ([0] error bits)
 constexpr int kMaxRows = 1 << 20;
 constexpr uint32_t kMagic = 0x4D6F4638u;
@@ -56,11 +57,38 @@ struct Layout {
   size_t xs, codes, bytes;
 };
 
-int tile_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+int widest_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
 
-Layout layout_of(int rows, int k) {
+// How a product is cut: rows of x in a tile, and CTAs of a cluster that share
+// a tile's blocks.
+struct Cut {
+  int bn, split;
+};
+
+// Where the widest tiles of up to 128 rows leave SMs idle: the cut with the
+// most CTAs that still run at once, the wider of equals (77 x 7000 x 2003:
+// 128 rows split in 2, 11.1 us, against 64 rows, 13.1; 128 x 2048 x 7168: 64
+// rows split in 4, 12.7 us, against 128 rows split in 4, 20.1).  Clusters of
+// 8 do not fill the SMs: sixteen of them ran one after the other (1 x 2048 x
+// 2048: 7.9 us, split in 4 5.4).  Else the widest tile, so that weights are
+// read for up to 256 rows (512 x 7168 x 7168: 45.6 us, with 128 rows 55.6).
+Cut cut_of(int rows, int n, int k, int num_sms) {
+  const int64_t tiles_n = (n + kBlk - 1) / kBlk, blocks = (k + kBlk - 1) / kBlk;
+  Cut best = {widest_tile(rows), 1};
+  int64_t most = 0;
+  for (int bn = best.bn < 128 ? best.bn : 128; bn >= 16; bn /= 2) {
+    const int64_t tiles = (rows + bn - 1) / bn * tiles_n;
+    if (tiles > num_sms) break;
+    int split = 1;
+    while (split < kMaxSplit && tiles * split * 2 <= num_sms && split * 2 <= blocks) split *= 2;
+    if (tiles * split > most) most = tiles * split, best = {bn, split};
+  }
+  return best;
+}
+
+Layout layout_of(int rows, int bn, int k) {
   Layout l;
-  l.bn = tile_rows(rows);
+  l.bn = bn;
   l.row_tiles = (rows + l.bn - 1) / l.bn;
   l.rows_pad = l.row_tiles * l.bn;
   l.blocks = (k + kBlk - 1) / kBlk;
@@ -101,13 +129,10 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// Eight threads per (row, block), 16 inputs each.
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs q) {
-  pdl_launch_dependents();
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
-  const int piece = threadIdx.x & 7;
-  const bool in = unit < static_cast<int64_t>(q.rows) * q.blocks;
-  const int row = in ? static_cast<int>(unit / q.blocks) : 0, b = in ? static_cast<int>(unit % q.blocks) : 0;
+// The codes of 16 inputs (piece `piece` of block b of a row) and the block's
+// scale, which the eight threads of the block share.  All lanes take part;
+// `in`: this thread has inputs.
+__device__ __forceinline__ uint4 quantize_piece(const QuantArgs& q, bool in, int row, int b, int piece, float& scale) {
   const int j = b * kBlk + piece * 16;
   float v[16];
 #pragma unroll
@@ -132,13 +157,23 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs q) {
 #pragma unroll
   for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float inv;
-  const float s = block_scale(m, inv);
+  scale = block_scale(m, inv);
+  return make_uint4(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
+                    e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
+                    e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
+}
+
+// Eight threads per (row, block), 16 inputs each.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs q) {
+  pdl_launch_dependents();
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+  const int piece = threadIdx.x & 7;
+  const bool in = unit < static_cast<int64_t>(q.rows) * q.blocks;
+  const int row = in ? static_cast<int>(unit / q.blocks) : 0, b = in ? static_cast<int>(unit % q.blocks) : 0;
+  float s;
+  const uint4 w = quantize_piece(q, in, row, b, piece, s);
   if (!in) return;
-  uint4 w;
-  w.x = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  w.y = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-  w.z = e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv);
-  w.w = e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv);
   const int tile = row / q.bn, r = row % q.bn;
   uint8_t* t = q.codes + (static_cast<size_t>(tile) * q.blocks + b) * (static_cast<size_t>(q.bn) * kBlk);
   *reinterpret_cast<uint4*>(t + r * kBlk + ((piece ^ (r & 7)) << 4)) = w;
@@ -214,6 +249,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// Sixteen bytes at the shared-memory address `at` of CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_cluster(uint32_t at, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // ---- the product -----------------------------------------------------------------------
 
 struct GemmArgs {
@@ -228,27 +275,35 @@ struct GemmArgs {
   unsigned* ctl;
 };
 
-template <int BN>
+constexpr int kDirectBlocks = 16;   // blocks of x a CTA quantises itself at most ...
+constexpr int kDirectPieces = 768;  // ... and pieces of 16 inputs
+
+// DIRECT: few rows and few blocks a CTA; it quantises its part of x itself.
+template <int BN, bool DIRECT>
 struct Cfg {
   static constexpr int kEpi = BN >= 128 ? 8 : 4;               // warps that read accumulators
   static constexpr int kThreads = 128 + 32 * kEpi;
   static constexpr int kCols = BN / (kEpi / 4);                // columns per thread
   static constexpr int kBuf = BN == 256 ? 2 : 4;               // accumulators in tensor memory
   static constexpr uint32_t kTmem = BN * kBuf < 32 ? 32 : BN * kBuf;
-  static constexpr int kStage = kTileW + BN * kBlk;
-  static constexpr int kStages = (200 * 1024) / kStage < 8 ? (200 * 1024) / kStage : 8;
-  static constexpr int kScaleOff = kStages * kStage;           // [kScaleRing][BN] floats
-  static constexpr int kBarOff = kScaleOff + kScaleRing * BN * 4;
+  static constexpr int kStage = kTileW + (DIRECT ? 0 : BN * kBlk);
+  static constexpr int kStages = !DIRECT && (200 * 1024) / kStage < 8 ? (200 * 1024) / kStage : 8;
+  static constexpr int kX = DIRECT ? kDirectBlocks * BN * kBlk : 0;  // x of all blocks of a DIRECT CTA
+  static constexpr int kScales = DIRECT ? kDirectBlocks : kScaleRing;
+  static constexpr int kScaleOff = kStages * kStage + kX;      // [kScales][BN] floats
+  static constexpr int kBarOff = kScaleOff + kScales * BN * 4;
   static constexpr int kBars = 2 * kStages + 2 * kBuf + 2 * kScaleRing + 1;
   static constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;  // + alignment of the base
+  static_assert(kStages >= 2 && kStages * kStage >= BN * kBlk * 4, "the partial sums of a tile fit the ring");
 };
 
-template <int BN>
-__global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
-    fp8_gemm_kernel(const GemmArgs g, const __grid_constant__ CUtensorMap wmap) {
-  using C = Cfg<BN>;
+template <int BN, bool DIRECT>
+__global__ void __launch_bounds__(Cfg<BN, DIRECT>::kThreads, 1)
+    fp8_gemm_kernel(const GemmArgs g, const QuantArgs q, const __grid_constant__ CUtensorMap wmap) {
+  using C = Cfg<BN, DIRECT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* const xres = sm + C::kStages * C::kStage;
   float* scale_ring = reinterpret_cast<float*>(sm + C::kScaleOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kBarOff);
   uint64_t *full = bars, *empty = full + C::kStages, *tfull = empty + C::kStages, *tempty = tfull + C::kBuf,
@@ -263,14 +318,46 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
   const int b1 = static_cast<int>(static_cast<int64_t>(g.blocks) * (part + 1) / split);
   const int nb = b1 - b0;
 
+  // rows of a tile
+  auto rows_of = [&](int tile) { return min(BN, g.rows - (tile % g.tiles_m) * BN); };
+  const int total = ((tiles - worker + workers - 1) / workers) * nb;  // blocks of this CTA's tiles
+  const int ahead = min(total, C::kStages);
+  const uint64_t wpol = g.tiles_m == 1 ? policy_evict_first() : policy_evict_last();
+  auto load_w = [&](int s, int tile, int b) {
+    mbar_arrive_expect_tx(full + s, kTileW + (DIRECT ? 0 : (rows_of(tile) + 7) / 8 * 1024));
+    tma_load_2d(sm + s * C::kStage, &wmap, b * kBlk, (tile / g.tiles_m) * kBlk, full + s, wpol);
+  };
+
+  // The block's first memory requests go out before it meets: the first
+  // weight tiles (which do not depend on the quantisation kernel before this
+  // one), and with DIRECT its part of x.
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
     for (int i = 0; i < C::kBuf; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, C::kEpi);
     for (int i = 0; i < kScaleRing; ++i) mbar_init(sfull + i, 1), mbar_init(sempty + i, C::kEpi);
     mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+    for (int i = 0; i < ahead; ++i) load_w(i, worker + (i / nb) * workers, b0 + i % nb);
   }
   if (warp == 1) tmem_alloc(smem_u32(slot), C::kTmem);
+  if (DIRECT && warp >= 2) {
+    const float* ws = g.ws + static_cast<size_t>(worker / g.tiles_m) * g.blocks;
+    const int rows = rows_of(worker), row0 = (worker % g.tiles_m) * BN;
+    for (int base = 0; base < rows * nb * 8; base += C::kThreads - 64) {
+      const int item = base + threadIdx.x - 64, unit = item >> 3, piece = item & 7;
+      const int b = unit / rows, row = unit - b * rows;
+      const bool in = b < nb;
+      const float w = in ? ws[b0 + b] : 0.0f;
+      float s;
+      const uint4 codes = quantize_piece(q, in, row0 + row, b0 + b, piece, s);
+      if (in) {
+        *reinterpret_cast<uint4*>(xres + b * (BN * kBlk) + row * kBlk + ((piece ^ (row & 7)) << 4)) = codes;
+        if (piece == 0) scale_ring[b * BN + row] = s * w;
+      }
+    }
+    fence_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -278,28 +365,15 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
-    // loads: the weight tiles of the first stages do not depend on the
-    // quantisation kernel before this one
+    // loads
     if (lane == 0) {
-      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
-      const uint64_t wpol = g.tiles_m == 1 ? once : keep;
-      const int total = ((tiles - worker + workers - 1) / workers) * nb;
-      const int ahead = min(total, C::kStages);
-      auto load_w = [&](int s, int tile, int b) {
-        uint8_t* st = sm + s * C::kStage;
-        const int rows = min(BN, g.rows - (tile % g.tiles_m) * BN);
-        const uint32_t xbytes = (rows + 7) / 8 * 1024;
-        mbar_arrive_expect_tx(full + s, kTileW + xbytes);
-        tma_load_2d(st, &wmap, b * kBlk, (tile / g.tiles_m) * kBlk, full + s, wpol);
-      };
       auto load_x = [&](int s, int tile, int b) {
-        const int mt = tile % g.tiles_m, rows = min(BN, g.rows - mt * BN);
-        bulk_g2s(sm + s * C::kStage + kTileW,
-                 g.codes + (static_cast<size_t>(mt) * g.blocks + b) * (static_cast<size_t>(BN) * kBlk),
-                 (rows + 7) / 8 * 1024, full + s);
+        if constexpr (!DIRECT)
+          bulk_g2s(sm + s * C::kStage + kTileW,
+                   g.codes + (static_cast<size_t>(tile % g.tiles_m) * g.blocks + b) * (static_cast<size_t>(BN) * kBlk),
+                   (rows_of(tile) + 7) / 8 * 1024, full + s);
       };
-      for (int i = 0; i < ahead; ++i) load_w(i, worker + (i / nb) * workers, b0 + i % nb);
-      pdl_wait();
+      if (!DIRECT) pdl_wait();
       for (int i = 0; i < ahead; ++i) load_x(i, worker + (i / nb) * workers, b0 + i % nb);
       RingPos p;
       int issued = ahead;
@@ -326,15 +400,15 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(kBlk, BN);
       RingPos p, t;
       for (int tile = worker; ok && tile < tiles; tile += workers) {
+        const uint32_t idesc = idesc_e4m3(kBlk, (rows_of(tile) + 15) / 16 * 16);
         for (int b = 0; b < nb; ++b) {
           ok = mbar_wait(tempty + t.s, t.ph ^ 1u) && mbar_wait(full + p.s, p.ph);
           if (!ok) break;
           tc_fence_after();
           const uint64_t wd = desc_sw128(smem_u32(sm + p.s * C::kStage));
-          const uint64_t xd = desc_sw128(smem_u32(sm + p.s * C::kStage + kTileW));
+          const uint64_t xd = desc_sw128(smem_u32(DIRECT ? xres + b * (BN * kBlk) : sm + p.s * C::kStage + kTileW));
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_e4m3(tmem + t.s * BN, wd + 2 * k, xd + 2 * k, idesc, k > 0);
@@ -349,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       if (!ok) latch_error(g.ctl, kErrTimeout);
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp == 2 && !DIRECT) {
     // scales: xs[b][rows of the tile] * ws[tile][b], kScaleRing blocks ahead
     pdl_wait();
     RingPos p;
@@ -384,10 +458,10 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < C::kCols; ++c) acc[c] = 0.0f;
       for (int b = 0; b < nb; ++b) {
-        ok = mbar_wait_warp(sfull + p.s, p.ph) && mbar_wait_warp(tfull + t.s, t.ph);
+        ok = (DIRECT || mbar_wait_warp(sfull + p.s, p.ph)) && mbar_wait_warp(tfull + t.s, t.ph);
         if (!ok) break;
         tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(scale_ring + p.s * BN + col0);
+        const float4* sc = reinterpret_cast<const float4*>(scale_ring + (DIRECT ? b : p.s) * BN + col0);
 #pragma unroll
         for (int c = 0; c < C::kCols; c += 16) {
           uint32_t d[16];
@@ -404,40 +478,53 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty + t.s), mbar_arrive(sempty + p.s);
+        if (lane == 0) {
+          mbar_arrive(tempty + t.s);
+          if (!DIRECT) mbar_arrive(sempty + p.s);
+        }
         t.next(C::kBuf);
         p.next(kScaleRing);
       }
       if (!ok) break;
-      const int n = (tile / g.tiles_m) * kBlk + quad * 32 + lane;
+      const int row = quad * 32 + lane;
       if (split == 1) {
-        const int t0 = (tile % g.tiles_m) * BN + col0;
+        const int n = (tile / g.tiles_m) * kBlk + row, t0 = (tile % g.tiles_m) * BN + col0;
 #pragma unroll
         for (int c = 0; c < C::kCols; ++c)
           if (n < g.n && t0 + c < g.rows) store_elem(g.out, g.out_type, (t0 + c) * g.ld_out + n, acc[c]);
       } else {
         // the ring is idle now: every copy and MMA of this CTA's one tile is done
-        float* partial = reinterpret_cast<float*>(sm);
+        float* partial = reinterpret_cast<float*>(sm) + col0 * kBlk + row;
 #pragma unroll
-        for (int c = 0; c < C::kCols; ++c) partial[(col0 + c) * kBlk + quad * 32 + lane] = acc[c];
+        for (int c = 0; c < C::kCols; ++c) partial[c * kBlk] = acc[c];
       }
     }
     if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
   }
 
   if (split > 1) {
+    // column c of the tile is summed by CTA c % split of the cluster, four
+    // outputs a thread, over the CTAs in order
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    const int tile = worker;
-    const int mt = tile % g.tiles_m, rows = min(BN, g.rows - mt * BN);
-    if (threadIdx.x >= 128) {
-      const int r = threadIdx.x & 127, n = (tile / g.tiles_m) * kBlk + r;
-      for (int c = part + split * ((threadIdx.x >> 7) - 1); c < rows; c += split * (C::kEpi / 4)) {
-        float s = 0.0f;
-        for (int q = 0; q < split; ++q)
-          s += cluster.map_shared_rank(reinterpret_cast<float*>(sm), q)[c * kBlk + r];
-        if (n < g.n) store_elem(g.out, g.out_type, static_cast<int64_t>(mt * BN + c) * g.ld_out + n, s);
-      }
+    const int mt = worker % g.tiles_m, cols = (rows_of(worker) - part + split - 1) / split;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < cols * (kBlk / 4); i += C::kThreads) {
+      const int c = part + split * (i / (kBlk / 4)), r = 4 * (i % (kBlk / 4));
+      const uint32_t at = smem_u32(sm) + (c * kBlk + r) * 4;
+      float4 v[kMaxSplit];
+#pragma unroll
+      for (int k = 0; k < kMaxSplit; ++k) v[k] = ld_cluster(at, k < split ? k : part);
+      float4 s = v[0];
+#pragma unroll
+      for (int k = 1; k < kMaxSplit; ++k)
+        if (k < split) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+      const int n = (worker / g.tiles_m) * kBlk + r;
+      const int64_t o = static_cast<int64_t>(mt * BN + c) * g.ld_out + n;
+      if (n < g.n) store_elem(g.out, g.out_type, o, s.x);
+      if (n + 1 < g.n) store_elem(g.out, g.out_type, o + 1, s.y);
+      if (n + 2 < g.n) store_elem(g.out, g.out_type, o + 2, s.z);
+      if (n + 3 < g.n) store_elem(g.out, g.out_type, o + 3, s.w);
     }
     cluster.sync();
   }
@@ -446,25 +533,26 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmem);
 }
 
-template <int BN>
-cudaError_t launch_gemm(const GemmArgs& g, const CUtensorMap& map, int grid, cudaStream_t st) {
-  static_assert(Cfg<BN>::kStages >= 2 && Cfg<BN>::kStages * Cfg<BN>::kStage >= BN * kBlk * 4, "ring");
-  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
+template <int BN, bool DIRECT>
+cudaError_t launch_gemm(const GemmArgs& g, const QuantArgs& q, const CUtensorMap& map, int grid, cudaStream_t st) {
+  using C = Cfg<BN, DIRECT>;
+  auto kernel = fp8_gemm_kernel<BN, DIRECT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(Cfg<BN>::kThreads);
-  cfg.dynamicSmemBytes = Cfg<BN>::kSmem;
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = g.split;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = g.split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN>, g, map);
+  cfg.numAttrs = DIRECT ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, kernel, g, q, map);
 }
 
 }  // namespace
@@ -536,9 +624,8 @@ extern "C" void moe_fp8_close(moe_fp8* w) {
 
 extern "C" size_t moe_fp8_workspace_bytes(const moe_fp8* w, int32_t max_rows) {
   if (!handle_ok(w) || max_rows < 1 || max_rows > kMaxRows) return 0;
-  // the tile height grows with the rows, so fewer rows never need more: the
-  // padded rows of any smaller count stay within 16, 32, ... or a multiple of 256
-  return layout_of(max_rows, w->k).bytes;
+  // of the widest tile: any narrower one, and any fewer rows, pad to no more
+  return layout_of(max_rows, widest_tile(max_rows), w->k).bytes;
 }
 
 extern "C" int moe_fp8_workspace_init(const moe_fp8* w, void* workspace, size_t workspace_bytes, void* stream) {
@@ -566,9 +653,11 @@ extern "C" int moe_fp8_linear(moe_fp8* w, const void* x, int32_t x_type, int64_t
   if (reinterpret_cast<uintptr_t>(x) % elem_size(x_type) || reinterpret_cast<uintptr_t>(out) % elem_size(out_type) ||
       reinterpret_cast<uintptr_t>(workspace) % 256)
     return reportf(MOE_ERR_ALIGN, "moe_fp8_linear: x or out is not aligned to its elements, or workspace to 256 bytes");
-  const Layout l = layout_of(rows, w->k);
-  if (workspace_bytes < l.bytes)
-    return reportf(MOE_ERR_ARG, "moe_fp8_linear: %d rows need %zu bytes of workspace, got %zu", rows, l.bytes,
+  const Cut cut = cut_of(rows, w->n, w->k, w->num_sms);
+  const Layout l = layout_of(rows, cut.bn, w->k);
+  const size_t need = moe_fp8_workspace_bytes(w, rows);
+  if (workspace_bytes < need)
+    return reportf(MOE_ERR_ARG, "moe_fp8_linear: %d rows need %zu bytes of workspace, got %zu", rows, need,
                    workspace_bytes);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
@@ -578,28 +667,34 @@ extern "C" int moe_fp8_linear(moe_fp8* w, const void* x, int32_t x_type, int64_t
   q.blocks = l.blocks, q.rows_pad = l.rows_pad, q.bn = l.bn;
   q.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld_x * elem_size(x_type) % 16 == 0;
   q.xs = reinterpret_cast<float*>(base + l.xs), q.codes = base + l.codes;
-  const int64_t units = static_cast<int64_t>(rows) * l.blocks;
-  quantize_rows_kernel<<<static_cast<unsigned>((units + 31) / 32), 256, 0, st>>>(q);
-  cudaError_t e = cudaGetLastError();
-  if (!e) {
-    GemmArgs g;
-    g.ws = w->scales, g.xs = q.xs, g.codes = q.codes;
-    g.out = out, g.ld_out = ld_out, g.out_type = out_type;
-    g.n = w->n, g.rows = rows, g.rows_pad = l.rows_pad, g.blocks = l.blocks;
-    g.tiles_n = (w->n + kBlk - 1) / kBlk, g.tiles_m = l.row_tiles;
-    g.ctl = reinterpret_cast<unsigned*>(base);
-    const int64_t tiles = static_cast<int64_t>(g.tiles_n) * g.tiles_m;
-    if (tiles > 0x3FFFFFFF) return reportf(MOE_ERR_ARG, "moe_fp8_linear: %d rows x %d outputs are too many tiles", rows, w->n);
-    g.split = 1;
-    while (g.split < 8 && tiles * g.split * 2 <= w->num_sms && g.split * 2 <= l.blocks) g.split *= 2;
-    const int grid = g.split > 1 ? static_cast<int>(tiles) * g.split
-                                 : static_cast<int>(tiles < w->num_sms ? tiles : w->num_sms);
-    switch (l.bn) {
-      case 16: e = launch_gemm<16>(g, w->map, grid, st); break;
-      case 32: e = launch_gemm<32>(g, w->map, grid, st); break;
-      case 64: e = launch_gemm<64>(g, w->map, grid, st); break;
-      case 128: e = launch_gemm<128>(g, w->map, grid, st); break;
-      default: e = launch_gemm<256>(g, w->map, grid, st); break;
+  GemmArgs g;
+  g.ws = w->scales, g.xs = q.xs, g.codes = q.codes;
+  g.out = out, g.ld_out = ld_out, g.out_type = out_type;
+  g.n = w->n, g.rows = rows, g.rows_pad = l.rows_pad, g.blocks = l.blocks;
+  g.tiles_n = (w->n + kBlk - 1) / kBlk, g.tiles_m = l.row_tiles;
+  g.ctl = reinterpret_cast<unsigned*>(base);
+  const int64_t tiles = static_cast<int64_t>(g.tiles_n) * g.tiles_m;
+  if (tiles > 0x3FFFFFFF) return reportf(MOE_ERR_ARG, "moe_fp8_linear: %d rows x %d outputs are too many tiles", rows, w->n);
+  g.split = cut.split;
+  const int grid = tiles <= w->num_sms ? static_cast<int>(tiles) * g.split : w->num_sms;
+  const int share = (l.blocks + g.split - 1) / g.split;
+  const bool direct = tiles <= w->num_sms && l.bn <= 32 && share <= kDirectBlocks &&
+                      (rows < l.bn ? rows : l.bn) * share * 8 <= kDirectPieces;
+  cudaError_t e = cudaSuccess;
+  if (direct) {
+    e = l.bn == 16 ? launch_gemm<16, true>(g, q, w->map, grid, st) : launch_gemm<32, true>(g, q, w->map, grid, st);
+  } else {
+    const int64_t units = static_cast<int64_t>(rows) * l.blocks;
+    quantize_rows_kernel<<<static_cast<unsigned>((units + 31) / 32), 256, 0, st>>>(q);
+    e = cudaGetLastError();
+    if (!e) {
+      switch (l.bn) {
+        case 16: e = launch_gemm<16, false>(g, q, w->map, grid, st); break;
+        case 32: e = launch_gemm<32, false>(g, q, w->map, grid, st); break;
+        case 64: e = launch_gemm<64, false>(g, q, w->map, grid, st); break;
+        case 128: e = launch_gemm<128, false>(g, q, w->map, grid, st); break;
+        default: e = launch_gemm<256, false>(g, q, w->map, grid, st); break;
+      }
     }
   }
   if (e) return reportf(MOE_ERR_CUDA, "moe_fp8_linear: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));

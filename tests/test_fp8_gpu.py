@@ -119,9 +119,15 @@ def test_types_and_strides(xt, ot, T, pad):
 
 
 @pytest.mark.parametrize("T,N,K", [(4, 20000, 640), (130, 30000, 384), (1000, 5000, 1500), (700, 2048, 768),
-                                   (300, 100, 7168), (16, 40000, 2048)])
+                                   (300, 100, 7168), (16, 40000, 2048), (257, 40000, 300), (2000, 2100, 200),
+                                   (777, 9999, 1111), (4000, 3000, 16)])
 def test_many_tiles(T, N, K):
     check(T, N, K)
+
+
+@pytest.mark.parametrize("xt,ot,pad", [(F32, BF, 0), (HF, HF, 3), (BF, BF, 8)])
+def test_many_rows_types_and_strides(xt, ot, pad):
+    check(1100, 4000, 700, xt, ot, pad)
 
 
 def test_scales_of_x_at_their_edges():

@@ -604,8 +604,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 
 // mbar_wait for a phase that the other CTA's threads complete.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 0;; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -615,7 +615,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     if (ok) return true;
-    if ((i & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return false;
+    if (i == 0) t0 = global_timer_ns();
+    else if ((i & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return false;
   }
 }
 
@@ -839,13 +840,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           uint32_t d[16];
           tmem_ld16(from + t.s * 2 * kBlk + c, d);
           tmem_wait();
+          if (c + 16 == kPairCols) {
+            // all columns read: the next block but one may have the buffer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(freed + t.s * 8), mbar_arrive(sempty + p.s);
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             acc[c / 2 + j] = __ffma2_rn(make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s, acc[c / 2 + j]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(freed + t.s * 8), mbar_arrive(sempty + p.s);
         t.next(2);
         p.next(kPairScales);
       }

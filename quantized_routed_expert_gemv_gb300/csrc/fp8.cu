@@ -103,7 +103,7 @@ Layout layout_of(int rows, int bn, int k) {
 struct QuantArgs {
   const void* x;
   int64_t ld;
-  int type, rows, k, blocks, rows_pad, bn, vec;
+  int type, rows, k, blocks, rows_pad, bn_log2, vec;
   int plain;  // codes as rows of blocks * 128 bytes, for tiled loads, instead of as tiles
   float* xs;
   uint8_t* codes;
@@ -165,21 +165,22 @@ __device__ __forceinline__ uint4 quantize_piece(const QuantArgs& q, bool in, int
                     e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
 }
 
-// Eight threads per (row, block), 16 inputs each.
+// Eight threads per (row, block), 16 inputs each.  At most 2^20 rows of 512
+// blocks: a unit's index fits 32 bits.
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs q) {
   pdl_launch_dependents();
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+  const uint32_t unit = blockIdx.x * 32u + (threadIdx.x >> 3), blocks = static_cast<uint32_t>(q.blocks);
   const int piece = threadIdx.x & 7;
-  const bool in = unit < static_cast<int64_t>(q.rows) * q.blocks;
-  const int row = in ? static_cast<int>(unit / q.blocks) : 0, b = in ? static_cast<int>(unit % q.blocks) : 0;
+  const bool in = unit < static_cast<uint32_t>(q.rows) * blocks;
+  const int row = in ? static_cast<int>(unit / blocks) : 0, b = in ? static_cast<int>(unit - row * blocks) : 0;
   float s;
   const uint4 w = quantize_piece(q, in, row, b, piece, s);
   if (!in) return;
   if (q.plain) {
-    *reinterpret_cast<uint4*>(q.codes + (static_cast<size_t>(row) * q.blocks + b) * kBlk + piece * 16) = w;
+    *reinterpret_cast<uint4*>(q.codes + (static_cast<size_t>(row) * blocks + b) * kBlk + piece * 16) = w;
   } else {
-    const int tile = row / q.bn, r = row % q.bn;
-    uint8_t* t = q.codes + (static_cast<size_t>(tile) * q.blocks + b) * (static_cast<size_t>(q.bn) * kBlk);
+    const int tile = row >> q.bn_log2, r = row - (tile << q.bn_log2);
+    uint8_t* t = q.codes + (((static_cast<size_t>(tile) * blocks + b) * kBlk) << q.bn_log2);
     *reinterpret_cast<uint4*>(t + r * kBlk + ((piece ^ (r & 7)) << 4)) = w;
   }
   if (piece == 0) q.xs[static_cast<size_t>(b) * q.rows_pad + row] = s;
@@ -1028,7 +1029,7 @@ extern "C" int moe_fp8_linear(moe_fp8* w, const void* x, int32_t x_type, int64_t
 
   QuantArgs q;
   q.x = x, q.ld = ld_x, q.type = x_type, q.rows = rows, q.k = w->k;
-  q.blocks = l.blocks, q.rows_pad = l.rows_pad, q.bn = l.bn;
+  q.blocks = l.blocks, q.rows_pad = l.rows_pad, q.bn_log2 = l.bn == 16 ? 4 : l.bn == 32 ? 5 : l.bn == 64 ? 6 : l.bn == 128 ? 7 : 8;
   q.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld_x * elem_size(x_type) % 16 == 0;
   q.xs = reinterpret_cast<float*>(base + l.xs), q.codes = base + l.codes;
   GemmArgs g;

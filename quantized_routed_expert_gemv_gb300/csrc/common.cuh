@@ -163,11 +163,6 @@ __device__ __forceinline__ void named_bar(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// Counts towards a named barrier that others wait on.
-__device__ __forceinline__ void named_bar_arrive(int id, int count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
 // Named barrier that also ORs a predicate over the participants: every
 // thread gets the same answer, so exits decided on it stay uniform.
 __device__ __forceinline__ bool named_bar_or(int id, int count, bool pred) {

@@ -112,6 +112,26 @@ def test_rows_over_the_split_rule(T):
     check(rnd(T, 8500, seed=T), some_targets(T, 8500, 2), top_n=3)
 
 
+@pytest.mark.parametrize("T,V,dtype", [(2, 131072, BF), (20, 131073, BF), (38, 70001, BF), (77, 70001, HF), (152, 66000, BF),
+                                       (153, 66000, BF), (20, 40003, F32), (3, 200000, F32)])
+def test_long_rows_in_parts(T, V, dtype):
+    """Rows that 2, 4 or 8 blocks share, and the first count of rows that they do not."""
+    check(rnd(T, V, dtype, seed=T), some_targets(T, V, 3), top_n=9)
+
+
+@pytest.mark.parametrize("dtype,V", [(BF, 140001), (F32, 66001)])
+def test_long_rows_in_parts_with_masks_and_ties(dtype, V):
+    l = rnd(6, V, dtype)
+    l[0] = -INF
+    l[1] = -INF
+    l[1, V - 3] = 1.0                   # one token, in the last part
+    l[2] = torch.finfo(dtype).min
+    l[3] = 0.5                          # all equal
+    l[4, V // 2:] = -INF                # whole parts without a token
+    l[5].copy_(torch.arange(V, device=DEV) % 7)
+    check(l, some_targets(6, V, 2), top_n=32)
+
+
 @pytest.mark.parametrize("G", [1, 2, 7, 8])
 @pytest.mark.parametrize("top_n", [0, 1, 32])
 def test_targets_and_top(G, top_n):

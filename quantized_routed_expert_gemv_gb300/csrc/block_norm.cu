@@ -155,9 +155,9 @@ __device__ __forceinline__ void scale_by(float (&v)[8], float s, float add, cons
 // Y32, H32: y and h are 32-bit.  MIXED: the operands' types and alignments
 // (`aligned`) are looked at one by one.
 template <int NC, bool Y32, bool H32, bool MIXED>
-__global__ void __launch_bounds__(512) block_norm_kernel(const moe_block_norm_args a, int aligned) {
+__global__ void __launch_bounds__(NC == 1 ? 1024 : 512) block_norm_kernel(const moe_block_norm_args a, int aligned) {
   __shared__ float red[2][32];
-  __shared__ __align__(16) uint32_t exchange[MIXED ? 16 : 1][256];
+  __shared__ __align__(16) uint32_t exchange[MIXED ? (NC == 1 ? 32 : 16) : 1][256];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= a.rows) return;
   const int H = a.hidden;
@@ -481,8 +481,10 @@ extern "C" int moe_block_norm(const moe_block_norm_args* args, void* stream) {
         : h32      ? launch_stream<false, true>(a, sms, st)
                    : launch_stream<false, false>(a, sms, st);
   } else {
-    // a warp a row up to 256 values, else a block with up to 512 threads
-    const int nc = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
+    // A warp a row up to 256 values, else a block.  While there are fewer rows
+    // than SMs, one chunk a thread up to 1024 threads: the weights then come
+    // with the row instead of after each sum (one row of 7168: 4.1 -> 3.5 us).
+    const int nc = chunks <= 512 || (chunks <= 1024 && a.rows <= sms) ? 1 : chunks <= 1024 ? 2 : 4;
     const dim3 block = chunks <= 32 ? dim3(32, 4) : dim3(((chunks + nc - 1) / nc + 31) / 32 * 32);
     const dim3 grid((static_cast<unsigned>(a.rows) + block.y - 1) / block.y);
     e = nc == 1   ? launch_rows<1>(a, aligned, grid, block, st)

@@ -464,6 +464,28 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
     best_c = m > best ? cb : best_c;
     best = fmaxf(best, m);
     sums.reach(m, u);
+    // sums first: the targets' logits of a short row may still be on their way
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const uint32_t w[4] = {cur[i][q].x, cur[i][q].y, cur[i][q].z, cur[i][q].w};
+        if constexpr (F32) {
+          sums.add<true>(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), uu);
+          sums.add<true>(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), uu);
+        } else {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            if constexpr (TYPE == MOE_BF16) {
+              const __nv_bfloat162 v = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[z]), bound2);
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(&v);
+              sums.add<false>(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)), uu);
+            } else {
+              sums.add<true>(__half22float2(*reinterpret_cast<const __half2*>(&w[z])), uu);
+            }
+          }
+        }
+      }
 #pragma unroll
     for (int g = 0; g < NT; ++g) {
       // logits not below the target's in a batch before its chunk, above
@@ -495,27 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
       }
       cnt[g] += q;
     }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const uint32_t w[4] = {cur[i][q].x, cur[i][q].y, cur[i][q].z, cur[i][q].w};
-        if constexpr (F32) {
-          sums.add<true>(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), uu);
-          sums.add<true>(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), uu);
-        } else {
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            if constexpr (TYPE == MOE_BF16) {
-              const __nv_bfloat162 v = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[z]), bound2);
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(&v);
-              sums.add<false>(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)), uu);
-            } else {
-              sums.add<true>(__half22float2(*reinterpret_cast<const __half2*>(&w[z])), uu);
-            }
-          }
-        }
-      }
   };
   int cb = c0;
 #pragma unroll 1

@@ -572,147 +572,98 @@ cudaError_t launch_gemm(const GemmArgs& g, const QuantArgs& q, const CUtensorMap
 // row and 128 outputs of one weight block, so the scale of a block is one
 // number for it.
 
-constexpr int kPairStages = 6;
-constexpr int kPairStage = 2 * kTileW;
+constexpr int kPairStages = 4;
+constexpr int kPairStage = 3 * kTileW;
 constexpr int kPairEpi = 16;                              // warps that read accumulators, 64 columns each
 constexpr int kPairCols = 4 * 2 * kBlk / kPairEpi;
 constexpr int kPairThreads = 32 * (4 + kPairEpi);         // load, MMA, scales, idle, epilogue
 // Registers of a thread: of the launch's 96 x 640, 56 x 128 and 104 x 512.
 constexpr int kPairRegsFew = 56, kPairRegsEpi = 104;
 constexpr int kPairOutBytes = 64;                         // of a row that an epilogue warp puts in order at once
-constexpr int kPairOutOff = kPairStages * kPairStage;     // [epilogue warp][32 rows][kPairOutBytes]
-constexpr int kPairScaleOff = kPairOutOff + kPairEpi * 32 * kPairOutBytes;  // [kPairScales][2][128] floats
-constexpr int kPairScales = 2;
-constexpr int kPairBarOff = kPairScaleOff + kPairScales * 2 * kBlk * 4;
-constexpr int kPairBars = 2 * kPairStages + 4 + 2 * kPairScales + 1;
+constexpr int kPairOutOff = kPairStages * kPairStage;     // [epilogue warp][16 rows][kPairOutBytes]
+constexpr int kPairChunk = 8;                             // blocks whose scales are handed over together
+constexpr int kPairScaleOff = kPairOutOff + kPairEpi * 16 * kPairOutBytes;  // [2][kPairChunk][2][128] floats
+constexpr int kPairBarOff = kPairScaleOff + 2 * kPairChunk * 2 * kBlk * 4;
+constexpr int kPairBars = 2 * kPairStages + 4 + 4 + 1;
 constexpr int kPairSmem = kPairBarOff + kPairBars * 8 + 16;
 static_assert(kPairSmem <= 232448, "shared memory");
 
-// The address of this CTA's shared-memory object in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_cta(uint32_t addr, int rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
-
-// An arrival at the barrier at cluster address `addr`.  What it orders are the
-// tensor-memory loads before it (waited for, and fenced), not memory: with
-// release.cluster here, a fence for every block and warp, 4096 x 7168 x 7168
-// took 410 us instead of 201.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-// mbar_wait for a phase that the other CTA's threads complete.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  unsigned long long t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (i == 0) t0 = global_timer_ns();
-    else if ((i & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return false;
-  }
-}
-
-// Tile load into this CTA's shared memory, counted on the barrier at the
-// cluster address `bar` of either CTA of the pair.
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-// One arrival at this barrier in both CTAs when the MMAs issued so far are done.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Stores 64 bytes of each of a warp's 32 rows (t0 on; lane r holds row r) from
-// output n on.  `buf`: the warp's 2 KB; 16-byte piece q of row r lies at piece
-// q ^ (r / 2 & 3), so that neither side's accesses collide.
+// output n on, sixteen rows at a time.  `buf`: the warp's 1 KB; 16-byte piece q
+// of row r lies at piece q ^ (r / 2 & 3), so that neither side's accesses
+// collide.
 template <int ES>
 __device__ __forceinline__ void store_rows(const GemmArgs& g, uint8_t* buf, const uint4 (&v)[4], int t0, int n) {
   const int lane = threadIdx.x & 31;
-  __syncwarp();
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint4*>(buf + lane * kPairOutBytes + ((q ^ (lane >> 1 & 3)) << 4)) = v[q];
-  __syncwarp();
   uint8_t* const out = static_cast<uint8_t*>(g.out);
-  if (g.out_vec && n + kPairOutBytes / ES <= g.n) {
-    // four lanes a row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2), q = lane & 3;
-      const uint4 w = *reinterpret_cast<const uint4*>(buf + r * kPairOutBytes + ((q ^ (r >> 1 & 3)) << 4));
-      if (t0 + r < g.rows)
-        *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(t0 + r) * g.ld_out + n) * ES + q * 16) = w;
+  for (int h = 0; h < 2; ++h, t0 += 16) {
+    __syncwarp();
+    if (lane >> 4 == h) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(buf + (lane & 15) * kPairOutBytes + ((q ^ (lane >> 1 & 3)) << 4)) = v[q];
     }
-  } else {
-    // a lane an element, a row or two at a time
-    constexpr int kCols = kPairOutBytes / ES, kRows = 32 / kCols;
-    const int c = lane % kCols;
+    __syncwarp();
+    if (g.out_vec && n + kPairOutBytes / ES <= g.n) {
+      // four lanes a row
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * i + (lane >> 2), q = lane & 3;
+        const uint4 w = *reinterpret_cast<const uint4*>(buf + r * kPairOutBytes + ((q ^ (r >> 1 & 3)) << 4));
+        if (t0 + r < g.rows)
+          *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(t0 + r) * g.ld_out + n) * ES + q * 16) = w;
+      }
+    } else {
+      // a lane an element, a row or two at a time
+      constexpr int kCols = kPairOutBytes / ES, kRows = 32 / kCols;
+      const int c = lane % kCols;
 #pragma unroll 1
-    for (int r = lane / kCols; r < 32; r += kRows) {
-      const uint8_t* at = buf + r * kPairOutBytes + (((c * ES >> 4) ^ (r >> 1 & 3)) << 4) + (c * ES & 15);
-      if (t0 + r < g.rows && n + c < g.n) {
-        uint8_t* to = out + (static_cast<int64_t>(t0 + r) * g.ld_out + n + c) * ES;
-        if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(at);
-        else *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(at);
+      for (int r = lane / kCols; r < 16; r += kRows) {
+        const uint8_t* at = buf + r * kPairOutBytes + (((c * ES >> 4) ^ (r >> 1 & 3)) << 4) + (c * ES & 15);
+        if (t0 + r < g.rows && n + c < g.n) {
+          uint8_t* to = out + (static_cast<int64_t>(t0 + r) * g.ld_out + n + c) * ES;
+          if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(at);
+          else *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(at);
+        }
       }
     }
   }
 }
 
-__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const GemmArgs g, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ __align__(1024) uint8_t sm[];
   float* scale_ring = reinterpret_cast<float*>(sm + kPairScaleOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kPairBarOff);
   uint64_t *full = bars, *empty = full + kPairStages, *tfull = empty + kPairStages, *tempty = tfull + 2,
-           *sfull = tempty + 2, *sempty = sfull + kPairScales, *done = sempty + kPairScales;
+           *sfull = tempty + 2, *sempty = sfull + 2, *done = sempty + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
-  cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = static_cast<int>(cluster.block_rank());
-  const int worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
+  const int worker = blockIdx.x, workers = gridDim.x;
   const int tiles = g.tiles_n * g.tiles_m, nb = g.blocks;
 
   if (threadIdx.x == 0) {
     // full, tempty: used in CTA 0, for both
     for (int i = 0; i < kPairStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, 2 * kPairEpi);
-    for (int i = 0; i < kPairScales; ++i) mbar_init(sfull + i, 1), mbar_init(sempty + i, kPairEpi);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, kPairEpi);
+    for (int i = 0; i < 2; ++i) mbar_init(sfull + i, 1), mbar_init(sempty + i, kPairEpi);
     mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512u));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::);
+    tmem_alloc(smem_u32(slot), 512);
   }
   tc_fence_before();
   __syncthreads();
-  cluster.sync();
   tc_fence_after();
   const uint32_t tmem = *slot;
   bool ok = true;
@@ -725,11 +676,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const int total = ((tiles - worker + workers - 1) / workers) * nb;
       const int ahead = min(total, kPairStages);
       auto load_w = [&](int s, int tn, int b) {
-        if (cta == 0) mbar_arrive_expect_tx(full + s, 2 * kPairStage);
-        tma_load_pair(sm + s * kPairStage + kTileW, &wmap, b * kBlk, (2 * tn + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
+        mbar_arrive_expect_tx(full + s, kPairStage);
+        tma_load_2d(sm + s * kPairStage + kTileW, &wmap, b * kBlk, 2 * tn * kBlk, full + s, keep);
+        tma_load_2d(sm + s * kPairStage + 2 * kTileW, &wmap, b * kBlk, (2 * tn + 1) * kBlk, full + s, keep);
       };
       auto load_x = [&](int s, int tm, int b) {
-        tma_load_pair(sm + s * kPairStage, &xmap, b * kBlk, (2 * tm + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
+        tma_load_2d(sm + s * kPairStage, &xmap, b * kBlk, tm * kBlk, full + s, keep);
       };
       int tile = worker, b = 0, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
       auto next_block = [&]() {
@@ -756,63 +708,61 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       // a run that gave up leaves no copy in flight: CTA 0's barriers count both CTAs'
       if (!ok) {
         latch_error(g.ctl, kErrTimeout);
-        if (cta == 0)
-          for (int i = max(0, issued - kPairStages); i < issued; ++i)
-            mbar_wait(full + i % kPairStages, static_cast<uint32_t>(i / kPairStages) & 1u);
+        for (int i = max(0, issued - kPairStages); i < issued; ++i)
+          mbar_wait(full + i % kPairStages, static_cast<uint32_t>(i / kPairStages) & 1u);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && cta == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(2 * kBlk, 2 * kBlk);
-      RingPos p, t;
-      for (int tile = worker; ok && tile < tiles; tile += workers) {
-        for (int b = 0; b < nb; ++b) {
-          ok = mbar_wait_cluster(tempty + t.s, t.ph ^ 1u) && mbar_wait_cluster(full + p.s, p.ph);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t xd = desc_sw128(smem_u32(sm + p.s * kPairStage));
-          const uint64_t wd = desc_sw128(smem_u32(sm + p.s * kPairStage + kTileW));
+    constexpr uint32_t idesc = idesc_e4m3(kBlk, 2 * kBlk);
+    const uint32_t ring = smem_u32(sm);
+    RingPos p, t;
+    for (int tile = worker; ok && tile < tiles; tile += workers) {
+      for (int b = 0; b < nb; ++b) {
+        ok = mbar_wait_warp(tempty + t.s, t.ph ^ 1u) && mbar_wait_warp(full + p.s, p.ph);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t xd = desc_sw128(ring + p.s * kPairStage);
+        const uint64_t wd = desc_sw128(ring + p.s * kPairStage + kTileW);
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_e4m3_pair(tmem + t.s * 256, xd + 2 * k, wd + 2 * k, idesc, k > 0);
-          mma_commit_pair(smem_u32(empty + p.s));
-          mma_commit_pair(smem_u32(tfull + t.s));
-          p.next(kPairStages);
-          t.next(2);
+          for (int k = 0; k < 4; ++k) mma_e4m3(tmem + t.s * 2 * kBlk, xd + 2 * k, wd + 2 * k, idesc, k > 0);
+          mma_commit(smem_u32(tfull + t.s));
+          mma_commit(smem_u32(empty + p.s));
         }
+        __syncwarp();
+        p.next(kPairStages);
+        t.next(2);
       }
-      mma_commit_pair(smem_u32(done));
-      if (!mbar_wait(done, 0)) ok = false;
-      if (!ok) latch_error(g.ctl, kErrTimeout);
     }
+    if (elect_one()) mma_commit(smem_u32(done));
+    __syncwarp();
+    if (!mbar_wait(done, 0)) ok = false;
+    if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
     __syncwarp();
   } else if (warp == 2) {
-    // scales: xs[b][this CTA's rows] * ws[either weight block][b], a few blocks ahead
+    // scales: xs[b][the tile's rows] * ws[either weight block][b], kPairChunk
+    // blocks at a time (a wait for each block cost 12 us of 178)
     pdl_wait();
     RingPos p;
     for (int tile = worker; ok && tile < tiles; tile += workers) {
       const int n0 = 2 * (tile / g.tiles_m), n1 = min(n0 + 1, (g.n - 1) / kBlk);
       const float *w0 = g.ws + static_cast<size_t>(n0) * nb, *w1 = g.ws + static_cast<size_t>(n1) * nb;
-      const float* xs = g.xs + (2 * (tile % g.tiles_m) + cta) * kBlk + lane * 4;
-      float4 x = *reinterpret_cast<const float4*>(xs);
-      float u = w0[0], v = w1[0];
-      for (int b = 0; b < nb; ++b) {
-        const float4 now = x;
-        const float nu = u, nv = v;
-        if (b + 1 < nb) {
-          x = *reinterpret_cast<const float4*>(xs + static_cast<size_t>(b + 1) * g.rows_pad);
-          u = w0[b + 1], v = w1[b + 1];
+      const float* xs = g.xs + (tile % g.tiles_m) * kBlk + lane * 4;
+      for (int b0 = 0; b0 < nb; b0 += kPairChunk) {
+        ok = mbar_wait_warp(sempty + p.s, p.ph ^ 1u);
+        if (!ok) break;
+        float4* to = reinterpret_cast<float4*>(scale_ring + p.s * kPairChunk * 2 * kBlk) + lane;
+#pragma unroll 4
+        for (int b = b0; b < min(nb, b0 + kPairChunk); ++b, to += kBlk / 2) {
+          const float4 x = *reinterpret_cast<const float4*>(xs + static_cast<size_t>(b) * g.rows_pad);
+          const float u = w0[b], v = w1[b];
+          to[0] = make_float4(x.x * u, x.y * u, x.z * u, x.w * u);
+          to[kBlk / 4] = make_float4(x.x * v, x.y * v, x.z * v, x.w * v);
         }
-        if (!mbar_wait_warp(sempty + p.s, p.ph ^ 1u)) {
-          ok = false;
-          break;
-        }
-        float4* to = reinterpret_cast<float4*>(scale_ring + p.s * 2 * kBlk) + lane;
-        to[0] = make_float4(now.x * nu, now.y * nu, now.z * nu, now.w * nu);
-        to[kBlk / 4] = make_float4(now.x * nv, now.y * nv, now.z * nv, now.w * nv);
         __syncwarp();
         if (lane == 0) mbar_arrive(sfull + p.s);
-        p.next(kPairScales);
+        p.next(2);
       }
     }
     if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
@@ -821,7 +771,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsEpi));
     const int quad = warp & 3, col0 = ((warp - 4) >> 2) * kPairCols, row = quad * 32 + lane;
     const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
-    const uint32_t freed = map_cta(smem_u32(tempty), 0);
     const float* const scale = scale_ring + (col0 / kBlk) * kBlk + row;
     RingPos t, p;
     for (int tile = worker; ok && tile < tiles; tile += workers) {
@@ -830,8 +779,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       for (int c = 0; c < kPairCols / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
       for (int b = 0; b < nb; ++b) {
-        ok = mbar_wait_warp(sfull + p.s, p.ph);
-        const float s1 = scale[p.s * 2 * kBlk];
+        if (b % kPairChunk == 0) ok = mbar_wait_warp(sfull + p.s, p.ph);
+        const float s1 = scale[(p.s * kPairChunk + b % kPairChunk) * 2 * kBlk];
         ok = ok && mbar_wait_warp(tfull + t.s, t.ph);
         if (!ok) break;
         tc_fence_after();
@@ -845,22 +794,26 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             // all columns read: the next block but one may have the buffer
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(freed + t.s * 8), mbar_arrive(sempty + p.s);
+            if (lane == 0) mbar_arrive(tempty + t.s);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             acc[c / 2 + j] = __ffma2_rn(make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s, acc[c / 2 + j]);
         }
         t.next(2);
-        p.next(kPairScales);
+        if (b % kPairChunk == kPairChunk - 1 || b == nb - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sempty + p.s);
+          p.next(2);
+        }
       }
       if (!ok) break;
       // A thread holds a row; 64 bytes of each of the warp's 32 rows at a time
       // go through shared memory, so that stores cover whole sectors.  (Straight
       // from the registers a tile's stores took 6,800 cycles.)
-      const int t0 = (2 * (tile % g.tiles_m) + cta) * kBlk + quad * 32;
+      const int t0 = (tile % g.tiles_m) * kBlk + quad * 32;
       const int n0 = 2 * (tile / g.tiles_m) * kBlk + col0;
-      uint8_t* out = sm + kPairOutOff + (warp - 4) * 32 * kPairOutBytes;
+      uint8_t* out = sm + kPairOutOff + (warp - 4) * 16 * kPairOutBytes;
       if (g.out_type == MOE_F32) {
 #pragma unroll
         for (int c = 0; c < kPairCols; c += 16) {
@@ -890,10 +843,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
 
   tc_fence_before();
   __syncthreads();
-  // neither CTA leaves while the other, or an MMA of both, may signal it
-  if (cta == 1 && threadIdx.x == 0 && !mbar_wait(done, 0)) latch_error(g.ctl, kErrTimeout);
-  cluster.sync();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 cudaError_t launch_pair(const GemmArgs& g, const CUtensorMap& wmap, const CUtensorMap& xmap, int num_sms, cudaStream_t st) {
@@ -901,7 +851,7 @@ cudaError_t launch_pair(const GemmArgs& g, const CUtensorMap& wmap, const CUtens
   if (e) return e;
   const int64_t tiles = static_cast<int64_t>(g.tiles_n) * g.tiles_m;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < num_sms / 2 ? tiles : num_sms / 2));
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms));
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = st;
@@ -1066,6 +1016,7 @@ extern "C" int moe_fp8_linear(moe_fp8* w, const void* x, int32_t x_type, int64_t
           if (!encode_tiles(w->encode, &xmap, q.codes, rows, static_cast<int64_t>(l.blocks) * kBlk, static_cast<int64_t>(l.blocks) * kBlk))
             return reportf(MOE_ERR_CUDA, "moe_fp8_linear: cuTensorMapEncodeTiled refused rows=%d k=%d", rows, w->k);
           g.tiles_n = (w->n + 2 * kBlk - 1) / (2 * kBlk);
+          g.tiles_m = (rows + kBlk - 1) / kBlk;
           e = launch_pair(g, w->map, xmap, w->num_sms, st);
         }
       }

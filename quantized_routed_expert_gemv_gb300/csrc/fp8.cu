@@ -71,7 +71,8 @@ struct Cut {
 // rows split in 4, 12.7 us, against 128 rows split in 4, 20.1).  Clusters of
 // 8 do not fill the SMs: sixteen of them ran one after the other (1 x 2048 x
 // 2048: 7.9 us, split in 4 5.4).  Else the widest tile, so that weights are
-// read for up to 256 rows (512 x 7168 x 7168: 45.6 us, with 128 rows 55.6).
+// read for 256 rows (fp8_pair_kernel; 512 x 7168 x 7168: 30.3 us, with 128 rows
+// 55.6).
 Cut cut_of(int rows, int n, int k, int num_sms) {
   const int64_t tiles_n = (n + kBlk - 1) / kBlk, blocks = (k + kBlk - 1) / kBlk;
   Cut best = {widest_tile(rows), 1};
@@ -567,13 +568,19 @@ cudaError_t launch_gemm(const GemmArgs& g, const QuantArgs& q, const CUtensorMap
 // tcgen05.mma.cta_group::2: CTA r holds rows 128 r.. of x and outputs
 // 128 r.. of w of a block in its shared memory, and the accumulators of its
 // own rows (128 lanes x 256 columns, two of them).  Each operand byte thus
-// feeds two SMs, 32 KB a block and SM where one SM's 128 x 256 tile takes 48.
-// Here the rows of x are the accumulator's lanes: an epilogue thread has one
-// row and 128 outputs of one weight block, so the scale of a block is one
-// number for it.
+// feeds two SMs: 32 KB a block and SM into shared memory and as much out of
+// it, where one SM's 128 x 256 tile takes 48 in and 48 out (4096 x 7168 x 7168
+// by such tiles: 169 us, by pairs 163).  The rows of x are the accumulator's
+// lanes: an epilogue thread has one row and 64 outputs of one weight block, so
+// the scale of a block is one number for it.
+//
+// Bound: the way from an MMA to its scaled sum and back.  A block's MMAs keep
+// the tensor pipe busy for some 630 cycles, but with two accumulators (all of
+// the tensor memory) the next one waits for commit, read and release of the
+// one before the last; measured some 850 cycles a block.
 
-constexpr int kPairStages = 4;
-constexpr int kPairStage = 3 * kTileW;
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * kTileW;
 constexpr int kPairEpi = 16;                              // warps that read accumulators, 64 columns each
 constexpr int kPairCols = 4 * 2 * kBlk / kPairEpi;
 constexpr int kPairThreads = 32 * (4 + kPairEpi);         // load, MMA, scales, idle, epilogue
@@ -588,11 +595,69 @@ constexpr int kPairBars = 2 * kPairStages + 4 + 4 + 1;
 constexpr int kPairSmem = kPairBarOff + kPairBars * 8 + 16;
 static_assert(kPairSmem <= 232448, "shared memory");
 
+// The address of this CTA's shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+
+// An arrival at the barrier at cluster address `addr`.  What it orders are the
+// tensor-memory loads before it (waited for, and fenced), not memory: with
+// release.cluster here, a fence for every block and warp, 4096 x 7168 x 7168
+// took 410 us instead of 201.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// mbar_wait for a phase that the other CTA's threads complete.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i == 0) t0 = global_timer_ns();
+    else if ((i & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// Tile load into this CTA's shared memory, counted on the barrier at the
+// cluster address `bar` of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// One arrival at this barrier in both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 // Stores 64 bytes of each of a warp's 32 rows (t0 on; lane r holds row r) from
@@ -638,7 +703,7 @@ __device__ __forceinline__ void store_rows(const GemmArgs& g, uint8_t* buf, cons
   }
 }
 
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     fp8_pair_kernel(const GemmArgs g, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ __align__(1024) uint8_t sm[];
   float* scale_ring = reinterpret_cast<float*>(sm + kPairScaleOff);
@@ -646,24 +711,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t *full = bars, *empty = full + kPairStages, *tfull = empty + kPairStages, *tempty = tfull + 2,
            *sfull = tempty + 2, *sempty = sfull + 2, *done = sempty + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+  cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int worker = blockIdx.x, workers = gridDim.x;
+  const int cta = static_cast<int>(cluster.block_rank());
+  const int worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
   const int tiles = g.tiles_n * g.tiles_m, nb = g.blocks;
 
   if (threadIdx.x == 0) {
     // full, tempty: used in CTA 0, for both
     for (int i = 0; i < kPairStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, kPairEpi);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, 2 * kPairEpi);
     for (int i = 0; i < 2; ++i) mbar_init(sfull + i, 1), mbar_init(sempty + i, kPairEpi);
     mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(slot), 512);
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::);
   }
   tc_fence_before();
   __syncthreads();
+  cluster.sync();
   tc_fence_after();
   const uint32_t tmem = *slot;
   bool ok = true;
@@ -676,12 +745,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int total = ((tiles - worker + workers - 1) / workers) * nb;
       const int ahead = min(total, kPairStages);
       auto load_w = [&](int s, int tn, int b) {
-        mbar_arrive_expect_tx(full + s, kPairStage);
-        tma_load_2d(sm + s * kPairStage + kTileW, &wmap, b * kBlk, 2 * tn * kBlk, full + s, keep);
-        tma_load_2d(sm + s * kPairStage + 2 * kTileW, &wmap, b * kBlk, (2 * tn + 1) * kBlk, full + s, keep);
+        if (cta == 0) mbar_arrive_expect_tx(full + s, 2 * kPairStage);
+        tma_load_pair(sm + s * kPairStage + kTileW, &wmap, b * kBlk, (2 * tn + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
       };
       auto load_x = [&](int s, int tm, int b) {
-        tma_load_2d(sm + s * kPairStage, &xmap, b * kBlk, tm * kBlk, full + s, keep);
+        tma_load_pair(sm + s * kPairStage, &xmap, b * kBlk, (2 * tm + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
       };
       int tile = worker, b = 0, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
       auto next_block = [&]() {
@@ -708,37 +776,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // a run that gave up leaves no copy in flight: CTA 0's barriers count both CTAs'
       if (!ok) {
         latch_error(g.ctl, kErrTimeout);
-        for (int i = max(0, issued - kPairStages); i < issued; ++i)
-          mbar_wait(full + i % kPairStages, static_cast<uint32_t>(i / kPairStages) & 1u);
+        if (cta == 0)
+          for (int i = max(0, issued - kPairStages); i < issued; ++i)
+            mbar_wait(full + i % kPairStages, static_cast<uint32_t>(i / kPairStages) & 1u);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_e4m3(kBlk, 2 * kBlk);
-    const uint32_t ring = smem_u32(sm);
-    RingPos p, t;
-    for (int tile = worker; ok && tile < tiles; tile += workers) {
-      for (int b = 0; b < nb; ++b) {
-        ok = mbar_wait_warp(tempty + t.s, t.ph ^ 1u) && mbar_wait_warp(full + p.s, p.ph);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t xd = desc_sw128(ring + p.s * kPairStage);
-        const uint64_t wd = desc_sw128(ring + p.s * kPairStage + kTileW);
-        if (elect_one()) {
+    // the whole warp keeps the loop, so that its values stay uniform; one lane issues
+    if (cta == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(2 * kBlk, 2 * kBlk);
+      const uint32_t ring = smem_u32(sm);
+      RingPos p, t;
+      for (int tile = worker; ok && tile < tiles; tile += workers) {
+        for (int b = 0; b < nb; ++b) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(tempty + t.s, t.ph ^ 1u) && mbar_wait_cluster(full + p.s, p.ph));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t xd = desc_sw128(ring + p.s * kPairStage);
+          const uint64_t wd = desc_sw128(ring + p.s * kPairStage + kTileW);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_e4m3(tmem + t.s * 2 * kBlk, xd + 2 * k, wd + 2 * k, idesc, k > 0);
-          mma_commit(smem_u32(tfull + t.s));
-          mma_commit(smem_u32(empty + p.s));
+            for (int k = 0; k < 4; ++k) mma_e4m3_pair(tmem + t.s * 2 * kBlk, xd + 2 * k, wd + 2 * k, idesc, k > 0);
+            mma_commit_pair(smem_u32(tfull + t.s));
+            mma_commit_pair(smem_u32(empty + p.s));
+          }
+          __syncwarp();
+          p.next(kPairStages);
+          t.next(2);
         }
-        __syncwarp();
-        p.next(kPairStages);
-        t.next(2);
       }
+      if (elect_one()) mma_commit_pair(smem_u32(done));
+      __syncwarp();
+      if (!mbar_wait(done, 0)) ok = false;
+      if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
     }
-    if (elect_one()) mma_commit(smem_u32(done));
-    __syncwarp();
-    if (!mbar_wait(done, 0)) ok = false;
-    if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
     __syncwarp();
   } else if (warp == 2) {
     // scales: xs[b][the tile's rows] * ws[either weight block][b], kPairChunk
@@ -748,7 +820,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int tile = worker; ok && tile < tiles; tile += workers) {
       const int n0 = 2 * (tile / g.tiles_m), n1 = min(n0 + 1, (g.n - 1) / kBlk);
       const float *w0 = g.ws + static_cast<size_t>(n0) * nb, *w1 = g.ws + static_cast<size_t>(n1) * nb;
-      const float* xs = g.xs + (tile % g.tiles_m) * kBlk + lane * 4;
+      const float* xs = g.xs + (2 * (tile % g.tiles_m) + cta) * kBlk + lane * 4;
       for (int b0 = 0; b0 < nb; b0 += kPairChunk) {
         ok = mbar_wait_warp(sempty + p.s, p.ph ^ 1u);
         if (!ok) break;
@@ -771,6 +843,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsEpi));
     const int quad = warp & 3, col0 = ((warp - 4) >> 2) * kPairCols, row = quad * 32 + lane;
     const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
+    const uint32_t freed = map_cta(smem_u32(tempty), 0);
     const float* const scale = scale_ring + (col0 / kBlk) * kBlk + row;
     RingPos t, p;
     for (int tile = worker; ok && tile < tiles; tile += workers) {
@@ -794,7 +867,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // all columns read: the next block but one may have the buffer
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty + t.s);
+            if (lane == 0) mbar_arrive_cluster(freed + t.s * 8);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -811,7 +884,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // A thread holds a row; 64 bytes of each of the warp's 32 rows at a time
       // go through shared memory, so that stores cover whole sectors.  (Straight
       // from the registers a tile's stores took 6,800 cycles.)
-      const int t0 = (tile % g.tiles_m) * kBlk + quad * 32;
+      const int t0 = (2 * (tile % g.tiles_m) + cta) * kBlk + quad * 32;
       const int n0 = 2 * (tile / g.tiles_m) * kBlk + col0;
       uint8_t* out = sm + kPairOutOff + (warp - 4) * 16 * kPairOutBytes;
       if (g.out_type == MOE_F32) {
@@ -843,7 +916,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  // neither CTA leaves while the other, or an MMA of both, may signal it
+  if (cta == 1 && threadIdx.x == 0 && !mbar_wait(done, 0)) latch_error(g.ctl, kErrTimeout);
+  cluster.sync();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
 cudaError_t launch_pair(const GemmArgs& g, const CUtensorMap& wmap, const CUtensorMap& xmap, int num_sms, cudaStream_t st) {
@@ -851,7 +927,7 @@ cudaError_t launch_pair(const GemmArgs& g, const CUtensorMap& wmap, const CUtens
   if (e) return e;
   const int64_t tiles = static_cast<int64_t>(g.tiles_n) * g.tiles_m;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms));
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < num_sms / 2 ? tiles : num_sms / 2));
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = st;
@@ -1016,7 +1092,6 @@ extern "C" int moe_fp8_linear(moe_fp8* w, const void* x, int32_t x_type, int64_t
           if (!encode_tiles(w->encode, &xmap, q.codes, rows, static_cast<int64_t>(l.blocks) * kBlk, static_cast<int64_t>(l.blocks) * kBlk))
             return reportf(MOE_ERR_CUDA, "moe_fp8_linear: cuTensorMapEncodeTiled refused rows=%d k=%d", rows, w->k);
           g.tiles_n = (w->n + 2 * kBlk - 1) / (2 * kBlk);
-          g.tiles_m = (rows + kBlk - 1) / kBlk;
           e = launch_pair(g, w->map, xmap, w->num_sms, st);
         }
       }

@@ -11,6 +11,8 @@
 // kernels: block_norm_kernel takes one row per block (or per warp);
 // block_norm_stream_kernel keeps one block on each SM whose teams of threads
 // load their next rows while they work on one, with the weights at hand.
+// Measured: 8192 rows of 7168, fp32 y and bf16 h, h' and x, 94.3 us (6.23 TB/s,
+// 92% of the measured copy rate); one such row 3.4 us a call in a graph.
 #include <cstdint>
 
 #include <cuda_runtime.h>

@@ -12,13 +12,18 @@
 // no tensor-core row idle, and the weights, which bound that case, are read
 // once.  Roles: one warp loads (TMA tiles of w, bulk copies of x), one issues
 // the MMAs, one multiplies the scales of each block into shared memory, four
-// or eight read the accumulators.  Accumulators are double or quadruple
-// buffered in tensor memory, so the MMAs of the next blocks run while a block
-// is scaled.
+// or eight read the accumulators.  There are four accumulators in tensor
+// memory, so the MMAs of the next blocks run while a block is scaled.  More
+// than 128 rows go to pairs of SMs, below.
 //
-// Bound: reading w for few rows, the tensor cores for many.  With fewer tiles
-// than SMs a cluster of 2, 4 or 8 CTAs splits the blocks of a tile and joins
-// its partial sums through distributed shared memory in rank order.
+// Bound: reading w for few rows, the tensor cores' round trip for many.  With
+// fewer tiles than SMs a cluster of 2 or 4 CTAs splits the blocks of a tile and
+// joins its partial sums through distributed shared memory in rank order.
+// Measured: 16 x 131072 x 7168 to fp32 146 to 154 us (6.2 to 6.5 TB/s, 91 to
+// 95% of the measured copy rate; 1024 tiles on 152 SMs leave the last round a
+// quarter empty); 1 x 2048 x 2048 5.4 us and 77 x 7000 x 2003 10.9 us a call in
+// a graph; 4096 x 7168 x 7168 177 us (2380 TFLOP/s, 127% of the measured bf16
+// rate).
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -51,7 +56,8 @@ constexpr uint32_t kMagic = 0x4D6F4638u;
 // Workspace: control words, xs [blocks][rows_pad] floats, then the codes of x
 // as tiles [row tile of bn][block][bn rows x 128 bytes], each in the 128-byte
 // swizzled order the tensor core reads (16-byte piece p of row r at
-// r * 128 + ((p ^ (r & 7)) << 4)), so a plain bulk copy loads a tile.
+// r * 128 + ((p ^ (r & 7)) << 4)), so a plain bulk copy loads a tile; for pairs
+// of SMs as rows of whole blocks, which tiled loads bring into that order.
 struct Layout {
   int bn, row_tiles, rows_pad, blocks;
   size_t xs, codes, bytes;
@@ -68,7 +74,7 @@ struct Cut {
 // Where the widest tiles of up to 128 rows leave SMs idle: the cut with the
 // most CTAs that still run at once, the wider of equals (77 x 7000 x 2003:
 // 128 rows split in 2, 11.1 us, against 64 rows, 13.1; 128 x 2048 x 7168: 64
-// rows split in 4, 12.7 us, against 128 rows split in 4, 20.1).  Clusters of
+// rows split in 4, 12.7 us, against 128 rows split in 4, 13.8).  Clusters of
 // 8 do not fill the SMs: sixteen of them ran one after the other (1 x 2048 x
 // 2048: 7.9 us, split in 4 5.4).  Else the widest tile, so that weights are
 // read for 256 rows (fp8_pair_kernel; 512 x 7168 x 7168: 30.3 us, with 128 rows
@@ -292,8 +298,8 @@ struct Cfg {
   static constexpr int kEpi = BN >= 128 ? 8 : 4;               // warps that read accumulators
   static constexpr int kThreads = 128 + 32 * kEpi;
   static constexpr int kCols = BN / (kEpi / 4);                // columns per thread
-  static constexpr int kBuf = BN == 256 ? 2 : 4;               // accumulators in tensor memory
-  static constexpr uint32_t kTmem = BN * kBuf < 32 ? 32 : BN * kBuf;
+  static constexpr int kBuf = 4;                               // accumulators in tensor memory
+  static constexpr uint32_t kTmem = BN * kBuf;
   static constexpr int kStage = kTileW + (DIRECT ? 0 : BN * kBlk);
   static constexpr int kStages = !DIRECT && (200 * 1024) / kStage < 8 ? (200 * 1024) / kStage : 8;
   static constexpr int kX = DIRECT ? kDirectBlocks * BN * kBlk : 0;  // x of all blocks of a DIRECT CTA
@@ -738,107 +744,107 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   bool ok = true;
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsFew));
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t keep = policy_evict_last();
-      const int total = ((tiles - worker + workers - 1) / workers) * nb;
-      const int ahead = min(total, kPairStages);
-      auto load_w = [&](int s, int tn, int b) {
-        if (cta == 0) mbar_arrive_expect_tx(full + s, 2 * kPairStage);
-        tma_load_pair(sm + s * kPairStage + kTileW, &wmap, b * kBlk, (2 * tn + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
-      };
-      auto load_x = [&](int s, int tm, int b) {
-        tma_load_pair(sm + s * kPairStage, &xmap, b * kBlk, (2 * tm + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
-      };
-      int tile = worker, b = 0, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
-      auto next_block = [&]() {
-        if (++b == nb) b = 0, tile += workers, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
-      };
-      // the weights do not depend on the quantisation kernel before this one
-      for (int i = 0; i < ahead; ++i, next_block()) load_w(i, tn, b);
-      pdl_wait();
-      tile = worker, b = 0, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
-      for (int i = 0; i < ahead; ++i, next_block()) load_x(i, tm, b);
-      RingPos p;
-      if (ahead == kPairStages) p.ph = 1;
-      else p.s = ahead;
-      int issued = ahead;
-      for (; issued < total; ++issued, next_block()) {
-        if (!mbar_wait(empty + p.s, p.ph ^ 1u)) {
-          ok = false;
-          break;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsFew));
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint64_t keep = policy_evict_last();
+        const int total = ((tiles - worker + workers - 1) / workers) * nb;
+        const int ahead = min(total, kPairStages);
+        auto load_w = [&](int s, int tn, int b) {
+          if (cta == 0) mbar_arrive_expect_tx(full + s, 2 * kPairStage);
+          tma_load_pair(sm + s * kPairStage + kTileW, &wmap, b * kBlk, (2 * tn + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
+        };
+        auto load_x = [&](int s, int tm, int b) {
+          tma_load_pair(sm + s * kPairStage, &xmap, b * kBlk, (2 * tm + cta) * kBlk, map_cta(smem_u32(full + s), 0), keep);
+        };
+        int tile = worker, b = 0, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
+        auto next_block = [&]() {
+          if (++b == nb) b = 0, tile += workers, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
+        };
+        // the weights do not depend on the quantisation kernel before this one
+        for (int i = 0; i < ahead; ++i, next_block()) load_w(i, tn, b);
+        pdl_wait();
+        tile = worker, b = 0, tm = tile % g.tiles_m, tn = tile / g.tiles_m;
+        for (int i = 0; i < ahead; ++i, next_block()) load_x(i, tm, b);
+        RingPos p;
+        if (ahead == kPairStages) p.ph = 1;
+        else p.s = ahead;
+        int issued = ahead;
+        for (; issued < total; ++issued, next_block()) {
+          if (!mbar_wait(empty + p.s, p.ph ^ 1u)) {
+            ok = false;
+            break;
+          }
+          load_w(p.s, tn, b);
+          load_x(p.s, tm, b);
+          p.next(kPairStages);
         }
-        load_w(p.s, tn, b);
-        load_x(p.s, tm, b);
-        p.next(kPairStages);
+        // a run that gave up leaves no copy in flight: CTA 0's barriers count both CTAs'
+        if (!ok) {
+          latch_error(g.ctl, kErrTimeout);
+          if (cta == 0)
+            for (int i = max(0, issued - kPairStages); i < issued; ++i)
+              mbar_wait(full + i % kPairStages, static_cast<uint32_t>(i / kPairStages) & 1u);
+        }
       }
-      // a run that gave up leaves no copy in flight: CTA 0's barriers count both CTAs'
-      if (!ok) {
-        latch_error(g.ctl, kErrTimeout);
-        if (cta == 0)
-          for (int i = max(0, issued - kPairStages); i < issued; ++i)
-            mbar_wait(full + i % kPairStages, static_cast<uint32_t>(i / kPairStages) & 1u);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // the whole warp keeps the loop, so that its values stay uniform; one lane issues
-    if (cta == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(2 * kBlk, 2 * kBlk);
-      const uint32_t ring = smem_u32(sm);
-      RingPos p, t;
-      for (int tile = worker; ok && tile < tiles; tile += workers) {
-        for (int b = 0; b < nb; ++b) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(tempty + t.s, t.ph ^ 1u) && mbar_wait_cluster(full + p.s, p.ph));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t xd = desc_sw128(ring + p.s * kPairStage);
-          const uint64_t wd = desc_sw128(ring + p.s * kPairStage + kTileW);
-          if (elect_one()) {
+      __syncwarp();
+    } else if (warp == 1) {
+      // the whole warp keeps the loop, so that its values stay uniform; one lane issues
+      if (cta == 0) {
+        constexpr uint32_t idesc = idesc_e4m3(2 * kBlk, 2 * kBlk);
+        const uint32_t ring = smem_u32(sm);
+        RingPos p, t;
+        for (int tile = worker; ok && tile < tiles; tile += workers) {
+          for (int b = 0; b < nb; ++b) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(tempty + t.s, t.ph ^ 1u) && mbar_wait_cluster(full + p.s, p.ph));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t xd = desc_sw128(ring + p.s * kPairStage);
+            const uint64_t wd = desc_sw128(ring + p.s * kPairStage + kTileW);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_e4m3_pair(tmem + t.s * 2 * kBlk, xd + 2 * k, wd + 2 * k, idesc, k > 0);
-            mma_commit_pair(smem_u32(tfull + t.s));
-            mma_commit_pair(smem_u32(empty + p.s));
+              for (int k = 0; k < 4; ++k) mma_e4m3_pair(tmem + t.s * 2 * kBlk, xd + 2 * k, wd + 2 * k, idesc, k > 0);
+              mma_commit_pair(smem_u32(tfull + t.s));
+              mma_commit_pair(smem_u32(empty + p.s));
+            }
+            __syncwarp();
+            p.next(kPairStages);
+            t.next(2);
+          }
+        }
+        if (elect_one()) mma_commit_pair(smem_u32(done));
+        __syncwarp();
+        if (!mbar_wait(done, 0)) ok = false;
+        if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // scales: xs[b][the tile's rows] * ws[either weight block][b], kPairChunk
+      // blocks at a time (a wait for each block cost 12 us of 178)
+      pdl_wait();
+      RingPos p;
+      for (int tile = worker; ok && tile < tiles; tile += workers) {
+        const int n0 = 2 * (tile / g.tiles_m), n1 = min(n0 + 1, (g.n - 1) / kBlk);
+        const float *w0 = g.ws + static_cast<size_t>(n0) * nb, *w1 = g.ws + static_cast<size_t>(n1) * nb;
+        const float* xs = g.xs + (2 * (tile % g.tiles_m) + cta) * kBlk + lane * 4;
+        for (int b0 = 0; b0 < nb; b0 += kPairChunk) {
+          ok = mbar_wait_warp(sempty + p.s, p.ph ^ 1u);
+          if (!ok) break;
+          float4* to = reinterpret_cast<float4*>(scale_ring + p.s * kPairChunk * 2 * kBlk) + lane;
+#pragma unroll 4
+          for (int b = b0; b < min(nb, b0 + kPairChunk); ++b, to += kBlk / 2) {
+            const float4 x = *reinterpret_cast<const float4*>(xs + static_cast<size_t>(b) * g.rows_pad);
+            const float u = w0[b], v = w1[b];
+            to[0] = make_float4(x.x * u, x.y * u, x.z * u, x.w * u);
+            to[kBlk / 4] = make_float4(x.x * v, x.y * v, x.z * v, x.w * v);
           }
           __syncwarp();
-          p.next(kPairStages);
-          t.next(2);
+          if (lane == 0) mbar_arrive(sfull + p.s);
+          p.next(2);
         }
       }
-      if (elect_one()) mma_commit_pair(smem_u32(done));
-      __syncwarp();
-      if (!mbar_wait(done, 0)) ok = false;
       if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
     }
-    __syncwarp();
-  } else if (warp == 2) {
-    // scales: xs[b][the tile's rows] * ws[either weight block][b], kPairChunk
-    // blocks at a time (a wait for each block cost 12 us of 178)
-    pdl_wait();
-    RingPos p;
-    for (int tile = worker; ok && tile < tiles; tile += workers) {
-      const int n0 = 2 * (tile / g.tiles_m), n1 = min(n0 + 1, (g.n - 1) / kBlk);
-      const float *w0 = g.ws + static_cast<size_t>(n0) * nb, *w1 = g.ws + static_cast<size_t>(n1) * nb;
-      const float* xs = g.xs + (2 * (tile % g.tiles_m) + cta) * kBlk + lane * 4;
-      for (int b0 = 0; b0 < nb; b0 += kPairChunk) {
-        ok = mbar_wait_warp(sempty + p.s, p.ph ^ 1u);
-        if (!ok) break;
-        float4* to = reinterpret_cast<float4*>(scale_ring + p.s * kPairChunk * 2 * kBlk) + lane;
-#pragma unroll 4
-        for (int b = b0; b < min(nb, b0 + kPairChunk); ++b, to += kBlk / 2) {
-          const float4 x = *reinterpret_cast<const float4*>(xs + static_cast<size_t>(b) * g.rows_pad);
-          const float u = w0[b], v = w1[b];
-          to[0] = make_float4(x.x * u, x.y * u, x.z * u, x.w * u);
-          to[kBlk / 4] = make_float4(x.x * v, x.y * v, x.z * v, x.w * v);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfull + p.s);
-        p.next(2);
-      }
-    }
-    if (!ok && lane == 0) latch_error(g.ctl, kErrTimeout);
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsEpi));
     const int quad = warp & 3, col0 = ((warp - 4) >> 2) * kPairCols, row = quad * 32 + lane;
@@ -1035,6 +1041,9 @@ extern "C" int moe_fp8_linear(moe_fp8* w, const void* x, int32_t x_type, int64_t
   if (!handle_ok(w)) return reportf(MOE_ERR_ARG, "moe_fp8_linear: invalid handle");
   if (rows < 0 || rows > kMaxRows) return reportf(MOE_ERR_ARG, "moe_fp8_linear: rows=%d must be in [0, %d]", rows, kMaxRows);
   if (rows == 0) return MOE_OK;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != w->device)
+    return reportf(MOE_ERR_ARG, "moe_fp8_linear: the handle's device %d must be the current device", w->device);
   if (!x || !out || !workspace) return reportf(MOE_ERR_ARG, "moe_fp8_linear: x, out or workspace is NULL");
   if (!elem_type_ok(x_type) || !elem_type_ok(out_type))
     return reportf(MOE_ERR_ARG, "moe_fp8_linear: unknown type (x %d, out %d)", x_type, out_type);

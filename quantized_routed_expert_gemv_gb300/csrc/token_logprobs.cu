@@ -25,6 +25,14 @@
 // contiguous part, when there are too few rows for the SMs; the parts meet in
 // the first block's shared memory and are joined in rank order, so results do
 // not depend on timing.
+//
+// Bound: for many rows the instructions of the pass (some 6 a logit: bound,
+// widening, fma, exponential, sum, weighted sum, maximum, comparison; pairs
+// where the machine has them) and the latency of a row's end, which the
+// pass of the SM's three other blocks covers in part: 4096 rows of 131072
+// bf16 199 us, 5.4 TB/s, 79% of the measured copy rate.  Larger blocks (512
+// threads) took 215 us, warps of their own for the rows' ends 224.  For few
+// rows the chain of steps: one row of 131072 with 20 alternatives 10.4 us.
 #include <cmath>
 #include <cstdint>
 

@@ -26,9 +26,9 @@
 // the first block's shared memory and are joined in rank order, so results do
 // not depend on timing.
 //
-// Bound: for many rows the instructions of the pass (some 6 a logit: bound,
-// widening, fma, exponential, sum, weighted sum, maximum, comparison; pairs
-// where the machine has them) and the latency of a row's end, which the
+// Bound: for many rows the instructions (8.2 a thread and logit, rows' ends
+// included; the pass has bound, widening, fma, exponential, sum, weighted sum,
+// maximum, comparison, in pairs where the machine has them) and the latency of a row's end, which the
 // pass of the SM's three other blocks covers in part: 4096 rows of 131072
 // bf16 199 us, 5.4 TB/s, 79% of the measured copy rate.  Larger blocks (512
 // threads) took 215 us, warps of their own for the rows' ends 224.  For few

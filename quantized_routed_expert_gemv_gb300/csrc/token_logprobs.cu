@@ -28,11 +28,12 @@
 //
 // Bound: for many rows the instructions (8.2 a thread and logit, rows' ends
 // included; the pass has bound, widening, fma, exponential, sum, weighted sum,
-// maximum, comparison, in pairs where the machine has them) and the latency of a row's end, which the
-// pass of the SM's three other blocks covers in part: 4096 rows of 131072
-// bf16 199 us, 5.4 TB/s, 79% of the measured copy rate.  Larger blocks (512
-// threads) took 215 us, warps of their own for the rows' ends 224.  For few
-// rows the chain of steps: one row of 131072 with 20 alternatives 10.4 us.
+// maximum, comparison, in pairs where the machine has them) and the latency of
+// a row's end, which the pass of the SM's three other blocks covers in part:
+// 4096 rows of 131072 bf16 199 us, 5.4 TB/s, 79% of the measured copy rate.
+// Larger blocks (512 threads) took 215 us, warps of their own for the rows'
+// ends 224.  For few rows the chain of steps: one row of 131072 with 20
+// alternatives 10.4 us.
 #include <cmath>
 #include <cstdint>
 

@@ -26,14 +26,12 @@
 // the first block's shared memory and are joined in rank order, so results do
 // not depend on timing.
 //
-// Bound: for many rows the instructions (8.2 a thread and logit, rows' ends
-// included; the pass has bound, widening, fma, exponential, sum, weighted sum,
-// maximum, comparison, in pairs where the machine has them) and the latency of
-// a row's end, which the pass of the SM's three other blocks covers in part:
-// 4096 rows of 131072 bf16 199 us, 5.4 TB/s, 79% of the measured copy rate.
-// Larger blocks (512 threads) took 215 us, warps of their own for the rows'
-// ends 224.  For few rows the chain of steps: one row of 131072 with 20
-// alternatives 10.4 us.
+// Bound: for many long rows memory, and the latency of a row's end (a fifth of
+// a block's time), which the pass of the SM's other blocks covers in part: 4096
+// rows of 131072 bf16 177 us, 6.05 TB/s, 89% of the measured copy rate.  For
+// shorter rows the rows' ends: 4096 rows of 32000 56 us.  For few rows the
+// chain of steps: one row of 131072 with 20 alternatives 10 us.  Tried: blocks
+// of 512 threads 215 us, warps of their own for the rows' ends 224.
 #include <cmath>
 #include <cstdint>
 
@@ -51,13 +49,18 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 // chunks of 8 logits a thread loads at once
 __host__ __device__ constexpr int batch_of(int type) { return type == MOE_F32 ? 2 : 4; }
+constexpr int kBatchBytes = 64;        // of a thread
+// Batches a thread has in shared memory where it copies through there: one in
+// use, two on their way.  A thread copies for itself, so the pass has no
+// barrier; registers have room for one batch on its way.
+constexpr int kRing = 3;
 constexpr int kMaxTop = 32;
 constexpr int kMaxTargets = 8;
 constexpr int kMaxSplit = 8;
+constexpr int kSplitThreads = 256;     // of blocks that may read parts of a row
+constexpr int kSmallVocab = 56 * 1024, kRingVocab = 12 * 1024;  // launch_type's
 constexpr int64_t kPartBytes = 32 * 1024;  // of a row, at least, in a part
 constexpr int kCand = 1024;            // candidate buffer of the top selection
 constexpr float kRefSlack = 80.0f;     // powers of two a logit may lie above the reference
@@ -169,7 +172,7 @@ __device__ __forceinline__ float max_warp(float v) {
 
 // Calls emit(place, i) for the keys among the first n of keys[0..m): a key's
 // place is the number of keys before it.  A warp takes a key at a time.
-template <class Emit>
+template <int kWarps, class Emit>
 __device__ __forceinline__ void place_keys(const Key* keys, int m, int n, Emit emit) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -212,27 +215,45 @@ struct Row {
   }
 };
 
+template <int THREADS>
+struct Picks {                 // of the top selection
+  Key group[THREADS];          // groups at or above the cut: best token ...
+  int owner[THREADS];          // ... and thread
+  Key cand[kCand];
+};
+
+template <int THREADS, bool RING>
+union Shared {
+  Picks<THREADS> picks;
+};
+template <int THREADS>
+union Shared<THREADS, true> {
+  Picks<THREADS> picks;                             // after the pass
+  uint4 ring[kRing][kBatchBytes / 16][THREADS];     // the pass: batches of the threads
+};
+
+template <int THREADS, bool RING>
 struct Smem {
-  Part parts[kMaxSplit];       // the cluster's first block: one per part
+  static constexpr int kWarps = THREADS / 32;
+  Shared<THREADS, RING> u;
+  Part parts[THREADS == kSplitThreads ? kMaxSplit : 1];  // the cluster's first block: one per part
   Part mine;
-  float team[32];              // best value of each team of kThreads / 32 threads
+  float team[32];              // best value of each team of THREADS / 32 threads
   float cut;                   // value no group of the top n lies below
   int ngroup, ncand;
-  Key group[kThreads];         // groups at or above it: best token ...
-  int owner[kThreads];         // ... and thread
   Key sel[kMaxTop];            // the n first groups
   int sel_owner[kMaxTop];
-  Key cand[kCand];
   Key last, best[kWarps];
   float r[kWarps], S[kWarps], A[kWarps];
   int cnt[kWarps][kMaxTargets];
 };
 
 // The first n tokens of this block's part to part.top.
-template <int TYPE>
-__device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n, int c0, int c1, float best, int best_b,
+template <int TYPE, int THREADS, bool RING>
+__device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem<THREADS, RING>& sm, int n, int c0, int c1, float best, int best_b,
                                            float edge_v, int edge_j) {
-  constexpr int kBatch = batch_of(TYPE);
+  constexpr int kBatch = batch_of(TYPE), kThreads = THREADS, kWarps = THREADS / 32;
+  Picks<THREADS>& pk = sm.u.picks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // a value that n groups reach: the n-th largest of 32 teams' best
   constexpr int kTeam = kThreads / 32;
@@ -269,18 +290,18 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n
       }
     }
     const int s = atomicAdd(&sm.ngroup, 1);
-    sm.group[s].v = best, sm.group[s].id = id, sm.owner[s] = tid;
+    pk.group[s].v = best, pk.group[s].id = id, pk.owner[s] = tid;
   }
   __syncthreads();
   const int m = sm.ngroup;
-  place_keys(sm.group, m, n, [&](int place, int i) { sm.sel[place] = sm.group[i], sm.sel_owner[place] = sm.owner[i]; });
+  place_keys<THREADS / 32>(pk.group, m, n, [&](int place, int i) { sm.sel[place] = pk.group[i], sm.sel_owner[place] = pk.owner[i]; });
   __syncthreads();
   const Key cut = sm.sel[n - 1];
   auto push = [&](float v, int id) {
     const Key k = {v, id};
     if (v > -INFINITY && (cut.id < 0 || !before(cut, k))) {
       const int s = atomicAdd(&sm.ncand, 1);
-      if (s < kCand) sm.cand[s] = k;
+      if (s < kCand) pk.cand[s] = k;
     }
   };
   if (edge_j >= 0) push(edge_v, edge_j);
@@ -299,7 +320,7 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n
   __syncthreads();
   const int nc = sm.ncand;
   if (nc <= kCand) {
-    place_keys(sm.cand, nc, n, [&](int place, int i) { sm.mine.top[place] = sm.cand[i]; });
+    place_keys<THREADS / 32>(pk.cand, nc, n, [&](int place, int i) { sm.mine.top[place] = pk.cand[i]; });
     return;
   }
   // many tokens in few groups: one round over the winning groups per place
@@ -341,13 +362,17 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem& sm, int n
 }
 
 // NT: targets whose ranks are counted, rounded up to 0, 1, 2, 4 or 8.
-template <int TYPE, int NT>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kernel(const moe_token_logprobs_args a, int split) {
-  __shared__ Smem sm;
+template <int TYPE, int NT, int THREADS, bool RING>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel(const moe_token_logprobs_args a, int parts) {
+  extern __shared__ uint4 dyn_smem[];
+  constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+  using Sm = Smem<THREADS, RING>;
+  Sm& sm = *reinterpret_cast<Sm*>(dyn_smem);
   constexpr bool F32 = TYPE == MOE_F32;
   constexpr int kBatch = batch_of(TYPE);
   constexpr int NG = NT > 0 ? NT : 1;
   cg::cluster_group cluster = cg::this_cluster();
+  const int split = THREADS == kSplitThreads ? parts : 1;
   const int rank = split > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   if (split > 1) cluster.barrier_arrive();  // paired with the wait before the parts meet
   const int64_t t = blockIdx.x / split;
@@ -361,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   // The batches before the last are whole for every thread.
   constexpr int Q = F32 ? 2 : 1, kStep = kBatch * kThreads;
   using Batch = uint4[kBatch][Q];
+  static_assert(sizeof(Batch) == kBatchBytes && !(RING && F32), "a batch in the ring, of 16-bit logits");
+  constexpr uint32_t fill = F32 ? 0xFF800000u : TYPE == MOE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
   auto fetch = [&](Batch& raw, int cb) {
     const uint4* p = row.chunk(cb + tid);
     if (cb + kStep <= c1) {
@@ -370,16 +397,41 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
         for (int q = 0; q < Q; ++q) raw[i][q] = __ldg(p + i * kThreads * Q + q);
     } else {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        constexpr uint32_t fill = F32 ? 0xFF800000u : TYPE == MOE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+      for (int i = 0; i < kBatch; ++i)
 #pragma unroll
         for (int q = 0; q < Q; ++q)
           raw[i][q] = cb + tid + i * kThreads < c1 ? __ldg(p + i * kThreads * Q + q) : make_uint4(fill, fill, fill, fill);
-      }
     }
   };
-  Batch even, odd;
-  fetch(even, c0);
+  auto copy = [&](int slot, int cb) {  // the same into the ring
+    if constexpr (RING) {
+      const uint4* p = row.chunk(cb + tid);
+      uint4* const to = &sm.u.ring[slot][0][tid];
+      auto one = [&](int i) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(
+                         __cvta_generic_to_shared(to + i * kThreads))),
+                     "l"(p + i * kThreads)
+                     : "memory");
+      };
+      if (cb + kStep <= c1) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) one(i);
+      } else if (cb < c1) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (cb + tid + i * kThreads < c1) one(i);
+          else to[i * kThreads] = make_uint4(fill, fill, fill, fill);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  Batch even;
+  if constexpr (RING) {
+    for (int i = 0; i < kRing - 1; ++i) copy(i, c0 + i * kStep);
+  } else {
+    fetch(even, c0);
+  }
 
   // the first block's first warp writes the row's answers: its targets' logits
   int my_target = -1;
@@ -417,8 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   }
 
   // Read early, used after the pass, in the first part: the row's edges, one
-  // thread each, and the logits before a target in its own chunk, a warp's
-  // first eight threads each.
+  // thread each, and the logits before a target in its own chunk, eight
+  // threads each.
   int edge_j = -1, fix_g = -1;
   float edge_v = -INFINITY, fix_v = NAN;
   if (rank == 0) {
@@ -427,8 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
     if constexpr (NT > 0) {
 #pragma unroll
       for (int g = 0; g < NT; ++g) {
-        const int j = 8 * tc[g] - row.off + lane;
-        if (warp == g && lane < 8 && tc[g] >= row.w0 && tc[g] < row.w1 && j < tj[g]) fix_g = g, fix_v = row.at(j);
+        const int j = 8 * tc[g] - row.off + (lane & 7);
+        if (warp == g % kWarps && lane >> 3 == g / kWarps && tc[g] >= row.w0 && tc[g] < row.w1 && j < tj[g])
+          fix_g = g, fix_v = row.at(j);
       }
     }
   }
@@ -528,15 +581,31 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
     }
   };
   int cb = c0;
+  if constexpr (RING) {
+    int slot = 0;
 #pragma unroll 1
-  while (cb < c1) {
-    if (cb + kStep < c1) fetch(odd, cb + kStep);
-    process(even, cb);
-    cb += kStep;
-    if (cb >= c1) break;
-    if (cb + kStep < c1) fetch(even, cb + kStep);
-    process(odd, cb);
-    cb += kStep;
+    for (; cb < c1; cb += kStep) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      Batch cur;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) cur[i][0] = sm.u.ring[slot][i][tid];
+      // into the slot before this one, whose batch the last turn has read
+      copy(slot == 0 ? kRing - 1 : slot - 1, cb + (kRing - 1) * kStep);
+      process(cur, cb);
+      slot = slot == kRing - 1 ? 0 : slot + 1;
+    }
+  } else {
+    Batch odd;
+#pragma unroll 1
+    while (cb < c1) {
+      if (cb + kStep < c1) fetch(odd, cb + kStep);
+      process(even, cb);
+      cb += kStep;
+      if (cb >= c1) break;
+      if (cb + kStep < c1) fetch(even, cb + kStep);
+      process(odd, cb);
+      cb += kStep;
+    }
   }
 
   if (edge_j >= 0) {
@@ -587,14 +656,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
       sm.mine.cnt[lane] = q;
     }
   }
-  if (n > 0) select_top<TYPE>(row, sm, n, c0, c1, best, best_c, edge_v, edge_j);
+  if (n > 0) select_top<TYPE, THREADS, RING>(row, sm, n, c0, c1, best, best_c, edge_v, edge_j);
   __syncthreads();
 
   // the parts meet in the first block
   Part* all = &sm.mine;
   if (split > 1) {
     constexpr int words = sizeof(Part) / 4;
-    static_assert(words <= kThreads, "one word a thread");
+    static_assert(words <= kSplitThreads && kMaxSplit * kMaxTop <= kSplitThreads, "one word, one token a thread");
     uint32_t* to = reinterpret_cast<uint32_t*>(cluster.map_shared_rank(&sm.parts[rank], 0));
     cluster.barrier_wait();  // the first block has started
     if (tid < words) to[tid] = reinterpret_cast<const uint32_t*>(&sm.mine)[tid];
@@ -691,24 +760,60 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   }
 }
 
-template <int TYPE>
-cudaError_t launch_type(const moe_token_logprobs_args& a, int split, cudaStream_t st) {
+template <int TYPE, int NT, int THREADS, bool RING>
+cudaError_t launch(const moe_token_logprobs_args& a, int split, cudaStream_t st) {
+  auto kernel = token_logprobs_kernel<TYPE, NT, THREADS, RING>;
+  const int parts = THREADS == kSplitThreads ? split : 1;  // as the kernel has it
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * split);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * parts);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = sizeof(Smem<THREADS, RING>);
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = split;
+  at.val.clusterDim.x = parts;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
+  if (cfg.dynamicSmemBytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.dynamicSmemBytes);
+    if (e) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, a, parts);
+}
+
+template <int TYPE, int THREADS, bool RING>
+cudaError_t launch_nt(const moe_token_logprobs_args& a, int split, cudaStream_t st) {
   const int nt = a.target_ranks ? a.n_targets : 0;
-  if (nt == 0) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 0>, a, split);
-  if (nt == 1) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 1>, a, split);
-  if (nt == 2) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 2>, a, split);
-  if (nt <= 4) return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, 4>, a, split);
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<TYPE, kMaxTargets>, a, split);
+  if (nt == 0) return launch<TYPE, 0, THREADS, RING>(a, split, st);
+  if (nt == 1) return launch<TYPE, 1, THREADS, RING>(a, split, st);
+  if (nt == 2) return launch<TYPE, 2, THREADS, RING>(a, split, st);
+  if (nt <= 4) return launch<TYPE, 4, THREADS, RING>(a, split, st);
+  return launch<TYPE, kMaxTargets, THREADS, RING>(a, split, st);
+}
+
+template <int TYPE>
+cudaError_t launch_type(const moe_token_logprobs_args& a, int split, int sms, cudaStream_t st) {
+  // Measured in graphs, bf16, one target, 5 alternatives where not said.
+  // Blocks of 128 threads have shorter ends and leave an SM more rows to cover
+  // them with, while a winning group, twice as long, costs more to read again:
+  // 4096 rows of 8192 30.4 us against 44.8 with 256 threads, of 32000 56.5 / 73.2,
+  // of 50001 82.4 / 97.0, of 65536 104.1 / 99.5, of 131072 206 / 177; 600 rows of
+  // 32000, a wave of the larger blocks, 13.0 / 13.2.
+  // Copies through shared memory: 4096 rows of 131072 177 us against 197 into
+  // registers, of 65536 with 8 targets and 20 alternatives 237 / 319, of 20000
+  // (128 threads) 47.9 / 51.5, of 8192 33.5 / 32.2; 304 rows of 4000 7.0 / 6.6.
+  // fp32 rows of 131072 take 267 / 152 that way (no targets) and keep to
+  // registers.
+  const bool many = a.rows > 4 * sms, small = many && a.vocab <= kSmallVocab;
+  if constexpr (TYPE == MOE_F32) {
+    return small ? launch_nt<TYPE, 128, false>(a, split, st) : launch_nt<TYPE, kSplitThreads, false>(a, split, st);
+  } else {
+    if (small && a.vocab >= kRingVocab) return launch_nt<TYPE, 128, true>(a, split, st);
+    if (small) return launch_nt<TYPE, 128, false>(a, split, st);
+    if (many) return launch_nt<TYPE, kSplitThreads, true>(a, split, st);
+    return launch_nt<TYPE, kSplitThreads, false>(a, split, st);
+  }
 }
 
 }  // namespace
@@ -758,11 +863,11 @@ extern "C" int moe_token_logprobs(const moe_token_logprobs_args* args, void* str
     while (split < kMaxSplit && static_cast<int64_t>(a.rows) * split <= sms && row_bytes / (2 * split) >= kPartBytes) split *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.logits_type == MOE_BF16)
-    e = launch_type<MOE_BF16>(a, split, st);
+    e = launch_type<MOE_BF16>(a, split, sms, st);
   else if (a.logits_type == MOE_F16)
-    e = launch_type<MOE_F16>(a, split, st);
+    e = launch_type<MOE_F16>(a, split, sms, st);
   else
-    e = launch_type<MOE_F32>(a, split, st);
+    e = launch_type<MOE_F32>(a, split, sms, st);
   if (e != cudaSuccess)
     return reportf(MOE_ERR_CUDA, "moe_token_logprobs: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
   return MOE_OK;

@@ -18,20 +18,21 @@
 // that thread visited.  Any token of the row's top n lies in one of the n
 // groups whose best tokens come first: the best of each group before its own
 // comes before it too.  So the pass keeps one value per thread, and afterwards
-// only the n winning groups are read again (from cache), for the tokens that
-// do not come after the n-th group's best.
+// only winning groups are read again, for the tokens that do not come after
+// the n-th group's best, or after a lower value that n groups reach.
 //
 // A row is read by one block, or by a cluster of up to 8 blocks, each a
 // contiguous part, when there are too few rows for the SMs; the parts meet in
 // the first block's shared memory and are joined in rank order, so results do
 // not depend on timing.
 //
-// Bound: for many long rows memory, and the latency of a row's end (a fifth of
-// a block's time), which the pass of the SM's other blocks covers in part: 4096
-// rows of 131072 bf16 177 us, 6.05 TB/s, 89% of the measured copy rate.  For
-// shorter rows the rows' ends: 4096 rows of 32000 56 us.  For few rows the
-// chain of steps: one row of 131072 with 20 alternatives 10 us.  Tried: blocks
-// of 512 threads 215 us, warps of their own for the rows' ends 224.
+// Bound: for many long rows memory, and the latency of a row's end, which the
+// pass of the SM's other blocks covers in part: 4096 rows of 131072 bf16 171 us,
+// 6.3 TB/s, 92% of the measured copy rate.  For shorter rows the rows' ends:
+// 4096 rows of 32000 53 us.  For few rows the chain of steps: one row of 131072
+// with 20 alternatives 9.1 us.  Tried: blocks of 512 threads 215 us, warps of
+// their own for the rows' ends 224.
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -171,18 +172,31 @@ __device__ __forceinline__ float max_warp(float v) {
 }
 
 // Calls emit(place, i) for the keys among the first n of keys[0..m): a key's
-// place is the number of keys before it.  A warp takes a key at a time.
+// place is the number of keys before it.  A warp takes four keys at a time
+// (32 alternatives in 4096 rows of 32000: 116 us with one, 102 with four; 5
+// alternatives 52.2 and 52.9).
 template <int kWarps, class Emit>
 __device__ __forceinline__ void place_keys(const Key* keys, int m, int n, Emit emit) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int i = threadIdx.x >> 5; i < m; i += kWarps) {
-    const Key k = keys[i];
-    int c = 0;
+  for (int i = 4 * (threadIdx.x >> 5); i < m; i += 4 * kWarps) {
+    Key k[4];
+    int c[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = keys[min(i + j, m - 1)];
 #pragma unroll 1
-    for (int q = lane; q < m; q += 32) c += before(keys[q], k);
-    c = __reduce_add_sync(0xFFFFFFFFu, c);
-    if (lane == 0 && c < n) emit(c, i);
+    for (int q = lane; q < m; q += 32) {
+      const Key o = keys[q];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] += before(o, k[j]);
+    }
+    int place = n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[j] = __reduce_add_sync(0xFFFFFFFFu, c[j]);
+      if (lane == j) place = c[j];
+    }
+    if (lane < 4 && i + lane < m && place < n) emit(place, i + lane);
   }
 }
 
@@ -250,8 +264,8 @@ struct Smem {
 
 // The first n tokens of this block's part to part.top.
 template <int TYPE, int THREADS, bool RING>
-__device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem<THREADS, RING>& sm, int n, int c0, int c1, float best, int best_b,
-                                           float edge_v, int edge_j) {
+__device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem<THREADS, RING>& sm, int n, int c0, int c1,
+                                           float best, int best_b, float edge_v, int edge_j) {
   constexpr int kBatch = batch_of(TYPE), kThreads = THREADS, kWarps = THREADS / 32;
   Picks<THREADS>& pk = sm.u.picks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -262,7 +276,7 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem<THREADS, R
   for (int o = kTeam / 2; o; o >>= 1) h = fmaxf(h, __shfl_xor_sync(0xFFFFFFFFu, h, o));
   if (tid % kTeam == 0) sm.team[tid / kTeam] = h;
   if (tid == 0) sm.ngroup = sm.ncand = 0, sm.cut = -INFINITY;
-  if (tid < kMaxTop) sm.sel[tid].v = -INFINITY, sm.sel[tid].id = -1, sm.mine.top[tid].v = -INFINITY, sm.mine.top[tid].id = -1;
+  if (tid < kMaxTop) sm.mine.top[tid].v = -INFINITY, sm.mine.top[tid].id = -1;
   __syncthreads();
   if (warp == 0) {
     const float v = sm.team[lane];
@@ -275,41 +289,60 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem<THREADS, R
     if (place == n - 1) sm.cut = v;
   }
   __syncthreads();
+  // Groups that reach it.  Where these are little more than n, all of their
+  // tokens that reach it are candidates: that spares looking for the groups'
+  // tokens and their order (4096 rows of 8192 bf16 with 5 alternatives 30.4 us
+  // without, 26.3 with; of 131072 176 and 171).  Else the n-th group's best is
+  // the bound, and fewer groups are read again.
+  int slot = -1;
   if (best > -INFINITY && best >= sm.cut) {
-    // the token: the first place of that value in the batch it was seen in
-    int id = -1;
-#pragma unroll
-    for (int i = kBatch - 1; i >= 0; --i) {
-      const int c = best_b + i * kThreads + tid;
-      if (c < c1) {
-        float v[8];
-        row.load(c, v);
-#pragma unroll
-        for (int k = 7; k >= 0; --k)
-          if (v[k] == best) id = 8 * c - row.off + k;
-      }
-    }
-    const int s = atomicAdd(&sm.ngroup, 1);
-    pk.group[s].v = best, pk.group[s].id = id, pk.owner[s] = tid;
+    slot = atomicAdd(&sm.ngroup, 1);
+    pk.owner[slot] = tid;
   }
   __syncthreads();
   const int m = sm.ngroup;
-  place_keys<THREADS / 32>(pk.group, m, n, [&](int place, int i) { sm.sel[place] = pk.group[i], sm.sel_owner[place] = pk.owner[i]; });
-  __syncthreads();
-  const Key cut = sm.sel[n - 1];
+  int winners = m;
+  const int* owner = pk.owner;
+  Key cut = {sm.cut, INT_MAX};
+  if (m > n + n / 2 + 4) {
+    if (slot >= 0) {
+      // the token: the first place of that value in the batch it was seen in
+      int id = -1;
+#pragma unroll
+      for (int i = kBatch - 1; i >= 0; --i) {
+        const int c = best_b + i * kThreads + tid;
+        if (c < c1) {
+          float v[8];
+          row.load(c, v);
+#pragma unroll
+          for (int k = 7; k >= 0; --k)
+            if (v[k] == best) id = 8 * c - row.off + k;
+        }
+      }
+      pk.group[slot].v = best, pk.group[slot].id = id;
+    }
+    __syncthreads();
+    place_keys<kWarps>(pk.group, m, n, [&](int place, int i) {
+      sm.sel[place] = pk.group[i], sm.sel_owner[place] = pk.owner[i];
+    });
+    __syncthreads();
+    cut = sm.sel[n - 1];  // there are more than n
+    owner = sm.sel_owner;
+    winners = n;
+  }
   auto push = [&](float v, int id) {
     const Key k = {v, id};
-    if (v > -INFINITY && (cut.id < 0 || !before(cut, k))) {
+    if (v > -INFINITY && !before(cut, k)) {
       const int s = atomicAdd(&sm.ncand, 1);
       if (s < kCand) pk.cand[s] = k;
     }
   };
   if (edge_j >= 0) push(edge_v, edge_j);
   // chunk k of winner g is item g * chunks + k, one thread each
-  const int chunks = (c1 - c0 + kThreads - 1) / kThreads, items = min(n, m) * chunks;
+  const int chunks = (c1 - c0 + kThreads - 1) / kThreads, items = winners * chunks;
 #pragma unroll 1
   for (int e = tid; e < items; e += kThreads) {
-    const int g = e / chunks, c = c0 + sm.sel_owner[g] + (e - g * chunks) * kThreads;
+    const int g = e / chunks, c = c0 + owner[g] + (e - g * chunks) * kThreads;
     if (c < c1) {
       float v[8];
       row.load(c, v);
@@ -335,7 +368,7 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem<THREADS, R
     };
     if (edge_j >= 0) look(edge_v, edge_j);
     for (int e = tid; e < items; e += kThreads) {
-      const int g = e / chunks, c = c0 + sm.sel_owner[g] + (e - g * chunks) * kThreads;
+      const int g = e / chunks, c = c0 + owner[g] + (e - g * chunks) * kThreads;
       if (c < c1) {
         float v[8];
         row.load(c, v);
@@ -363,7 +396,8 @@ __device__ __forceinline__ void select_top(const Row<TYPE>& row, Smem<THREADS, R
 
 // NT: targets whose ranks are counted, rounded up to 0, 1, 2, 4 or 8.
 template <int TYPE, int NT, int THREADS, bool RING>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel(const moe_token_logprobs_args a, int parts) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    token_logprobs_kernel(const moe_token_logprobs_args a, int parts) {
   extern __shared__ uint4 dyn_smem[];
   constexpr int kThreads = THREADS, kWarps = THREADS / 32;
   using Sm = Smem<THREADS, RING>;
@@ -667,36 +701,29 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
     uint32_t* to = reinterpret_cast<uint32_t*>(cluster.map_shared_rank(&sm.parts[rank], 0));
     cluster.barrier_wait();  // the first block has started
     if (tid < words) to[tid] = reinterpret_cast<const uint32_t*>(&sm.mine)[tid];
+    if (tid == 0) sm.ncand = 0;
     cluster.sync();
     if (rank != 0) return;
     all = sm.parts;
     if (n > 0) {
+      // a token that n of the lists' tokens do not come after: the last of
+      // the lists' c-th, with c parts = n or a little more; only those tokens
+      // are ranked (searches of all lists for every token took 1 us more)
+      const int c = (n + split - 1) / split - 1;
+      Key cut = all[0].top[c];
+#pragma unroll
+      for (int q = 1; q < kMaxSplit; ++q) {
+        const Key k = all[q < split ? q : 0].top[c];
+        if (before(cut, k)) cut = k;
+      }
+      Picks<THREADS>& pk = sm.u.picks;
+      if (tid < split * kMaxTop && tid % kMaxTop < n) {
+        const Key k = all[tid / kMaxTop].top[tid % kMaxTop];
+        if (k.id >= 0 && !before(cut, k)) pk.cand[atomicAdd(&sm.ncand, 1)] = k;
+      }
       if (tid < kMaxTop) sm.mine.top[tid].v = -INFINITY, sm.mine.top[tid].id = -1;
       __syncthreads();
-      if (tid < split * kMaxTop && tid % kMaxTop < n) {
-        // a token's place: its own in its part's list, and in every other
-        // list (sorted, at most 32 long) the number of tokens before it
-        const int own = tid / kMaxTop;
-        const Key k = all[own].top[tid % kMaxTop];
-        int at[kMaxSplit] = {};
-#pragma unroll 1
-        for (int step = 32; step; step >>= 1) {
-          // no branch around the loads, so that the lists' go out together
-          // (entries of absent lists are read and not used)
-          Key o[kMaxSplit];
-#pragma unroll
-          for (int q = 0; q < kMaxSplit; ++q) o[q] = all[q].top[min(at[q] + step, kMaxTop) - 1];
-#pragma unroll
-          for (int q = 0; q < kMaxSplit; ++q) {
-            const bool first = (o[q].v > k.v) | ((o[q].v == k.v) & (o[q].id < k.id));
-            at[q] += (first & (q < split) & (at[q] + step <= n)) ? step : 0;
-          }
-        }
-        int place = 0;
-#pragma unroll
-        for (int q = 0; q < kMaxSplit; ++q) place += at[q];
-        if (k.id >= 0 && place < n) sm.mine.top[place] = k;
-      }
+      place_keys<kWarps>(pk.cand, sm.ncand, n, [&](int place, int i) { sm.mine.top[place] = pk.cand[i]; });
       __syncthreads();
     }
   }
@@ -776,7 +803,8 @@ cudaError_t launch(const moe_token_logprobs_args& a, int split, cudaStream_t st)
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   if (cfg.dynamicSmemBytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.dynamicSmemBytes);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.dynamicSmemBytes);
     if (e) return e;
   }
   return cudaLaunchKernelEx(&cfg, kernel, a, parts);
@@ -794,7 +822,8 @@ cudaError_t launch_nt(const moe_token_logprobs_args& a, int split, cudaStream_t 
 
 template <int TYPE>
 cudaError_t launch_type(const moe_token_logprobs_args& a, int split, int sms, cudaStream_t st) {
-  // Measured in graphs, bf16, one target, 5 alternatives where not said.
+  // Measured in graphs, bf16, one target, 5 alternatives where not said, before
+  // rows' ends were shortened once more.
   // Blocks of 128 threads have shorter ends and leave an SM more rows to cover
   // them with, while a winning group, twice as long, costs more to read again:
   // 4096 rows of 8192 30.4 us against 44.8 with 256 threads, of 32000 56.5 / 73.2,

@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       for (int i = 0; i < kBatch; ++i)
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-          raw[i][q] = cb + tid + i * kThreads < c1 ? __ldg(p + i * kThreads * Q + q) : make_uint4(fill, fill, fill, fill);
+          raw[i][q] =
+              cb + tid + i * kThreads < c1 ? __ldg(p + i * kThreads * Q + q) : make_uint4(fill, fill, fill, fill);
     }
   };
   auto copy = [&](int slot, int cb) {  // the same into the ring
@@ -879,17 +880,23 @@ extern "C" int moe_token_logprobs(const moe_token_logprobs_args* args, void* str
 
   if (!a.top_ids && !a.top_logprobs) a.top_n = 0;
 
-  // Long rows, and few of them: parts of at least 32 KB, up to two blocks an SM.
-  // Joining the parts costs some 2 us.  One row of 131072 bf16: 14.9 us whole, 8.7
-  // in 8 parts; 152 of them 15.2 whole, 14.2 in 2; one row of 32000 7.7 whole, 8.8
-  // in 2; 64 rows of 50001 bf16 9.5 whole, 9.9 in 4, fp32 17.5 whole, 13.1 in 4.
+  // Long rows, and few of them, are read in parts.  Parts of at least 32 KB of
+  // rows of 128 KB, up to two blocks an SM: 152 rows of 131072 bf16 14.2 us in 2
+  // parts, 15.2 whole (when rows' ends took longer: now 12.5 in 2); 152 rows of
+  // 32000 (64 KB) would take 8.6 in 2 parts, 7.8 whole.  Parts down to 16 KB of
+  // rows of 96 KB while they leave SMs idle: one row of 50001 bf16 7.8 us in 4
+  // parts, 9.0 whole; 32 of them 8.0 / 9.3; but 150 of them 10.1 in 2, 9.5 whole.
   int dev = 0, sms = 0, split = 1;
   cudaError_t e = cudaGetDevice(&dev);
   if (!e) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e) return reportf(MOE_ERR_CUDA, "moe_token_logprobs: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
   const int64_t row_bytes = static_cast<int64_t>(a.vocab) * elem_size(a.logits_type);
-  if (row_bytes >= 4 * kPartBytes)
-    while (split < kMaxSplit && static_cast<int64_t>(a.rows) * split <= sms && row_bytes / (2 * split) >= kPartBytes) split *= 2;
+  for (; split < kMaxSplit; split *= 2) {
+    const int64_t part = row_bytes / (2 * split), blocks = static_cast<int64_t>(a.rows) * split;
+    const bool wide = row_bytes >= 4 * kPartBytes && part >= kPartBytes && blocks <= sms;
+    const bool few = row_bytes >= 3 * kPartBytes && part >= kPartBytes / 2 && blocks <= sms / 2;
+    if (!wide && !few) break;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.logits_type == MOE_BF16)
     e = launch_type<MOE_BF16>(a, split, sms, st);

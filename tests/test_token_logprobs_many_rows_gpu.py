@@ -1,5 +1,6 @@
 """moe_token_logprobs on more rows than four an SM, where blocks of 128 threads
-or copies through shared memory read a row, against its definition in 64 bits.
+or copies through shared memory read a row, and in small parts of rows, against
+its definition in 64 bits.
 
 Few different rows are repeated, so that the definition is worked out once a
 row.  The tolerance is the one derived for fewer rows, with the sequence of a
@@ -131,3 +132,19 @@ def test_repeats_give_the_same_bits():
     a, b = (token_logprobs(l, tg, top_n=10) for _ in range(2))
     for k in a:
         assert torch.equal(a[k], b[k]), k
+
+
+@pytest.mark.parametrize("T,V,dtype", [(1, 49152, BF), (37, 50001, HF), (38, 50001, BF), (76, 50001, BF), (77, 50001, BF),
+                                       (2, 24577, F32), (75, 33000, F32), (76, 70003, BF), (3, 131072, BF)])
+def test_parts_of_16_kb(T, V, dtype):
+    """Rows in 2, 4 or 8 parts, around the counts of rows where that changes."""
+    l, tg = rnd(T, V, dtype, seed=V), some_targets(T, V, 2)
+    l[0, V // 3:] = -INF
+    ref = reference(l, tg.cpu().numpy(), 32, 1.0)
+    out = token_logprobs(l, tg, top_n=32)
+    ent = ref["entropy"]
+    e = 2.0 ** -24 * (8 * -(-V // 4096) + 8 + 20 + 4 * (ent + 56))
+    near(out["entropy"], ent, 3 * e * (57 + ent), "entropy")
+    near(out["lse"], ref["lse"], e + 2.0 ** -22 * (np.abs(ref["lse"]) + ent + 1), "lse")
+    assert np.array_equal(out["rank"].cpu().numpy(), ref["rank"])
+    assert np.array_equal(out["top_ids"].cpu().numpy(), ref["top_ids"])

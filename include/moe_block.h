@@ -94,7 +94,7 @@ int moe_block_norm(const moe_block_norm_args *args, void *stream);
  * and entropy 0.  A target outside [0, vocab) gives log probability -inf and
  * rank 0.  A row with a NaN or a z of +inf gives NaN for lse, entropy and the
  * log probabilities of its tokens; NaNs are never listed and come before no
- * target. */
+ * target, and a target whose logit is NaN has rank 1. */
 typedef struct moe_token_logprobs_args {
     const void *logits;
     const int32_t *targets;

@@ -100,6 +100,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ float next_up(float v) {
   const uint32_t u = __float_as_uint(v);
   if (v == 0.0f) return __uint_as_float(1u);
+  if (v != v) return v;  // NaN stays NaN
   return __uint_as_float(v > 0.0f ? u + 1 : u - 1);
 }
 __device__ __forceinline__ uint32_t next_up16(uint32_t bits, uint32_t inf) {

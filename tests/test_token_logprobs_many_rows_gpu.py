@@ -148,3 +148,31 @@ def test_parts_of_16_kb(T, V, dtype):
     near(out["lse"], ref["lse"], e + 2.0 ** -22 * (np.abs(ref["lse"]) + ent + 1), "lse")
     assert np.array_equal(out["rank"].cpu().numpy(), ref["rank"])
     assert np.array_equal(out["top_ids"].cpu().numpy(), ref["top_ids"])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T,V", [(3, 5001), (2, 131072), (700, 5001), (700, 20001)])
+def test_a_nan_target_has_rank_1(T, V, dtype):
+    l = rnd(T, V, dtype)
+    tg = some_targets(T, V, 2)
+    tg[:, 1] = (tg[:, 0] + 1) % V
+    rows = torch.arange(T, device=DEV)
+    l[rows, tg[:, 0].long()] = float("nan")
+    out = token_logprobs(l, tg, top_n=2)
+    other = l[rows, tg[:, 1].long()].float()[:, None]
+    above = (l.float() > other).sum(1)
+    assert (out["rank"][:, 0] == 1).all()
+    assert (out["rank"][:, 1] > above).all()            # NaNs come before no target
+    assert out["logprob"].isnan().all() and not (out["top_ids"] == tg[:, :1]).any()
+
+
+@pytest.mark.parametrize("bits", [0x7F800001, 0xFF800001, 0x7FFFFFFF, 0xFFFFFFFF])
+def test_any_nan_target_has_rank_1(bits):
+    """NaNs next to the infinities too: no step from their bits may reach them."""
+    l = rnd(4, 5001, F32)
+    l[1] = INF
+    l[2] = -INF
+    tg = some_targets(4, 5001, 1)
+    l.view(torch.int32)[torch.arange(4, device=DEV), tg[:, 0].long()] = bits - (1 << 32) if bits >> 31 else bits
+    assert l.isnan().sum() == 4
+    assert (token_logprobs(l, tg)["rank"] == 1).all()

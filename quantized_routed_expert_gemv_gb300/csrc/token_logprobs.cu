@@ -125,7 +125,8 @@ struct Sums {
       A.x = fmaf(S.x, d, A.x) * e, A.y = fmaf(S.y, d, A.y) * e;
       S.x *= e, S.y *= e;
       nr = make_float2(-z, -z);
-      limit = m + kRefSlack / u;
+      // rounded down: to nearest, the next float above a large m could pass
+      limit = __fadd_rd(m, kRefSlack / u);
     }
   }
   // Two logits (already bounded below unless CLAMP); uu is u twice.

@@ -8,11 +8,19 @@
 //     logprob_t = ln 2 (u l_t - r - log2 S).
 // One fma gives u l - r with a single rounding.  Every thread keeps its own
 // (r, S, A) in fp32 and moves r only when a logit lies more than kRefSlack
-// powers of two above it, so the usual step has no rescaling.  Values whose
-// u l is below -2^99 (masks of the type's lowest value) add 0; a row that
-// has nothing else, or whose u l overflows upwards, has all of its
-// probability on the logits equal to its largest (neighbouring values are
-// more than 2^75 powers of two apart there), which are counted instead.
+// powers of two above it, so the usual step has no rescaling.
+//
+// r is a rounded product itself, so the term of the logit that it came from is
+// 2^(u l - r), up to 2^64 where |r| < 2^31 and without bound above.  So from
+// |u l| = 2^31 on nothing is summed: values there are 128 powers of two and
+// more from their neighbours, whatever the type.  Those below -2^31 (masks such
+// as -1e10 or the type's lowest value) add 0, and a row whose largest is that
+// far from 0 has all of its probability on the logits equal to it, which are
+// counted instead.
+//
+// No sum overflows: a term is at most 2^88 (kRefSlack and a residual of 2^3
+// below |r| = 2^28, 2^64 above, where r moves with every larger logit), there
+// are at most 2^24 of them, and A has a factor of 2^14 at most.
 //
 // Top tokens: a thread's running maximum is the best of the group of tokens
 // that thread visited.  Any token of the row's top n lies in one of the n
@@ -66,7 +74,8 @@ constexpr int64_t kPartBytes = 32 * 1024;  // of a row, at least, in a part
 constexpr int kCand = 1024;            // candidate buffer of the top selection
 constexpr float kRefSlack = 80.0f;     // powers of two a logit may lie above the reference
 constexpr float kUnset = 3.402823466e38f;
-constexpr float kFloor = -6.338253e29f;  // -2^99: what lies below adds no probability
+constexpr float kSlackBelow = 268435456.0f;  // 2^28: |r| from which r moves with every larger logit
+constexpr float kFar = 2147483648.0f;  // 2^31: |u l| from which logits are not summed
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Key {  // order: value descending, id ascending; id < 0: none
@@ -114,7 +123,7 @@ __device__ __forceinline__ uint32_t next_up16(uint32_t bits, uint32_t inf) {
 struct Sums {
   float2 nr = {-kUnset, -kUnset}, S = {0.0f, 0.0f}, A = {0.0f, 0.0f};
   float limit;
-  __device__ __forceinline__ explicit Sums(float u) : limit(kFloor / u) {}
+  __device__ __forceinline__ explicit Sums(float u) : limit(-kFar / u) {}
 
   // Makes room for logits up to m.
   __device__ __forceinline__ void reach(float m, float u) {
@@ -126,7 +135,7 @@ struct Sums {
       S.x *= e, S.y *= e;
       nr = make_float2(-z, -z);
       // rounded down: to nearest, the next float above a large m could pass
-      limit = __fadd_rd(m, kRefSlack / u);
+      limit = fabsf(z) < kSlackBelow ? __fadd_rd(m, kRefSlack / u) : m;
     }
   }
   // Two logits (already bounded below unless CLAMP); uu is u twice.
@@ -526,8 +535,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   Sums sums(u);
   float best = -INFINITY;
   int best_c = -1;
-  // bf16 logits are bounded below before they are widened, so that a value
-  // under the floor gives 0 * finite in A
+  // bf16 logits are bounded below before they are widened, so that a value far
+  // under the reference gives 0 * finite in A
   const float bound = __bfloat162float(__float2bfloat16_rn(fmaxf(-1.2676506e30f / u, -3.3895314e38f)));
   const __nv_bfloat162 bound2 = __float2bfloat162_rn(bound);
   const float2 uu = make_float2(u, u);
@@ -737,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const bool empty = (S == 0.0f && top_v == -INFINITY) || top_v * a.scale == -INFINITY;
   // all probability on the largest logits: count them
   const bool flat = !empty && top_v > -INFINITY && top_v < INFINITY &&
-                    (S == 0.0f || fabsf(top_v * u) > 1e38f || (TYPE == MOE_BF16 && top_v <= bound));
+                    (S == 0.0f || fabsf(top_v * u) >= kFar);
   bool bad = top_v == INFINITY || top_v * a.scale == INFINITY || (!flat && S != S);
   __syncthreads();
   if (flat) {

@@ -410,7 +410,10 @@ cudaError_t launch_stream(const moe_block_norm_args& a, int num_sms, cudaStream_
   const int fit = kStreamThreads / threads, teams = fit < kMaxTeams ? fit : kMaxTeams;
   const int smem = 2 * threads * 16 * static_cast<int>(sizeof(float));
   auto kernel = block_norm_stream_kernel<Y32, H32>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the widest rows' size whatever this call's: the attribute is the process's,
+  // and another thread's call may lie between this line and the launch
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             2 * kStreamHidden * static_cast<int>(sizeof(float)));
   if (e) return e;
   const int64_t blocks = (static_cast<int64_t>(a.rows) + teams - 1) / teams;
   kernel<<<static_cast<unsigned>(blocks < num_sms ? blocks : num_sms), threads * teams, smem, st>>>(

@@ -62,8 +62,9 @@ int moe_fp8_check(const moe_fp8 *w, void *workspace, void *stream);
 
 /* Quantises weights: device [n][ld_w] of type w_type to codes and scales as
  * moe_fp8_open takes them, scale = max |w| / 448 of each 128 x 128 block (1
- * for a block of zeros), rounded to nearest, ties to even.  Bytes past k in a
- * row of codes are set to 0.  NaNs and infinities are outside the contract. */
+ * for a block of zeros, or of values so small that this quotient is 0: their
+ * codes are 0), rounded to nearest, ties to even.  Bytes past k in a row of
+ * codes are set to 0.  NaNs and infinities are outside the contract. */
 int moe_fp8_quantize_weights(const void *weights, int32_t w_type, int64_t ld_w, int32_t n, int32_t k,
                              uint8_t *codes, int64_t ld_codes, float *scales, void *stream);
 

@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, in
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, wmax[i]);
-  const float s = m ? __uint_as_float(m) / 448.0f : 1.0f;
+  // 0 if there is nothing, or nothing that the quotient can tell from it (up to
+  // 224 units of 2^-149): such a block's codes are zeros
+  const float quotient = __uint_as_float(m) / 448.0f, s = quotient > 0.0f ? quotient : 1.0f;
   if (threadIdx.x == 0) scales[static_cast<size_t>(nb) * gridDim.x + kb] = s;
   for (int i = threadIdx.x; i < kBlk * kBlk; i += 256) {
     const int r = nb * kBlk + i / kBlk;

@@ -219,6 +219,15 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, in
     const float v = c < k ? load_elem(w, type, r * ld + c) / s : 0.0f;
     codes[r * ldc + c] = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
   }
+  // the last blocks of a row: zeros from their end to the row's, 16 bytes at a
+  // time (codes and ldc are multiples of 16)
+  const int64_t end = static_cast<int64_t>(kb + 1) * kBlk;
+  if (kb == static_cast<int>(gridDim.x) - 1 && end < ldc) {
+    const int64_t pieces = (ldc - end) / 16;
+    for (int r = nb * kBlk; r < min(n, (nb + 1) * kBlk); ++r)
+      for (int64_t i = threadIdx.x; i < pieces; i += 256)
+        *reinterpret_cast<uint4*>(codes + r * ldc + end + 16 * i) = make_uint4(0, 0, 0, 0);
+  }
 }
 
 // ---- tensor-core helpers -------------------------------------------------------------

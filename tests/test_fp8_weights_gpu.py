@@ -28,3 +28,19 @@ def test_blocks_of_the_smallest_values(most):
     assert not ((lin.codes[:, :k] & 127) == 127).any()
     assert (lin.scales > 0).all() and torch.isfinite(lin.scales).all()
     assert (out.abs() <= 2.0 * k * most * 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("n,k,ld", [(3, 100, 112), (130, 100, 128), (130, 100, 144), (5, 128, 256), (300, 300, 1040),
+                                    (129, 257, 4096), (1, 1, 16), (2, 384, 384)])
+def test_bytes_past_k_are_zero(n, k, ld):
+    """Whatever the width of a row of codes, and nothing after the last row."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    w = torch.randn(n, k, generator=g, device=DEV)
+    buf = torch.full((n * ld + 64,), 0xAB, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(-(-n // 128), -(-k // 128), device=DEV)
+    moe.moe_fp8_quantize_weights(w.data_ptr(), moe.MOE_F32, k, n, k, buf.data_ptr(), ld, scales.data_ptr())
+    torch.cuda.synchronize()
+    codes = buf[:n * ld].view(n, ld)
+    assert (codes[:, k:] == 0).all()
+    assert (buf[n * ld:] == 0xAB).all()
+    assert torch.equal(codes[:, :k], Fp8Linear.from_weights(w, 1).codes[:, :k])

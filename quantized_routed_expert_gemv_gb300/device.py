@@ -34,11 +34,29 @@ def _stream(device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index if device.index is not None else torch.cuda.current_device())
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Leading dimension of a matrix whose rows are contiguous."""
+def _refuse(where: str, what: str):
+    raise moe.MoEError(moe.MOE_ERR_ARG, where, what)
+
+
+def _type(t: torch.Tensor, where: str) -> int:
+    """The element type's code."""
+    code = _ELEM_TYPE.get(t.dtype)
+    if code is None:
+        _refuse(where, f"elements of type {t.dtype}")
+    return code
+
+
+def _matrix(t: torch.Tensor, shape, where: str, name: str) -> None:
+    """The library gets addresses only, so shapes are compared here."""
+    if t.shape != shape:
+        _refuse(where, f"{name} has the shape {tuple(t.shape)}, not {tuple(shape)}")
+
+
+def _ld(t: torch.Tensor, rows: int, cols: int, where: str) -> int:
+    """Leading dimension of a [rows][cols] matrix whose rows are contiguous."""
     ld, step = t.stride()
-    rows, cols = t.shape
-    assert step == 1 or cols == 1, "rows must be contiguous"
+    if step != 1 and cols != 1:
+        _refuse(where, f"rows must be contiguous, their elements are {step} apart")
     return ld if rows > 1 else max(ld, cols)
 
 
@@ -47,33 +65,46 @@ def block_norm(y=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=Tru
     """moe_block_norm of device tensors: y and h [rows][hidden] (either may be
     None); gate a tensor that broadcasts to [rows][hidden]; weights
     [hidden].  Returns (h', x), allocated unless given."""
+    me = "block_norm"
     like = h if h is not None else y
-    rows, hidden = like.shape
+    if like is None or like.dim() != 2:
+        _refuse(me, "y or h must be given, a matrix [rows][hidden]")
+    shape = rows, hidden = like.shape
     if h_out is None:
         h_out = torch.empty(rows, hidden, dtype=like.dtype, device=like.device)
     if x_out is None:
         x_out = torch.empty(rows, hidden, dtype=x_type, device=like.device)
+    _matrix(h_out, shape, me, "h_out")
+    _matrix(x_out, shape, me, "x_out")
     a = moe.moe_block_norm_args()
-    a.rows, a.hidden, a.h_type = rows, hidden, _ELEM_TYPE[h_out.dtype]
+    a.rows, a.hidden, a.h_type = rows, hidden, _type(h_out, me)
     if y is not None:
-        a.y, a.ld_y, a.y_type = y.data_ptr(), _ld(y), _ELEM_TYPE[y.dtype]
+        _matrix(y, shape, me, "y")
+        a.y, a.ld_y, a.y_type = y.data_ptr(), _ld(y, rows, hidden, me), _type(y, me)
     if h is not None:
-        assert h.dtype == h_out.dtype
-        a.h, a.ld_h = h.data_ptr(), _ld(h)
+        if h.dtype != h_out.dtype:
+            _refuse(me, f"h is of type {h.dtype}, h_out of {h_out.dtype}")
+        a.h, a.ld_h = h.data_ptr(), _ld(h, rows, hidden, me)
     if gate is not None:
-        g = gate.expand(rows, hidden)
-        a.gate, a.gate_type = g.data_ptr(), _ELEM_TYPE[g.dtype]
+        try:
+            g = gate.expand(rows, hidden)
+        except RuntimeError as e:
+            _refuse(me, f"gate: {e}")
+        a.gate, a.gate_type = g.data_ptr(), _type(g, me)
         a.ld_gate_row, a.ld_gate_col = (g.stride(0) if rows > 1 else 0), (g.stride(1) if hidden > 1 else 0)
     for name, w in (("w_post", w_post), ("w_pre", w_pre)):
         if w is not None:
-            assert w.shape == (hidden,) and w.is_contiguous()
+            _matrix(w, (hidden,), me, name)
+            if not w.is_contiguous():
+                _refuse(me, f"{name} must be contiguous")
             setattr(a, name, w.data_ptr())
-            a.w_type = _ELEM_TYPE[w.dtype]
-    assert w_post is None or w_pre is None or w_post.dtype == w_pre.dtype
+            a.w_type = _type(w, me)
+    if w_post is not None and w_pre is not None and w_post.dtype != w_pre.dtype:
+        _refuse(me, f"w_post is of type {w_post.dtype}, w_pre of {w_pre.dtype}")
     a.post_norm, a.pre_norm = int(post_norm), int(pre_norm)
     a.w_add, a.eps, a.residual_scale = w_add, eps, residual_scale
-    a.h_out, a.ld_h_out = h_out.data_ptr(), _ld(h_out)
-    a.x_out, a.ld_x_out, a.x_type = x_out.data_ptr(), _ld(x_out), _ELEM_TYPE[x_out.dtype]
+    a.h_out, a.ld_h_out = h_out.data_ptr(), _ld(h_out, rows, hidden, me)
+    a.x_out, a.ld_x_out, a.x_type = x_out.data_ptr(), _ld(x_out, rows, hidden, me), _type(x_out, me)
     moe.moe_block_norm(a, _stream(like.device, stream))
     return h_out, x_out
 
@@ -84,16 +115,20 @@ def token_logprobs(logits: torch.Tensor, targets=None, top_n: int = 0, scale: fl
     or [rows][n_targets].  Returns device tensors: lse, entropy [rows];
     logprob and rank in the targets' shape; top_ids, top_logprobs
     [rows][top_n]."""
+    me = "token_logprobs"
+    if logits.dim() != 2:
+        _refuse(me, "logits must be a matrix [rows][vocab]")
     rows, vocab = logits.shape
     dev = logits.device
     a = moe.moe_token_logprobs_args()
-    a.logits, a.ld_logits, a.logits_type = logits.data_ptr(), _ld(logits), _ELEM_TYPE[logits.dtype]
+    a.logits, a.ld_logits, a.logits_type = logits.data_ptr(), _ld(logits, rows, vocab, me), _type(logits, me)
     a.rows, a.vocab, a.top_n, a.scale = rows, vocab, top_n, scale
     out = {"lse": torch.empty(rows, dtype=torch.float32, device=dev),
            "entropy": torch.empty(rows, dtype=torch.float32, device=dev)}
     a.lse, a.entropy = out["lse"].data_ptr(), out["entropy"].data_ptr()
     if targets is not None:
-        assert targets.dtype == torch.int32 and targets.is_contiguous() and targets.shape[0] == rows
+        if targets.dtype != torch.int32 or not targets.is_contiguous() or targets.dim() < 1 or targets.shape[0] != rows:
+            _refuse(me, f"targets must be contiguous int32, {rows} or {rows} x n_targets of them")
         a.targets, a.n_targets = targets.data_ptr(), targets.numel() // max(rows, 1)
         out["logprob"] = torch.empty(targets.shape, dtype=torch.float32, device=dev)
         a.target_logprobs = out["logprob"].data_ptr()
@@ -115,11 +150,16 @@ class Fp8Linear:
     max_rows rows."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, k: int, max_rows: int, stream=None):
+        me = "Fp8Linear"
+        self.handle = None
+        if codes.dim() != 2 or codes.element_size() != 1 or codes.shape[1] < k:
+            _refuse(me, f"codes must be bytes [n][at least {k}]")
         self.codes, self.scales, self.k, self.n = codes, scales, k, codes.shape[0]
         self.max_rows = max_rows
-        assert scales.is_contiguous() and scales.dtype == torch.float32
-        assert scales.shape == (-(-self.n // 128), -(-k // 128))
-        self.handle = moe.moe_fp8_open(self.n, k, codes.data_ptr(), _ld(codes), scales.data_ptr())
+        _matrix(scales, (-(-self.n // 128), -(-k // 128)), me, "scales")
+        if not scales.is_contiguous() or scales.dtype != torch.float32:
+            _refuse(me, "scales must be contiguous float32")
+        self.handle = moe.moe_fp8_open(self.n, k, codes.data_ptr(), _ld(codes, self.n, codes.shape[1], me), scales.data_ptr())
         self.ws_bytes = moe.moe_fp8_workspace_bytes(self.handle, max_rows)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=codes.device)
         self.ws_ptr = self.ws.data_ptr()
@@ -128,22 +168,30 @@ class Fp8Linear:
     @classmethod
     def from_weights(cls, weights: torch.Tensor, max_rows: int, stream=None):
         """Quantises device weights [n][k] (moe_fp8_quantize_weights)."""
+        me = "Fp8Linear.from_weights"
+        if weights.dim() != 2:
+            _refuse(me, "weights must be a matrix [n][k]")
         n, k = weights.shape
         ld = -(-k // 16) * 16
         codes = torch.empty(n, ld, dtype=torch.uint8, device=weights.device)
         scales = torch.empty(-(-n // 128), -(-k // 128), dtype=torch.float32, device=weights.device)
-        moe.moe_fp8_quantize_weights(weights.data_ptr(), _ELEM_TYPE[weights.dtype], _ld(weights), n, k,
+        moe.moe_fp8_quantize_weights(weights.data_ptr(), _type(weights, me), _ld(weights, n, k, me), n, k,
                                      codes.data_ptr(), ld, scales.data_ptr(), _stream(weights.device, stream))
         return cls(codes, scales, k, max_rows, stream)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, out_type=torch.bfloat16, stream=None):
         """x [rows][k] -> [rows][n]."""
-        rows, k = x.shape
-        assert k == self.k
+        me = "Fp8Linear"
+        shape, n = x.shape, self.n
+        if len(shape) != 2 or shape[1] != self.k:
+            _refuse(me, f"x has the shape {tuple(shape)}, not [rows][{self.k}]")
+        rows, k = shape
         if out is None:
-            out = torch.empty(rows, self.n, dtype=out_type, device=x.device)
-        moe.moe_fp8_linear(self.handle, x.data_ptr(), _ELEM_TYPE[x.dtype], _ld(x), rows, out.data_ptr(),
-                           _ELEM_TYPE[out.dtype], _ld(out), self.ws_ptr, self.ws_bytes, _stream(x.device, stream))
+            out = torch.empty(rows, n, dtype=out_type, device=x.device)
+        elif out.shape != (rows, n):
+            _refuse(me, f"out has the shape {tuple(out.shape)}, not {rows, n}")
+        moe.moe_fp8_linear(self.handle, x.data_ptr(), _type(x, me), _ld(x, rows, k, me), rows, out.data_ptr(),
+                           _type(out, me), _ld(out, rows, n, me), self.ws_ptr, self.ws_bytes, _stream(x.device, stream))
         return out
 
     def check(self, stream=None) -> int:

@@ -52,6 +52,16 @@ def _matrix(t: torch.Tensor, shape, where: str, name: str) -> None:
         _refuse(where, f"{name} has the shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
+def _on_gpu(where: str, index: int, *tensors) -> None:
+    """All of them (None: no tensor) on the GPU `index`, and that the current
+    device, on which the library launches."""
+    for t in tensors:
+        if t is not None and (index < 0 or t.get_device() != index):
+            _refuse(where, f"a tensor is on {t.device}; all must be on the same GPU")
+    if index != torch.cuda.current_device():
+        _refuse(where, f"the tensors' device {index} must be the current device")
+
+
 def _ld(t: torch.Tensor, rows: int, cols: int, where: str) -> int:
     """Leading dimension of a [rows][cols] matrix whose rows are contiguous."""
     ld, step = t.stride()
@@ -105,6 +115,8 @@ def block_norm(y=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=Tru
     a.w_add, a.eps, a.residual_scale = w_add, eps, residual_scale
     a.h_out, a.ld_h_out = h_out.data_ptr(), _ld(h_out, rows, hidden, me)
     a.x_out, a.ld_x_out, a.x_type = x_out.data_ptr(), _ld(x_out, rows, hidden, me), _type(x_out, me)
+    index = like.get_device()
+    _on_gpu(me, index, like, y, gate, w_post, w_pre, h_out, x_out)
     moe.moe_block_norm(a, _stream(like.device, stream))
     return h_out, x_out
 
@@ -119,7 +131,7 @@ def token_logprobs(logits: torch.Tensor, targets=None, top_n: int = 0, scale: fl
     if logits.dim() != 2:
         _refuse(me, "logits must be a matrix [rows][vocab]")
     rows, vocab = logits.shape
-    dev = logits.device
+    dev, index = logits.device, logits.get_device()
     a = moe.moe_token_logprobs_args()
     a.logits, a.ld_logits, a.logits_type = logits.data_ptr(), _ld(logits, rows, vocab, me), _type(logits, me)
     a.rows, a.vocab, a.top_n, a.scale = rows, vocab, top_n, scale
@@ -139,6 +151,7 @@ def token_logprobs(logits: torch.Tensor, targets=None, top_n: int = 0, scale: fl
         out["top_ids"] = torch.empty(rows, top_n, dtype=torch.int32, device=dev)
         out["top_logprobs"] = torch.empty(rows, top_n, dtype=torch.float32, device=dev)
         a.top_ids, a.top_logprobs = out["top_ids"].data_ptr(), out["top_logprobs"].data_ptr()
+    _on_gpu(me, index, logits, targets)
     moe.moe_token_logprobs(a, _stream(dev, stream))
     return out
 
@@ -159,6 +172,8 @@ class Fp8Linear:
         _matrix(scales, (-(-self.n // 128), -(-k // 128)), me, "scales")
         if not scales.is_contiguous() or scales.dtype != torch.float32:
             _refuse(me, "scales must be contiguous float32")
+        self.index = codes.get_device()
+        _on_gpu(me, self.index, codes, scales)
         self.handle = moe.moe_fp8_open(self.n, k, codes.data_ptr(), _ld(codes, self.n, codes.shape[1], me), scales.data_ptr())
         self.ws_bytes = moe.moe_fp8_workspace_bytes(self.handle, max_rows)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=codes.device)
@@ -173,10 +188,12 @@ class Fp8Linear:
             _refuse(me, "weights must be a matrix [n][k]")
         n, k = weights.shape
         ld = -(-k // 16) * 16
+        w_type, ld_w, index = _type(weights, me), _ld(weights, n, k, me), weights.get_device()
+        _on_gpu(me, index, weights)
         codes = torch.empty(n, ld, dtype=torch.uint8, device=weights.device)
         scales = torch.empty(-(-n // 128), -(-k // 128), dtype=torch.float32, device=weights.device)
-        moe.moe_fp8_quantize_weights(weights.data_ptr(), _type(weights, me), _ld(weights, n, k, me), n, k,
-                                     codes.data_ptr(), ld, scales.data_ptr(), _stream(weights.device, stream))
+        moe.moe_fp8_quantize_weights(weights.data_ptr(), w_type, ld_w, n, k, codes.data_ptr(), ld, scales.data_ptr(),
+                                     _stream(weights.device, stream))
         return cls(codes, scales, k, max_rows, stream)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, out_type=torch.bfloat16, stream=None):
@@ -190,6 +207,8 @@ class Fp8Linear:
             out = torch.empty(rows, n, dtype=out_type, device=x.device)
         elif out.shape != (rows, n):
             _refuse(me, f"out has the shape {tuple(out.shape)}, not {rows, n}")
+        if x.get_device() != self.index or out.get_device() != self.index:
+            _on_gpu(me, self.index, x, out)
         moe.moe_fp8_linear(self.handle, x.data_ptr(), _type(x, me), _ld(x, rows, k, me), rows, out.data_ptr(),
                            _type(out, me), _ld(out, rows, n, me), self.ws_ptr, self.ws_bytes, _stream(x.device, stream))
         return out

@@ -1,6 +1,7 @@
 """What the tensor wrappers of device.py refuse before the library, which sees
 addresses only, could read or write past a tensor.  The library is replaced by
-a recorder, so nothing runs and no GPU is needed."""
+a recorder, so nothing runs and no GPU is needed; tensors of the CPU stand for a
+GPU's except where that is what is refused."""
 import pytest
 import torch
 
@@ -13,6 +14,7 @@ BF = torch.bfloat16
 def calls(monkeypatch):
     """The names of the library calls that a wrapper got through to."""
     got = []
+    monkeypatch.setattr(device, "_on_gpu", lambda *a: None, raising=False)
 
     def record(name, value=None):
         monkeypatch.setattr(moe, name, lambda *a: got.append(name) or value)
@@ -75,3 +77,33 @@ def test_fp8_weights(calls, kw, word):
 def test_fp8_linear(calls, x, out, word):
     lin = device.Fp8Linear(torch.zeros(200, 112, dtype=torch.uint8), torch.zeros(2, 1), 100, 8, stream=0)
     refused(calls, word, lin, x, out)
+
+
+def test_tensors_of_the_cpu(calls, monkeypatch):
+    lin = device.Fp8Linear(torch.zeros(200, 112, dtype=torch.uint8), torch.zeros(2, 1), 100, 8, stream=0)
+    monkeypatch.undo()
+    for name in ("moe_block_norm", "moe_token_logprobs", "moe_fp8_linear", "moe_fp8_open", "moe_fp8_quantize_weights"):
+        monkeypatch.setattr(moe, name, lambda *a, name=name: calls.append(name))
+    lin.index = 0
+    refused(calls, "cpu", device.block_norm, m(4, 64), m(4, 64))
+    refused(calls, "cpu", device.token_logprobs, m(4, 100))
+    refused(calls, "cpu", device.Fp8Linear, lin.codes, lin.scales, 100, 8)
+    refused(calls, "cpu", device.Fp8Linear.from_weights, m(4, 64), 8)
+    refused(calls, "cpu", lin, m(4, 100), m(4, 200))
+
+
+@pytest.mark.gpu
+def test_one_tensor_of_the_cpu(calls, monkeypatch):
+    c = lambda *s, dtype=BF: torch.zeros(*s, dtype=dtype, device="cuda:0")  # noqa: E731
+    lin = device.Fp8Linear(c(200, 112, dtype=torch.uint8), c(2, 1, dtype=torch.float32), 100, 8, stream=0)
+    monkeypatch.undo()
+    for name in ("moe_block_norm", "moe_token_logprobs", "moe_fp8_linear", "moe_fp8_open"):
+        monkeypatch.setattr(moe, name, lambda *a, name=name: calls.append(name))
+    lin.index = 0
+    for kw in (dict(y=m(4, 64)), dict(h=m(4, 64)), dict(gate=m(1, 64)), dict(w_post=m(1, 64)[0]), dict(w_pre=m(1, 64)[0]),
+               dict(h_out=m(4, 64)), dict(x_out=m(4, 64))):
+        refused(calls, "cpu", device.block_norm, **{**dict(y=c(4, 64), h=c(4, 64)), **kw})
+    refused(calls, "cpu", device.token_logprobs, c(4, 100), torch.zeros(4, dtype=torch.int32))
+    refused(calls, "cpu", device.Fp8Linear, lin.codes, lin.scales.cpu(), 100, 8)
+    refused(calls, "cpu", lin, m(4, 100), c(4, 200))
+    refused(calls, "cpu", lin, c(4, 100), m(4, 200))

@@ -34,15 +34,39 @@ def _stream(device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index if device.index is not None else torch.cuda.current_device())
 
 
+# Calls with stream= run on that stream, given as a raw handle.  The caller has
+# it wait for the inputs, keeps them until the work is done, and waits before it
+# reads the outputs.  What a wrapper allocates is safe on both streams:
+
+def _other(device, stream):
+    """The stream given to a call as torch has it; None if it is the current one."""
+    if stream is None or stream == _stream(device, None):
+        return None
+    return torch.cuda.ExternalStream(stream, device)
+
+
+def _empty(device, other, dtype, *shape) -> torch.Tensor:
+    """Memory that a call on the stream `other` writes.  It is that stream's, as
+    work queued on the current one may still use what the current one would
+    reuse; and the current one's too, so that it is not reused once freed
+    before work queued there by then is done."""
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _refuse(where: str, what: str):
     raise moe.MoEError(moe.MOE_ERR_ARG, where, what)
 
 
-def _type(t: torch.Tensor, where: str) -> int:
+def _type(dtype: torch.dtype, where: str) -> int:
     """The element type's code."""
-    code = _ELEM_TYPE.get(t.dtype)
+    code = _ELEM_TYPE.get(dtype)
     if code is None:
-        _refuse(where, f"elements of type {t.dtype}")
+        _refuse(where, f"elements of type {dtype}")
     return code
 
 
@@ -80,19 +104,15 @@ def block_norm(y=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=Tru
     if like is None or like.dim() != 2:
         _refuse(me, "y or h must be given, a matrix [rows][hidden]")
     shape = rows, hidden = like.shape
-    if h_out is None:
-        h_out = torch.empty(rows, hidden, dtype=like.dtype, device=like.device)
-    if x_out is None:
-        x_out = torch.empty(rows, hidden, dtype=x_type, device=like.device)
-    _matrix(h_out, shape, me, "h_out")
-    _matrix(x_out, shape, me, "x_out")
+    dev, index = like.device, like.get_device()
     a = moe.moe_block_norm_args()
-    a.rows, a.hidden, a.h_type = rows, hidden, _type(h_out, me)
+    a.rows, a.hidden, a.h_type = rows, hidden, _type(like.dtype if h_out is None else h_out.dtype, me)
+    a.x_type = _type(x_type if x_out is None else x_out.dtype, me)
     if y is not None:
         _matrix(y, shape, me, "y")
-        a.y, a.ld_y, a.y_type = y.data_ptr(), _ld(y, rows, hidden, me), _type(y, me)
+        a.y, a.ld_y, a.y_type = y.data_ptr(), _ld(y, rows, hidden, me), _type(y.dtype, me)
     if h is not None:
-        if h.dtype != h_out.dtype:
+        if h_out is not None and h.dtype != h_out.dtype:
             _refuse(me, f"h is of type {h.dtype}, h_out of {h_out.dtype}")
         a.h, a.ld_h = h.data_ptr(), _ld(h, rows, hidden, me)
     if gate is not None:
@@ -100,7 +120,7 @@ def block_norm(y=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=Tru
             g = gate.expand(rows, hidden)
         except RuntimeError as e:
             _refuse(me, f"gate: {e}")
-        a.gate, a.gate_type = g.data_ptr(), _type(g, me)
+        a.gate, a.gate_type = g.data_ptr(), _type(g.dtype, me)
         a.ld_gate_row, a.ld_gate_col = (g.stride(0) if rows > 1 else 0), (g.stride(1) if hidden > 1 else 0)
     for name, w in (("w_post", w_post), ("w_pre", w_pre)):
         if w is not None:
@@ -108,16 +128,23 @@ def block_norm(y=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=Tru
             if not w.is_contiguous():
                 _refuse(me, f"{name} must be contiguous")
             setattr(a, name, w.data_ptr())
-            a.w_type = _type(w, me)
+            a.w_type = _type(w.dtype, me)
     if w_post is not None and w_pre is not None and w_post.dtype != w_pre.dtype:
         _refuse(me, f"w_post is of type {w_post.dtype}, w_pre of {w_pre.dtype}")
     a.post_norm, a.pre_norm = int(post_norm), int(pre_norm)
     a.w_add, a.eps, a.residual_scale = w_add, eps, residual_scale
-    a.h_out, a.ld_h_out = h_out.data_ptr(), _ld(h_out, rows, hidden, me)
-    a.x_out, a.ld_x_out, a.x_type = x_out.data_ptr(), _ld(x_out, rows, hidden, me), _type(x_out, me)
-    index = like.get_device()
+    for name, t in (("h_out", h_out), ("x_out", x_out)):
+        if t is not None:
+            _matrix(t, shape, me, name)
+            _ld(t, rows, hidden, me)
     _on_gpu(me, index, like, y, gate, w_post, w_pre, h_out, x_out)
-    moe.moe_block_norm(a, _stream(like.device, stream))
+    if h_out is None or x_out is None:
+        other = _other(dev, stream)
+        h_out = _empty(dev, other, like.dtype, rows, hidden) if h_out is None else h_out
+        x_out = _empty(dev, other, x_type, rows, hidden) if x_out is None else x_out
+    a.h_out, a.ld_h_out = h_out.data_ptr(), _ld(h_out, rows, hidden, me)
+    a.x_out, a.ld_x_out = x_out.data_ptr(), _ld(x_out, rows, hidden, me)
+    moe.moe_block_norm(a, _stream(dev, stream))
     return h_out, x_out
 
 
@@ -133,25 +160,26 @@ def token_logprobs(logits: torch.Tensor, targets=None, top_n: int = 0, scale: fl
     rows, vocab = logits.shape
     dev, index = logits.device, logits.get_device()
     a = moe.moe_token_logprobs_args()
-    a.logits, a.ld_logits, a.logits_type = logits.data_ptr(), _ld(logits, rows, vocab, me), _type(logits, me)
+    a.logits, a.ld_logits, a.logits_type = logits.data_ptr(), _ld(logits, rows, vocab, me), _type(logits.dtype, me)
     a.rows, a.vocab, a.top_n, a.scale = rows, vocab, top_n, scale
-    out = {"lse": torch.empty(rows, dtype=torch.float32, device=dev),
-           "entropy": torch.empty(rows, dtype=torch.float32, device=dev)}
-    a.lse, a.entropy = out["lse"].data_ptr(), out["entropy"].data_ptr()
     if targets is not None:
         if targets.dtype != torch.int32 or not targets.is_contiguous() or targets.dim() < 1 or targets.shape[0] != rows:
             _refuse(me, f"targets must be contiguous int32, {rows} or {rows} x n_targets of them")
+    _on_gpu(me, index, logits, targets)
+    other = _other(dev, stream)
+    out = {"lse": _empty(dev, other, torch.float32, rows), "entropy": _empty(dev, other, torch.float32, rows)}
+    a.lse, a.entropy = out["lse"].data_ptr(), out["entropy"].data_ptr()
+    if targets is not None:
         a.targets, a.n_targets = targets.data_ptr(), targets.numel() // max(rows, 1)
-        out["logprob"] = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+        out["logprob"] = _empty(dev, other, torch.float32, *targets.shape)
         a.target_logprobs = out["logprob"].data_ptr()
         if ranks:
-            out["rank"] = torch.empty(targets.shape, dtype=torch.int32, device=dev)
+            out["rank"] = _empty(dev, other, torch.int32, *targets.shape)
             a.target_ranks = out["rank"].data_ptr()
     if top_n:
-        out["top_ids"] = torch.empty(rows, top_n, dtype=torch.int32, device=dev)
-        out["top_logprobs"] = torch.empty(rows, top_n, dtype=torch.float32, device=dev)
+        out["top_ids"] = _empty(dev, other, torch.int32, rows, top_n)
+        out["top_logprobs"] = _empty(dev, other, torch.float32, rows, top_n)
         a.top_ids, a.top_logprobs = out["top_ids"].data_ptr(), out["top_logprobs"].data_ptr()
-    _on_gpu(me, index, logits, targets)
     moe.moe_token_logprobs(a, _stream(dev, stream))
     return out
 
@@ -176,7 +204,7 @@ class Fp8Linear:
         _on_gpu(me, self.index, codes, scales)
         self.handle = moe.moe_fp8_open(self.n, k, codes.data_ptr(), _ld(codes, self.n, codes.shape[1], me), scales.data_ptr())
         self.ws_bytes = moe.moe_fp8_workspace_bytes(self.handle, max_rows)
-        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=codes.device)
+        self.ws = _empty(codes.device, _other(codes.device, stream), torch.uint8, self.ws_bytes)
         self.ws_ptr = self.ws.data_ptr()
         moe.moe_fp8_workspace_init(self.handle, self.ws_ptr, self.ws_bytes, _stream(codes.device, stream))
 
@@ -188,12 +216,13 @@ class Fp8Linear:
             _refuse(me, "weights must be a matrix [n][k]")
         n, k = weights.shape
         ld = -(-k // 16) * 16
-        w_type, ld_w, index = _type(weights, me), _ld(weights, n, k, me), weights.get_device()
+        w_type, ld_w, index = _type(weights.dtype, me), _ld(weights, n, k, me), weights.get_device()
         _on_gpu(me, index, weights)
-        codes = torch.empty(n, ld, dtype=torch.uint8, device=weights.device)
-        scales = torch.empty(-(-n // 128), -(-k // 128), dtype=torch.float32, device=weights.device)
+        dev, other = weights.device, _other(weights.device, stream)
+        codes = _empty(dev, other, torch.uint8, n, ld)
+        scales = _empty(dev, other, torch.float32, -(-n // 128), -(-k // 128))
         moe.moe_fp8_quantize_weights(weights.data_ptr(), w_type, ld_w, n, k, codes.data_ptr(), ld, scales.data_ptr(),
-                                     _stream(weights.device, stream))
+                                     _stream(dev, stream))
         return cls(codes, scales, k, max_rows, stream)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, out_type=torch.bfloat16, stream=None):
@@ -203,14 +232,19 @@ class Fp8Linear:
         if len(shape) != 2 or shape[1] != self.k:
             _refuse(me, f"x has the shape {tuple(shape)}, not [rows][{self.k}]")
         rows, k = shape
+        x_type, ld_x = _type(x.dtype, me), _ld(x, rows, k, me)
+        if x.get_device() != self.index or out is not None and out.get_device() != self.index:
+            _on_gpu(me, self.index, x, out)
+        other = None if stream is None else _other(x.device, stream)
+        if other is not None:
+            for t in (self.ws, self.codes, self.scales):
+                t.record_stream(other)
         if out is None:
-            out = torch.empty(rows, n, dtype=out_type, device=x.device)
+            out = _empty(x.device, other, out_type, rows, n)
         elif out.shape != (rows, n):
             _refuse(me, f"out has the shape {tuple(out.shape)}, not {rows, n}")
-        if x.get_device() != self.index or out.get_device() != self.index:
-            _on_gpu(me, self.index, x, out)
-        moe.moe_fp8_linear(self.handle, x.data_ptr(), _type(x, me), _ld(x, rows, k, me), rows, out.data_ptr(),
-                           _type(out, me), _ld(out, rows, n, me), self.ws_ptr, self.ws_bytes, _stream(x.device, stream))
+        moe.moe_fp8_linear(self.handle, x.data_ptr(), x_type, ld_x, rows, out.data_ptr(),
+                           _type(out.dtype, me), _ld(out, rows, n, me), self.ws_ptr, self.ws_bytes, _stream(x.device, stream))
         return out
 
     def check(self, stream=None) -> int:

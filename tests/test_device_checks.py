@@ -14,7 +14,8 @@ BF = torch.bfloat16
 def calls(monkeypatch):
     """The names of the library calls that a wrapper got through to."""
     got = []
-    monkeypatch.setattr(device, "_on_gpu", lambda *a: None, raising=False)
+    monkeypatch.setattr(device, "_on_gpu", lambda *a: None)
+    monkeypatch.setattr(device, "_other", lambda *a: None, raising=False)
 
     def record(name, value=None):
         monkeypatch.setattr(moe, name, lambda *a: got.append(name) or value)

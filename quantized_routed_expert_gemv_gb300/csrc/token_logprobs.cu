@@ -751,10 +751,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   __syncthreads();
   if (flat) {
     int eq = 0, nan = 0;
-    for (int j = tid; j < a.vocab; j += kThreads) {
-      const float v = row.at(j);
-      eq += v == top_v;
-      nan |= v != v;
+    auto look = [&](float v) { eq += v == top_v, nan |= v != v; };
+    if (edge_j >= 0) look(edge_v);
+#pragma unroll 2
+    for (int c = row.w0 + tid; c < row.w1; c += kThreads) {
+      float v[8];
+      row.load(c, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) look(v[k]);
     }
     eq = __reduce_add_sync(0xFFFFFFFFu, eq);
     nan = __reduce_add_sync(0xFFFFFFFFu, nan);

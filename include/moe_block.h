@@ -56,7 +56,13 @@ enum {
  *   eps > 0.
  *   h_out:  h' in type h_type, or NULL.  May be h itself (with ld_h_out =
  *           ld_h).
- *   x_out:  x in type x_type, or NULL.  At least one of the two is set. */
+ *   x_out:  x in type x_type, or NULL.  At least one of the two is set.
+ *
+ * Many rows are fastest, near the memory's rate, where y, h, h_out and x_out are
+ * all set, with both norms, `hidden` a multiple of 8 from 264 to 8192, rows and
+ * weights on 16-byte boundaries, and a gate per channel or none.  Any other form
+ * takes up to about twice as long for its bytes, rows off 16-byte boundaries
+ * or of a width that 8 does not divide three to four times. */
 typedef struct moe_block_norm_args {
     const void *y, *h, *gate, *w_post, *w_pre;
     void *h_out, *x_out;
@@ -78,7 +84,10 @@ int moe_block_norm(const moe_block_norm_args *args, void *stream);
  *     entropy = -sum_v p_v log p_v,  p = exp(z - lse), 0 log 0 = 0
  *     the top_n tokens by (logit descending, id ascending) with their
  *     log probabilities
- * in one pass over the logits, in 32 bits.
+ * in one pass over the logits, in 32 bits.  Where a row's largest z is 2^31 ln 2 or
+ * more from 0, two different logits differ by 88 or more in z, and the row's
+ * probability is that of its largest logits, in equal shares; such a row is read
+ * a second time.
  *
  *   rows in [0, 2^27] (0: no work); vocab in [1, 2^24]; n_targets in [0, 8]; top_n in [0, 32].
  *   scale:   in [2^-64, 2^64].

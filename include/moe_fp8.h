@@ -23,8 +23,9 @@ extern "C" {
  *        power of two keeps that division and the product with xs exact.
  * The products run on the tensor cores (tcgen05, 8-bit operands, fp32
  * accumulators in tensor memory over one block of 128 inputs); the blocks are
- * scaled and summed in fp32 registers, in an order that depends on the
- * shapes only.  A row of x that holds a NaN or an infinity gives NaN in all
+ * scaled by xs ws, one fp32 product (so that it should not leave fp32's normal
+ * range, as it may for inputs below 1e-35 with weight scales below 1), and summed
+ * in fp32 registers, in an order that depends on the shapes only.  A row of x that holds a NaN or an infinity gives NaN in all
  * of its outputs. */
 typedef struct moe_fp8 moe_fp8;
 

@@ -11,8 +11,18 @@
 // kernels: block_norm_kernel takes one row per block (or per warp);
 // block_norm_stream_kernel keeps one block on each SM whose teams of threads
 // load their next rows while they work on one, with the weights at hand.
-// Measured: 8192 rows of 7168, fp32 y and bf16 h, h' and x, 94.3 us (6.23 TB/s,
-// 92% of the measured copy rate); one such row 3.4 us a call in a graph.
+// Measured: 8192 rows of 7168, fp32 y and bf16 h, h' and x, 92 to 94 us (6.2 to
+// 6.4 TB/s, 92 to 94% of the measured copy rate); one such row 3.5 us a call in a
+// graph, 128 of them 4.0.
+// That is the streaming kernel's form, both norms and all of y, h, h' and x with a
+// gate of every channel or none.  Many rows of another form take a row a block,
+// whose loads, sums and stores follow one another (bytes at the copy rate in
+// brackets): 8192 x 7168 without the post-norm, bf16 y, 95 us (69), without y 86
+// (52); 4096 x 4096, bf16 y, with a gate of every token 42.7 (19.8), of every
+// element 46.1 (24.7), where the streaming form takes 26.6; rows of 16384 values,
+// 4096 of them, 181 (99).  8192 rows of 2000 bf16 values take 24.3 us (19.3), rows
+// of 1999 in 2000, a width that 8 does not divide, 61.8, of 2000 in 2001, off 16
+// bytes, 68.9.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -254,7 +264,11 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512) block_norm_kernel(const 
 // lie in shared memory as fp32, the gate in the post-norm's, in two planes of
 // 16 bytes a chunk; the arithmetic goes in pairs.  With the other kernel's
 // some 60 instructions a value and weights read from L1 between the sums,
-// issue and latency were the bound, not memory.
+// issue and latency were the bound, not memory.  With fp32 h a thread's 72
+// registers spill (28 bytes of stores, 92 with fp32 y too): 8192 x 7168 123 us
+// from bf16 y and 140 from fp32, 84 and 87% of the copy rate.  Widths whose teams
+// leave much of the 896 threads idle are slower: 4096 x 8192 (one team of 512)
+// 69.4 us, 71% of that rate.
 template <bool Y32, bool H32>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     block_norm_stream_kernel(const moe_block_norm_args a, int team_threads) {

@@ -35,11 +35,18 @@
 // not depend on timing.
 //
 // Bound: for many long rows memory, and the latency of a row's end, which the
-// pass of the SM's other blocks covers in part: 4096 rows of 131072 bf16 171 us,
-// 6.3 TB/s, 92% of the measured copy rate.  For shorter rows the rows' ends:
-// 4096 rows of 32000 53 us.  For few rows the chain of steps: one row of 131072
-// with 20 alternatives 9.1 us.  Tried: blocks of 512 threads 215 us, warps of
+// pass of the SM's other blocks covers in part: 4096 rows of 131072 bf16 with 5
+// alternatives 171 to 174 us, 6.2 to 6.3 TB/s, 91 to 92% of the measured copy
+// rate.  Reading alone goes faster than copying: 2048 rows of 131072 fp32
+// without targets or alternatives 155 us, 6.9 TB/s, 102% of that rate, so some
+// 10% are left there.  For shorter rows the rows' ends: 4096 rows of 32000 54 us,
+// of 4000 24.  For few rows the chain of steps: one row of 131072 with 20
+// alternatives 8.5 to 9.9 us.  Tried: blocks of 512 threads 215 us, warps of
 // their own for the rows' ends 224.
+// The instances for 8 targets of 16-bit logits spill at 64 registers, 216 to 372
+// bytes of stores a thread without the ring, 36 to 80 with it; those for 2 and 4
+// targets without it 16 to 96.  4096 rows of 65536 with 8 targets and 20 alternatives take 235 us,
+// where one target and 5 take 97.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -838,18 +845,20 @@ cudaError_t launch_nt(const moe_token_logprobs_args& a, int split, cudaStream_t 
 
 template <int TYPE>
 cudaError_t launch_type(const moe_token_logprobs_args& a, int split, int sms, cudaStream_t st) {
-  // Measured in graphs, bf16, one target, 5 alternatives where not said, before
-  // rows' ends were shortened once more.
+  // Measured in graphs over inputs larger than the L2, bf16, one target, 5
+  // alternatives where not said.
   // Blocks of 128 threads have shorter ends and leave an SM more rows to cover
   // them with, while a winning group, twice as long, costs more to read again:
-  // 4096 rows of 8192 30.4 us against 44.8 with 256 threads, of 32000 56.5 / 73.2,
-  // of 50001 82.4 / 97.0, of 65536 104.1 / 99.5, of 131072 206 / 177; 600 rows of
-  // 32000, a wave of the larger blocks, 13.0 / 13.2.
-  // Copies through shared memory: 4096 rows of 131072 177 us against 197 into
-  // registers, of 65536 with 8 targets and 20 alternatives 237 / 319, of 20000
-  // (128 threads) 47.9 / 51.5, of 8192 33.5 / 32.2; 304 rows of 4000 7.0 / 6.6.
-  // fp32 rows of 131072 take 267 / 152 that way (no targets) and keep to
-  // registers.
+  // 4096 rows of 4000 23.6 us against 44.3 with 256 threads, of 8192 29.6 / 44.9,
+  // of 32000 53.8 / 67.5, of 50001 80.7 / 92.6, of 65536 98.3 / 97.0, of 131072
+  // 206 / 174; 600 rows of 32000, a wave of the larger blocks, 12.7 / 13.9.
+  // Copies through shared memory: 4096 rows of 131072 174 us against 189 into
+  // registers, of 65536 97 / 109, of 65536 with 8 targets and 20 alternatives 235 /
+  // 318, of 20000 (128 threads) 41.6 / 43.5, of 8192 28.5 / 29.6, of 4000 24.7 /
+  // 23.6.
+  // fp32 rows keep to registers: 2048 of 131072 without targets or alternatives
+  // take 155 us, through shared memory 244 to 267 whatever the order of the
+  // copies, which is not explained.
   const bool many = a.rows > 4 * sms, small = many && a.vocab <= kSmallVocab;
   if constexpr (TYPE == MOE_F32) {
     return small ? launch_nt<TYPE, 128, false>(a, split, st) : launch_nt<TYPE, kSplitThreads, false>(a, split, st);

@@ -226,7 +226,7 @@ def prepare(case, seed):
         s["cache"] = device.PagedCache(s["k"], s["v"], s["k_scale"], s["v_scale"])
         s["seqs"] = device.Sequences(s["starts"], s["kv_lens"], s["table"], max_rows=s["max_rows"])
         if c["op"] == "attn":
-            s["attention"] = device.PagedAttention(c["kv_heads"] * c["group"], c["kv_heads"], c["dim"], max_rows=s["max_rows"])
+            s["attention"] = device.PagedAttention(c["kv_heads"] * c["group"], c["kv_heads"], c["dim"])
     return s
 
 

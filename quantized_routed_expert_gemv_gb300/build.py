@@ -17,8 +17,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 SO = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "decode.cu", "decode_b1.cu", "decode_bt.cu", "prefill.cu", "residency.cu", "noalloc.cu",
-           "rvq.cu", "block_norm.cu", "token_logprobs.cu", "fp8.cu"]
-HEADERS = ["common.cuh", "kernels.h", "tcgen05.cuh", "tma.cuh", "gemv.cuh", "fused.cuh", "elem.cuh"]
+           "rvq.cu", "block_norm.cu", "token_logprobs.cu", "fp8.cu", "cache.cu",
+           "attention.cu"]
+HEADERS = ["common.cuh", "kernels.h", "tcgen05.cuh", "tma.cuh", "gemv.cuh", "fused.cuh", "elem.cuh", "cache.cuh", "attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -30,7 +31,7 @@ def _nvcc():
 
 def _deps():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files += [os.path.join(ROOT, "include", h) for h in ("moe.h", "moe_block.h", "moe_fp8.h")]
+    files += [os.path.join(ROOT, "include", h) for h in ("moe.h", "moe_block.h", "moe_fp8.h", "moe_cache.h")]
     return [f for f in files if os.path.exists(f)]
 
 

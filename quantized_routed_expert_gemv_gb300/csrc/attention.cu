@@ -1,0 +1,777 @@
+// attention.cu -- attention of few rows over the paged cache, the join of units
+// that several CTAs share, and the entry points (include/moe_cache.h).
+//
+// Mathematics: a row's softmax over its positions is taken in one pass with a
+// running maximum m, sum l of 2^(z - m) and output o, all fp32 (z in powers of
+// two: scale * log2(e) q . k); when m grows, l and o shrink by 2^(old - new).
+// Parts of the positions, of one warp, one CTA or several, join the same way.
+//
+// Layout: a unit's tile has 16 rows (attention.cuh).  A CTA of four warps takes 64
+// positions at a time, each warp 16 of its own, with its own m, l and o, so
+// that warps never wait for one another until the unit ends.  Each warp copies its
+// positions' keys and values to a ring of stages in shared memory (cp.async, 16
+// bytes a lane), several steps ahead.  Products are m16n8k16 tensor-core
+// instructions with the 16 rows as M: the sum over a head's elements may run in any
+// order, so each lane reads keys in whole 16-byte pieces and takes the query's
+// elements in the same order; the outputs' order is free likewise, so values are
+// read in 16-byte pieces of four positions and paired in registers.  e4m3 codes
+// become 16-bit values, scale included, between shared memory and the product.
+//
+// Bound: reading the cache.
+#include <cuda_runtime.h>
+
+#include "attention.cuh"
+#include "common.cuh"
+
+namespace moe {
+int reportf(int code, const char* fmt, ...);
+
+namespace {
+
+constexpr int kRows = 16;     // rows of a tile
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 16;     // positions of a warp's step
+constexpr int kBn = kWarps * kStep;
+constexpr size_t kCtlBytes = 256;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// How the cache's elements and the query's type meet.
+enum Kind { kBf16, kF16, kE4m3Bf16, kE4m3F16 };
+template <int K>
+struct Traits {
+  static constexpr bool f16 = K == kF16 || K == kE4m3F16, e4m3 = K == kE4m3Bf16 || K == kE4m3F16;
+  static constexpr int size = e4m3 ? 1 : 2;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The bytes s of {a, b} (0..3 of a, 4..7 of b), lowest first.
+__device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+// What turns a head's e4m3 codes into 16-bit values of its scale.
+template <bool F16>
+struct Dequant;
+
+// bf16: a code's exponent and mantissa are bits 4 to 10 of a bf16 that is 2^-120
+// times the value; a scale of up to 2^7 is multiplied on with 2^120, a larger
+// one in a second product.  Both are powers of two: exact.
+template <>
+struct Dequant<false> {
+  __nv_bfloat162 m, more;
+  bool twice;
+  __device__ __forceinline__ void set(float s0, float s1) {
+    twice = __any_sync(0xFFFFFFFFu, s0 > 128.0f || s1 > 128.0f);
+    const float a0 = twice ? 1.329227995784916e36f : s0 * 1.329227995784916e36f;  // 2^120
+    const float a1 = twice ? 1.329227995784916e36f : s1 * 1.329227995784916e36f;
+    m = __floats2bfloat162_rn(a0, a1);
+    more = __floats2bfloat162_rn(s0, s1);
+  }
+  // codes in the high bytes of x's halves
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    const uint32_t bits = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
+    __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), m);
+    if (twice) v = __hmul2(v, more);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+// f16: the hardware's conversion, then the scale; one beyond float16's powers
+// of two is multiplied on in two steps (the first one exact, the second one cut to
+// where any code but 0 is infinite).
+template <>
+struct Dequant<true> {
+  __half2 m, more;
+  bool twice;
+  __device__ __forceinline__ void set(float s0, float s1) {
+    twice = __any_sync(0xFFFFFFFFu, fmaxf(s0, s1) > 32768.0f || fminf(s0, s1) < 6.103515625e-05f);
+    const float c0 = fminf(fmaxf(s0, 6.103515625e-05f), 32768.0f), c1 = fminf(fmaxf(s1, 6.103515625e-05f), 32768.0f);
+    m = __floats2half2_rn(s0 == s0 ? c0 : s0, s1 == s1 ? c1 : s1);
+    more = __floats2half2_rn(fminf(s0 / c0, 32768.0f), fminf(s1 / c1, 32768.0f));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(bytes_of(x, 0, 0x31));
+    __half2 v = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)), m);
+    if (twice) v = __hmul2(v, more);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+template <int DP, int K>
+struct Shape {
+  using T = Traits<K>;
+  static constexpr int row_bytes = DP * T::size;            // of one position in shared memory
+  static constexpr int pieces = row_bytes / 16;             // 16-byte pieces of it
+  static constexpr int ev = T::e4m3 && DP >= 128 ? 16 : 8;  // elements of a lane's piece of values
+  static constexpr int vgroups = DP / (8 * ev);
+  static constexpr int scale_bytes = T::e4m3 ? 2 * kStep * 4 : 0;
+  static constexpr int stage_bytes = 2 * kStep * row_bytes + scale_bytes + 16;  // 16: which positions count
+  static constexpr int ctas = DP <= 128 ? 2 : 1;            // on an SM
+  static constexpr int budget = (224 * 1024 / ctas - 6 * 1024) / kWarps;
+  static constexpr int fit = budget / stage_bytes;
+  static constexpr int stages = fit > 8 ? 8 : fit;
+  static constexpr int ring_bytes = stages * stage_bytes;   // of a warp
+  static_assert(stages >= 2, "ring");
+  static_assert(kWarps * ring_bytes >= kWarps * kRows * (DP + 2) * 4, "the join's buffers take the ring's place");
+};
+
+// Swizzles that spread a phase's lanes over the banks: keys are read in pieces
+// t = 0..3 of two neighbouring rows at a time, values in two pieces of every
+// other row.
+template <int RB>
+__device__ __forceinline__ uint32_t key_at(int row, int piece) {
+  return row * RB + ((RB >= 128 ? piece ^ ((row & 1) << 2) : piece) << 4);
+}
+template <int RB>
+__device__ __forceinline__ uint32_t value_at(int row, int piece) {
+  return row * RB + ((RB >= 128 ? piece ^ (row & 6) : piece) << 4);
+}
+
+__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// A lane's pieces of values of one group: positions 2t, 2t + 1, 2t + 8, 2t + 9.
+template <int DP, int K>
+struct Values {
+  using S = Shape<DP, K>;
+  uint32_t w[4][S::ev == 16 || !Traits<K>::e4m3 ? 4 : 2];
+  __device__ __forceinline__ void load(const uint8_t* v, int t, int gi, int h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 2 * t + (i & 1) + (i & 2) * 4;
+      if constexpr (S::ev == 8 && Traits<K>::e4m3) {
+        const uint2 u = *reinterpret_cast<const uint2*>(v + row * S::row_bytes + (gi + 8 * h) * 8);
+        w[i][0] = u.x, w[i][1] = u.y;
+      } else {
+        const uint4 u = lds128(v + value_at<S::row_bytes>(row, gi + 8 * h));
+        w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+      }
+    }
+  }
+  // element j of the piece: the pairs of positions (2t, 2t + 1) and (2t + 8, 2t + 9)
+  template <class D>
+  __device__ __forceinline__ void pair(int j, const D& lo, const D& hi, uint32_t& b0, uint32_t& b1) const {
+    if constexpr (Traits<K>::e4m3) {
+      const uint32_t s = 0x4000u | ((4u + (j & 3)) << 12) | ((j & 3) << 4);
+      b0 = lo(bytes_of(w[0][j / 4], w[1][j / 4], s));
+      b1 = hi(bytes_of(w[2][j / 4], w[3][j / 4], s));
+    } else {
+      const uint32_t s = j & 1 ? 0x7632u : 0x5410u;
+      b0 = bytes_of(w[0][j / 2], w[1][j / 2], s);
+      b1 = bytes_of(w[2][j / 2], w[3][j / 2], s);
+    }
+  }
+};
+
+struct NoScale {};
+
+// Whether one of two 16-bit values is an infinity or a NaN.
+template <bool F16>
+__device__ __forceinline__ bool odd_value(uint32_t x) {
+  constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+  return (x & e) == e || ((x >> 16) & e) == e;
+}
+
+template <int DP, int K>
+__global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_kernel(const AttnArgs a) {
+  using S = Shape<DP, K>;
+  using T = Traits<K>;
+  constexpr int RB = S::row_bytes, KS = DP / 16, NB = DP / 8, EV = S::ev;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ PlanSmem plan;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gi = lane >> 2, t = lane & 3;
+  pdl_launch_dependents();
+
+  int ctas;
+  int64_t begin, end;
+  Place at;
+  const int64_t total = find_work<kRows, kBn, kThreads>(a, plan, ctas, begin, end, at);
+  if (tid < 2) a.notes[2 * blockIdx.x + tid].count = 0;
+  if (begin == end) return;
+  __syncthreads();
+
+  uint8_t* ring = smem + warp * S::ring_bytes;
+  const uint32_t ring_s = smem_u32(ring);
+  const int pieces = a.head_dim * T::size / 16;
+  if (pieces < S::pieces) {  // elements past head_dim are zeros throughout
+    for (int i = lane; i < S::stages * S::stage_bytes / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+
+  Seq seq = load_seq(a.q, at.seq);
+  for (int64_t x = begin; x < end;) {
+    const Tile tile = tile_of<kRows, kBn>(a, seq, at.tile);
+    const int ta = tile.t0 + at.at;
+    const int tb = static_cast<int>(min(static_cast<int64_t>(tile.t1), ta + (end - x)));
+    const int64_t unit0 = x - at.at, unit1 = unit0 + (tile.t1 - tile.t0);
+    const int row0 = at.tile * kRows;
+
+    // the lane's two rows and what they see
+    int lo[2], hi[2];
+    int tight_lo, tight_hi;  // what all of the tile's rows see
+    {
+      const int base = seq.len - seq.n;
+      const int p0 = base + static_cast<int>(divide(row0, a.by_group));
+      const int p1 = base + static_cast<int>(divide(row0 + tile.rows - 1, a.by_group));
+      tight_hi = sees_to(a, seq.len, p0), tight_lo = sees_from(a, p1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = gi + 8 * i;
+        const int p = base + static_cast<int>(divide(row0 + min(r, tile.rows - 1), a.by_group));
+        lo[i] = sees_from(a, p);
+        hi[i] = r < tile.rows ? sees_to(a, seq.len, p) : 0;
+      }
+    }
+
+    // the query, in the order in which the keys are read
+    uint32_t qa[KS][4];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d = T::e4m3 ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 8 * (t + 4 * (s / 2)) + 4 * (s % 2);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = gi + 8 * i;
+        uint2 u = make_uint2(0, 0);
+        if (r < tile.rows && d < a.head_dim) {
+          const int token = static_cast<int>(divide(row0 + r, a.by_group)), g = row0 + r - token * a.group;
+          u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.query) + (seq.first + token) * a.ld_q +
+                                              static_cast<int64_t>(at.head * a.group + g) * a.head_dim + d);
+        }
+        qa[s][i] = u.x, qa[s][2 + i] = u.y;
+      }
+    }
+
+    const uint8_t* kh = static_cast<const uint8_t*>(a.k) + at.head * a.head_stride;
+    const uint8_t* vh = static_cast<const uint8_t*>(a.v) + at.head * a.head_stride;
+    // lane l copies for position (l & 15) of a step; its page is looked up a step before
+    const int steps = tb - ta;
+    auto position = [&](int step) { return (ta + step) * kBn + warp * kStep + (lane & 15); };
+    auto look_up = [&](int step, int& slot) {
+      const int pos = position(step);
+      return step < steps && pos >= tile.lo && pos < tile.hi ? page_of(a.q, at.seq, pos, slot) : -1;
+    };
+    int slot = 0, page = look_up(0, slot);
+    auto issue = [&](int step, int stage) {
+      const uint32_t base = ring_s + stage * S::stage_bytes;
+      const bool on = page >= 0;
+      const int64_t off = on ? page * a.page_stride + slot * a.slot_stride : -1;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on) & 0xFFFFu;
+      if (step < steps) {
+        if constexpr (T::e4m3) {
+          const float* s = (lane < 16 ? a.k_scale : a.v_scale) + at.head * a.scale_head_stride;
+          cp_async4(base + 2 * kStep * RB + lane * 4,
+                    on ? s + page * a.scale_page_stride + slot * a.scale_slot_stride : static_cast<const void*>(a.query), on);
+        }
+        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::stage_bytes + 2 * kStep * RB + S::scale_bytes) = mask;
+#pragma unroll
+        for (int i = 0; i < kStep * S::pieces / 32; ++i) {
+          const int n = lane + 32 * i, row = n / S::pieces, c = n % S::pieces;
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+          if (c < pieces) {
+            // nothing is read for a position that does not count, but the address is one of memory
+            const void* ka = o < 0 ? a.query : kh + o + c * 16;
+            const void* va = o < 0 ? a.query : vh + o + c * 16;
+            cp_async16(base + key_at<RB>(row, c), ka, o >= 0);
+            cp_async16(base + kStep * RB + (S::ev == 8 && T::e4m3 ? row * RB + c * 16 : value_at<RB>(row, c)), va, o >= 0);
+          }
+        }
+      }
+      cp_commit();
+      page = look_up(step + 1, slot);
+    };
+
+    float o[NB][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < NB; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+
+#pragma unroll 1
+    for (int i = 0; i < S::stages - 1; ++i) issue(i, i);
+    int stage = 0;
+#pragma unroll 1
+    for (int step = 0; step < steps; ++step) {
+      cp_wait<S::stages - 2>();
+      __syncwarp();
+      issue(step + S::stages - 1, stage == 0 ? S::stages - 1 : stage - 1);
+      const uint8_t* ks = ring + stage * S::stage_bytes;
+      const uint8_t* vs = ks + kStep * RB;
+      const uint32_t mask = *reinterpret_cast<const uint32_t*>(ks + 2 * kStep * RB + S::scale_bytes);
+      const float* sc = reinterpret_cast<const float*>(ks + 2 * kStep * RB);
+      if (++stage == S::stages) stage = 0;
+      if (mask == 0) continue;
+
+      // z: rows gi and gi + 8, positions 8 n + 2t and + 1
+      float z[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
+        if constexpr (T::e4m3) {
+          Dequant<T::f16> dq;
+          dq.set(sc[8 * n + gi], sc[8 * n + gi]);
+#pragma unroll
+          for (int i = 0; i < S::pieces / 4; ++i) {
+            const uint4 u = lds128(ks + key_at<RB>(8 * n + gi, t + 4 * i));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma16816<T::f16>(z[n], qa[4 * i + j], dq(bytes_of(w[j], 0, 0x1404)), dq(bytes_of(w[j], 0, 0x3424)));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::pieces / 4; ++i) {
+            const uint4 u = lds128(ks + key_at<RB>(8 * n + gi, t + 4 * i));
+            mma16816<T::f16>(z[n], qa[2 * i], u.x, u.y);
+            mma16816<T::f16>(z[n], qa[2 * i + 1], u.z, u.w);
+          }
+        }
+      }
+      const int first = (ta + step) * kBn + warp * kStep;
+      const bool edge = first < tight_lo || first + kStep > tight_hi || mask != 0xFFFFu;
+      uint32_t seen = 0;  // bit 4 n + c: value c of block n is seen
+      if (edge) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int k = 8 * n + 2 * t + (c & 1), pos = first + k;
+            const bool see = (mask >> k & 1) && pos >= lo[c >> 1] && pos < hi[c >> 1];
+            if (see) seen |= 1u << (4 * n + c);
+            else z[n][c] = -INFINITY;
+          }
+      }
+      // the running maximum
+      float shrink[2];
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = fmaxf(fmaxf(z[0][2 * i], z[0][2 * i + 1]), fmaxf(z[1][2 * i], z[1][2 * i + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+        x *= a.scale_log2;
+        shrink[i] = 1.0f;
+        if (x > m[i]) {
+          shrink[i] = exp2_approx(m[i] - x);  // 0 for the first
+          m[i] = x, moved = true;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, moved)) {
+        l[0] *= shrink[0], l[1] *= shrink[1];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) o[j][0] *= shrink[0], o[j][1] *= shrink[0], o[j][2] *= shrink[1], o[j][3] *= shrink[1];
+      }
+      const float ref[2] = {(m[0] == -INFINITY ? 0.0f : m[0]) - exp_lift<T::f16>(),
+                            (m[1] == -INFINITY ? 0.0f : m[1]) - exp_lift<T::f16>()};
+      uint32_t pa[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          z[n][c] = exp2_approx(fmaf(z[n][c], a.scale_log2, -ref[c >> 1]));
+          l[c >> 1] += z[n][c];
+        }
+        pa[2 * n] = pack2(z[n][0], z[n][1], T::f16 ? MOE_F16 : MOE_BF16);
+        pa[2 * n + 1] = pack2(z[n][2], z[n][3], T::f16 ? MOE_F16 : MOE_BF16);
+      }
+
+      Dequant<T::f16> dlo, dhi;
+      if constexpr (T::e4m3) {
+        dlo.set(sc[kStep + 2 * t], sc[kStep + 2 * t + 1]);
+        dhi.set(sc[kStep + 2 * t + 8], sc[kStep + 2 * t + 9]);
+      }
+      bool odd = false;
+      if (edge) {  // a value that some row must not see may be anything
+#pragma unroll
+        for (int h = 0; h < S::vgroups; ++h) {
+          Values<DP, K> v;
+          v.load(vs, t, gi, h);
+#pragma unroll
+          for (int j = 0; j < EV; ++j) {
+            uint32_t b0, b1;
+            v.pair(j, dlo, dhi, b0, b1);
+            odd |= odd_value<T::f16>(b0) || odd_value<T::f16>(b1);
+          }
+        }
+        odd = __any_sync(0xFFFFFFFFu, odd);
+      }
+      if (!odd) {
+#pragma unroll
+        for (int h = 0; h < S::vgroups; ++h) {
+          Values<DP, K> v;
+          v.load(vs, t, gi, h);
+#pragma unroll
+          for (int j = 0; j < EV; ++j) {
+            uint32_t b0, b1;
+            v.pair(j, dlo, dhi, b0, b1);
+            mma16816<T::f16>(o[h * EV + j], pa, b0, b1);
+          }
+        }
+      } else {
+        // One position at a time, into the rows that see it: its values are in the
+        // lanes of its pair, column n of theirs in group n's lane.
+#pragma unroll 1
+        for (int k = 0; k < kStep; ++k) {
+          const int from = (gi << 2) | ((k & 7) >> 1);
+          const uint32_t who = __shfl_sync(0xFFFFFFFFu, seen, from) >> (4 * (k >> 3) + (k & 1));
+          float p[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float lo8 = __shfl_sync(0xFFFFFFFFu, k & 1 ? z[0][2 * i + 1] : z[0][2 * i], from);
+            const float hi8 = __shfl_sync(0xFFFFFFFFu, k & 1 ? z[1][2 * i + 1] : z[1][2 * i], from);
+            p[i] = k < 8 ? lo8 : hi8;
+          }
+#pragma unroll
+          for (int h = 0; h < S::vgroups; ++h) {
+            Values<DP, K> v;
+            v.load(vs, t, gi, h);
+#pragma unroll
+            for (int j = 0; j < EV; ++j) {
+              uint32_t b0, b1;
+              v.pair(j, dlo, dhi, b0, b1);
+              const uint32_t b = k < 8 ? b0 : b1, bits = k & 1 ? b >> 16 : b & 0xFFFFu;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float val = half_bits_to_f32(__shfl_sync(0xFFFFFFFFu, bits, ((2 * t + c) << 2) | ((k & 7) >> 1)),
+                                                   T::f16 ? MOE_F16 : MOE_BF16);
+                if (who & 1) o[h * EV + j][c] += p[0] * val;
+                if (who & 4) o[h * EV + j][2 + c] += p[1] * val;
+              }
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+    }
+
+    // the four warps' parts, through the ring's place
+    __syncthreads();
+    float* jo = reinterpret_cast<float*>(smem);            // [warp][row][DP]
+    float* jm = jo + kWarps * kRows * DP;                  // [warp][row][2]
+    // a lane has, of rows gi and gi + 8, the elements EV (n + 8 h) + j for n = 2t, 2t + 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = gi + 8 * i;
+      if (r >= tile.rows) continue;
+      float* row = jo + (warp * kRows + r) * DP;
+#pragma unroll
+      for (int h = 0; h < S::vgroups; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < EV; j += 4) {
+            const int b = h * EV + j;
+            *reinterpret_cast<float4*>(row + EV * (2 * t + c + 8 * h) + j) =
+                make_float4(o[b][2 * i + c], o[b + 1][2 * i + c], o[b + 2][2 * i + c], o[b + 3][2 * i + c]);
+          }
+      if (t == 0) jm[(warp * kRows + r) * 2] = m[i], jm[(warp * kRows + r) * 2 + 1] = l[i];
+    }
+    __syncthreads();
+    const bool whole = ta == tile.t0 && tb == tile.t1;
+    const int which = ta == tile.t0 ? 1 : 0;
+    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + which;
+    const int d4 = a.head_dim / 4;
+    for (int i = tid; i < tile.rows * d4; i += kThreads) {
+      const int r = i / d4, d = (i - r * d4) * 4;
+      float mw[kWarps], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mw[w] = jm[(w * kRows + r) * 2], top = fmaxf(top, mw[w]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_approx(mw[w] - ref);
+        const float4 v = *reinterpret_cast<const float4*>(jo + (w * kRows + r) * DP + d);
+        sum += f * jm[(w * kRows + r) * 2 + 1];
+        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+      }
+      if (whole) {
+        const int token = static_cast<int>(divide(row0 + r, a.by_group)), g = row0 + r - token * a.group;
+        const int64_t row = seq.first + token;
+        const int head = at.head * a.group + g;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint2 u;
+        u.x = pack2(acc.x * inv, acc.y * inv, T::f16 ? MOE_F16 : MOE_BF16);
+        u.y = pack2(acc.z * inv, acc.w * inv, T::f16 ? MOE_F16 : MOE_BF16);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d) = u;
+        if (d == 0 && a.lse)
+          a.lse[row * a.kv_heads * a.group + head] =
+              sum == 0.0f ? -INFINITY : (top + (log2f(sum) - exp_lift<T::f16>())) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (part * kRows + r) * a.head_dim + d) = acc;
+        if (d == 0) a.part_ml[(part * kRows + r) * 2] = top, a.part_ml[(part * kRows + r) * 2 + 1] = sum;
+      }
+    }
+    if (!whole && tid == 0) {
+      Note n;
+      n.c0 = cta_of(unit0, total, ctas), n.count = cta_of(unit1 - 1, total, ctas) - n.c0 + 1;
+      n.row = row0, n.rows = tile.rows, n.first = seq.first, n.head = at.head;
+      a.notes[part] = n;
+    }
+    __syncthreads();  // the ring is free again
+    if (pieces < S::pieces) {
+      for (int i = lane; i < S::stages * S::stage_bytes / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+    x += tb - ta;
+    next_unit<kRows>(a, at, seq);
+  }
+}
+
+// ---- the join ---------------------------------------------------------------------
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinItems = 8;                              // groups of four outputs at a time
+constexpr int kJoinLanes = kJoinThreads / kJoinItems;      // threads that share a group's parts
+
+// o, l and m of a group of four outputs.
+struct Part {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float m2, float l2, float4 o2) {
+    const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
+    const float f = exp2_approx(m - ref), f2 = exp2_approx(m2 - ref);
+    m = top, l = l * f + l2 * f2;
+    o = make_float4(o.x * f + o2.x * f2, o.y * f + o2.y * f2, o.z * f + o2.z * f2, o.w * f + o2.w * f2);
+  }
+};
+
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, int tile_rows, int type, float lift) {
+  __shared__ Part parts[kJoinThreads / 32][kJoinItems];
+  pdl_wait();
+  const int item = threadIdx.x % kJoinItems, pl = threadIdx.x / kJoinItems, warp = threadIdx.x >> 5;
+  const int d4 = a.head_dim / 4;
+  for (int which = 0; which < 2; ++which) {
+    const Note n = a.notes[2 * blockIdx.x + which];
+    if (n.count == 0) continue;
+    const int all = n.rows * d4, each = (all + n.count - 1) / n.count;
+    const int from = (blockIdx.x - n.c0) * each, to = min(all, from + each);
+    for (int i0 = from; i0 < to; i0 += kJoinItems) {
+      const int i = i0 + item;
+      const bool on = i < to;
+      const int r = on ? i / d4 : 0, d = on ? (i - r * d4) * 4 : 0;
+      Part p = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+      if (on)
+        for (int c = pl; c < n.count; c += kJoinLanes) {
+          const int64_t at = (2 * static_cast<int64_t>(n.c0 + c) + (c == 0 ? 1 : 0)) * tile_rows + r;
+          p.add(a.part_ml[at * 2], a.part_ml[at * 2 + 1], *reinterpret_cast<const float4*>(a.part_o + at * a.head_dim + d));
+        }
+#pragma unroll
+      for (int s = kJoinItems; s < 32; s <<= 1) {
+        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, p.m, s), l2 = __shfl_xor_sync(0xFFFFFFFFu, p.l, s);
+        const float4 o2 = make_float4(__shfl_xor_sync(0xFFFFFFFFu, p.o.x, s), __shfl_xor_sync(0xFFFFFFFFu, p.o.y, s),
+                                      __shfl_xor_sync(0xFFFFFFFFu, p.o.z, s), __shfl_xor_sync(0xFFFFFFFFu, p.o.w, s));
+        p.add(m2, l2, o2);
+      }
+      if ((threadIdx.x & 31) < kJoinItems) parts[warp][item] = p;
+      __syncthreads();
+      if (threadIdx.x < kJoinItems && on) {
+        p = parts[0][item];
+        for (int w = 1; w < kJoinThreads / 32; ++w) p.add(parts[w][item].m, parts[w][item].l, parts[w][item].o);
+        const int token = static_cast<int>(divide(n.row + r, a.by_group)), g = n.row + r - token * a.group;
+        const int64_t row = n.first + token;
+        const int head = n.head * a.group + g;
+        const float inv = p.l == 0.0f ? 0.0f : 1.0f / p.l;
+        uint2 u;
+        u.x = pack2(p.o.x * inv, p.o.y * inv, type), u.y = pack2(p.o.z * inv, p.o.w * inv, type);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d) = u;
+        if (d == 0 && a.lse)
+          a.lse[row * a.kv_heads * a.group + head] = p.l == 0.0f ? -INFINITY : (p.m + (log2f(p.l) - lift)) * kLn2;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---- host --------------------------------------------------------------------------
+
+// CTAs of the widest grid that a workspace serves, on an SM.
+constexpr int kMaxCtas = 2;
+
+struct Parts {
+  size_t notes, ml, o, bytes;
+};
+
+Parts parts_of(int grid, int tile_rows, int head_dim) {
+  Parts p;
+  p.notes = kCtlBytes;
+  p.ml = (p.notes + sizeof(Note) * 2 * grid + 255) / 256 * 256;
+  p.o = (p.ml + sizeof(float) * 4 * grid * tile_rows + 255) / 256 * 256;
+  p.bytes = p.o + sizeof(float) * 2 * static_cast<size_t>(grid) * tile_rows * head_dim;
+  return p;
+}
+
+template <int DP, int K>
+cudaError_t launch_rows(const AttnArgs& a, int num_sms, cudaStream_t st) {
+  using S = Shape<DP, K>;
+  auto kernel = attention_rows_kernel<DP, K>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * S::ring_bytes);
+  if (e) return e;
+  kernel<<<num_sms * S::ctas, kThreads, kWarps * S::ring_bytes, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int DP>
+cudaError_t launch_rows(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st) {
+  switch (k) {
+    case kBf16: return launch_rows<DP, kBf16>(a, num_sms, st);
+    case kF16: return launch_rows<DP, kF16>(a, num_sms, st);
+    case kE4m3Bf16: return launch_rows<DP, kE4m3Bf16>(a, num_sms, st);
+    default: return launch_rows<DP, kE4m3F16>(a, num_sms, st);
+  }
+}
+
+bool heads_ok(int32_t q_heads, int32_t kv_heads) {
+  return kv_heads >= 1 && kv_heads <= 1024 && q_heads >= 1 && q_heads <= 4096 && q_heads % kv_heads == 0 &&
+         q_heads / kv_heads <= 128;
+}
+
+int sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (!e) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_join(const AttnArgs& a, int grid, int tile_rows, bool f16, float lift, cudaStream_t st) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid), c.blockDim = dim3(kJoinThreads), c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, attention_join_kernel, a, tile_rows, static_cast<int>(f16 ? MOE_F16 : MOE_BF16), lift);
+}
+
+}  // namespace moe
+
+extern "C" size_t moe_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  using namespace moe;
+  int sms = 0;
+  if (!heads_ok(q_heads, kv_heads) || head_dim < 16 || head_dim > 256 || head_dim % 16 || sm_count(&sms)) return 0;
+  return parts_of(sms * kMaxCtas, kRows, head_dim).bytes;
+}
+
+extern "C" int moe_attention_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace moe;
+  if (!workspace || workspace_bytes < kCtlBytes)
+    return reportf(MOE_ERR_ARG, "moe_attention_workspace_init: workspace is NULL or smaller than %zu bytes", kCtlBytes);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return reportf(MOE_ERR_ALIGN, "moe_attention_workspace_init: workspace is not 256-byte aligned");
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, kCtlBytes, static_cast<cudaStream_t>(stream));
+  if (e) return reportf(MOE_ERR_CUDA, "moe_attention_workspace_init: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  return MOE_OK;
+}
+
+extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache* cache, const moe_sequences* seqs,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace moe;
+  if (!args) return reportf(MOE_ERR_ARG, "moe_attention: args is NULL");
+  const moe_attention_args& g = *args;
+  AttnArgs a = {};
+  const int rc = check_cache("moe_attention", cache, seqs, &a.q);
+  if (rc) return rc;
+  const moe_kv_cache& c = *cache;
+  if (g.q_type != MOE_BF16 && g.q_type != MOE_F16)
+    return reportf(MOE_ERR_ARG, "moe_attention: q has an unknown type %d", g.q_type);
+  if (c.type != MOE_E4M3 && c.type != g.q_type)
+    return reportf(MOE_ERR_UNSUPPORTED, "moe_attention: q is of type %d, the cache of %d", g.q_type, c.type);
+  if (!heads_ok(g.q_heads, c.kv_heads))
+    return reportf(MOE_ERR_ARG, "moe_attention: q_heads=%d must be at most 4096, a multiple of kv_heads=%d and at most 128 times it",
+                   g.q_heads, c.kv_heads);
+  if ((g.causal != 0 && g.causal != 1) || g.window < 0)
+    return reportf(MOE_ERR_ARG, "moe_attention: causal=%d must be 0 or 1, window=%d not negative", g.causal, g.window);
+  if (!(g.scale > 0.0f) || g.scale > 3.0e38f / 1.5f)
+    return reportf(MOE_ERR_ARG, "moe_attention: scale must be positive and below 2^127");
+  if (seqs->rows == 0 || seqs->n_seqs == 0) return MOE_OK;
+  const int group = g.q_heads / c.kv_heads;
+  if (static_cast<int64_t>(seqs->rows) * group > (1 << 30))
+    return reportf(MOE_ERR_ARG, "moe_attention: %d rows of %d query heads a key head are more than 2^30", seqs->rows, group);
+  if (!g.q || !g.out || !workspace) return reportf(MOE_ERR_ARG, "moe_attention: q, out or workspace is NULL");
+  const int64_t width = static_cast<int64_t>(g.q_heads) * c.head_dim;
+  if (g.ld_q < width || g.ld_out < width || g.ld_q % 8 || g.ld_out % 8)
+    return reportf(MOE_ERR_ARG, "moe_attention: ld_q=%lld and ld_out=%lld must be multiples of 8, at least %lld",
+                   static_cast<long long>(g.ld_q), static_cast<long long>(g.ld_out), static_cast<long long>(width));
+  if ((reinterpret_cast<uintptr_t>(g.q) | reinterpret_cast<uintptr_t>(g.out)) % 16 || reinterpret_cast<uintptr_t>(g.lse) % 4 ||
+      reinterpret_cast<uintptr_t>(workspace) % 256)
+    return reportf(MOE_ERR_ALIGN, "moe_attention: q or out is not 16-byte aligned, lse not 4, or workspace not 256");
+  int sms = 0;
+  cudaError_t e = static_cast<cudaError_t>(sm_count(&sms));
+  if (e) return reportf(MOE_ERR_CUDA, "moe_attention: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  const size_t need = moe_attention_workspace_bytes(g.q_heads, c.kv_heads, c.head_dim);
+  if (workspace_bytes < need)
+    return reportf(MOE_ERR_ARG, "moe_attention: these heads need %zu bytes of workspace, got %zu", need, workspace_bytes);
+
+  a.query = g.q, a.out = g.out, a.lse = g.lse, a.ld_q = g.ld_q, a.ld_out = g.ld_out;
+  const int size = c.type == MOE_E4M3 ? 1 : 2;
+  a.k = c.k, a.v = c.v, a.k_scale = c.k_scale, a.v_scale = c.v_scale;
+  a.page_stride = c.page_stride * size, a.slot_stride = c.slot_stride * size, a.head_stride = c.head_stride * size;
+  a.scale_page_stride = c.scale_page_stride, a.scale_slot_stride = c.scale_slot_stride, a.scale_head_stride = c.scale_head_stride;
+  a.head_dim = c.head_dim, a.kv_heads = c.kv_heads, a.group = group, a.causal = g.causal, a.window = g.window;
+  a.scale_log2 = g.scale * 1.4426950408889634f;
+  a.by_group = divisor(static_cast<uint32_t>(group));
+  const Kind kind = c.type == MOE_BF16 ? kBf16 : c.type == MOE_F16 ? kF16 : g.q_type == MOE_BF16 ? kE4m3Bf16 : kE4m3F16;
+  const bool f16 = g.q_type == MOE_F16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  const int grid = sms * (c.head_dim <= 128 ? 2 : 1);
+  const Parts p = parts_of(grid, kRows, c.head_dim);
+  a.ctl = reinterpret_cast<unsigned*>(base);
+  a.notes = reinterpret_cast<Note*>(base + p.notes);
+  a.part_ml = reinterpret_cast<float*>(base + p.ml), a.part_o = reinterpret_cast<float*>(base + p.o);
+  e = c.head_dim <= 64    ? launch_rows<64>(a, kind, sms, st)
+      : c.head_dim <= 128 ? launch_rows<128>(a, kind, sms, st)
+                          : launch_rows<256>(a, kind, sms, st);
+  if (!e) e = launch_join(a, grid, kRows, f16, f16 ? exp_lift<true>() : exp_lift<false>(), st);
+  if (e) return reportf(MOE_ERR_CUDA, "moe_attention: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  return MOE_OK;
+}
+
+extern "C" int moe_attention_check(void* workspace, void* stream) {
+  using namespace moe;
+  if (!workspace) return reportf(MOE_ERR_ARG, "moe_attention_check: workspace is NULL");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned bits = 0;
+  cudaError_t e = cudaMemcpyAsync(&bits, workspace, sizeof bits, cudaMemcpyDeviceToHost, st);
+  if (!e) e = cudaStreamSynchronize(st);
+  if (!e && bits) {
+    e = cudaMemsetAsync(workspace, 0, kCtlBytes, st);
+    if (!e) e = cudaStreamSynchronize(st);
+  }
+  if (e) return reportf(MOE_ERR_CUDA, "moe_attention_check: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
+  if (bits) return reportf(MOE_ERR_TIMEOUT, "moe_attention_check: a bounded device-side wait ran out (bits 0x%x)", bits);
+  return MOE_OK;
+}

@@ -1,0 +1,245 @@
+// attention.cuh -- how attention over the paged cache is cut into work, shared
+// by its kernels (attention.cu, attention_tc.cu).
+//
+// A unit is a tile of `tile_rows` rows of one key head of one sequence, a row
+// being one token's query head of the head's group (row r: token r / group,
+// head r % group); it has the key tiles of `bn` positions that its rows may
+// see, one at least.  All units' key tiles, ordered by sequence, head and row
+// tile, make one line of T tiles, which is cut into equal parts, one a CTA:
+// CTA c of G (G cut to T) has tiles T c / G to T (c + 1) / G.  So the work is
+// even whatever the lengths, which the kernels alone know; neighbours share a head's
+// keys in L2; and the cut, hence the order of every sum, depends on the sequences and
+// the number of SMs only.
+//
+// A unit that lies in one CTA is finished there.  Of one that is cut, each CTA
+// leaves its rows' maximum, sum and unnormalised output (fp32) in the
+// workspace, in slot 0 if it continues the unit, in slot 1 if it begins it,
+// with a note on who shares it, and the join kernel, launched behind, adds them up: each
+// CTA's block there does an equal share of the unit's outputs.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "cache.cuh"
+
+namespace moe {
+
+struct AttnArgs {
+  Seqs q;
+  const void* query;
+  void* out;
+  float* lse;
+  int64_t ld_q, ld_out;
+  const void *k, *v;  // the cache
+  const float *k_scale, *v_scale;
+  int64_t page_stride, slot_stride, head_stride;                 // bytes
+  int64_t scale_page_stride, scale_slot_stride, scale_head_stride;  // floats
+  int head_dim, kv_heads, group, causal, window;
+  float scale_log2;  // scale * log2(e)
+  Divisor by_group;
+  unsigned* ctl;    // [0] error bits
+  struct Note* notes;  // [G][2]
+  float* part_ml;   // [G][2][tile_rows][2]
+  float* part_o;    // [G][2][tile_rows][head_dim]
+};
+
+// Who shares the unit of a slot.
+struct Note {
+  int c0, count;      // CTAs c0 .. c0 + count - 1 (0: the slot is not used)
+  int row, rows;      // the unit's first row of the sequence, and its rows
+  int first, head;    // the sequence's first row in the call's tensors, key head
+};
+
+// What a row tile sees: positions [lo, hi) over all of its rows.
+struct Tile {
+  int rows;    // rows in the tile
+  int lo, hi;
+  int t0, t1;  // key tiles
+};
+
+// The positions that the token at position `pos` sees are [lo, hi).
+__device__ __forceinline__ int sees_from(const AttnArgs& a, int pos) {
+  return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+__device__ __forceinline__ int sees_to(const AttnArgs& a, int len, int pos) {
+  return a.causal ? max(0, min(len, pos + 1)) : len;
+}
+
+template <int R, int BN>
+__device__ __forceinline__ Tile tile_of(const AttnArgs& a, const Seq& s, int r) {
+  Tile t;
+  const int first = r * R, all = s.n * a.group;
+  t.rows = min(R, all - first);
+  const int base = s.len - s.n;
+  t.lo = sees_from(a, base + static_cast<int>(divide(first, a.by_group)));
+  t.hi = sees_to(a, s.len, base + static_cast<int>(divide(first + t.rows - 1, a.by_group)));
+  t.t0 = t.lo / BN;
+  t.t1 = max(t.t0 + 1, (t.hi + BN - 1) / BN);
+  return t;
+}
+
+template <int R>
+__device__ __forceinline__ int row_tiles(const AttnArgs& a, const Seq& s) {
+  return (s.n * a.group + R - 1) / R;
+}
+
+// Place in the line: unit (seq, head, tile) and a key tile of it, counted
+// from the unit's first.
+struct Place {
+  int seq, head, tile, at;
+};
+
+// Key tiles of one head of the sequences of this warp's lanes (all lanes;
+// n = 0 for a lane without one): few row tiles a lane by itself, many by the
+// whole warp.
+template <int R, int BN>
+__device__ __forceinline__ int64_t head_cost(const AttnArgs& a, const Seq& s) {
+  const int nt = row_tiles<R>(a, s), lane = threadIdx.x & 31;
+  int64_t cost = 0;
+  if (nt <= 2)
+    for (int r = 0; r < nt; ++r) {
+      const Tile t = tile_of<R, BN>(a, s, r);
+      cost += t.t1 - t.t0;
+    }
+  for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nt > 2); many; many &= many - 1) {
+    const int l = __ffs(many) - 1;
+    Seq o;
+    o.first = 0, o.n = __shfl_sync(0xFFFFFFFFu, s.n, l), o.len = __shfl_sync(0xFFFFFFFFu, s.len, l);
+    const int tiles = row_tiles<R>(a, o);
+    int64_t sum = 0;
+    for (int r = lane; r < tiles; r += 32) {
+      const Tile t = tile_of<R, BN>(a, o, r);
+      sum += t.t1 - t.t0;
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
+    if (lane == l) cost = sum;
+  }
+  return cost;
+}
+
+struct PlanSmem {
+  int64_t warp_sum[32];
+  int64_t chunk_sum[kMaxSeqs / 128];
+  int64_t rem;
+  Place start;
+};
+
+// All of a CTA's threads (THREADS, a multiple of 128) find the total T and
+// the place of this CTA's first tile.  Returns T; G, first and last tile by reference.
+template <int R, int BN, int THREADS>
+__device__ int64_t find_work(const AttnArgs& a, PlanSmem& sm, int& ctas, int64_t& begin, int64_t& end, Place& start) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunks = (a.q.n + THREADS - 1) / THREADS;
+  int64_t total = 0, before = 0;
+  int chunk_held = -1;
+  int64_t cost = 0, incl = 0;  // tiles of the chunk's sequences up to this thread's
+  auto scan = [&](int ch) {
+    const int s = ch * THREADS + tid;
+    Seq q = {0, 0, 0};
+    if (s < a.q.n) q = load_seq(a.q, s);
+    cost = head_cost<R, BN>(a, q);
+    incl = cost * a.kv_heads;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) sm.warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) incl += sm.warp_sum[w];
+      all += sm.warp_sum[w];
+    }
+    __syncthreads();
+    chunk_held = ch;
+    return all;
+  };
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int64_t all = scan(ch);
+    if (tid == 0) sm.chunk_sum[ch] = all;
+    total += all;
+  }
+  const int64_t g = gridDim.x, c = blockIdx.x;
+  ctas = static_cast<int>(g < total ? g : total);
+  if (c >= ctas) {
+    begin = end = 0;
+    return total;
+  }
+  begin = total * c / ctas, end = total * (c + 1) / ctas;
+  __syncthreads();
+  int ch = 0;
+  for (; ch + 1 < chunks && before + sm.chunk_sum[ch] <= begin; ++ch) before += sm.chunk_sum[ch];
+  if (ch != chunk_held) scan(ch);
+  const int64_t mine = cost * a.kv_heads;
+  const bool here = before + incl > begin && before + incl - mine <= begin;
+  if (here) {
+    const int64_t off = begin - (before + incl - mine);
+    sm.start.seq = ch * THREADS + tid;
+    sm.start.head = static_cast<int>(off / cost);
+    sm.rem = off % cost;
+  }
+  __syncthreads();
+  if (warp == 0) {  // the row tile: 32 tiles at a time
+    const Seq s = load_seq(a.q, sm.start.seq);
+    int64_t rem = sm.rem;
+    const int tiles = row_tiles<R>(a, s);
+    for (int r0 = 0; r0 < tiles; r0 += 32) {
+      int n = 0;
+      if (r0 + lane < tiles) {
+        const Tile t = tile_of<R, BN>(a, s, r0 + lane);
+        n = t.t1 - t.t0;
+      }
+      int64_t up_to = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, up_to, o);
+        if (lane >= o) up_to += up;
+      }
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, up_to > rem);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        if (lane == l) sm.start.tile = r0 + l, sm.start.at = static_cast<int>(rem - (up_to - n));
+        break;
+      }
+      rem -= __shfl_sync(0xFFFFFFFFu, up_to, 31);
+    }
+  }
+  __syncthreads();
+  start = sm.start;
+  return total;
+}
+
+// The CTA that has tile x of T.
+__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int ctas) {
+  return static_cast<int>(((x + 1) * ctas - 1) / total);
+}
+
+// Moves to the next unit (a sequence without rows has none).  The sequence's
+// values are loaded again where it changes.
+template <int R>
+__device__ __forceinline__ void next_unit(const AttnArgs& a, Place& p, Seq& s) {
+  p.at = 0;
+  if (++p.tile < row_tiles<R>(a, s)) return;
+  p.tile = 0;
+  if (++p.head < a.kv_heads) return;
+  p.head = 0;
+  do {
+    if (++p.seq >= a.q.n) return;
+    s = load_seq(a.q, p.seq);
+  } while (s.n == 0);
+}
+
+// log2 of the factor that all exponentials carry: float16 holds fewer small
+// values than large ones, so the largest exponential is 2^15 there.
+template <bool F16>
+__host__ __device__ constexpr float exp_lift() {
+  return F16 ? 15.0f : 0.0f;
+}
+
+cudaError_t launch_join(const AttnArgs& a, int grid, int tile_rows, bool f16, float lift, cudaStream_t st);
+
+}  // namespace moe

@@ -1,11 +1,13 @@
 // elem.cuh -- element types of the operators around the layer
 // (include/moe_block.h): loads, stores and conversions of bf16, f16 and f32
-// values, one at a time or as aligned vectors of eight.
+// values, one at a time or as aligned vectors of eight; scales and codes of
+// blocks quantised to e4m3.
 #pragma once
 
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "../../include/moe_block.h"
@@ -89,6 +91,27 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t i, const float
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8(v, type);
   }
+}
+
+// The scale of a block whose largest |x| has these bits: the smallest power
+// of two s >= 2^-126 with max <= 448 s (448 = 1.75 * 2^8), 1 for zeros, NaN
+// if there is an infinity or a NaN.  `inv` is 1 / s (0 for NaN).
+__device__ __forceinline__ float block_scale(uint32_t max_bits, float& inv) {
+  if (max_bits == 0) return inv = 1.0f;
+  if (max_bits >= 0x7F800000u) {
+    inv = 0.0f;
+    return __uint_as_float(0x7FC00000u);
+  }
+  int p = static_cast<int>(max_bits >> 23) - 127 - ((max_bits & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
+  p = max(p, -126);
+  inv = __uint_as_float(static_cast<uint32_t>(127 - p) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + p) << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
 }
 
 }  // namespace moe

@@ -7,6 +7,8 @@ pointers to ``moe_decode`` / ``moe_prefill_chunk``.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -260,6 +262,198 @@ class Fp8Linear:
             self.close()
         except Exception:
             pass
+
+
+def _heads(t: torch.Tensor, rows, heads: int, dim: int, where: str, name: str) -> int:
+    """Leading dimension of a [rows][heads][dim] tensor whose heads follow each
+    other (rows None: any)."""
+    if t.dim() != 3 or t.shape[1:] != (heads, dim) or rows is not None and t.shape[0] != rows:
+        _refuse(where, f"{name} has the shape {tuple(t.shape)}, not [{'rows' if rows is None else rows}][{heads}][{dim}]")
+    ld, head, step = t.stride()
+    if step != 1 or heads > 1 and head != dim:
+        _refuse(where, f"{name}'s rows must be contiguous")
+    return ld if t.shape[0] > 1 else -(-max(ld, heads * dim) // 8) * 8
+
+
+class Sequences:
+    """The sequences of a step (moe_sequences): starts int32 [n_seqs + 1],
+    kv_lens int32 [n_seqs], page_table int32 [n_seqs][width], on the GPU.
+    max_rows: the most rows of one sequence, or more, if known; it chooses
+    between kernels.  One object serves every layer of the step, and later steps if
+    the tensors are filled anew (in place, as for a captured graph)."""
+
+    def __init__(self, starts: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, max_rows: int | None = None):
+        me = "Sequences"
+        for name, t, dims in (("starts", starts, 1), ("kv_lens", kv_lens, 1), ("page_table", page_table, 2)):
+            if t.dtype != torch.int32 or t.dim() != dims:
+                _refuse(me, f"{name} must be int32 with {dims} dimension{'s' * (dims > 1)}")
+        n = kv_lens.shape[0]
+        _matrix(starts, (n + 1,), me, "starts")
+        width = page_table.shape[1]
+        _matrix(page_table, (n, width), me, "page_table")
+        if not starts.is_contiguous() or not kv_lens.is_contiguous():
+            _refuse(me, "starts and kv_lens must be contiguous")
+        if max_rows is not None and max_rows < 0:
+            _refuse(me, f"max_rows={max_rows} is negative")
+        self.index = starts.get_device()
+        _on_gpu(me, self.index, starts, kv_lens, page_table)
+        self.tensors = (starts, kv_lens, page_table)
+        self.n_seqs, self.max_rows = n, max_rows
+        self._fields = (starts.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
+                        _ld(page_table, n, width, me) if width else 0, n)
+        self._width, self._args = width, {}
+
+    def args(self, rows: int) -> moe.moe_sequences:
+        """The call's argument for tensors of `rows` rows (one object for each
+        number of rows, never changed: two threads may hold it)."""
+        a = self._args.get(rows)
+        if a is None:
+            if len(self._args) >= 64:
+                self._args = {}
+            most = rows if self.max_rows is None else min(rows, self.max_rows)
+            a = self._args[rows] = moe.moe_sequences(*self._fields, rows, most, self._width)
+        return a
+
+
+class PagedCache:
+    """The paged keys and values of one layer (moe_kv_cache): k and v
+    [n_pages][page_size][kv_heads][head_dim] in bfloat16, float16 or
+    float8_e4m3fn, each head's elements contiguous, other strides free; for float8
+    also k_scale and v_scale, float32 [n_pages][page_size][kv_heads]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        me = "PagedCache"
+        quant = k.dtype == torch.float8_e4m3fn
+        if k.dtype not in (torch.bfloat16, torch.float16) and not quant:
+            _refuse(me, f"elements of type {k.dtype}")
+        if k.dim() != 4 or v.dtype != k.dtype or v.shape != k.shape:
+            _refuse(me, "k and v must have the same type and shape, [n_pages][page_size][kv_heads][head_dim]")
+        strides = self._strides(k)
+        if strides != self._strides(v) or strides[3] != 1:
+            _refuse(me, "k and v must have the same strides, their heads' elements contiguous")
+        scales = (0, 0, 0)
+        if quant:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None or t.dtype != torch.float32 or t.shape != k.shape[:3]:
+                    _refuse(me, f"{name} must be float32 {tuple(k.shape[:3])}")
+            scales = self._strides(k_scale)
+            if scales != self._strides(v_scale):
+                _refuse(me, "k_scale and v_scale must have the same strides")
+        elif k_scale is not None or v_scale is not None:
+            _refuse(me, f"a cache of type {k.dtype} has no scales")
+        self.index = k.get_device()
+        _on_gpu(me, self.index, k, v, k_scale, v_scale)
+        self.tensors = tuple(t for t in (k, v, k_scale, v_scale) if t is not None)
+        self.dtype, self.device = k.dtype, k.device
+        self.n_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        self.args = moe.moe_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if quant else None,
+                                     v_scale.data_ptr() if quant else None, *strides[:3], *scales,
+                                     moe.MOE_E4M3 if quant else _ELEM_TYPE[k.dtype], *k.shape)
+
+    @staticmethod
+    def _strides(t: torch.Tensor) -> tuple:
+        return tuple(s if n > 1 else 1 if i == 3 else 0 for i, (s, n) in enumerate(zip(t.stride(), t.shape)))
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
+        """A cache of its own memory, a page's slots head by head."""
+        new = lambda *s, t=dtype: torch.empty(*s, dtype=t, device=device).transpose(1, 2)  # noqa: E731
+        shape = (n_pages, kv_heads, page_size)
+        scales = [new(*shape, t=torch.float32) for _ in range(2)] if dtype == torch.float8_e4m3fn else []
+        return cls(new(*shape, head_dim), new(*shape, head_dim), *scales)
+
+    def _move(self, me, fn, seqs, k, v, stream):
+        rows = k.shape[0]
+        ld_k, ld_v = (_heads(t, rows, self.kv_heads, self.head_dim, me, n) for t, n in ((k, "k"), (v, "v")))
+        if k.dtype != v.dtype:
+            _refuse(me, f"k is of type {k.dtype}, v of {v.dtype}")
+        if not k.get_device() == v.get_device() == seqs.index == self.index or self.index != torch.cuda.current_device():
+            _on_gpu(me, self.index, k, v, *seqs.tensors)
+        other = None if stream is None else _other(self.device, stream)
+        if other is not None:
+            for t in self.tensors + seqs.tensors:
+                t.record_stream(other)
+        fn(self.args, seqs.args(rows), k.data_ptr(), ld_k, v.data_ptr(), ld_v, _type(k.dtype, me),
+           _stream(self.device, stream))
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, seqs: Sequences, stream=None) -> None:
+        """moe_cache_write of k and v [rows][kv_heads][head_dim]."""
+        self._move("PagedCache.write", moe.moe_cache_write, seqs, k, v, stream)
+
+    def read(self, seqs: Sequences, rows: int | None = None, out_type=None, k_out: torch.Tensor | None = None,
+             v_out: torch.Tensor | None = None, stream=None):
+        """moe_cache_read into k_out and v_out [rows][kv_heads][head_dim], allocated
+        unless given (as zeros, of `rows` rows).  Returns both."""
+        me = "PagedCache.read"
+        if (k_out is None) != (v_out is None) or k_out is None and rows is None:
+            _refuse(me, "k_out and v_out, or rows, must be given")
+        if k_out is None:
+            dtype = out_type or (torch.bfloat16 if self.dtype == torch.float8_e4m3fn else self.dtype)
+            other = _other(self.device, stream)
+            k_out, v_out = (_empty(self.device, other, dtype, rows, self.kv_heads, self.head_dim) for _ in range(2))
+            with torch.cuda.stream(other) if other is not None else contextlib.nullcontext():
+                k_out.zero_(), v_out.zero_()
+        self._move(me, moe.moe_cache_read, seqs, k_out, v_out, stream)
+        return k_out, v_out
+
+
+class PagedAttention:
+    """Attention of new tokens over paged caches (moe_attention_*).  Owns a
+    workspace that serves every layer with these heads, one call after another."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, device=None, stream=None):
+        me = "PagedAttention"
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.index = self.device.index
+        _on_gpu(me, self.index)
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.ws_bytes = moe.moe_attention_workspace_bytes(q_heads, kv_heads, head_dim)
+        if not self.ws_bytes:
+            _refuse(me, f"q_heads={q_heads}, kv_heads={kv_heads}, head_dim={head_dim}")
+        self.ws = _empty(self.device, _other(self.device, stream), torch.uint8, self.ws_bytes)
+        self.ws_ptr = self.ws.data_ptr()
+        moe.moe_attention_workspace_init(self.ws_ptr, self.ws_bytes, _stream(self.device, stream))
+
+    def __call__(self, q: torch.Tensor, cache: PagedCache, seqs: Sequences, scale: float | None = None, causal: bool = True,
+                 window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+        """q [rows][q_heads][head_dim] -> out of the same shape and type,
+        allocated unless given (rows of no sequence are then not set).  scale:
+        head_dim ** -0.5 unless given.  lse: float32 [rows][q_heads] to fill."""
+        me = "PagedAttention"
+        if cache.kv_heads != self.kv_heads or cache.head_dim != self.head_dim:
+            _refuse(me, f"the cache has {cache.kv_heads} heads of {cache.head_dim}, not {self.kv_heads} of {self.head_dim}")
+        ld_q = _heads(q, None, self.q_heads, self.head_dim, me, "q")
+        rows = q.shape[0]
+        index = self.index
+        if not q.get_device() == cache.index == seqs.index == index or index != torch.cuda.current_device():
+            _on_gpu(me, index, q, *cache.tensors, *seqs.tensors)
+        other = None if stream is None else _other(self.device, stream)
+        if other is not None:
+            for t in (self.ws, *cache.tensors, *seqs.tensors):
+                t.record_stream(other)
+        if out is None:
+            out = _empty(self.device, other, q.dtype, rows, self.q_heads, self.head_dim)
+            ld_out = self.q_heads * self.head_dim
+        else:
+            ld_out = _heads(out, rows, self.q_heads, self.head_dim, me, "out")
+            if out.dtype != q.dtype or out.get_device() != index:
+                _refuse(me, f"out is of type {out.dtype} on {out.device}, q of {q.dtype} on {q.device}")
+        lse_ptr = None
+        if lse is not None:
+            _matrix(lse, (rows, self.q_heads), me, "lse")
+            if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != index:
+                _refuse(me, "lse must be contiguous float32 on the same GPU")
+            lse_ptr = lse.data_ptr()
+        a = moe.moe_attention_args(q.data_ptr(), out.data_ptr(), lse_ptr, ld_q, ld_out, _type(q.dtype, me), self.q_heads,
+                                   int(causal), window, self.head_dim ** -0.5 if scale is None else scale)
+        moe.moe_attention(a, cache.args, seqs.args(rows), self.ws_ptr, self.ws_bytes, _stream(self.device, stream))
+        return out
+
+    def check(self, stream=None) -> int:
+        return moe.moe_attention_check(self.ws_ptr, _stream(self.device, stream))
 
 
 class DeviceLayer:

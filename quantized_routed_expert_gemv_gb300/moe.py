@@ -1,5 +1,5 @@
-"""Python binding of the C ABI in ``include/moe.h``, ``include/moe_block.h`` and
-``include/moe_fp8.h`` (ctypes, marshalling only).
+"""Python binding of the C ABI in ``include/moe.h``, ``include/moe_block.h``,
+``include/moe_fp8.h`` and ``include/moe_cache.h`` (ctypes, marshalling only).
 
 Every function keeps the C name and takes raw addresses (ints) for device and
 host buffers, exactly like the C call.  No step of the layer runs here: if
@@ -56,6 +56,8 @@ class moe_residency_stats_t(ctypes.Structure):
 
 # element types of the operators in include/moe_block.h
 MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+# and of the caches in include/moe_cache.h
+MOE_E4M3 = 3
 
 
 class moe_block_norm_args(ctypes.Structure):
@@ -73,6 +75,23 @@ class moe_token_logprobs_args(ctypes.Structure):
                 [("ld_logits", ctypes.c_int64)] +
                 [(n, ctypes.c_int32) for n in ("rows", "vocab", "logits_type", "n_targets", "top_n")] +
                 [("scale", ctypes.c_float)])
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] +
+                [(n, ctypes.c_int64) for n in ("page_stride", "slot_stride", "head_stride", "scale_page_stride",
+                                               "scale_slot_stride", "scale_head_stride")] +
+                [(n, ctypes.c_int32) for n in ("type", "n_pages", "page_size", "kv_heads", "head_dim")])
+
+
+class moe_sequences(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("starts", "kv_lens", "page_table")] + [("ld_table", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("n_seqs", "rows", "max_rows", "table_width")])
+
+
+class moe_attention_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "out", "lse")] + [(n, ctypes.c_int64) for n in ("ld_q", "ld_out")] +
+                [(n, ctypes.c_int32) for n in ("q_type", "q_heads", "causal", "window")] + [("scale", ctypes.c_float)])
 
 
 class MoEError(RuntimeError):
@@ -126,6 +145,15 @@ SIGNATURES = {
     "moe_fp8_check": (ctypes.c_int, [_vp, _vp, _vp]),
     "moe_fp8_quantize_weights": (ctypes.c_int, [_vp, _i32, ctypes.c_int64, _i32, _i32, _vp, ctypes.c_int64, _vp,
                                                 _vp]),
+    "moe_cache_write": (ctypes.c_int, [ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_sequences), _vp, ctypes.c_int64,
+                                       _vp, ctypes.c_int64, _i32, _vp]),
+    "moe_cache_read": (ctypes.c_int, [ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_sequences), _vp, ctypes.c_int64,
+                                      _vp, ctypes.c_int64, _i32, _vp]),
+    "moe_attention_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_attention_workspace_init": (ctypes.c_int, [_vp, _sz, _vp]),
+    "moe_attention": (ctypes.c_int, [ctypes.POINTER(moe_attention_args), ctypes.POINTER(moe_kv_cache),
+                                     ctypes.POINTER(moe_sequences), _vp, _sz, _vp]),
+    "moe_attention_check": (ctypes.c_int, [_vp, _vp]),
 }
 
 
@@ -310,3 +338,28 @@ def moe_fp8_check(w: int, ws: int, stream: int = 0) -> int:
 def moe_fp8_quantize_weights(weights, w_type, ld_w, n, k, codes, ld_codes, scales, stream=0) -> None:
     check(lib().moe_fp8_quantize_weights(weights, w_type, ld_w, n, k, codes, ld_codes, scales, stream),
           "moe_fp8_quantize_weights")
+
+
+def moe_cache_write(cache: moe_kv_cache, seqs: moe_sequences, k, ld_k, v, ld_v, type, stream=0) -> None:
+    check(lib().moe_cache_write(cache, seqs, k, ld_k, v, ld_v, type, stream), "moe_cache_write")
+
+
+def moe_cache_read(cache: moe_kv_cache, seqs: moe_sequences, k, ld_k, v, ld_v, type, stream=0) -> None:
+    check(lib().moe_cache_read(cache, seqs, k, ld_k, v, ld_v, type, stream), "moe_cache_read")
+
+
+def moe_attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().moe_attention_workspace_bytes(q_heads, kv_heads, head_dim))
+
+
+def moe_attention_workspace_init(ws: int, nbytes: int, stream: int = 0) -> None:
+    check(lib().moe_attention_workspace_init(ws, nbytes, stream), "moe_attention_workspace_init")
+
+
+def moe_attention(args: moe_attention_args, cache: moe_kv_cache, seqs: moe_sequences, ws, ws_bytes, stream=0) -> None:
+    check(lib().moe_attention(args, cache, seqs, ws, ws_bytes, stream), "moe_attention")
+
+
+def moe_attention_check(ws: int, stream: int = 0) -> int:
+    """Returns the device-latched status code (MOE_OK or MOE_ERR_TIMEOUT)."""
+    return int(lib().moe_attention_check(ws, stream))

@@ -18,7 +18,7 @@ BUILD = os.path.join(ROOT, "_build")
 SO = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "decode.cu", "decode_b1.cu", "decode_bt.cu", "prefill.cu", "residency.cu", "noalloc.cu",
            "rvq.cu", "block_norm.cu", "token_logprobs.cu", "fp8.cu", "cache.cu",
-           "attention.cu"]
+           "attention.cu", "attention_tc.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tcgen05.cuh", "tma.cuh", "gemv.cuh", "fused.cuh", "elem.cuh", "cache.cuh", "attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]

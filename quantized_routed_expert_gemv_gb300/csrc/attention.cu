@@ -28,39 +28,19 @@ int reportf(int code, const char* fmt, ...);
 
 namespace {
 
+// log2 of the factor that all exponentials carry: float16 holds fewer small
+// values than large ones, so the largest exponential is 2^15 there.
+template <bool F16>
+__host__ __device__ constexpr float exp_lift() {
+  return F16 ? 15.0f : 0.0f;
+}
+
 constexpr int kRows = 16;     // rows of a tile
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;     // positions of a warp's step
 constexpr int kBn = kWarps * kStep;
 constexpr size_t kCtlBytes = 256;
-constexpr float kLn2 = 0.69314718055994531f;
-
-// How the cache's elements and the query's type meet.
-enum Kind { kBf16, kF16, kE4m3Bf16, kE4m3F16 };
-template <int K>
-struct Traits {
-  static constexpr bool f16 = K == kF16 || K == kE4m3F16, e4m3 = K == kE4m3Bf16 || K == kE4m3F16;
-  static constexpr int size = e4m3 ? 1 : 2;
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -75,57 +55,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// The bytes s of {a, b} (0..3 of a, 4..7 of b), lowest first.
-__device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
-
-// What turns a head's e4m3 codes into 16-bit values of its scale.
-template <bool F16>
-struct Dequant;
-
-// bf16: a code's exponent and mantissa are bits 4 to 10 of a bf16 that is 2^-120
-// times the value; a scale of up to 2^7 is multiplied on with 2^120, a larger
-// one in a second product.  Both are powers of two: exact.
-template <>
-struct Dequant<false> {
-  __nv_bfloat162 m, more;
-  bool twice;
-  __device__ __forceinline__ void set(float s0, float s1) {
-    twice = __any_sync(0xFFFFFFFFu, s0 > 128.0f || s1 > 128.0f);
-    const float a0 = twice ? 1.329227995784916e36f : s0 * 1.329227995784916e36f;  // 2^120
-    const float a1 = twice ? 1.329227995784916e36f : s1 * 1.329227995784916e36f;
-    m = __floats2bfloat162_rn(a0, a1);
-    more = __floats2bfloat162_rn(s0, s1);
-  }
-  // codes in the high bytes of x's halves
-  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
-    const uint32_t bits = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
-    __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), m);
-    if (twice) v = __hmul2(v, more);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-};
-
-// f16: the hardware's conversion, then the scale; one beyond float16's powers
-// of two is multiplied on in two steps (the first one exact, the second one cut to
-// where any code but 0 is infinite).
-template <>
-struct Dequant<true> {
-  __half2 m, more;
-  bool twice;
-  __device__ __forceinline__ void set(float s0, float s1) {
-    twice = __any_sync(0xFFFFFFFFu, fmaxf(s0, s1) > 32768.0f || fminf(s0, s1) < 6.103515625e-05f);
-    const float c0 = fminf(fmaxf(s0, 6.103515625e-05f), 32768.0f), c1 = fminf(fmaxf(s1, 6.103515625e-05f), 32768.0f);
-    m = __floats2half2_rn(s0 == s0 ? c0 : s0, s1 == s1 ? c1 : s1);
-    more = __floats2half2_rn(fminf(s0 / c0, 32768.0f), fminf(s1 / c1, 32768.0f));
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
-    const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(bytes_of(x, 0, 0x31));
-    __half2 v = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)), m);
-    if (twice) v = __hmul2(v, more);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-};
 
 template <int DP, int K>
 struct Shape {
@@ -191,15 +120,6 @@ struct Values {
     }
   }
 };
-
-struct NoScale {};
-
-// Whether one of two 16-bit values is an infinity or a NaN.
-template <bool F16>
-__device__ __forceinline__ bool odd_value(uint32_t x) {
-  constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
-  return (x & e) == e || ((x >> 16) & e) == e;
-}
 
 template <int DP, int K>
 __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_kernel(const AttnArgs a) {
@@ -552,8 +472,6 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
 // ---- the join ---------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinItems = 8;                              // groups of four outputs at a time
-constexpr int kJoinLanes = kJoinThreads / kJoinItems;      // threads that share a group's parts
 
 // o, l and m of a group of four outputs.
 struct Part {
@@ -567,38 +485,37 @@ struct Part {
   }
 };
 
+// A group's parts are shared by `lanes` threads of a warp, a power of two that
+// covers them (32 at most), so that few parts leave no thread idle and many
+// are read at once; neighbouring groups lie in neighbouring threads.
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, int tile_rows, int type, float lift) {
-  __shared__ Part parts[kJoinThreads / 32][kJoinItems];
   pdl_wait();
-  const int item = threadIdx.x % kJoinItems, pl = threadIdx.x / kJoinItems, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int d4 = a.head_dim / 4;
   for (int which = 0; which < 2; ++which) {
     const Note n = a.notes[2 * blockIdx.x + which];
     if (n.count == 0) continue;
-    const int all = n.rows * d4, each = (all + n.count - 1) / n.count;
-    const int from = (blockIdx.x - n.c0) * each, to = min(all, from + each);
-    for (int i0 = from; i0 < to; i0 += kJoinItems) {
+    const int lanes = n.count > 16 ? 32 : n.count > 8 ? 16 : n.count > 4 ? 8 : n.count > 2 ? 4 : 2;
+    const int per_warp = 32 / lanes, item = lane & (per_warp - 1), first = lane / per_warp;
+    const int all = n.rows * d4, shares = n.count * gridDim.y, each = (all + shares - 1) / shares;
+    const int from = ((blockIdx.x - n.c0) * gridDim.y + blockIdx.y) * each, to = min(all, from + each);
+    for (int i0 = from + warp * per_warp; i0 < to; i0 += per_warp * (kJoinThreads / 32)) {
       const int i = i0 + item;
       const bool on = i < to;
       const int r = on ? i / d4 : 0, d = on ? (i - r * d4) * 4 : 0;
       Part p = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
       if (on)
-        for (int c = pl; c < n.count; c += kJoinLanes) {
+        for (int c = first; c < n.count; c += lanes) {
           const int64_t at = (2 * static_cast<int64_t>(n.c0 + c) + (c == 0 ? 1 : 0)) * tile_rows + r;
           p.add(a.part_ml[at * 2], a.part_ml[at * 2 + 1], *reinterpret_cast<const float4*>(a.part_o + at * a.head_dim + d));
         }
-#pragma unroll
-      for (int s = kJoinItems; s < 32; s <<= 1) {
+      for (int s = per_warp; s < 32; s <<= 1) {
         const float m2 = __shfl_xor_sync(0xFFFFFFFFu, p.m, s), l2 = __shfl_xor_sync(0xFFFFFFFFu, p.l, s);
         const float4 o2 = make_float4(__shfl_xor_sync(0xFFFFFFFFu, p.o.x, s), __shfl_xor_sync(0xFFFFFFFFu, p.o.y, s),
                                       __shfl_xor_sync(0xFFFFFFFFu, p.o.z, s), __shfl_xor_sync(0xFFFFFFFFu, p.o.w, s));
         p.add(m2, l2, o2);
       }
-      if ((threadIdx.x & 31) < kJoinItems) parts[warp][item] = p;
-      __syncthreads();
-      if (threadIdx.x < kJoinItems && on) {
-        p = parts[0][item];
-        for (int w = 1; w < kJoinThreads / 32; ++w) p.add(parts[w][item].m, parts[w][item].l, parts[w][item].o);
+      if (on && first == 0) {
         const int token = static_cast<int>(divide(n.row + r, a.by_group)), g = n.row + r - token * a.group;
         const int64_t row = n.first + token;
         const int head = n.head * a.group + g;
@@ -609,12 +526,15 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         if (d == 0 && a.lse)
           a.lse[row * a.kv_heads * a.group + head] = p.l == 0.0f ? -INFINITY : (p.m + (log2f(p.l) - lift)) * kLn2;
       }
-      __syncthreads();
     }
   }
 }
 
 // ---- host --------------------------------------------------------------------------
+
+// Rows of a sequence times query heads of a key head up to which tiles of 16
+// rows are taken.
+constexpr int kFewRows = 48;
 
 // CTAs of the widest grid that a workspace serves, on an SM.
 constexpr int kMaxCtas = 2;
@@ -668,7 +588,7 @@ int sm_count(int* sms) {
 
 cudaError_t launch_join(const AttnArgs& a, int grid, int tile_rows, bool f16, float lift, cudaStream_t st) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(grid), c.blockDim = dim3(kJoinThreads), c.stream = st;
+  c.gridDim = dim3(grid, tile_rows > kRows ? 4 : 1), c.blockDim = dim3(kJoinThreads), c.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -682,7 +602,8 @@ extern "C" size_t moe_attention_workspace_bytes(int32_t q_heads, int32_t kv_head
   using namespace moe;
   int sms = 0;
   if (!heads_ok(q_heads, kv_heads) || head_dim < 16 || head_dim > 256 || head_dim % 16 || sm_count(&sms)) return 0;
-  return parts_of(sms * kMaxCtas, kRows, head_dim).bytes;
+  const size_t few = parts_of(sms * kMaxCtas, kRows, head_dim).bytes, many = parts_of(sms, tiles_rows(head_dim), head_dim).bytes;
+  return few > many ? few : many;
 }
 
 extern "C" int moe_attention_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {
@@ -747,15 +668,18 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   const bool f16 = g.q_type == MOE_F16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  const int grid = sms * (c.head_dim <= 128 ? 2 : 1);
-  const Parts p = parts_of(grid, kRows, c.head_dim);
+  const bool many = static_cast<int64_t>(seqs->max_rows) * group > kFewRows;
+  const int grid = many ? sms : sms * (c.head_dim <= 128 ? 2 : 1), tile_rows = many ? tiles_rows(c.head_dim) : kRows;
+  const Parts p = parts_of(grid, tile_rows, c.head_dim);
   a.ctl = reinterpret_cast<unsigned*>(base);
   a.notes = reinterpret_cast<Note*>(base + p.notes);
   a.part_ml = reinterpret_cast<float*>(base + p.ml), a.part_o = reinterpret_cast<float*>(base + p.o);
-  e = c.head_dim <= 64    ? launch_rows<64>(a, kind, sms, st)
-      : c.head_dim <= 128 ? launch_rows<128>(a, kind, sms, st)
-                          : launch_rows<256>(a, kind, sms, st);
-  if (!e) e = launch_join(a, grid, kRows, f16, f16 ? exp_lift<true>() : exp_lift<false>(), st);
+  e = many                 ? launch_tiles(a, kind, sms, st)
+      : c.head_dim <= 64   ? launch_rows<64>(a, kind, sms, st)
+      : c.head_dim <= 128  ? launch_rows<128>(a, kind, sms, st)
+                           : launch_rows<256>(a, kind, sms, st);
+  if (!e)
+    e = launch_join(a, grid, tile_rows, f16, many ? tiles_lift(f16) : f16 ? exp_lift<true>() : exp_lift<false>(), st);
   if (e) return reportf(MOE_ERR_CUDA, "moe_attention: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
   return MOE_OK;
 }

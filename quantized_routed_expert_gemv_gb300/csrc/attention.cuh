@@ -25,6 +25,92 @@
 
 namespace moe {
 
+constexpr float kLn2 = 0.69314718055994531f;
+
+// How the cache's elements and the query's type meet.
+enum Kind { kBf16, kF16, kE4m3Bf16, kE4m3F16 };
+template <int K>
+struct Traits {
+  static constexpr bool f16 = K == kF16 || K == kE4m3F16, e4m3 = K == kE4m3Bf16 || K == kE4m3F16;
+  static constexpr int size = e4m3 ? 1 : 2;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The bytes s of {a, b} (0..3 of a, 4..7 of b), lowest first.
+__device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+// What turns a head's e4m3 codes into 16-bit values of its scale.
+template <bool F16>
+struct Dequant;
+
+// bf16: a code's exponent and mantissa are bits 4 to 10 of a bf16 that is 2^-120
+// times the value; a scale of up to 2^7 is multiplied on with 2^120, a larger
+// one in a second product.  Both are powers of two: exact.
+template <>
+struct Dequant<false> {
+  __nv_bfloat162 m, more;
+  bool twice;
+  __device__ __forceinline__ void set(float s0, float s1) {
+    twice = __any_sync(0xFFFFFFFFu, s0 > 128.0f || s1 > 128.0f);
+    const float a0 = twice ? 1.329227995784916e36f : s0 * 1.329227995784916e36f;  // 2^120
+    const float a1 = twice ? 1.329227995784916e36f : s1 * 1.329227995784916e36f;
+    m = __floats2bfloat162_rn(a0, a1);
+    more = __floats2bfloat162_rn(s0, s1);
+  }
+  // codes in the high bytes of x's halves
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    const uint32_t bits = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
+    __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), m);
+    if (twice) v = __hmul2(v, more);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+// f16: the hardware's conversion, then the scale; one beyond float16's powers
+// of two is multiplied on in two steps (the first one exact, the second one cut to
+// where any code but 0 is infinite).
+template <>
+struct Dequant<true> {
+  __half2 m, more;
+  bool twice;
+  __device__ __forceinline__ void set(float s0, float s1) {
+    twice = __any_sync(0xFFFFFFFFu, fmaxf(s0, s1) > 32768.0f || fminf(s0, s1) < 6.103515625e-05f);
+    const float c0 = fminf(fmaxf(s0, 6.103515625e-05f), 32768.0f), c1 = fminf(fmaxf(s1, 6.103515625e-05f), 32768.0f);
+    m = __floats2half2_rn(s0 == s0 ? c0 : s0, s1 == s1 ? c1 : s1);
+    more = __floats2half2_rn(fminf(s0 / c0, 32768.0f), fminf(s1 / c1, 32768.0f));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(bytes_of(x, 0, 0x31));
+    __half2 v = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)), m);
+    if (twice) v = __hmul2(v, more);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+// Whether one of two 16-bit values is an infinity or a NaN.
+template <bool F16>
+__device__ __forceinline__ bool odd_value(uint32_t x) {
+  constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+  return (x & e) == e || ((x >> 16) & e) == e;
+}
+
 struct AttnArgs {
   Seqs q;
   const void* query;
@@ -233,13 +319,9 @@ __device__ __forceinline__ void next_unit(const AttnArgs& a, Place& p, Seq& s) {
   } while (s.n == 0);
 }
 
-// log2 of the factor that all exponentials carry: float16 holds fewer small
-// values than large ones, so the largest exponential is 2^15 there.
-template <bool F16>
-__host__ __device__ constexpr float exp_lift() {
-  return F16 ? 15.0f : 0.0f;
-}
-
+cudaError_t launch_tiles(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st);
+int tiles_rows(int head_dim);   // rows of launch_tiles' tiles
+float tiles_lift(bool f16);     // its exponentials' factor, in powers of two
 cudaError_t launch_join(const AttnArgs& a, int grid, int tile_rows, bool f16, float lift, cudaStream_t st);
 
 }  // namespace moe

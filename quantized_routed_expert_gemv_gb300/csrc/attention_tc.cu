@@ -1,0 +1,781 @@
+// attention_tc.cu -- attention of many rows over the paged cache on the
+// fifth-generation tensor cores.
+//
+// Mathematics: as in attention.cu, a softmax in one pass with a running maximum
+// m, sum l and output o in fp32.  A row's reference m moves only when a tile's
+// maximum is more than 2^8 above it, so that o, which lies in tensor memory, is
+// seldom touched between products; exponentials reach 2^8 (float16 carries a
+// factor of 2^7 on top, as attention.cu's 2^15: 2^15 at most).
+//
+// Layout: a unit's tile (attention.cuh) has two halves of 128 rows (heads of up to
+// 128) or one (of 256).  z = q k^T is a product of M = 128 rows, N = the key
+// tile's positions, both operands in shared memory, the fp32 result in tensor
+// memory; a thread of the half's four warps has one row of it, takes exponentials
+// and stores them over z as 16-bit values, and o += p v takes them from there, v
+// being read position by position (N-major).  With two halves one's softmax runs
+// while the other's products do; with one half z has two buffers, so that the next
+// tile's product runs during a softmax.
+// Roles: eight warps (four with one half) take softmaxes, four bring keys and
+// values into a ring of tiles in 128-byte swizzled order (16-byte copies to places
+// looked up page by page, so that pages may have any size; e4m3 codes become 16-bit
+// values on the way), one issues the products.
+//
+// What a row does not see but its tile does (the diagonal, a window's edge) gets
+// exponential 0, which an infinity or a NaN among the values would turn into
+// NaN: rows whose output is not finite are looked at again one by one.
+//
+// Bound: the tensor cores.
+#include <cuda_runtime.h>
+
+#include "attention.cuh"
+#include "common.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kHalf = 128;         // rows of a half
+constexpr float kMove = 8.0f;      // how far the reference may lie below the maximum, in powers of two
+
+template <bool F16>
+__host__ __device__ constexpr float tile_lift() {
+  return F16 ? 7.0f : 0.0f;
+}
+
+template <int DP>
+struct Geo {
+  static constexpr int halves = DP <= 128 ? 2 : 1;
+  static constexpr int rows = halves * kHalf;
+  static constexpr int bn = DP <= 128 ? 128 : 64;
+  static constexpr int q_bytes = kHalf * DP * 2;        // of a half
+  static constexpr int stage_bytes = bn * DP * 2;       // a tile of keys or of values
+  static constexpr int stages = DP == 64 ? 6 : 4;
+  static constexpr int smem = halves * q_bytes + stages * stage_bytes + 1024;
+  // tensor memory columns: z (and p) at [0, 256), o from 256 on
+  static constexpr int z_cols = bn;
+  static constexpr int o_col = 256, o_cols = DP;
+};
+
+template <int DP>
+struct Shared {
+  using G = Geo<DP>;
+  uint64_t full[G::stages], empty[G::stages];
+  uint64_t z_full[2], p_ready[2], o_full[2], q_full[2], pv_done;
+  // Of the tiles under way.  A slow producer thread may be at tile t - 1 while a
+  // fast one writes tile t + 1; softmaxes may be three tiles behind.
+  int64_t off[4][G::bn];                 // byte offsets of a tile's positions, -1: none
+  float scale[4][2][G::bn];              // e4m3: of its keys and values
+  uint32_t bits[8][G::bn / 32];          // which of its positions count
+  uint32_t tmem;
+  int failed;
+  PlanSmem plan;
+};
+
+// K-major operand in 128-byte swizzled slabs of 64 elements.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= 1ull << 16;                                   // leading offset: unused with a swizzle
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // between groups of 8 rows
+  d |= 1ull << 46;                                   // descriptor version
+  d |= 2ull << 61;                                   // 128-byte swizzle
+  return d;
+}
+// N-major operand: rows are positions (K), a slab's 64 elements are N.
+__device__ __forceinline__ uint64_t desc_n(uint32_t saddr, uint32_t slab_bytes) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(slab_bytes >> 4) << 16;  // between slabs
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;        // between groups of 8 positions
+  d |= 1ull << 46;
+  d |= 2ull << 61;
+  return d;
+}
+
+template <bool F16>
+__host__ __device__ constexpr uint32_t idesc(uint32_t N, bool b_n_major) {
+  return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (b_n_major ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void reg_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// x * s - t of two values at once.
+__device__ __forceinline__ void fma_pair(float& a, float& b, float s, float t) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(t));
+}
+__device__ __forceinline__ void add_pair(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
+// Waits unless some role has given up; latches the error if this one does.
+template <class S>
+__device__ __forceinline__ bool wait(S& sm, const AttnArgs& a, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (*reinterpret_cast<volatile int*>(&sm.failed)) return false;
+  if (mbar_wait(bar, parity)) return true;
+  *reinterpret_cast<volatile int*>(&sm.failed) = 1;
+  latch_error(a.ctl, kErrTimeout);
+  return false;
+}
+
+// One CTA's pieces of units, in order: the same for every role.
+template <int DP>
+struct Walk {
+  using G = Geo<DP>;
+  Place at;
+  Seq seq;
+  Tile tile;
+  int64_t x, end;
+  int ta, tb;  // key tiles of this piece
+  __device__ __forceinline__ Walk(const AttnArgs& a, const Place& start, int64_t begin, int64_t end_) : at(start), x(begin), end(end_) {
+    seq = load_seq(a.q, at.seq);
+    if (x < end) cut(a);
+  }
+  __device__ __forceinline__ void cut(const AttnArgs& a) {
+    tile = tile_of<G::rows, G::bn>(a, seq, at.tile);
+    ta = tile.t0 + at.at;
+    tb = static_cast<int>(min(static_cast<int64_t>(tile.t1), ta + (end - x)));
+  }
+  __device__ __forceinline__ bool more() const { return x < end; }
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    x += tb - ta;
+    next_unit<G::rows>(a, at, seq);
+    if (x < end) cut(a);
+  }
+};
+
+// A cached 16-byte piece's eight 16-bit values as the products see them.
+template <int K>
+__device__ __forceinline__ uint4 values_at(const void* base, int64_t off, int d, float scale) {
+  using T = Traits<K>;
+  if constexpr (!T::e4m3) {
+    return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + off + d * 2);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + off + d);
+    // no warp-wide agreement here: both factors, whatever the scale
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
+      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+      r[i] = pack2(f.x * scale, f.y * scale, T::f16 ? MOE_F16 : MOE_BF16);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
+
+// What positions [k0, k1) add to a row's output, taken one position at a time, with
+// exponentials relative to `ref` (all lanes, one row): lane l returns the sums of
+// elements 4 l + 128 i to 4 l + 3 + 128 i.
+template <int DP, int K>
+__device__ __noinline__ void row_again(const AttnArgs& a, int seq, int head, const uint16_t* q, int k0, int k1, float ref,
+                                       float (&o)[(DP + 127) / 128][4]) {
+  using T = Traits<K>;
+  constexpr int type = T::f16 ? MOE_F16 : MOE_BF16;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < (DP + 127) / 128; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+  for (int b = k0; b < k1; b += 32) {
+    const int pos = b + lane;
+    int slot = 0;
+    const int page = pos < k1 ? page_of(a.q, seq, pos, slot) : -1;
+    const int64_t off = page * a.page_stride + slot * a.slot_stride + head * a.head_stride;
+    const int64_t soff = page * a.scale_page_stride + slot * a.scale_slot_stride + head * a.scale_head_stride;
+    float p = 0.0f, vs = 1.0f;
+    if (page >= 0) {
+      float ks = 1.0f, z = 0.0f;
+      if constexpr (T::e4m3) ks = a.k_scale[soff], vs = a.v_scale[soff];
+      for (int d = 0; d < a.head_dim; d += 8) {
+        float x[8], y[8];
+        unpack8(values_at<K>(a.k, off, d, ks), type, x);
+        unpack8(*reinterpret_cast<const uint4*>(q + d), type, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z = fmaf(x[i], y[i], z);
+      }
+      p = half_bits_to_f32(f32_to_half_bits(exp2_approx(fmaf(z, a.scale_log2, -ref)), type), type);
+    }
+    for (uint32_t m = __ballot_sync(0xFFFFFFFFu, page >= 0); m; m &= m - 1) {
+      const int l = __ffs(m) - 1;
+      const float w = __shfl_sync(0xFFFFFFFFu, p, l), s = __shfl_sync(0xFFFFFFFFu, vs, l);
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, off, l);
+#pragma unroll
+      for (int i = 0; i < (DP + 127) / 128; ++i) {
+        const int d = 4 * lane + 128 * i;
+        if (d < a.head_dim) {
+          float x[8];
+          unpack8(values_at<K>(a.v, at, d & ~7, s), type, x);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[i][c] = fmaf(w, x[(lane & 1) * 4 + c], o[i][c]);
+        }
+      }
+    }
+  }
+}
+
+// Whether a value among positions [k0, k1) is not finite (all lanes).
+template <int K>
+__device__ __noinline__ bool odd_values(const AttnArgs& a, int seq, int head, int k0, int k1) {
+  bool odd = false;
+  for (int pos = k0 + (threadIdx.x & 31); pos < k1; pos += 32) {
+    int slot = 0;
+    const int page = page_of(a.q, seq, pos, slot);
+    if (page < 0) continue;
+    const int64_t off = page * a.page_stride + slot * a.slot_stride + head * a.head_stride;
+    float s = 1.0f;
+    if constexpr (Traits<K>::e4m3) s = a.v_scale[page * a.scale_page_stride + slot * a.scale_slot_stride + head * a.scale_head_stride];
+    for (int d = 0; d < a.head_dim; d += 8) {
+      const uint4 u = values_at<K>(a.v, off, d, s);
+      odd |= odd_value<Traits<K>::f16>(u.x) || odd_value<Traits<K>::f16>(u.y) || odd_value<Traits<K>::f16>(u.z) ||
+             odd_value<Traits<K>::f16>(u.w);
+    }
+  }
+  return __any_sync(0xFFFFFFFFu, odd) != 0;
+}
+
+template <int DP, int K>
+__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP> w, int64_t total, int ctas,
+                                             int half, int wtid) {
+  using G = Geo<DP>;
+  using T = Traits<K>;
+  constexpr int type = T::f16 ? MOE_F16 : MOE_BF16, BN = G::bn;
+  const int lane = threadIdx.x & 31, warp = wtid >> 5;
+  const uint32_t tm = sm.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const uint32_t oaddr = tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0);
+  uint32_t n_tile = 0, n_piece = 0, tiles = 0;  // this half's tiles and pieces; all tiles of the CTA
+  for (; w.more(); w.next(a)) {
+    const int nt = w.tb - w.ta;
+    if (half * kHalf >= w.tile.rows) {
+      tiles += nt;
+      continue;
+    }
+    const int r = half * kHalf + wtid, rc = min(r, w.tile.rows - 1), row0 = w.at.tile * G::rows;
+    const bool valid = r < w.tile.rows;
+    const int token = static_cast<int>(divide(row0 + rc, a.by_group)), g = row0 + rc - token * a.group;
+    const int64_t row = w.seq.first + token;
+    const int head = w.at.head * a.group + g;
+    const uint16_t* q = static_cast<const uint16_t*>(a.query) + row * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
+    const int pos = w.seq.len - w.seq.n + token;
+    const int lo = sees_from(a, pos), hi = sees_to(a, w.seq.len, pos);
+    const bool some = half * kHalf + warp * 32 < w.tile.rows;  // the warp has rows
+    {
+      uint8_t* dst = qs + half * G::q_bytes + wtid * 128;
+#pragma unroll 4
+      for (int p = 0; p < DP / 8; ++p) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (valid && p * 8 < a.head_dim) u = *reinterpret_cast<const uint4*>(q + p * 8);
+        *reinterpret_cast<uint4*>(dst + (p / 8) * (kHalf * 128) + (((p & 7) ^ (wtid & 7)) << 4)) = u;
+      }
+      fence_async_smem();
+      mbar_arrive(&sm.q_full[half]);
+    }
+    const int all_lo = __reduce_max_sync(0xFFFFFFFFu, lo), all_hi = __reduce_min_sync(0xFFFFFFFFu, hi);
+    float m = -INFINITY, l = 0.0f;  // m: the reference, scaled
+#pragma unroll 1
+    for (int j = 0; j < nt; ++j, ++n_tile, ++tiles) {
+      const int buf = G::halves == 2 ? half : n_tile & 1;
+      const uint32_t zaddr = tm + buf * G::z_cols;
+      if (!wait(sm, a, &sm.z_full[buf], (G::halves == 2 ? n_tile : n_tile >> 1) & 1)) return;
+      tc_fence_after();
+      if (some) {
+        float z[BN];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tmem_ld32(zaddr + 32 * c, *reinterpret_cast<float(*)[32]>(&z[32 * c]));
+        tmem_wait();
+        const int first = (w.ta + j) * BN;
+        uint32_t ok = 0xFFFFFFFFu, bits[BN / 32];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) bits[c] = sm.bits[tiles & 7][c], ok &= bits[c];
+        if (first < all_lo || first + BN > all_hi || ok != 0xFFFFFFFFu) {
+          const int from = lo - first, to = hi - first;
+#pragma unroll
+          for (int k = 0; k < BN; ++k)
+            if (k < from || k >= to || !(bits[k / 32] >> (k & 31) & 1)) z[k] = -INFINITY;
+        }
+        float top[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int k = 4; k < BN; k += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = k + 4 + i < BN ? fmaxf(fmaxf(top[i], z[k + i]), z[k + 4 + i]) : fmaxf(top[i], z[k + i]);
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        const bool moves = mx > m + kMove || (m == -INFINITY && mx > m);
+        if (__any_sync(0xFFFFFFFFu, moves)) {
+          const float f = moves ? exp2_approx(m - mx) : 1.0f;
+          if (moves) m = mx;
+          l *= f;
+          if (j > 0) {
+            if (G::halves == 1 && !wait(sm, a, &sm.pv_done, (n_tile - 1) & 1)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < DP; c += 16) {
+              uint32_t v[16];
+              {
+                uint32_t x[8], y[8];
+                tmem_ld8(oaddr + c, x);
+                tmem_ld8(oaddr + c + 8, y);
+                tmem_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  v[i] = __float_as_uint(__uint_as_float(x[i]) * f), v[8 + i] = __float_as_uint(__uint_as_float(y[i]) * f);
+              }
+              tmem_st16(oaddr + c, v);
+            }
+          }
+        }
+        const float ref = tile_lift<T::f16>() - (m == -INFINITY ? 0.0f : m);
+        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            float &x0 = z[c + k], &x1 = z[c + k + 1], &x2 = z[c + k + 2], &x3 = z[c + k + 3];
+            fma_pair(x0, x1, a.scale_log2, ref);
+            fma_pair(x2, x3, a.scale_log2, ref);
+            x0 = exp2_approx(x0), x1 = exp2_approx(x1), x2 = exp2_approx(x2), x3 = exp2_approx(x3);
+            add_pair(s0, s1, x0, x1);
+            add_pair(s2, s3, x2, x3);
+            p[k / 2] = pack2(x0, x1, type), p[k / 2 + 1] = pack2(x2, x3, type);
+          }
+          tmem_st16(zaddr + c / 2, p);
+        }
+        l += (s0 + s1) + (s2 + s3);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.p_ready[buf]);
+    }
+
+    // the piece is done: this thread's row
+    if (!wait(sm, a, &sm.o_full[half], n_piece++ & 1)) return;
+    tc_fence_after();
+    if (!some) {
+      tc_fence_before();
+      continue;
+    }
+    const bool whole = w.ta == w.tile.t0 && w.tb == w.tile.t1;
+    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (w.ta == w.tile.t0 ? 1 : 0);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim;
+    float* po = a.part_o + (part * G::rows + r) * a.head_dim;
+    bool fine = true;
+#pragma unroll
+    for (int c = 0; c < DP; c += 32) {
+      float v[32];
+      tmem_ld32(oaddr + c, v);
+      tmem_wait();
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) fine &= fabsf(v[i + k]) < INFINITY || c + i >= a.head_dim;
+        if (valid && c + i < a.head_dim) {
+          if (whole) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = v[i + k] * inv;
+            *reinterpret_cast<uint4*>(out + c + i) = pack8(x, type);
+          } else {
+            *reinterpret_cast<float4*>(po + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            *reinterpret_cast<float4*>(po + c + i + 4) = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    if (valid) {
+      if (!whole) {
+        float* ml = a.part_ml + (part * G::rows + r) * 2;
+        ml[0] = m, ml[1] = l;
+      } else if (a.lse) {
+        a.lse[row * a.kv_heads * a.group + head] = l == 0.0f ? -INFINITY : (m + (log2f(l) - tile_lift<T::f16>())) * kLn2;
+      }
+    }
+    // rows that an unseen value may have spoilt
+    __syncwarp();
+    const int k0 = max(w.ta * BN, w.tile.lo), k1 = min(w.tb * BN, w.tile.hi);
+    const int v0 = max(k0, lo), v1 = min(k1, hi);
+    for (uint32_t bad = __ballot_sync(0xFFFFFFFFu, valid && !fine && (v0 > k0 || v1 < k1)); bad; bad &= bad - 1) {
+      const int src = __ffs(bad) - 1;
+      const int b0 = __shfl_sync(0xFFFFFFFFu, v0, src), b1 = __shfl_sync(0xFFFFFFFFu, v1, src);
+      const bool odd = odd_values<K>(a, w.at.seq, w.at.head, k0, min(b0, k1)) || odd_values<K>(a, w.at.seq, w.at.head, max(b1, k0), k1);
+      if (!odd) continue;
+      const float mr = __shfl_sync(0xFFFFFFFFu, m, src), f = __shfl_sync(0xFFFFFFFFu, inv, src);
+      const uint16_t* qr = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(q), src));
+      uint16_t* orow = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(out), src));
+      float* prow = reinterpret_cast<float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(po), src));
+      float o[(DP + 127) / 128][4];
+      row_again<DP, K>(a, w.at.seq, w.at.head, qr, b0, b1, (mr == -INFINITY ? 0.0f : mr) - tile_lift<T::f16>(), o);
+#pragma unroll
+      for (int i = 0; i < (DP + 127) / 128; ++i) {
+        const int d = 4 * lane + 128 * i;
+        if (d < a.head_dim) {
+          if (whole)
+            *reinterpret_cast<uint2*>(orow + d) = make_uint2(pack2(o[i][0] * f, o[i][1] * f, type), pack2(o[i][2] * f, o[i][3] * f, type));
+          else
+            *reinterpret_cast<float4*>(prow + d) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        }
+      }
+    }
+    if (!whole && half == 0 && wtid == 0) {
+      const int64_t unit0 = w.x - w.at.at, unit1 = unit0 + (w.tile.t1 - w.tile.t0);
+      Note n;
+      n.c0 = cta_of(unit0, total, ctas), n.count = cta_of(unit1 - 1, total, ctas) - n.c0 + 1;
+      n.row = row0, n.rows = w.tile.rows, n.first = w.seq.first, n.head = w.at.head;
+      a.notes[part] = n;
+    }
+  }
+}
+
+template <int DP, int K>
+__device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, Walk<DP> w, int tid) {
+  using G = Geo<DP>;
+  using T = Traits<K>;
+  constexpr int BN = G::bn;
+  constexpr int PR = DP * T::size / 16;      // 16-byte pieces of a position in the cache
+  constexpr int PER = BN * PR / 128;         // of a tile, for each thread
+  constexpr int LAG = 2;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int pieces = a.head_dim * T::size / 16;
+  const uint32_t ring_s = smem_u32(ring);
+  RingPos load, tell;
+  uint32_t tiles = 0, groups = 0;
+  // thread t looks up position t of the next tile
+  int64_t off = -1;
+  float ks = 0.0f, vs = 0.0f;
+  auto look_up = [&](const Walk<DP>& u, int j) {
+    off = -1;
+    const int pos = (u.ta + j) * BN + tid;
+    if (tid < BN && pos >= u.tile.lo && pos < u.tile.hi) {
+      int slot;
+      const int page = page_of(a.q, u.at.seq, pos, slot);
+      if (page >= 0) {
+        off = page * a.page_stride + slot * a.slot_stride + u.at.head * a.head_stride;
+        if constexpr (T::e4m3) {
+          const int64_t s = page * a.scale_page_stride + slot * a.scale_slot_stride + u.at.head * a.scale_head_stride;
+          ks = a.k_scale[s], vs = a.v_scale[s];
+        }
+      }
+    }
+  };
+  auto post = [&] {  // the looked-up tile, for all producers
+    if (tid < BN) {
+      const uint32_t on = __ballot_sync(0xFFFFFFFFu, off >= 0);
+      sm.off[tiles & 3][tid] = off;
+      if constexpr (T::e4m3) sm.scale[tiles & 3][0][tid] = ks, sm.scale[tiles & 3][1][tid] = vs;
+      if (lane == 0) sm.bits[tiles & 7][warp] = on;
+    }
+    named_bar(1, 128);
+  };
+  look_up(w, 0);
+  if constexpr (!T::e4m3) {
+    for (; w.more();) {
+      const int nt = w.tb - w.ta;
+      Walk<DP> u = w;
+      w.next(a);
+#pragma unroll 1
+      for (int j = 0; j < nt; ++j, ++tiles) {
+        post();
+        const int64_t* offs = sm.off[tiles & 3];
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++groups) {
+          if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) {
+            cp_wait<0>();
+            return;
+          }
+          const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k);
+          const uint32_t dst = ring_s + load.s * G::stage_bytes;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int n = tid + 128 * i, row = n / PR, c = n % PR;
+            const int64_t o = offs[row];
+            const bool on = o >= 0 && c < pieces;
+            cp_async16(dst + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                       on ? static_cast<const void*>(base + o + c * 16) : a.query, on);
+          }
+          cp_commit();
+          load.next(G::stages);
+          if (groups >= LAG) {
+            cp_wait<LAG>();
+            fence_async_smem();
+            mbar_arrive(&sm.full[tell.s]);
+            tell.next(G::stages);
+          }
+          if (kv == 0) {
+            if (j + 1 < nt) look_up(u, j + 1);
+            else if (w.more()) look_up(w, 0);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    fence_async_smem();
+    for (uint32_t i = groups < LAG ? groups : LAG; i; --i) {
+      mbar_arrive(&sm.full[tell.s]);
+      tell.next(G::stages);
+    }
+  } else {
+    // codes wait in registers, half a tile ahead
+    uint4 kb[PER], vb[PER];
+    auto fetch = [&](uint4 (&b)[PER], const void* base, uint32_t t) {
+      const int64_t* offs = sm.off[t & 3];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int n = tid + 128 * i, row = n / PR, c = n % PR;
+        const int64_t o = offs[row];
+        b[i] = make_uint4(0, 0, 0, 0);
+        if (o >= 0 && c < pieces) b[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + o + c * 16);
+      }
+    };
+    auto store = [&](const uint4 (&b)[PER], int kv, uint32_t t) {
+      if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return false;
+      uint8_t* dst = ring + load.s * G::stage_bytes;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int n = tid + 128 * i, row = n / PR, c = n % PR;
+        Dequant<T::f16> dq;
+        // a position that does not count has no scale: its codes, and values, are 0
+        const float s = sm.off[t & 3][row] >= 0 ? sm.scale[t & 3][kv][row] : 1.0f;
+        dq.set(s, s);
+        const uint32_t x[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        uint32_t v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[2 * k] = dq(bytes_of(x[k], 0, 0x1404)), v[2 * k + 1] = dq(bytes_of(x[k], 0, 0x3424));
+        uint8_t* at = dst + (c / 4) * (BN * 128) + row * 128;
+        const int p = (2 * c) & 7;
+        *reinterpret_cast<uint4*>(at + (((p) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4*>(at + (((p + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+      }
+      fence_async_smem();
+      mbar_arrive(&sm.full[load.s]);
+      load.next(G::stages);
+      ++groups;
+      return true;
+    };
+    if (w.more()) {
+      post();
+      fetch(kb, a.k, 0);
+    }
+    while (w.more()) {
+      const int nt = w.tb - w.ta;
+      Walk<DP> u = w;
+      w.next(a);
+#pragma unroll 1
+      for (int j = 0; j < nt; ++j) {
+        fetch(vb, a.v, tiles);
+        const bool more = j + 1 < nt || w.more();
+        if (j + 1 < nt) look_up(u, j + 1);
+        else if (w.more()) look_up(w, 0);
+        if (!store(kb, 0, tiles)) return;
+        ++tiles;
+        if (more) {
+          post();
+          fetch(kb, a.k, tiles);
+        }
+        if (!store(vb, 1, tiles - 1)) return;
+      }
+    }
+  }
+}
+
+template <int DP, int K>
+__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint32_t qs, uint32_t ring, Walk<DP> w) {
+  using G = Geo<DP>;
+  using T = Traits<K>;
+  constexpr int BN = G::bn;
+  constexpr uint32_t id_z = idesc<T::f16>(BN, false), id_o = idesc<T::f16>(DP, true);
+  const uint32_t tm = sm.tmem;
+  RingPos p;                  // next tile to take, keys and values in turn
+  uint32_t n_p[2] = {0, 0};   // exponentials taken, by half or buffer
+  uint32_t n_q[2] = {0, 0};
+  auto z_product = [&](int half, int buf, int stage) {
+    const uint32_t k0 = ring + stage * G::stage_bytes, q0 = qs + half * G::q_bytes;
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+      mma_bf16(tm + buf * G::z_cols, desc_k(q0 + (k / 4) * (kHalf * 128) + (k & 3) * 32), desc_k(k0 + (k / 4) * (BN * 128) + (k & 3) * 32),
+               id_z, k > 0);
+    mma_commit(smem_u32(&sm.z_full[buf]));
+  };
+  auto o_product = [&](int half, int buf, int stage, bool more) {
+    const uint32_t v0 = ring + stage * G::stage_bytes;
+#pragma unroll
+    for (int k = 0; k < BN / 16; ++k)
+      mma_bf16_ta(tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0), tm + buf * G::z_cols + k * 8,
+                  desc_n(v0 + k * 2048, BN * 128), id_o, more || k > 0);
+  };
+  auto take = [&](RingPos& r) {  // waits for the tile at r and steps on; its stage, or -1
+    if (!wait(sm, a, &sm.full[r.s], r.ph)) return -1;
+    const int s = r.s;
+    r.next(G::stages);
+    return s;
+  };
+  for (; w.more(); w.next(a)) {
+    const int nt = w.tb - w.ta;
+    if constexpr (G::halves == 2) {
+      const int halves = w.tile.rows > kHalf ? 2 : 1;
+      int ks = take(p);
+      if (ks < 0) return;
+      for (int h = 0; h < halves; ++h) {
+        if (!wait(sm, a, &sm.q_full[h], n_q[h]++ & 1)) return;
+        tc_fence_after();
+        z_product(h, h, ks);
+      }
+      mma_commit(smem_u32(&sm.empty[ks]));
+      for (int j = 0; j < nt; ++j) {
+        const int vs = take(p);
+        if (vs < 0) return;
+        if (j + 1 < nt) ks = p.s;  // the next keys follow these values
+        for (int h = 0; h < halves; ++h) {
+          if (!wait(sm, a, &sm.p_ready[h], n_p[h]++ & 1)) return;
+          tc_fence_after();
+          o_product(h, h, vs, j > 0);
+          if (h == halves - 1) mma_commit(smem_u32(&sm.empty[vs]));
+          if (j + 1 < nt) {
+            if (h == 0 && take(p) < 0) return;
+            z_product(h, h, ks);
+            if (h == halves - 1) mma_commit(smem_u32(&sm.empty[ks]));
+          } else {
+            mma_commit(smem_u32(&sm.o_full[h]));
+          }
+        }
+      }
+    } else {
+      // tiles in the ring: k0 v0 k1 v1 ...; products: z0 z1 o0 z2 o1 ...
+      if (!wait(sm, a, &sm.q_full[0], n_q[0]++ & 1)) return;
+      tc_fence_after();
+      const uint32_t base = n_p[0] + n_p[1];  // tiles before this piece: their parity names the buffers
+      int ks = take(p);
+      if (ks < 0) return;
+      z_product(0, base & 1, ks);
+      mma_commit(smem_u32(&sm.empty[ks]));
+      for (int j = 0; j < nt; ++j) {
+        RingPos v = p;
+        p.next(G::stages);
+        if (j + 1 < nt) {
+          ks = take(p);
+          if (ks < 0) return;
+          z_product(0, (base + j + 1) & 1, ks);
+          mma_commit(smem_u32(&sm.empty[ks]));
+        }
+        const int vs = take(v), buf = (base + j) & 1;
+        if (vs < 0 || !wait(sm, a, &sm.p_ready[buf], n_p[buf]++ & 1)) return;
+        tc_fence_after();
+        o_product(0, buf, vs, j > 0);
+        mma_commit(smem_u32(&sm.empty[vs]));
+        mma_commit(smem_u32(&sm.pv_done));
+        if (j + 1 == nt) mma_commit(smem_u32(&sm.o_full[0]));
+      }
+    }
+  }
+}
+
+template <int DP, int K>
+__global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const AttnArgs a) {
+  using G = Geo<DP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Shared<DP> sm;
+  uint8_t* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t* ring = base + G::halves * G::q_bytes;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  pdl_launch_dependents();
+  int ctas;
+  int64_t begin, end;
+  Place start;
+  const int64_t total = find_work<G::rows, G::bn, kThreads>(a, sm.plan, ctas, begin, end, start);
+  if (tid < 2) a.notes[2 * blockIdx.x + tid].count = 0;
+  if (begin == end) return;
+  if (tid == 0) {
+    for (int i = 0; i < G::stages; ++i) mbar_init(&sm.full[i], 128), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < 2; ++i)
+      mbar_init(&sm.z_full[i], 1), mbar_init(&sm.p_ready[i], kHalf), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.q_full[i], kHalf);
+    mbar_init(&sm.pv_done, 1);
+    sm.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+  }
+  if (warp == 12) tmem_alloc(smem_u32(&sm.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  {
+    const Walk<DP> w(a, start, begin, end);
+    // registers: 2 x 128 x 184 + 128 x 104 + 128 x 40 = 512 x 128
+    if (warp < 8) {
+      reg_up<184>();
+      if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, total, ctas, warp >> 2, tid & 127);
+    } else if (warp < 12) {
+      reg_down<104>();
+      producer_role<DP, K>(a, sm, ring, w, tid - 256);
+    } else {
+      reg_down<40>();
+      if (tid == 384) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring), w);
+    }
+  }
+  if (tid == 384 && *reinterpret_cast<volatile int*>(&sm.failed)) {
+    // products in flight end before the memory they use is given back
+    mma_commit(smem_u32(&sm.pv_done));
+    const unsigned long long t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {}
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(sm.tmem, 512);
+}
+
+template <int DP, int K>
+cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
+  auto kernel = attention_tiles_kernel<DP, K>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<DP>::smem);
+  if (e) return e;
+  kernel<<<num_sms, kThreads, Geo<DP>::smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int DP>
+cudaError_t launch(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st) {
+  switch (k) {
+    case kBf16: return launch<DP, kBf16>(a, num_sms, st);
+    case kF16: return launch<DP, kF16>(a, num_sms, st);
+    case kE4m3Bf16: return launch<DP, kE4m3Bf16>(a, num_sms, st);
+    default: return launch<DP, kE4m3F16>(a, num_sms, st);
+  }
+}
+
+}  // namespace
+
+int tiles_rows(int head_dim) { return head_dim <= 64 ? Geo<64>::rows : head_dim <= 128 ? Geo<128>::rows : Geo<256>::rows; }
+float tiles_lift(bool f16) { return f16 ? tile_lift<true>() : tile_lift<false>(); }
+
+cudaError_t launch_tiles(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st) {
+  return a.head_dim <= 64    ? launch<64>(a, k, num_sms, st)
+         : a.head_dim <= 128 ? launch<128>(a, k, num_sms, st)
+                             : launch<256>(a, k, num_sms, st);
+}
+
+}  // namespace moe

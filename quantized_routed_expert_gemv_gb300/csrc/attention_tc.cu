@@ -58,6 +58,40 @@ struct Geo {
   static constexpr int o_col = 256, o_cols = DP;
 };
 
+// One CTA's pieces of units, in order: the same for every role.  Each warp has
+// one in shared memory, which its first lane moves on: registers are short.
+template <int DP>
+struct Walk {
+  using G = Geo<DP>;
+  Place at;
+  Seq seq;
+  Tile tile;
+  int64_t x, end;
+  int ta, tb;  // key tiles of this piece
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Place& start, int64_t from, int64_t to) {
+    at = start, x = from, end = to;
+    seq = load_seq(a.q, at.seq);
+    cut(a);
+  }
+  __device__ __forceinline__ void cut(const AttnArgs& a) {
+    tile = tile_of<G::rows, G::bn>(a, seq, at.tile);
+    ta = tile.t0 + at.at;
+    tb = static_cast<int>(min(static_cast<int64_t>(tile.t1), ta + (end - x)));
+  }
+  __device__ __forceinline__ bool more() const { return x < end; }
+  // all lanes of the warp
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) step(a);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void step(const AttnArgs& a) {
+    x += tb - ta;
+    next_unit<G::rows>(a, at, seq);
+    if (x < end) cut(a);
+  }
+};
+
 template <int DP>
 struct Shared {
   using G = Geo<DP>;
@@ -70,26 +104,29 @@ struct Shared {
   uint32_t bits[8][G::bn / 32];          // which of its positions count
   uint32_t tmem;
   int failed;
+  Walk<DP> walk[13];
   PlanSmem plan;
 };
 
-// K-major operand in 128-byte swizzled slabs of 64 elements.
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
-  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= 1ull << 16;                                   // leading offset: unused with a swizzle
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // between groups of 8 rows
-  d |= 1ull << 46;                                   // descriptor version
-  d |= 2ull << 61;                                   // 128-byte swizzle
-  return d;
+// Descriptors of operands in 128-byte swizzled slabs of 64 elements.  Upper half:
+// 1024 bytes between groups of 8 rows (or positions), descriptor version 1,
+// 128-byte swizzle; lower half: start address >> 4 and, of an N-major operand (rows are
+// positions, a slab's 64 elements are N), the distance between slabs.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t slab_bytes) { return (saddr >> 4) | (slab_bytes >> 4) << 16; }
+
+// D[tmem] (+)= A[smem] * B[smem]^T and A[tmem] * B[smem], issued by one thread.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(id), "r"(accumulate), "n"(kDescHi));
 }
-// N-major operand: rows are positions (K), a slab's 64 elements are N.
-__device__ __forceinline__ uint64_t desc_n(uint32_t saddr, uint32_t slab_bytes) {
-  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(slab_bytes >> 4) << 16;  // between slabs
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;        // between groups of 8 positions
-  d |= 1ull << 46;
-  d |= 2ull << 61;
-  return d;
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(id), "r"(accumulate), "n"(kDescHi));
 }
 
 template <bool F16>
@@ -134,41 +171,17 @@ __device__ __forceinline__ void add_pair(float& a, float& b, float x, float y) {
 }
 
 // Waits unless some role has given up; latches the error if this one does.
-template <class S>
-__device__ __forceinline__ bool wait(S& sm, const AttnArgs& a, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (*reinterpret_cast<volatile int*>(&sm.failed)) return false;
+__device__ __forceinline__ bool wait_long(unsigned* ctl, int* failed, uint64_t* bar, uint32_t parity) {
+  if (*reinterpret_cast<volatile int*>(failed)) return false;
   if (mbar_wait(bar, parity)) return true;
-  *reinterpret_cast<volatile int*>(&sm.failed) = 1;
-  latch_error(a.ctl, kErrTimeout);
+  *reinterpret_cast<volatile int*>(failed) = 1;
+  latch_error(ctl, kErrTimeout);
   return false;
 }
-
-// One CTA's pieces of units, in order: the same for every role.
-template <int DP>
-struct Walk {
-  using G = Geo<DP>;
-  Place at;
-  Seq seq;
-  Tile tile;
-  int64_t x, end;
-  int ta, tb;  // key tiles of this piece
-  __device__ __forceinline__ Walk(const AttnArgs& a, const Place& start, int64_t begin, int64_t end_) : at(start), x(begin), end(end_) {
-    seq = load_seq(a.q, at.seq);
-    if (x < end) cut(a);
-  }
-  __device__ __forceinline__ void cut(const AttnArgs& a) {
-    tile = tile_of<G::rows, G::bn>(a, seq, at.tile);
-    ta = tile.t0 + at.at;
-    tb = static_cast<int>(min(static_cast<int64_t>(tile.t1), ta + (end - x)));
-  }
-  __device__ __forceinline__ bool more() const { return x < end; }
-  __device__ __forceinline__ void next(const AttnArgs& a) {
-    x += tb - ta;
-    next_unit<G::rows>(a, at, seq);
-    if (x < end) cut(a);
-  }
-};
+template <class S>
+__device__ __forceinline__ bool wait(S& sm, const AttnArgs& a, uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_long(a.ctl, &sm.failed, bar, parity);
+}
 
 // A cached 16-byte piece's eight 16-bit values as the products see them.
 template <int K>
@@ -259,7 +272,7 @@ __device__ __noinline__ bool odd_values(const AttnArgs& a, int seq, int head, in
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP> w, int64_t total, int ctas,
+__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP>& w, int64_t total, int ctas,
                                              int half, int wtid) {
   using G = Geo<DP>;
   using T = Traits<K>;
@@ -452,7 +465,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, Walk<DP> w, int tid) {
+__device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, Walk<DP>& w, int tid) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn;
@@ -467,16 +480,20 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm,
   // thread t looks up position t of the next tile
   int64_t off = -1;
   float ks = 0.0f, vs = 0.0f;
-  auto look_up = [&](const Walk<DP>& u, int j) {
+  struct View {
+    int first, nt, lo, hi, seq, head;
+  };
+  auto view = [&] { return View{w.ta * BN, w.tb - w.ta, w.tile.lo, w.tile.hi, w.at.seq, w.at.head}; };
+  auto look_up = [&](const View& u, int j) {
     off = -1;
-    const int pos = (u.ta + j) * BN + tid;
-    if (tid < BN && pos >= u.tile.lo && pos < u.tile.hi) {
+    const int pos = u.first + j * BN + tid;
+    if (tid < BN && pos >= u.lo && pos < u.hi) {
       int slot;
-      const int page = page_of(a.q, u.at.seq, pos, slot);
+      const int page = page_of(a.q, u.seq, pos, slot);
       if (page >= 0) {
-        off = page * a.page_stride + slot * a.slot_stride + u.at.head * a.head_stride;
+        off = page * a.page_stride + slot * a.slot_stride + u.head * a.head_stride;
         if constexpr (T::e4m3) {
-          const int64_t s = page * a.scale_page_stride + slot * a.scale_slot_stride + u.at.head * a.scale_head_stride;
+          const int64_t s = page * a.scale_page_stride + slot * a.scale_slot_stride + u.head * a.scale_head_stride;
           ks = a.k_scale[s], vs = a.v_scale[s];
         }
       }
@@ -491,11 +508,11 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm,
     }
     named_bar(1, 128);
   };
-  look_up(w, 0);
+  look_up(view(), 0);
   if constexpr (!T::e4m3) {
-    for (; w.more();) {
-      const int nt = w.tb - w.ta;
-      Walk<DP> u = w;
+    while (w.more()) {
+      const View u = view();
+      const int nt = u.nt;
       w.next(a);
 #pragma unroll 1
       for (int j = 0; j < nt; ++j, ++tiles) {
@@ -527,7 +544,7 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm,
           }
           if (kv == 0) {
             if (j + 1 < nt) look_up(u, j + 1);
-            else if (w.more()) look_up(w, 0);
+            else if (w.more()) look_up(view(), 0);
           }
         }
       }
@@ -582,15 +599,15 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm,
       fetch(kb, a.k, 0);
     }
     while (w.more()) {
-      const int nt = w.tb - w.ta;
-      Walk<DP> u = w;
+      const View u = view();
+      const int nt = u.nt;
       w.next(a);
 #pragma unroll 1
       for (int j = 0; j < nt; ++j) {
         fetch(vb, a.v, tiles);
         const bool more = j + 1 < nt || w.more();
         if (j + 1 < nt) look_up(u, j + 1);
-        else if (w.more()) look_up(w, 0);
+        else if (w.more()) look_up(view(), 0);
         if (!store(kb, 0, tiles)) return;
         ++tiles;
         if (more) {
@@ -604,29 +621,33 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm,
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint32_t qs, uint32_t ring, Walk<DP> w) {
+__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint32_t qs, uint32_t ring, Walk<DP>& w) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn;
   constexpr uint32_t id_z = idesc<T::f16>(BN, false), id_o = idesc<T::f16>(DP, true);
   const uint32_t tm = sm.tmem;
   RingPos p;                  // next tile to take, keys and values in turn
-  uint32_t n_p[2] = {0, 0};   // exponentials taken, by half or buffer
-  uint32_t n_q[2] = {0, 0};
+  uint32_t ph_p = 0, ph_q = 0;  // parities of p_ready (by half or buffer) and of q_full, a bit each
+  uint32_t tile0 = 0;         // one half: parity of the piece's first tile, which names its buffer
+  auto flip = [](uint32_t& ph, int i) {
+    const uint32_t was = ph >> i & 1;
+    ph ^= 1u << i;
+    return was;
+  };
   auto z_product = [&](int half, int buf, int stage) {
-    const uint32_t k0 = ring + stage * G::stage_bytes, q0 = qs + half * G::q_bytes;
+    const uint32_t k0 = desc_lo(ring + stage * G::stage_bytes, 16), q0 = desc_lo(qs + half * G::q_bytes, 16);
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k)
-      mma_bf16(tm + buf * G::z_cols, desc_k(q0 + (k / 4) * (kHalf * 128) + (k & 3) * 32), desc_k(k0 + (k / 4) * (BN * 128) + (k & 3) * 32),
-               id_z, k > 0);
+      mma_ss(tm + buf * G::z_cols, q0 + ((k / 4) * (kHalf * 128) + (k & 3) * 32) / 16, k0 + ((k / 4) * (BN * 128) + (k & 3) * 32) / 16,
+             id_z, k > 0);
     mma_commit(smem_u32(&sm.z_full[buf]));
   };
   auto o_product = [&](int half, int buf, int stage, bool more) {
-    const uint32_t v0 = ring + stage * G::stage_bytes;
+    const uint32_t v0 = desc_lo(ring + stage * G::stage_bytes, BN * 128);
 #pragma unroll
     for (int k = 0; k < BN / 16; ++k)
-      mma_bf16_ta(tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0), tm + buf * G::z_cols + k * 8,
-                  desc_n(v0 + k * 2048, BN * 128), id_o, more || k > 0);
+      mma_ts(tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0), tm + buf * G::z_cols + k * 8, v0 + k * 128, id_o, more || k > 0);
   };
   auto take = [&](RingPos& r) {  // waits for the tile at r and steps on; its stage, or -1
     if (!wait(sm, a, &sm.full[r.s], r.ph)) return -1;
@@ -634,14 +655,14 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
     r.next(G::stages);
     return s;
   };
-  for (; w.more(); w.next(a)) {
+  for (; w.more(); w.step(a)) {
     const int nt = w.tb - w.ta;
     if constexpr (G::halves == 2) {
       const int halves = w.tile.rows > kHalf ? 2 : 1;
       int ks = take(p);
       if (ks < 0) return;
       for (int h = 0; h < halves; ++h) {
-        if (!wait(sm, a, &sm.q_full[h], n_q[h]++ & 1)) return;
+        if (!wait(sm, a, &sm.q_full[h], flip(ph_q, h))) return;
         tc_fence_after();
         z_product(h, h, ks);
       }
@@ -651,7 +672,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
         if (vs < 0) return;
         if (j + 1 < nt) ks = p.s;  // the next keys follow these values
         for (int h = 0; h < halves; ++h) {
-          if (!wait(sm, a, &sm.p_ready[h], n_p[h]++ & 1)) return;
+          if (!wait(sm, a, &sm.p_ready[h], flip(ph_p, h))) return;
           tc_fence_after();
           o_product(h, h, vs, j > 0);
           if (h == halves - 1) mma_commit(smem_u32(&sm.empty[vs]));
@@ -666,9 +687,10 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
       }
     } else {
       // tiles in the ring: k0 v0 k1 v1 ...; products: z0 z1 o0 z2 o1 ...
-      if (!wait(sm, a, &sm.q_full[0], n_q[0]++ & 1)) return;
+      if (!wait(sm, a, &sm.q_full[0], flip(ph_q, 0))) return;
       tc_fence_after();
-      const uint32_t base = n_p[0] + n_p[1];  // tiles before this piece: their parity names the buffers
+      const uint32_t base = tile0;
+      tile0 = (tile0 + nt) & 1;
       int ks = take(p);
       if (ks < 0) return;
       z_product(0, base & 1, ks);
@@ -683,7 +705,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
           mma_commit(smem_u32(&sm.empty[ks]));
         }
         const int vs = take(v), buf = (base + j) & 1;
-        if (vs < 0 || !wait(sm, a, &sm.p_ready[buf], n_p[buf]++ & 1)) return;
+        if (vs < 0 || !wait(sm, a, &sm.p_ready[buf], flip(ph_p, buf))) return;
         tc_fence_after();
         o_product(0, buf, vs, j > 0);
         mma_commit(smem_u32(&sm.empty[vs]));
@@ -723,16 +745,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
   __syncthreads();
   tc_fence_after();
   {
-    const Walk<DP> w(a, start, begin, end);
-    // registers: 2 x 128 x 184 + 128 x 104 + 128 x 40 = 512 x 128
+    Walk<DP>& w = sm.walk[warp < 13 ? warp : 12];
+    if (warp < 13 && (tid & 31) == 0) w.begin(a, start, begin, end);
+    __syncwarp();
+    // registers: 2 x 128 x 184 + 128 x 96 + 128 x 48 = 512 x 128
     if (warp < 8) {
       reg_up<184>();
       if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, total, ctas, warp >> 2, tid & 127);
     } else if (warp < 12) {
-      reg_down<104>();
+      reg_down<96>();
       producer_role<DP, K>(a, sm, ring, w, tid - 256);
     } else {
-      reg_down<40>();
+      reg_down<48>();
       if (tid == 384) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring), w);
     }
   }

@@ -25,6 +25,7 @@
 // NaN: rows whose output is not finite are looked at again one by one.
 //
 // Bound: the tensor cores.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
@@ -99,7 +100,8 @@ struct Shared {
   uint64_t z_full[2], p_ready[2], o_full[2], q_full[2], pv_done;
   // Of the tiles under way.  A slow producer thread may be at tile t - 1 while a
   // fast one writes tile t + 1; softmaxes may be three tiles behind.
-  int64_t off[4][G::bn];                 // byte offsets of a tile's positions, -1: none
+  int64_t off[4][G::bn];                 // byte offsets of a tile's positions, -1: not seen
+  int2 place[4][G::bn];                  // their pages and slots
   float scale[4][2][G::bn];              // e4m3: of its keys and values
   uint32_t bits[8][G::bn / 32];          // which of its positions count
   uint32_t tmem;
@@ -428,10 +430,10 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
         a.lse[row * a.kv_heads * a.group + head] = l == 0.0f ? -INFINITY : (m + (log2f(l) - tile_lift<T::f16>())) * kLn2;
       }
     }
-    // rows that an unseen value may have spoilt
+    // rows that an unseen value of the tiles may have spoilt
     __syncwarp();
-    const int k0 = max(w.ta * BN, w.tile.lo), k1 = min(w.tb * BN, w.tile.hi);
-    const int v0 = max(k0, lo), v1 = min(k1, hi);
+    const int k0 = w.ta * BN, k1 = min(w.tb * BN, w.seq.len);
+    const int v0 = min(max(k0, lo), max(k0, k1)), v1 = min(k1, hi);
     for (uint32_t bad = __ballot_sync(0xFFFFFFFFu, valid && !fine && (v0 > k0 || v1 < k1)); bad; bad &= bad - 1) {
       const int src = __ffs(bad) - 1;
       const int b0 = __shfl_sync(0xFFFFFFFFu, v0, src), b1 = __shfl_sync(0xFFFFFFFFu, v1, src);
@@ -464,49 +466,65 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
   }
 }
 
+// Tiled loads of the cache's pages: boxes of `rows` positions of one head (0: pages
+// that no box of 8 positions divides, or no pages).
+struct alignas(64) Maps {
+  CUtensorMap k, v;
+  int rows;
+  Divisor row_boxes;  // boxes that a slab of a tile takes
+};
+
+// Box of 64 elements and `rows` slots of (head, page) to shared memory,
+// completion counted on `bar` in bytes; elements past the head's end are zeros.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int d, int slot, int head, int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int DP, int K>
-__device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, Walk<DP>& w, int tid) {
+__device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& maps, Shared<DP>& sm, uint8_t* ring, Walk<DP>& w, int tid) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn;
   constexpr int PR = DP * T::size / 16;      // 16-byte pieces of a position in the cache
   constexpr int PER = BN * PR / 128;         // of a tile, for each thread
-  constexpr int LAG = 2;
   const int lane = tid & 31, warp = tid >> 5;
   const int pieces = a.head_dim * T::size / 16;
   const uint32_t ring_s = smem_u32(ring);
-  RingPos load, tell;
+  RingPos load;
   uint32_t tiles = 0, groups = 0;
   // thread t looks up position t of the next tile
-  int64_t off = -1;
+  int page = -1, slot = 0, head = 0;
+  bool seen = false;
   float ks = 0.0f, vs = 0.0f;
   struct View {
-    int first, nt, lo, hi, seq, head;
+    int first, nt, lo, hi, seq, head, len;
   };
-  auto view = [&] { return View{w.ta * BN, w.tb - w.ta, w.tile.lo, w.tile.hi, w.at.seq, w.at.head}; };
+  auto view = [&] { return View{w.ta * BN, w.tb - w.ta, w.tile.lo, w.tile.hi, w.at.seq, w.at.head, w.seq.len}; };
   auto look_up = [&](const View& u, int j) {
-    off = -1;
+    page = -1, head = u.head;
     const int pos = u.first + j * BN + tid;
-    if (tid < BN && pos >= u.lo && pos < u.hi) {
-      int slot;
-      const int page = page_of(a.q, u.seq, pos, slot);
-      if (page >= 0) {
-        off = page * a.page_stride + slot * a.slot_stride + u.head * a.head_stride;
-        if constexpr (T::e4m3) {
-          const int64_t s = page * a.scale_page_stride + slot * a.scale_slot_stride + u.head * a.scale_head_stride;
-          ks = a.k_scale[s], vs = a.v_scale[s];
-        }
+    if (tid < BN && pos < u.len) page = page_of(a.q, u.seq, pos, slot);
+    seen = page >= 0 && pos >= u.lo && pos < u.hi;
+    if constexpr (T::e4m3) {
+      if (seen) {
+        const int64_t s = page * a.scale_page_stride + slot * a.scale_slot_stride + head * a.scale_head_stride;
+        ks = a.k_scale[s], vs = a.v_scale[s];
       }
     }
   };
-  auto post = [&] {  // the looked-up tile, for all producers
+  // The looked-up tile, for all producers; whether all of its positions exist.
+  auto post = [&] {
     if (tid < BN) {
-      const uint32_t on = __ballot_sync(0xFFFFFFFFu, off >= 0);
-      sm.off[tiles & 3][tid] = off;
+      const uint32_t on = __ballot_sync(0xFFFFFFFFu, seen);
+      sm.off[tiles & 3][tid] = seen ? page * a.page_stride + slot * a.slot_stride + head * a.head_stride : -1;
       if constexpr (T::e4m3) sm.scale[tiles & 3][0][tid] = ks, sm.scale[tiles & 3][1][tid] = vs;
+      else sm.place[tiles & 3][tid] = make_int2(page, slot);
       if (lane == 0) sm.bits[tiles & 7][warp] = on;
     }
-    named_bar(1, 128);
+    return !named_bar_or(1, 128, tid < BN && page < 0);
   };
   look_up(view(), 0);
   if constexpr (!T::e4m3) {
@@ -516,44 +534,41 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared<DP>& sm,
       w.next(a);
 #pragma unroll 1
       for (int j = 0; j < nt; ++j, ++tiles) {
-        post();
+        const bool all = post();
+        if (j + 1 < nt) look_up(u, j + 1);
+        else if (w.more()) look_up(view(), 0);
         const int64_t* offs = sm.off[tiles & 3];
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++groups) {
-          if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) {
-            cp_wait<0>();
-            return;
-          }
-          const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k);
+          if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return;
           const uint32_t dst = ring_s + load.s * G::stage_bytes;
+          if (all && maps.rows) {
+            if (tid == 0) mbar_arrive_expect_tx(&sm.full[load.s], G::stage_bytes);
+            else mbar_arrive(&sm.full[load.s]);
+            const int slab = static_cast<int>(divide(tid, maps.row_boxes)), row = (tid - slab * static_cast<int>(maps.row_boxes.d)) * maps.rows;
+            if (slab < DP / 64) {
+              const int2 at = sm.place[tiles & 3][row];
+              load_box(dst + slab * (BN * 128) + row * 128, kv ? &maps.v : &maps.k, slab * 64, at.y, u.head, at.x, &sm.full[load.s]);
+            }
+          } else {
+            // a tile that the sequence ends in, or whose pages are small: what does not count is zeros
+            const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k);
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int n = tid + 128 * i, row = n / PR, c = n % PR;
-            const int64_t o = offs[row];
-            const bool on = o >= 0 && c < pieces;
-            cp_async16(dst + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                       on ? static_cast<const void*>(base + o + c * 16) : a.query, on);
-          }
-          cp_commit();
-          load.next(G::stages);
-          if (groups >= LAG) {
-            cp_wait<LAG>();
+            for (int i = 0; i < PER; ++i) {
+              const int n = tid + 128 * i, row = n / PR, c = n % PR;
+              const int64_t o = offs[row];
+              const bool on = o >= 0 && c < pieces;
+              cp_async16(dst + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                         on ? static_cast<const void*>(base + o + c * 16) : a.query, on);
+            }
+            cp_commit();
+            cp_wait<0>();
             fence_async_smem();
-            mbar_arrive(&sm.full[tell.s]);
-            tell.next(G::stages);
+            mbar_arrive(&sm.full[load.s]);
           }
-          if (kv == 0) {
-            if (j + 1 < nt) look_up(u, j + 1);
-            else if (w.more()) look_up(view(), 0);
-          }
+          load.next(G::stages);
         }
       }
-    }
-    cp_wait<0>();
-    fence_async_smem();
-    for (uint32_t i = groups < LAG ? groups : LAG; i; --i) {
-      mbar_arrive(&sm.full[tell.s]);
-      tell.next(G::stages);
     }
   } else {
     // codes wait in registers, half a tile ahead
@@ -717,7 +732,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
 }
 
 template <int DP, int K>
-__global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const AttnArgs a, const __grid_constant__ Maps maps) {
   using G = Geo<DP>;
   extern __shared__ uint8_t raw[];
   __shared__ Shared<DP> sm;
@@ -754,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
       if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, total, ctas, warp >> 2, tid & 127);
     } else if (warp < 12) {
       reg_down<96>();
-      producer_role<DP, K>(a, sm, ring, w, tid - 256);
+      producer_role<DP, K>(a, maps, sm, ring, w, tid - 256);
     } else {
       reg_down<48>();
       if (tid == 384) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring), w);
@@ -772,12 +787,55 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
   if (warp == 12) tmem_dealloc(sm.tmem, 512);
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// The tensor (elements, slots, heads, pages) of keys or values of a 16-bit
+// cache.  False if the driver refuses it.
+bool encode(CUtensorMap* map, const void* base, const AttnArgs& a, int rows, bool f16) {
+  const EncodeFn fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim), a.q.page.d, static_cast<cuuint64_t>(a.kv_heads),
+                              static_cast<cuuint64_t>(a.q.n_pages)};
+  // a stride of 0 belongs to a dimension of 1 (or to places that are the same): any other does as well for the former
+  const auto step = [](int64_t s, cuuint64_t n) { return static_cast<cuuint64_t>(n == 1 && s == 0 ? 16 : s); };
+  const cuuint64_t strides[3] = {step(a.slot_stride, dims[1]), step(a.head_stride, dims[2]), step(a.page_stride, dims[3])};
+  for (const cuuint64_t s : strides)
+    if (s == 0 || s >= (1ull << 40)) return false;
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, one[4] = {1, 1, 1, 1};
+  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DP, int K>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
   auto kernel = attention_tiles_kernel<DP, K>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<DP>::smem);
   if (e) return e;
-  kernel<<<num_sms, kThreads, Geo<DP>::smem, st>>>(a);
+  Maps maps = {};
+  maps.row_boxes = divisor(1);
+  if (!Traits<K>::e4m3 && a.q.n_pages > 0) {
+    // the largest power of two that divides a page, up to a tile; a box starts on a swizzle's 1024 bytes from 8 on
+    int rows = static_cast<int>(a.q.page.d & (0u - a.q.page.d));
+    if (rows > Geo<DP>::bn) rows = Geo<DP>::bn;
+    if (rows >= 8 && encode(&maps.k, a.k, a, rows, Traits<K>::f16) && encode(&maps.v, a.v, a, rows, Traits<K>::f16)) {
+      maps.rows = rows;
+      maps.row_boxes = divisor(static_cast<uint32_t>(Geo<DP>::bn / rows));
+    }
+  }
+  kernel<<<num_sms, kThreads, Geo<DP>::smem, st>>>(a, maps);
   return cudaGetLastError();
 }
 

@@ -97,7 +97,7 @@ template <int DP>
 struct Shared {
   using G = Geo<DP>;
   uint64_t full[G::stages], empty[G::stages];
-  uint64_t z_full[2], p_ready[2], o_full[2], q_full[2], pv_done;
+  uint64_t z_full[2], p_half[2], p_ready[2], o_full[2], q_full[2], pv_done;
   // Of the tiles under way.  A slow producer thread may be at tile t - 1 while a
   // fast one writes tile t + 1; softmaxes may be three tiles behind.
   int64_t off[4][G::bn];                 // byte offsets of a tile's positions, -1: not seen
@@ -159,7 +159,14 @@ __device__ __forceinline__ void reg_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// x * s - t of two values at once.
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// x * s + t of two values at once.
 __device__ __forceinline__ void fma_pair(float& a, float& b, float s, float t) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
       "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
@@ -319,68 +326,92 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       tc_fence_after();
       if (some) {
         float z[BN];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_ld32(zaddr + 32 * c, *reinterpret_cast<float(*)[32]>(&z[32 * c]));
-        tmem_wait();
         const int first = (w.ta + j) * BN;
         uint32_t ok = 0xFFFFFFFFu, bits[BN / 32];
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) bits[c] = sm.bits[tiles & 7][c], ok &= bits[c];
-        if (first < all_lo || first + BN > all_hi || ok != 0xFFFFFFFFu) {
-          const int from = lo - first, to = hi - first;
+        const bool edge = first < all_lo || first + BN > all_hi || ok != 0xFFFFFFFFu;
+        auto load = [&] {
 #pragma unroll
-          for (int k = 0; k < BN; ++k)
-            if (k < from || k >= to || !(bits[k / 32] >> (k & 31) & 1)) z[k] = -INFINITY;
-        }
-        float top[4] = {z[0], z[1], z[2], z[3]};
+          for (int c = 0; c < BN / 32; ++c) tmem_ld32(zaddr + 32 * c, *reinterpret_cast<float(*)[32]>(&z[32 * c]));
+          tmem_wait();
+          if (edge) {
+            const int from = lo - first, to = hi - first;
 #pragma unroll
-        for (int k = 4; k < BN; k += 8)
+            for (int k = 0; k < BN; ++k)
+              if (k < from || k >= to || !(bits[k / 32] >> (k & 31) & 1)) z[k] = -INFINITY;
+          }
+        };
+        auto maximum = [&] {
+          float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top[i] = k + 4 + i < BN ? fmaxf(fmaxf(top[i], z[k + i]), z[k + 4 + i]) : fmaxf(top[i], z[k + i]);
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-        const bool moves = mx > m + kMove || (m == -INFINITY && mx > m);
-        if (__any_sync(0xFFFFFFFFu, moves)) {
+          for (int k = 4; k < BN; k += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top[i] = k + 4 + i < BN ? fmaxf(fmaxf(top[i], z[k + i]), z[k + 4 + i]) : fmaxf(top[i], z[k + i]);
+          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        };
+        float s[4];
+        // exponentials of positions [c, c + 32), as 16-bit values in p
+        auto take = [&](int c, float ref, uint32_t (&p)[16]) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            float x0 = z[c + k], x1 = z[c + k + 1], x2 = z[c + k + 2], x3 = z[c + k + 3];
+            fma_pair(x0, x1, a.scale_log2, ref);
+            fma_pair(x2, x3, a.scale_log2, ref);
+            x0 = exp2_approx(x0), x1 = exp2_approx(x1), x2 = exp2_approx(x2), x3 = exp2_approx(x3);
+            add_pair(s[0], s[1], x0, x1);
+            add_pair(s[2], s[3], x2, x3);
+            p[k / 2] = pack2(x0, x1, type), p[k / 2 + 1] = pack2(x2, x3, type);
+          }
+        };
+        load();
+        if (j == 0) m = maximum();
+        // The first half's exponentials are taken with the reference as it is while the
+        // maximum is found; where that is too far above it, they are taken again.
+        uint32_t pa[BN / 64][16];
+        float ref;
+        for (;;) {
+          ref = tile_lift<T::f16>() - (m == -INFINITY ? 0.0f : m);
+          s[0] = s[1] = s[2] = s[3] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) take(32 * c, ref, pa[c]);
+          const float mx = maximum();
+          const bool moves = mx > m + kMove || (m == -INFINITY && mx > m);
+          if (!__any_sync(0xFFFFFFFFu, moves)) break;
           const float f = moves ? exp2_approx(m - mx) : 1.0f;
           if (moves) m = mx;
           l *= f;
           if (j > 0) {
             if (G::halves == 1 && !wait(sm, a, &sm.pv_done, (n_tile - 1) & 1)) return;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DP; c += 16) {
-              uint32_t v[16];
-              {
-                uint32_t x[8], y[8];
-                tmem_ld8(oaddr + c, x);
-                tmem_ld8(oaddr + c + 8, y);
-                tmem_wait();
+              uint32_t x[8], y[8], v[16];
+              tmem_ld8(oaddr + c, x);
+              tmem_ld8(oaddr + c + 8, y);
+              tmem_wait();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  v[i] = __float_as_uint(__uint_as_float(x[i]) * f), v[8 + i] = __float_as_uint(__uint_as_float(y[i]) * f);
-              }
+              for (int i = 0; i < 8; ++i)
+                v[i] = __float_as_uint(__uint_as_float(x[i]) * f), v[8 + i] = __float_as_uint(__uint_as_float(y[i]) * f);
               tmem_st16(oaddr + c, v);
             }
           }
         }
-        const float ref = tile_lift<T::f16>() - (m == -INFINITY ? 0.0f : m);
-        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) {
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float &x0 = z[c + k], &x1 = z[c + k + 1], &x2 = z[c + k + 2], &x3 = z[c + k + 3];
-            fma_pair(x0, x1, a.scale_log2, ref);
-            fma_pair(x2, x3, a.scale_log2, ref);
-            x0 = exp2_approx(x0), x1 = exp2_approx(x1), x2 = exp2_approx(x2), x3 = exp2_approx(x3);
-            add_pair(s0, s1, x0, x1);
-            add_pair(s2, s3, x2, x3);
-            p[k / 2] = pack2(x0, x1, type), p[k / 2 + 1] = pack2(x2, x3, type);
-          }
-          tmem_st16(zaddr + c / 2, p);
-        }
-        l += (s0 + s1) + (s2 + s3);
+        for (int c = 0; c < BN / 64; ++c) tmem_st16(zaddr + 16 * c, pa[c]);
         tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_half[buf]);
+#pragma unroll
+        for (int c = BN / 64; c < BN / 32; ++c) {
+          take(32 * c, ref, pa[0]);
+          tmem_st16(zaddr + 16 * c, pa[0]);
+        }
+        l += (s[0] + s[1]) + (s[2] + s[3]);
+        tmem_wait_st();
+      } else {
+        mbar_arrive(&sm.p_half[buf]);
       }
       tc_fence_before();
       mbar_arrive(&sm.p_ready[buf]);
@@ -650,19 +681,36 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
     ph ^= 1u << i;
     return was;
   };
+  const bool lead = elect();
+  // loops stay rolled: the code of eight products is fetched anew each time, of one it is at hand
   auto z_product = [&](int half, int buf, int stage) {
-    const uint32_t k0 = desc_lo(ring + stage * G::stage_bytes, 16), q0 = desc_lo(qs + half * G::q_bytes, 16);
+    uint32_t k0 = desc_lo(ring + stage * G::stage_bytes, 16), q0 = desc_lo(qs + half * G::q_bytes, 16);
+    if (lead) {
+#pragma unroll 1
+      for (int c = 0; c < DP / 64; ++c, q0 += kHalf * 128 / 16, k0 += BN * 128 / 16)
 #pragma unroll
-    for (int k = 0; k < DP / 16; ++k)
-      mma_ss(tm + buf * G::z_cols, q0 + ((k / 4) * (kHalf * 128) + (k & 3) * 32) / 16, k0 + ((k / 4) * (BN * 128) + (k & 3) * 32) / 16,
-             id_z, k > 0);
-    mma_commit(smem_u32(&sm.z_full[buf]));
+        for (int k = 0; k < 4; ++k) mma_ss(tm + buf * G::z_cols, q0 + k * 2, k0 + k * 2, id_z, c > 0 || k > 0);
+      mma_commit(smem_u32(&sm.z_full[buf]));
+    }
   };
+  // the first half of the positions, then the second: their exponentials come one after the other
   auto o_product = [&](int half, int buf, int stage, bool more) {
-    const uint32_t v0 = desc_lo(ring + stage * G::stage_bytes, BN * 128);
+    const uint32_t parity = flip(ph_p, buf);
+    uint32_t v0 = desc_lo(ring + stage * G::stage_bytes, BN * 128), p0 = tm + buf * G::z_cols;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c, v0 += BN / 32 * 128, p0 += BN / 4) {
+      if (!wait(sm, a, c ? &sm.p_ready[buf] : &sm.p_half[buf], parity)) return false;
+      tc_fence_after();
+      if (lead) {
 #pragma unroll
-    for (int k = 0; k < BN / 16; ++k)
-      mma_ts(tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0), tm + buf * G::z_cols + k * 8, v0 + k * 128, id_o, more || k > 0);
+        for (int k = 0; k < BN / 32; ++k)
+          mma_ts(tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0), p0 + k * 8, v0 + k * 128, id_o, more || c > 0 || k > 0);
+      }
+    }
+    return true;
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (lead) mma_commit(smem_u32(bar));
   };
   auto take = [&](RingPos& r) {  // waits for the tile at r and steps on; its stage, or -1
     if (!wait(sm, a, &sm.full[r.s], r.ph)) return -1;
@@ -670,7 +718,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
     r.next(G::stages);
     return s;
   };
-  for (; w.more(); w.step(a)) {
+  for (; w.more(); w.next(a)) {
     const int nt = w.tb - w.ta;
     if constexpr (G::halves == 2) {
       const int halves = w.tile.rows > kHalf ? 2 : 1;
@@ -681,22 +729,20 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
         tc_fence_after();
         z_product(h, h, ks);
       }
-      mma_commit(smem_u32(&sm.empty[ks]));
+      commit(&sm.empty[ks]);
       for (int j = 0; j < nt; ++j) {
         const int vs = take(p);
         if (vs < 0) return;
         if (j + 1 < nt) ks = p.s;  // the next keys follow these values
         for (int h = 0; h < halves; ++h) {
-          if (!wait(sm, a, &sm.p_ready[h], flip(ph_p, h))) return;
-          tc_fence_after();
-          o_product(h, h, vs, j > 0);
-          if (h == halves - 1) mma_commit(smem_u32(&sm.empty[vs]));
+          if (!o_product(h, h, vs, j > 0)) return;
+          if (h == halves - 1) commit(&sm.empty[vs]);
           if (j + 1 < nt) {
             if (h == 0 && take(p) < 0) return;
             z_product(h, h, ks);
-            if (h == halves - 1) mma_commit(smem_u32(&sm.empty[ks]));
+            if (h == halves - 1) commit(&sm.empty[ks]);
           } else {
-            mma_commit(smem_u32(&sm.o_full[h]));
+            commit(&sm.o_full[h]);
           }
         }
       }
@@ -709,7 +755,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
       int ks = take(p);
       if (ks < 0) return;
       z_product(0, base & 1, ks);
-      mma_commit(smem_u32(&sm.empty[ks]));
+      commit(&sm.empty[ks]);
       for (int j = 0; j < nt; ++j) {
         RingPos v = p;
         p.next(G::stages);
@@ -717,15 +763,13 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
           ks = take(p);
           if (ks < 0) return;
           z_product(0, (base + j + 1) & 1, ks);
-          mma_commit(smem_u32(&sm.empty[ks]));
+          commit(&sm.empty[ks]);
         }
         const int vs = take(v), buf = (base + j) & 1;
-        if (vs < 0 || !wait(sm, a, &sm.p_ready[buf], flip(ph_p, buf))) return;
-        tc_fence_after();
-        o_product(0, buf, vs, j > 0);
-        mma_commit(smem_u32(&sm.empty[vs]));
-        mma_commit(smem_u32(&sm.pv_done));
-        if (j + 1 == nt) mma_commit(smem_u32(&sm.o_full[0]));
+        if (vs < 0 || !o_product(0, buf, vs, j > 0)) return;
+        commit(&sm.empty[vs]);
+        commit(&sm.pv_done);
+        if (j + 1 == nt) commit(&sm.o_full[0]);
       }
     }
   }
@@ -749,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
   if (tid == 0) {
     for (int i = 0; i < G::stages; ++i) mbar_init(&sm.full[i], 128), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&sm.z_full[i], 1), mbar_init(&sm.p_ready[i], kHalf), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.q_full[i], kHalf);
+      mbar_init(&sm.z_full[i], 1), mbar_init(&sm.p_half[i], kHalf), mbar_init(&sm.p_ready[i], kHalf), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.q_full[i], kHalf);
     mbar_init(&sm.pv_done, 1);
     sm.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -772,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
       producer_role<DP, K>(a, maps, sm, ring, w, tid - 256);
     } else {
       reg_down<48>();
-      if (tid == 384) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring), w);
+      if (warp == 12) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring), w);
     }
   }
   if (tid == 384 && *reinterpret_cast<volatile int*>(&sm.failed)) {

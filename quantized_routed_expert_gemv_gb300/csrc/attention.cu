@@ -588,7 +588,7 @@ int sm_count(int* sms) {
 
 cudaError_t launch_join(const AttnArgs& a, int grid, int tile_rows, bool f16, float lift, cudaStream_t st) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(grid, tile_rows > kRows ? 4 : 1), c.blockDim = dim3(kJoinThreads), c.stream = st;
+  c.gridDim = dim3(grid, tile_rows > kRows ? 16 : 1), c.blockDim = dim3(kJoinThreads), c.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

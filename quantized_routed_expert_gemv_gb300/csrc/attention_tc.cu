@@ -86,7 +86,18 @@ struct Walk {
     if ((threadIdx.x & 31) == 0) step(a);
     __syncwarp();
   }
+  // all lanes: a copy, and a copy one piece ahead
+  __device__ __forceinline__ void become(const Walk& o) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) *this = o;
+    __syncwarp();
+  }
+  __device__ __forceinline__ void follow(const AttnArgs& a, const Walk& o) {
+    become(o);
+    next(a);
+  }
   __device__ __forceinline__ void step(const AttnArgs& a) {
+    if (x >= end) return;
     x += tb - ta;
     next_unit<G::rows>(a, at, seq);
     if (x < end) cut(a);
@@ -102,11 +113,10 @@ struct Shared {
   // fast one writes tile t + 1; softmaxes may be three tiles behind.
   int64_t off[4][G::bn];                 // byte offsets of a tile's positions, -1: not seen
   int2 place[4][G::bn];                  // their pages and slots
-  float scale[4][2][G::bn];              // e4m3: of its keys and values
   uint32_t bits[8][G::bn / 32];          // which of its positions count
   uint32_t tmem;
   int failed;
-  Walk<DP> walk[13];
+  Walk<DP> walk[13], ahead[8];           // of each warp; the softmax warps' next pieces
   PlanSmem plan;
 };
 
@@ -281,7 +291,7 @@ __device__ __noinline__ bool odd_values(const AttnArgs& a, int seq, int head, in
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP>& w, int64_t total, int ctas,
+__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP>& w, Walk<DP>& nx, int64_t total, int ctas,
                                              int half, int wtid) {
   using G = Geo<DP>;
   using T = Traits<K>;
@@ -290,32 +300,48 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
   const uint32_t tm = sm.tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const uint32_t oaddr = tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0);
   uint32_t n_tile = 0, n_piece = 0, tiles = 0;  // this half's tiles and pieces; all tiles of the CTA
-  for (; w.more(); w.next(a)) {
+  // A piece's queries are on their way while the one before it ends: from its last
+  // product with the old ones on their place is free.
+  auto load_q = [&](const Walk<DP>& u) {
+    const int r = half * kHalf + wtid, row0 = u.at.tile * G::rows;
+    const int token = static_cast<int>(divide(row0 + min(r, u.tile.rows - 1), a.by_group)), g = row0 + r - token * a.group;
+    const uint16_t* q = static_cast<const uint16_t*>(a.query) + (u.seq.first + token) * a.ld_q +
+                        static_cast<int64_t>(u.at.head * a.group + g) * a.head_dim;
+    const uint32_t dst = smem_u32(qs) + half * G::q_bytes + wtid * 128;
+#pragma unroll 4
+    for (int p = 0; p < DP / 8; ++p) {
+      const bool on = r < u.tile.rows && p * 8 < a.head_dim;
+      cp_async16(dst + (p / 8) * (kHalf * 128) + (((p & 7) ^ (wtid & 7)) << 4), on ? q + p * 8 : a.query, on);
+    }
+    cp_commit();
+  };
+  auto hand_q = [&] {
+    cp_wait<0>();
+    fence_async_smem();
+    mbar_arrive(&sm.q_full[half]);
+  };
+  const auto here = [&](const Walk<DP>& u) { return u.more() && half * kHalf < u.tile.rows; };
+  nx.follow(a, w);
+  if (here(w)) {
+    load_q(w);
+    hand_q();
+  }
+  for (; w.more(); w.become(nx), nx.next(a)) {
     const int nt = w.tb - w.ta;
-    if (half * kHalf >= w.tile.rows) {
+    if (!here(w)) {
       tiles += nt;
+      if (here(nx)) {
+        load_q(nx);
+        hand_q();
+      }
       continue;
     }
     const int r = half * kHalf + wtid, rc = min(r, w.tile.rows - 1), row0 = w.at.tile * G::rows;
     const bool valid = r < w.tile.rows;
-    const int token = static_cast<int>(divide(row0 + rc, a.by_group)), g = row0 + rc - token * a.group;
-    const int64_t row = w.seq.first + token;
-    const int head = w.at.head * a.group + g;
-    const uint16_t* q = static_cast<const uint16_t*>(a.query) + row * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
+    const int token = static_cast<int>(divide(row0 + rc, a.by_group));
     const int pos = w.seq.len - w.seq.n + token;
     const int lo = sees_from(a, pos), hi = sees_to(a, w.seq.len, pos);
     const bool some = half * kHalf + warp * 32 < w.tile.rows;  // the warp has rows
-    {
-      uint8_t* dst = qs + half * G::q_bytes + wtid * 128;
-#pragma unroll 4
-      for (int p = 0; p < DP / 8; ++p) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (valid && p * 8 < a.head_dim) u = *reinterpret_cast<const uint4*>(q + p * 8);
-        *reinterpret_cast<uint4*>(dst + (p / 8) * (kHalf * 128) + (((p & 7) ^ (wtid & 7)) << 4)) = u;
-      }
-      fence_async_smem();
-      mbar_arrive(&sm.q_full[half]);
-    }
     const int all_lo = __reduce_max_sync(0xFFFFFFFFu, lo), all_hi = __reduce_min_sync(0xFFFFFFFFu, hi);
     float m = -INFINITY, l = 0.0f;  // m: the reference, scaled
 #pragma unroll 1
@@ -324,6 +350,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       const uint32_t zaddr = tm + buf * G::z_cols;
       if (!wait(sm, a, &sm.z_full[buf], (G::halves == 2 ? n_tile : n_tile >> 1) & 1)) return;
       tc_fence_after();
+      if (j == nt - 1 && here(nx)) load_q(nx);
       if (some) {
         float z[BN];
         const int first = (w.ta + j) * BN;
@@ -416,6 +443,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       tc_fence_before();
       mbar_arrive(&sm.p_ready[buf]);
     }
+    if (here(nx)) hand_q();
 
     // the piece is done: this thread's row
     if (!wait(sm, a, &sm.o_full[half], n_piece++ & 1)) return;
@@ -427,6 +455,8 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
     const bool whole = w.ta == w.tile.t0 && w.tb == w.tile.t1;
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (w.ta == w.tile.t0 ? 1 : 0);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int head = w.at.head * a.group + (row0 + rc - token * a.group);
+    const int64_t row = w.seq.first + token;
     uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim;
     float* po = a.part_o + (part * G::rows + r) * a.head_dim;
     bool fine = true;
@@ -471,6 +501,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       const bool odd = odd_values<K>(a, w.at.seq, w.at.head, k0, min(b0, k1)) || odd_values<K>(a, w.at.seq, w.at.head, max(b1, k0), k1);
       if (!odd) continue;
       const float mr = __shfl_sync(0xFFFFFFFFu, m, src), f = __shfl_sync(0xFFFFFFFFu, inv, src);
+      const uint16_t* q = static_cast<const uint16_t*>(a.query) + row * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
       const uint16_t* qr = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(q), src));
       uint16_t* orow = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(out), src));
       float* prow = reinterpret_cast<float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(po), src));
@@ -529,7 +560,6 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
   // thread t looks up position t of the next tile
   int page = -1, slot = 0, head = 0;
   bool seen = false;
-  float ks = 0.0f, vs = 0.0f;
   struct View {
     int first, nt, lo, hi, seq, head, len;
   };
@@ -539,130 +569,150 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
     const int pos = u.first + j * BN + tid;
     if (tid < BN && pos < u.len) page = page_of(a.q, u.seq, pos, slot);
     seen = page >= 0 && pos >= u.lo && pos < u.hi;
-    if constexpr (T::e4m3) {
-      if (seen) {
-        const int64_t s = page * a.scale_page_stride + slot * a.scale_slot_stride + head * a.scale_head_stride;
-        ks = a.k_scale[s], vs = a.v_scale[s];
-      }
-    }
   };
   // The looked-up tile, for all producers; whether all of its positions exist.
   auto post = [&] {
     if (tid < BN) {
       const uint32_t on = __ballot_sync(0xFFFFFFFFu, seen);
       sm.off[tiles & 3][tid] = seen ? page * a.page_stride + slot * a.slot_stride + head * a.head_stride : -1;
-      if constexpr (T::e4m3) sm.scale[tiles & 3][0][tid] = ks, sm.scale[tiles & 3][1][tid] = vs;
-      else sm.place[tiles & 3][tid] = make_int2(page, slot);
+      sm.place[tiles & 3][tid] = make_int2(page, slot);
       if (lane == 0) sm.bits[tiles & 7][warp] = on;
     }
     return !named_bar_or(1, 128, tid < BN && page < 0);
   };
   look_up(view(), 0);
-  if constexpr (!T::e4m3) {
-    while (w.more()) {
-      const View u = view();
-      const int nt = u.nt;
-      w.next(a);
+  while (w.more()) {
+    const View u = view();
+    const int nt = u.nt;
+    w.next(a);
 #pragma unroll 1
-      for (int j = 0; j < nt; ++j, ++tiles) {
-        const bool all = post();
-        if (j + 1 < nt) look_up(u, j + 1);
-        else if (w.more()) look_up(view(), 0);
-        const int64_t* offs = sm.off[tiles & 3];
+    for (int j = 0; j < nt; ++j, ++tiles) {
+      const bool all = post();
+      if (j + 1 < nt) look_up(u, j + 1);
+      else if (w.more()) look_up(view(), 0);
+      const int64_t* offs = sm.off[tiles & 3];
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++groups) {
-          if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return;
-          const uint32_t dst = ring_s + load.s * G::stage_bytes;
-          if (all && maps.rows) {
-            if (tid == 0) mbar_arrive_expect_tx(&sm.full[load.s], G::stage_bytes);
-            else mbar_arrive(&sm.full[load.s]);
-            const int slab = static_cast<int>(divide(tid, maps.row_boxes)), row = (tid - slab * static_cast<int>(maps.row_boxes.d)) * maps.rows;
-            if (slab < DP / 64) {
-              const int2 at = sm.place[tiles & 3][row];
-              load_box(dst + slab * (BN * 128) + row * 128, kv ? &maps.v : &maps.k, slab * 64, at.y, u.head, at.x, &sm.full[load.s]);
-            }
-          } else {
-            // a tile that the sequence ends in, or whose pages are small: what does not count is zeros
-            const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const int n = tid + 128 * i, row = n / PR, c = n % PR;
-              const int64_t o = offs[row];
-              const bool on = o >= 0 && c < pieces;
-              cp_async16(dst + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                         on ? static_cast<const void*>(base + o + c * 16) : a.query, on);
-            }
-            cp_commit();
-            cp_wait<0>();
-            fence_async_smem();
-            mbar_arrive(&sm.full[load.s]);
+      for (int kv = 0; kv < 2; ++kv, ++groups) {
+        if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return;
+        const uint32_t dst = ring_s + load.s * G::stage_bytes;
+        if (all && maps.rows) {
+          if (tid == 0) mbar_arrive_expect_tx(&sm.full[load.s], G::stage_bytes);
+          else mbar_arrive(&sm.full[load.s]);
+          const int slab = static_cast<int>(divide(tid, maps.row_boxes)), row = (tid - slab * static_cast<int>(maps.row_boxes.d)) * maps.rows;
+          if (slab < DP / 64) {
+            const int2 at = sm.place[tiles & 3][row];
+            load_box(dst + slab * (BN * 128) + row * 128, kv ? &maps.v : &maps.k, slab * 64, at.y, u.head, at.x, &sm.full[load.s]);
           }
-          load.next(G::stages);
+        } else {
+          // a tile that the sequence ends in, or whose pages are small: what does not count is zeros
+          const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int n = tid + 128 * i, row = n / PR, c = n % PR;
+            const int64_t o = offs[row];
+            const bool on = o >= 0 && c < pieces;
+            cp_async16(dst + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                       on ? static_cast<const void*>(base + o + c * 16) : a.query, on);
+          }
+          cp_commit();
+          cp_wait<0>();
+          fence_async_smem();
+          mbar_arrive(&sm.full[load.s]);
         }
+        load.next(G::stages);
       }
     }
-  } else {
-    // codes wait in registers, half a tile ahead
-    uint4 kb[PER], vb[PER];
-    auto fetch = [&](uint4 (&b)[PER], const void* base, uint32_t t) {
-      const int64_t* offs = sm.off[t & 3];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int n = tid + 128 * i, row = n / PR, c = n % PR;
-        const int64_t o = offs[row];
-        b[i] = make_uint4(0, 0, 0, 0);
-        if (o >= 0 && c < pieces) b[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + o + c * 16);
-      }
-    };
-    auto store = [&](const uint4 (&b)[PER], int kv, uint32_t t) {
-      if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return false;
-      uint8_t* dst = ring + load.s * G::stage_bytes;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int n = tid + 128 * i, row = n / PR, c = n % PR;
-        Dequant<T::f16> dq;
-        // a position that does not count has no scale: its codes, and values, are 0
-        const float s = sm.off[t & 3][row] >= 0 ? sm.scale[t & 3][kv][row] : 1.0f;
-        dq.set(s, s);
-        const uint32_t x[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-        uint32_t v[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[2 * k] = dq(bytes_of(x[k], 0, 0x1404)), v[2 * k + 1] = dq(bytes_of(x[k], 0, 0x3424));
-        uint8_t* at = dst + (c / 4) * (BN * 128) + row * 128;
-        const int p = (2 * c) & 7;
-        *reinterpret_cast<uint4*>(at + (((p) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<uint4*>(at + (((p + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
-      }
-      fence_async_smem();
-      mbar_arrive(&sm.full[load.s]);
-      load.next(G::stages);
-      ++groups;
-      return true;
-    };
-    if (w.more()) {
-      post();
-      fetch(kb, a.k, 0);
-    }
-    while (w.more()) {
-      const View u = view();
-      const int nt = u.nt;
-      w.next(a);
-#pragma unroll 1
-      for (int j = 0; j < nt; ++j) {
-        fetch(vb, a.v, tiles);
-        const bool more = j + 1 < nt || w.more();
-        if (j + 1 < nt) look_up(u, j + 1);
-        else if (w.more()) look_up(view(), 0);
-        if (!store(kb, 0, tiles)) return;
-        ++tiles;
-        if (more) {
-          post();
-          fetch(kb, a.k, tiles);
-        }
-        if (!store(vb, 1, tiles - 1)) return;
+  }
+}
+
+// As above for e4m3 caches: a thread has one position of each tile (with 64 of them, half a
+// position), whose codes wait in registers, half a tile ahead, and become 16-bit values on
+// their way to shared memory.  One scale a tile and thread, and no exchange but
+// of which positions count.
+template <int DP, int K>
+__device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, Walk<DP>& w, int tid) {
+  using G = Geo<DP>;
+  using T = Traits<K>;
+  constexpr int BN = G::bn, PER = DP / 16 * BN / 128;  // 16-byte pieces of a thread
+  const int lane = tid & 31, row = tid * BN / 128, piece0 = (tid & (128 / BN - 1)) * PER;
+  const int pieces = a.head_dim / 16;
+  RingPos load;
+  uint32_t tiles = 0, groups = 0;
+  struct At {
+    int64_t off, soff;  // -1: not seen
+  };
+  auto look_up = [&](int j) {  // tile j of the walk's piece
+    At at = {-1, 0};
+    const int pos = (w.ta + j) * BN + row;
+    if (pos >= w.tile.lo && pos < w.tile.hi) {
+      int slot;
+      const int page = page_of(a.q, w.at.seq, pos, slot), head = w.at.head;
+      if (page >= 0) {
+        at.off = page * a.page_stride + slot * a.slot_stride + head * a.head_stride;
+        at.soff = page * a.scale_page_stride + slot * a.scale_slot_stride + head * a.scale_head_stride;
       }
     }
+    return at;
+  };
+  auto fetch = [&](uint4 (&b)[PER], const void* base, const float* scales, const At& at, float& scale) {
+    scale = 1.0f;  // a position that does not count: zeros
+#pragma unroll
+    for (int i = 0; i < PER; ++i) b[i] = make_uint4(0, 0, 0, 0);
+    if (at.off >= 0) {
+      scale = scales[at.soff];
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at.off) + piece0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (piece0 + i < pieces) b[i] = p[i];
+    }
+  };
+  auto store = [&](const uint4 (&b)[PER], float scale) {
+    if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return false;
+    uint8_t* dst = ring + load.s * G::stage_bytes + row * 128;
+    Dequant<T::f16> dq;
+    dq.set(scale, scale);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t x[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+      uint32_t v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[2 * k] = dq(bytes_of(x[k], 0, 0x1404)), v[2 * k + 1] = dq(bytes_of(x[k], 0, 0x3424));
+      const int p = 2 * (piece0 + i);
+      uint8_t* at = dst + (p / 8) * (BN * 128);
+      *reinterpret_cast<uint4*>(at + (((p & 7) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4*>(at + ((((p + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+    fence_async_smem();
+    mbar_arrive(&sm.full[load.s]);
+    load.next(G::stages);
+    ++groups;
+    return true;
+  };
+  if (!w.more()) return;
+  uint4 kb[PER], vb[PER];
+  float ks, vs;
+  At at = look_up(0);
+  fetch(kb, a.k, a.k_scale, at, ks);
+  int j = 0, nt = w.tb - w.ta;
+  for (;;) {
+    fetch(vb, a.v, a.v_scale, at, vs);
+    // which positions count, before the keys are handed over
+    uint32_t on = __ballot_sync(0xFFFFFFFFu, at.off >= 0);
+    if (BN == 64) {  // two threads a position
+      on &= 0x55555555u;
+      on = (on | on >> 1) & 0x33333333u, on = (on | on >> 2) & 0x0F0F0F0Fu, on = (on | on >> 4) & 0x00FF00FFu, on = (on | on >> 8) & 0xFFFFu;
+      if (lane == 0) reinterpret_cast<uint16_t*>(sm.bits[tiles & 7])[tid >> 5] = static_cast<uint16_t>(on);
+    } else if (lane == 0) {
+      sm.bits[tiles & 7][tid >> 5] = on;
+    }
+    ++tiles;
+    if (++j == nt) w.next(a), j = 0, nt = w.tb - w.ta;
+    const bool more = j > 0 || w.more();
+    if (more) at = look_up(j);
+    if (!store(kb, ks)) return;
+    if (more) fetch(kb, a.k, a.k_scale, at, ks);
+    if (!store(vb, vs)) return;
+    if (!more) return;
   }
 }
 
@@ -810,10 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
     // registers: 2 x 128 x 184 + 128 x 96 + 128 x 48 = 512 x 128
     if (warp < 8) {
       reg_up<184>();
-      if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, total, ctas, warp >> 2, tid & 127);
+      if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, sm.ahead[warp & 7], total, ctas, warp >> 2, tid & 127);
     } else if (warp < 12) {
       reg_down<96>();
-      producer_role<DP, K>(a, maps, sm, ring, w, tid - 256);
+      if constexpr (Traits<K>::e4m3) dequant_role<DP, K>(a, sm, ring, w, tid - 256);
+      else producer_role<DP, K>(a, maps, sm, ring, w, tid - 256);
     } else {
       reg_down<48>();
       if (warp == 12) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring), w);

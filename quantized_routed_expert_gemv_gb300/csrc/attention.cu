@@ -131,12 +131,9 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gi = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
 
-  int ctas;
-  int64_t begin, end;
-  Place at;
-  const int64_t total = find_work<kRows, kBn, kThreads>(a, plan, ctas, begin, end, at);
+  const Work work = find_work<kRows, kBn, kThreads>(a, plan);
   if (tid < 2) a.notes[2 * blockIdx.x + tid].count = 0;
-  if (begin == end) return;
+  if (work.begin == work.end) return;
   __syncthreads();
 
   uint8_t* ring = smem + warp * S::ring_bytes;
@@ -147,12 +144,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
     __syncwarp();
   }
 
-  Seq seq = load_seq(a.q, at.seq);
-  for (int64_t x = begin; x < end;) {
+  Place at = work.at;
+  Seq seq = work.seq;
+  const int end = work.end;
+  for (int x = work.begin; x < end;) {
     const Tile tile = tile_of<kRows, kBn>(a, seq, at.tile);
     const int ta = tile.t0 + at.at;
-    const int tb = static_cast<int>(min(static_cast<int64_t>(tile.t1), ta + (end - x)));
-    const int64_t unit0 = x - at.at, unit1 = unit0 + (tile.t1 - tile.t0);
+    const int tb = min(tile.t1, ta + (end - x)), unit0 = x - at.at;
     const int row0 = at.tile * kRows;
 
     // the lane's two rows and what they see
@@ -455,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
     }
     if (!whole && tid == 0) {
       Note n;
-      n.c0 = cta_of(unit0, total, ctas), n.count = cta_of(unit1 - 1, total, ctas) - n.c0 + 1;
+      n.c0 = work.cta_of(unit0), n.count = work.cta_of(unit0 + tile.t1 - tile.t0 - 1) - n.c0 + 1;
       n.row = row0, n.rows = tile.rows, n.first = seq.first, n.head = at.head;
       a.notes[part] = n;
     }
@@ -485,9 +483,10 @@ struct Part {
   }
 };
 
-// A group's parts are shared by `lanes` threads of a warp, a power of two that
-// covers them (32 at most), so that few parts leave no thread idle and many
-// are read at once; neighbouring groups lie in neighbouring threads.
+// A group's parts are shared by `lanes` threads of a warp, a power of two, as far
+// as a block's share of the groups leaves threads for it (32 rows' parts of
+// 128 CTAs: 32 lanes; 256 rows' parts of 5: one); neighbouring groups lie in
+// neighbouring threads.
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, int tile_rows, int type, float lift) {
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -495,20 +494,33 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
   for (int which = 0; which < 2; ++which) {
     const Note n = a.notes[2 * blockIdx.x + which];
     if (n.count == 0) continue;
-    const int lanes = n.count > 16 ? 32 : n.count > 8 ? 16 : n.count > 4 ? 8 : n.count > 2 ? 4 : 2;
-    const int per_warp = 32 / lanes, item = lane & (per_warp - 1), first = lane / per_warp;
     const int all = n.rows * d4, shares = n.count * gridDim.y, each = (all + shares - 1) / shares;
+    int lanes = 1;
+    while (lanes < 32 && lanes < n.count && 2 * lanes * each <= kJoinThreads) lanes *= 2;
+    const int per_warp = 32 / lanes, item = lane & (per_warp - 1), first = lane / per_warp;
     const int from = ((blockIdx.x - n.c0) * gridDim.y + blockIdx.y) * each, to = min(all, from + each);
     for (int i0 = from + warp * per_warp; i0 < to; i0 += per_warp * (kJoinThreads / 32)) {
       const int i = i0 + item;
       const bool on = i < to;
       const int r = on ? i / d4 : 0, d = on ? (i - r * d4) * 4 : 0;
       Part p = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-      if (on)
-        for (int c = first; c < n.count; c += lanes) {
-          const int64_t at = (2 * static_cast<int64_t>(n.c0 + c) + (c == 0 ? 1 : 0)) * tile_rows + r;
-          p.add(a.part_ml[at * 2], a.part_ml[at * 2 + 1], *reinterpret_cast<const float4*>(a.part_o + at * a.head_dim + d));
+      constexpr int kBatch = 4;  // parts read at once
+      for (int c0 = first; c0 < n.count; c0 += lanes * kBatch) {
+        float2 ml[kBatch];
+        float4 o[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int c = c0 + b * lanes;
+          ml[b] = make_float2(-INFINITY, 0.0f), o[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (on && c < n.count) {
+            const int64_t at = (2 * static_cast<int64_t>(n.c0 + c) + (c == 0 ? 1 : 0)) * tile_rows + r;
+            ml[b] = __ldg(reinterpret_cast<const float2*>(a.part_ml) + at);
+            o[b] = __ldg(reinterpret_cast<const float4*>(a.part_o + at * a.head_dim + d));
+          }
         }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) p.add(ml[b].x, ml[b].y, o[b]);
+      }
       for (int s = per_warp; s < 32; s <<= 1) {
         const float m2 = __shfl_xor_sync(0xFFFFFFFFu, p.m, s), l2 = __shfl_xor_sync(0xFFFFFFFFu, p.l, s);
         const float4 o2 = make_float4(__shfl_xor_sync(0xFFFFFFFFu, p.o.x, s), __shfl_xor_sync(0xFFFFFFFFu, p.o.y, s),
@@ -641,6 +653,11 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   const int group = g.q_heads / c.kv_heads;
   if (static_cast<int64_t>(seqs->rows) * group > (1 << 30))
     return reportf(MOE_ERR_ARG, "moe_attention: %d rows of %d query heads a key head are more than 2^30", seqs->rows, group);
+  // key tiles of 64 positions, row tiles of 16 rows, at the worst
+  const int64_t row_tiles = (static_cast<int64_t>(seqs->rows) * group / kRows + seqs->n_seqs) * c.kv_heads;
+  if (row_tiles * (a.q.cap / kBn + 1) > 0x7FFFFFFF)
+    return reportf(MOE_ERR_UNSUPPORTED, "moe_attention: %d rows in %d sequences of up to %d positions are more than 2^31 tiles of work",
+                   seqs->rows, seqs->n_seqs, a.q.cap);
   if (!g.q || !g.out || !workspace) return reportf(MOE_ERR_ARG, "moe_attention: q, out or workspace is NULL");
   const int64_t width = static_cast<int64_t>(g.q_heads) * c.head_dim;
   if (g.ld_q < width || g.ld_out < width || g.ld_q % 8 || g.ld_out % 8)

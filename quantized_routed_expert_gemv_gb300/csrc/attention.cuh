@@ -177,132 +177,64 @@ struct Place {
 };
 
 // Key tiles of one head of the sequences of this warp's lanes (all lanes;
-// n = 0 for a lane without one): few row tiles a lane by itself, many by the
+// n = 0 for a lane without one): one row tile a lane by itself, more by the
 // whole warp.
 template <int R, int BN>
-__device__ __forceinline__ int64_t head_cost(const AttnArgs& a, const Seq& s) {
+__device__ __forceinline__ int head_cost(const AttnArgs& a, const Seq& s) {
   const int nt = row_tiles<R>(a, s), lane = threadIdx.x & 31;
-  int64_t cost = 0;
-  if (nt <= 2)
-    for (int r = 0; r < nt; ++r) {
-      const Tile t = tile_of<R, BN>(a, s, r);
-      cost += t.t1 - t.t0;
-    }
-  for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nt > 2); many; many &= many - 1) {
+  int cost = 0;
+  if (nt == 1) {
+    const Tile t = tile_of<R, BN>(a, s, 0);
+    cost = t.t1 - t.t0;
+  }
+#pragma unroll 1
+  for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nt > 1); many; many &= many - 1) {
     const int l = __ffs(many) - 1;
     Seq o;
     o.first = 0, o.n = __shfl_sync(0xFFFFFFFFu, s.n, l), o.len = __shfl_sync(0xFFFFFFFFu, s.len, l);
     const int tiles = row_tiles<R>(a, o);
-    int64_t sum = 0;
+    int sum = 0;
+#pragma unroll 1
     for (int r = lane; r < tiles; r += 32) {
       const Tile t = tile_of<R, BN>(a, o, r);
       sum += t.t1 - t.t0;
     }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
+    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
     if (lane == l) cost = sum;
   }
   return cost;
 }
 
+__device__ __forceinline__ int warp_scan(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
 struct PlanSmem {
-  int64_t warp_sum[32];
-  int64_t chunk_sum[kMaxSeqs / 128];
-  int64_t rem;
-  Place start;
+  int tiles[32];                  // of each warp's sequences
+  int chunk[kMaxSeqs / 128];      // of THREADS sequences at a time
+  int off;                        // where the CTA's first tile lies in its head's tiles
+  Place at;
+  Seq seq;
 };
 
-// All of a CTA's threads (THREADS, a multiple of 128) find the total T and
-// the place of this CTA's first tile.  Returns T; G, first and last tile by reference.
-template <int R, int BN, int THREADS>
-__device__ int64_t find_work(const AttnArgs& a, PlanSmem& sm, int& ctas, int64_t& begin, int64_t& end, Place& start) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunks = (a.q.n + THREADS - 1) / THREADS;
-  int64_t total = 0, before = 0;
-  int chunk_held = -1;
-  int64_t cost = 0, incl = 0;  // tiles of the chunk's sequences up to this thread's
-  auto scan = [&](int ch) {
-    const int s = ch * THREADS + tid;
-    Seq q = {0, 0, 0};
-    if (s < a.q.n) q = load_seq(a.q, s);
-    cost = head_cost<R, BN>(a, q);
-    incl = cost * a.kv_heads;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += up;
-    }
-    if (lane == 31) sm.warp_sum[warp] = incl;
-    __syncthreads();
-    int64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) incl += sm.warp_sum[w];
-      all += sm.warp_sum[w];
-    }
-    __syncthreads();
-    chunk_held = ch;
-    return all;
-  };
-  for (int ch = 0; ch < chunks; ++ch) {
-    const int64_t all = scan(ch);
-    if (tid == 0) sm.chunk_sum[ch] = all;
-    total += all;
+// A CTA's part of the line.  The host refuses calls that might have 2^31 tiles.
+struct Work {
+  int total, begin, end;  // tiles in all; this CTA's (none: begin = end)
+  int each, more;         // the first `more` CTAs have one tile more than `each`
+  Place at;               // of the first tile
+  Seq seq;
+  __device__ __forceinline__ int cut(int c) const { return each * c + min(c, more); }
+  __device__ __forceinline__ int cta_of(int x) const {  // the CTA that has tile x
+    const int wide = more * (each + 1);
+    return x < wide ? static_cast<uint32_t>(x) / (each + 1u) : more + static_cast<uint32_t>(x - wide) / each;
   }
-  const int64_t g = gridDim.x, c = blockIdx.x;
-  ctas = static_cast<int>(g < total ? g : total);
-  if (c >= ctas) {
-    begin = end = 0;
-    return total;
-  }
-  begin = total * c / ctas, end = total * (c + 1) / ctas;
-  __syncthreads();
-  int ch = 0;
-  for (; ch + 1 < chunks && before + sm.chunk_sum[ch] <= begin; ++ch) before += sm.chunk_sum[ch];
-  if (ch != chunk_held) scan(ch);
-  const int64_t mine = cost * a.kv_heads;
-  const bool here = before + incl > begin && before + incl - mine <= begin;
-  if (here) {
-    const int64_t off = begin - (before + incl - mine);
-    sm.start.seq = ch * THREADS + tid;
-    sm.start.head = static_cast<int>(off / cost);
-    sm.rem = off % cost;
-  }
-  __syncthreads();
-  if (warp == 0) {  // the row tile: 32 tiles at a time
-    const Seq s = load_seq(a.q, sm.start.seq);
-    int64_t rem = sm.rem;
-    const int tiles = row_tiles<R>(a, s);
-    for (int r0 = 0; r0 < tiles; r0 += 32) {
-      int n = 0;
-      if (r0 + lane < tiles) {
-        const Tile t = tile_of<R, BN>(a, s, r0 + lane);
-        n = t.t1 - t.t0;
-      }
-      int64_t up_to = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, up_to, o);
-        if (lane >= o) up_to += up;
-      }
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, up_to > rem);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        if (lane == l) sm.start.tile = r0 + l, sm.start.at = static_cast<int>(rem - (up_to - n));
-        break;
-      }
-      rem -= __shfl_sync(0xFFFFFFFFu, up_to, 31);
-    }
-  }
-  __syncthreads();
-  start = sm.start;
-  return total;
-}
-
-// The CTA that has tile x of T.
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int ctas) {
-  return static_cast<int>(((x + 1) * ctas - 1) / total);
-}
+};
 
 // Moves to the next unit (a sequence without rows has none).  The sequence's
 // values are loaded again where it changes.
@@ -317,6 +249,81 @@ __device__ __forceinline__ void next_unit(const AttnArgs& a, Place& p, Seq& s) {
     if (++p.seq >= a.q.n) return;
     s = load_seq(a.q, p.seq);
   } while (s.n == 0);
+}
+
+// All of a CTA's threads (THREADS, a multiple of 128) find its part of the line.
+// It runs once a CTA, from instructions that come from afar, so its time goes by
+// its length: few and narrow operations (with 64-bit ones and divisions for
+// every cut it took 6500 clocks instead of 4000 in front of 128 rows over 32768).
+template <int R, int BN, int THREADS>
+__device__ __forceinline__ Work find_work(const AttnArgs& a, PlanSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunks = (a.q.n + THREADS - 1) / THREADS;
+  Work w;
+  w.total = 0;
+  int cost, incl;  // tiles of a head of this thread's sequence, and of the chunk's sequences up to it
+  Seq mine;
+  int ch = 0, before = 0;
+  bool again = false;
+#pragma unroll 1
+  for (;;) {
+    mine = {0, 0, 0};
+    if (ch * THREADS + tid < a.q.n) mine = load_seq(a.q, ch * THREADS + tid);
+    cost = head_cost<R, BN>(a, mine);
+    incl = warp_scan(cost * a.kv_heads);
+    if (lane == 31) sm.tiles[warp] = incl;
+    __syncthreads();
+    const int v = lane < THREADS / 32 ? sm.tiles[lane] : 0;
+    const int all = __reduce_add_sync(0xFFFFFFFFu, v);
+    incl += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? v : 0);
+    if (again) break;
+    if (chunks > 1 && tid == 0) sm.chunk[ch] = all;
+    w.total += all;
+    if (chunks > 1) __syncthreads();
+    if (++ch < chunks) continue;
+    // its first and last tile
+    const int grid = gridDim.x, ctas = grid < w.total ? grid : w.total, c = blockIdx.x;
+    w.begin = w.end = 0;
+    if (c >= ctas) return w;
+    w.each = static_cast<uint32_t>(w.total) / static_cast<uint32_t>(ctas), w.more = w.total - w.each * ctas;
+    w.begin = w.cut(c), w.end = w.cut(c + 1);
+    if (chunks == 1) break;
+    for (ch = 0; ch + 1 < chunks && before + sm.chunk[ch] <= w.begin; ++ch) before += sm.chunk[ch];
+    again = true;
+  }
+  if (chunks == 1) ch = 0;
+  const int from = before + incl - cost * a.kv_heads;
+  if (from <= w.begin && w.begin < before + incl) {
+    const int off = w.begin - from, head = static_cast<uint32_t>(off) / static_cast<uint32_t>(cost);
+    sm.at.seq = ch * THREADS + tid, sm.at.head = head, sm.at.tile = 0, sm.at.at = sm.off = off - head * cost;
+    sm.seq = mine;
+  }
+  __syncthreads();
+  const int tiles = row_tiles<R>(a, sm.seq);
+  if (tiles > 1) {  // the row tile, 32 of them at a time
+    if (warp == 0) {
+      const Seq s = sm.seq;
+      int rem = sm.off;
+#pragma unroll 1
+      for (int r0 = 0; r0 < tiles; r0 += 32) {
+        int n = 0;
+        if (r0 + lane < tiles) {
+          const Tile t = tile_of<R, BN>(a, s, r0 + lane);
+          n = t.t1 - t.t0;
+        }
+        const int up_to = warp_scan(n);
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, up_to > rem);
+        if (past) {
+          if (lane == __ffs(past) - 1) sm.at.tile = r0 + lane, sm.at.at = rem - (up_to - n);
+          break;
+        }
+        rem -= __shfl_sync(0xFFFFFFFFu, up_to, 31);
+      }
+    }
+    __syncthreads();
+  }
+  w.at = sm.at, w.seq = sm.seq;
+  return w;
 }
 
 cudaError_t launch_tiles(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st);

@@ -1,11 +1,12 @@
 // attention_tc.cu -- attention of many rows over the paged cache on the
 // fifth-generation tensor cores.
 //
-// Mathematics: as in attention.cu, a softmax in one pass with a running maximum
-// m, sum l and output o in fp32.  A row's reference m moves only when a tile's
-// maximum is more than 2^8 above it, so that o, which lies in tensor memory, is
-// seldom touched between products; exponentials reach 2^8 (float16 carries a
-// factor of 2^7 on top, as attention.cu's 2^15: 2^15 at most).
+// Mathematics: as in attention.cu, a softmax in one pass with a reference m, sum l
+// and output o in fp32.  m is the maximum of a row's first tile, and moves to a later
+// maximum only when the exponentials relative to it pass kMost, which their sum tells: so
+// o, which lies in tensor memory, is seldom touched between products, and no
+// maximum is looked for.  It never exceeds the maximum, so l is 1 at least (2^7 with float16,
+// whose exponentials carry that factor, as attention.cu's 2^15).
 //
 // Layout: a unit's tile (attention.cuh) has two halves of 128 rows (heads of up to
 // 128) or one (of 256).  z = q k^T is a product of M = 128 rows, N = the key
@@ -38,7 +39,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kHalf = 128;         // rows of a half
-constexpr float kMove = 8.0f;      // how far the reference may lie below the maximum, in powers of two
+// How large the exponentials of half a tile's positions may be in sum before the
+// row's reference is moved: what the largest float16 leaves room for (65504).
+constexpr float kMost = 49152.0f;
 
 template <bool F16>
 __host__ __device__ constexpr float tile_lift() {
@@ -67,17 +70,16 @@ struct Walk {
   Place at;
   Seq seq;
   Tile tile;
-  int64_t x, end;
+  int x, end;  // tiles of the line: the piece's first, the CTA's last
   int ta, tb;  // key tiles of this piece
-  __device__ __forceinline__ void begin(const AttnArgs& a, const Place& start, int64_t from, int64_t to) {
-    at = start, x = from, end = to;
-    seq = load_seq(a.q, at.seq);
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Work& work) {
+    at = work.at, seq = work.seq, x = work.begin, end = work.end;
     cut(a);
   }
   __device__ __forceinline__ void cut(const AttnArgs& a) {
     tile = tile_of<G::rows, G::bn>(a, seq, at.tile);
     ta = tile.t0 + at.at;
-    tb = static_cast<int>(min(static_cast<int64_t>(tile.t1), ta + (end - x)));
+    tb = min(tile.t1, ta + (end - x));
   }
   __device__ __forceinline__ bool more() const { return x < end; }
   // all lanes of the warp
@@ -108,7 +110,7 @@ template <int DP>
 struct Shared {
   using G = Geo<DP>;
   uint64_t full[G::stages], empty[G::stages];
-  uint64_t z_full[2], p_half[2], p_ready[2], o_full[2], q_full[2], pv_done;
+  uint64_t z_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], q_full[2], pv_done;
   // Of the tiles under way.  A slow producer thread may be at tile t - 1 while a
   // fast one writes tile t + 1; softmaxes may be three tiles behind.
   int64_t off[4][G::bn];                 // byte offsets of a tile's positions, -1: not seen
@@ -116,6 +118,7 @@ struct Shared {
   uint32_t bits[8][G::bn / 32];          // which of its positions count
   uint32_t tmem;
   int failed;
+  int holes;                             // a page was missing among those of a tile
   Walk<DP> walk[13], ahead[8];           // of each warp; the softmax warps' next pieces
   PlanSmem plan;
 };
@@ -158,6 +161,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 32 bytes at a 32-byte boundary: a whole sector for each lane, as lanes have rows of their own.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 template <int N>
@@ -291,7 +301,7 @@ __device__ __noinline__ bool odd_values(const AttnArgs& a, int seq, int head, in
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP>& w, Walk<DP>& nx, int64_t total, int ctas,
+__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP>& w, Walk<DP>& nx, const Work& work,
                                              int half, int wtid) {
   using G = Geo<DP>;
   using T = Traits<K>;
@@ -321,11 +331,9 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
     mbar_arrive(&sm.q_full[half]);
   };
   const auto here = [&](const Walk<DP>& u) { return u.more() && half * kHalf < u.tile.rows; };
+  if (here(w)) load_q(w);
   nx.follow(a, w);
-  if (here(w)) {
-    load_q(w);
-    hand_q();
-  }
+  if (here(w)) hand_q();
   for (; w.more(); w.become(nx), nx.next(a)) {
     const int nt = w.tb - w.ta;
     if (!here(w)) {
@@ -352,91 +360,102 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       tc_fence_after();
       if (j == nt - 1 && here(nx)) load_q(nx);
       if (some) {
-        float z[BN];
+        constexpr int HB = BN / 2;
         const int first = (w.ta + j) * BN;
-        uint32_t ok = 0xFFFFFFFFu, bits[BN / 32];
+        // Pages may be missing, which is rare: asked for here, looked at when the first
+        // exponentials are there, as shared memory answers late beside the products.
+        const int holes = *reinterpret_cast<volatile int*>(&sm.holes);
+        bool masked = first < all_lo || first + BN > all_hi;
+        // z of 32 positions, -inf where the row does not see
+        auto load = [&](int c, float (&z)[32]) {
+          tmem_ld32(zaddr + c, z);
+          if (masked) {
+            tmem_wait();
+            const int from = lo - first - c, to = hi - first - c;
+            const uint32_t bits = sm.bits[tiles & 7][c / 32];
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) bits[c] = sm.bits[tiles & 7][c], ok &= bits[c];
-        const bool edge = first < all_lo || first + BN > all_hi || ok != 0xFFFFFFFFu;
-        auto load = [&] {
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) tmem_ld32(zaddr + 32 * c, *reinterpret_cast<float(*)[32]>(&z[32 * c]));
-          tmem_wait();
-          if (edge) {
-            const int from = lo - first, to = hi - first;
-#pragma unroll
-            for (int k = 0; k < BN; ++k)
-              if (k < from || k >= to || !(bits[k / 32] >> (k & 31) & 1)) z[k] = -INFINITY;
+            for (int k = 0; k < 32; ++k)
+              if (k < from || k >= to || !(bits >> k & 1)) z[k] = -INFINITY;
           }
         };
-        auto maximum = [&] {
-          float top[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-          for (int k = 4; k < BN; k += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              top[i] = k + 4 + i < BN ? fmaxf(fmaxf(top[i], z[k + i]), z[k + 4 + i]) : fmaxf(top[i], z[k + i]);
-          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-        };
-        float s[4];
-        // exponentials of positions [c, c + 32), as 16-bit values in p
-        auto take = [&](int c, float ref, uint32_t (&p)[16]) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float x0 = z[c + k], x1 = z[c + k + 1], x2 = z[c + k + 2], x3 = z[c + k + 3];
-            fma_pair(x0, x1, a.scale_log2, ref);
-            fma_pair(x2, x3, a.scale_log2, ref);
-            x0 = exp2_approx(x0), x1 = exp2_approx(x1), x2 = exp2_approx(x2), x3 = exp2_approx(x3);
-            add_pair(s[0], s[1], x0, x1);
-            add_pair(s[2], s[3], x2, x3);
-            p[k / 2] = pack2(x0, x1, type), p[k / 2 + 1] = pack2(x2, x3, type);
-          }
-        };
-        load();
-        if (j == 0) m = maximum();
-        // The first half's exponentials are taken with the reference as it is while the
-        // maximum is found; where that is too far above it, they are taken again.
-        uint32_t pa[BN / 64][16];
-        float ref;
-        for (;;) {
-          ref = tile_lift<T::f16>() - (m == -INFINITY ? 0.0f : m);
-          s[0] = s[1] = s[2] = s[3] = 0.0f;
-#pragma unroll
-          for (int c = 0; c < BN / 64; ++c) take(32 * c, ref, pa[c]);
-          const float mx = maximum();
-          const bool moves = mx > m + kMove || (m == -INFINITY && mx > m);
-          if (!__any_sync(0xFFFFFFFFu, moves)) break;
-          const float f = moves ? exp2_approx(m - mx) : 1.0f;
-          if (moves) m = mx;
-          l *= f;
-          if (j > 0) {
-            if (G::halves == 1 && !wait(sm, a, &sm.pv_done, (n_tile - 1) & 1)) return;
-            tc_fence_after();
+        // One half of the positions after the other, in the same few instructions: code
+        // that runs once a tile comes from afar each time.
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              uint32_t x[8], y[8], v[16];
-              tmem_ld8(oaddr + c, x);
-              tmem_ld8(oaddr + c + 8, y);
-              tmem_wait();
+        for (int hb = 0; hb < 2; ++hb) {
+          uint32_t p[HB / 32][16];
+          float sum;
+          bool go = hb == 0 && j == 0, far = true;
+#pragma unroll 1
+          for (;;) {
+            if (go) {
+              // the reference moves to the maximum from here on, o (products under way
+              // first) and l with it
+              masked |= holes != 0;
+              const bool scale_o = j > 0 || hb > 0;
+              if (hb > 0 && !wait(sm, a, &sm.half_done[buf], (G::halves == 2 ? n_tile : n_tile >> 1) & 1)) return;
+              if (G::halves == 1 && hb == 0 && j > 0 && !wait(sm, a, &sm.pv_done, (n_tile - 1) & 1)) return;
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = hb * HB; c < BN; c += 32) {
+                float z[32];
+                load(c, z);
+                tmem_wait();
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                v[i] = __float_as_uint(__uint_as_float(x[i]) * f), v[8 + i] = __float_as_uint(__uint_as_float(y[i]) * f);
-              tmem_st16(oaddr + c, v);
+                for (int k = 0; k < 32; k += 2) top = fmaxf(fmaxf(top, z[k]), z[k + 1]);
+              }
+              top *= a.scale_log2;
+              const float f = far && top > m ? exp2_approx(m - top) : 1.0f;
+              if (far && top > m) m = top;
+              l *= f;
+              if (scale_o) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 16) {
+                  uint32_t x[8], y[8], v[16];
+                  tmem_ld8(oaddr + c, x);
+                  tmem_ld8(oaddr + c + 8, y);
+                  tmem_wait();
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    v[i] = __float_as_uint(__uint_as_float(x[i]) * f), v[8 + i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                  tmem_st16(oaddr + c, v);
+                }
+              }
             }
+            // exponentials, as 16-bit values in p, and their sum
+            const float ref = tile_lift<T::f16>() - (m == -INFINITY ? 0.0f : m);
+            float z[HB / 32][32], s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < HB / 32; ++c) load(hb * HB + 32 * c, z[c]);
+            tmem_wait();
+#pragma unroll
+            for (int c = 0; c < HB / 32; ++c)
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                float x0 = z[c][k], x1 = z[c][k + 1], x2 = z[c][k + 2], x3 = z[c][k + 3];
+                fma_pair(x0, x1, a.scale_log2, ref);
+                fma_pair(x2, x3, a.scale_log2, ref);
+                x0 = exp2_approx(x0), x1 = exp2_approx(x1), x2 = exp2_approx(x2), x3 = exp2_approx(x3);
+                add_pair(s[0], s[1], x0, x1);
+                add_pair(s[2], s[3], x2, x3);
+                p[c][k / 2] = pack2(x0, x1, type), p[c][k / 2 + 1] = pack2(x2, x3, type);
+              }
+            sum = (s[0] + s[1]) + (s[2] + s[3]);
+            if (go) break;
+            // a row that has seen nothing yet has no reference
+            far = sum > kMost || m == -INFINITY;
+            go = __any_sync(0xFFFFFFFFu, far || (holes != 0 && !masked));
+            if (!go) break;
+          }
+          l += sum;
+#pragma unroll
+          for (int c = 0; c < HB / 32; ++c) tmem_st16(zaddr + hb * (HB / 2) + 16 * c, p[c]);
+          tmem_wait_st();
+          if (hb == 0) {
+            tc_fence_before();
+            mbar_arrive(&sm.p_half[buf]);
           }
         }
-#pragma unroll
-        for (int c = 0; c < BN / 64; ++c) tmem_st16(zaddr + 16 * c, pa[c]);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&sm.p_half[buf]);
-#pragma unroll
-        for (int c = BN / 64; c < BN / 32; ++c) {
-          take(32 * c, ref, pa[0]);
-          tmem_st16(zaddr + 16 * c, pa[0]);
-        }
-        l += (s[0] + s[1]) + (s[2] + s[3]);
-        tmem_wait_st();
       } else {
         mbar_arrive(&sm.p_half[buf]);
       }
@@ -460,24 +479,35 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
     uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim;
     float* po = a.part_o + (part * G::rows + r) * a.head_dim;
     bool fine = true;
-#pragma unroll
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+#pragma unroll 1
     for (int c = 0; c < DP; c += 32) {
       float v[32];
       tmem_ld32(oaddr + c, v);
       tmem_wait();
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
+      for (int i = 0; i < 32; i += 16) {
+        if (c + i >= a.head_dim) continue;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) fine &= fabsf(v[i + k]) < INFINITY || c + i >= a.head_dim;
-        if (valid && c + i < a.head_dim) {
-          if (whole) {
-            float x[8];
+        for (int k = 0; k < 16; ++k) fine &= fabsf(v[i + k]) < INFINITY;
+        if (!valid) continue;
+        if (whole) {
+          uint32_t x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = v[i + k] * inv;
-            *reinterpret_cast<uint4*>(out + c + i) = pack8(x, type);
+          for (int k = 0; k < 8; ++k) x[k] = pack2(v[i + 2 * k] * inv, v[i + 2 * k + 1] * inv, type);
+          if (wide) {
+            store32(out + c + i, x);
           } else {
-            *reinterpret_cast<float4*>(po + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            *reinterpret_cast<float4*>(po + c + i + 4) = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+            *reinterpret_cast<uint4*>(out + c + i) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(out + c + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(v[i + h + k]);
+            store32(po + c + i + h, x);
           }
         }
       }
@@ -519,9 +549,9 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       }
     }
     if (!whole && half == 0 && wtid == 0) {
-      const int64_t unit0 = w.x - w.at.at, unit1 = unit0 + (w.tile.t1 - w.tile.t0);
       Note n;
-      n.c0 = cta_of(unit0, total, ctas), n.count = cta_of(unit1 - 1, total, ctas) - n.c0 + 1;
+      const int unit0 = w.x - w.at.at;
+      n.c0 = work.cta_of(unit0), n.count = work.cta_of(unit0 + w.tile.t1 - w.tile.t0 - 1) - n.c0 + 1;
       n.row = row0, n.rows = w.tile.rows, n.first = w.seq.first, n.head = w.at.head;
       a.notes[part] = n;
     }
@@ -568,7 +598,9 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
     page = -1, head = u.head;
     const int pos = u.first + j * BN + tid;
     if (tid < BN && pos < u.len) page = page_of(a.q, u.seq, pos, slot);
-    seen = page >= 0 && pos >= u.lo && pos < u.hi;
+    const bool counts = tid < BN && pos >= u.lo && pos < u.hi;
+    seen = page >= 0 && counts;
+    if (counts && page < 0) *reinterpret_cast<volatile int*>(&sm.holes) = 1;
   };
   // The looked-up tile, for all producers; whether all of its positions exist.
   auto post = [&] {
@@ -625,62 +657,62 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
   }
 }
 
-// As above for e4m3 caches: a thread has one position of each tile (with 64 of them, half a
-// position), whose codes wait in registers, half a tile ahead, and become 16-bit values on
-// their way to shared memory.  One scale a tile and thread, and no exchange but
-// of which positions count.
+// As above for e4m3 caches: codes wait in registers, half a tile ahead, and
+// become 16-bit values on their way to shared memory.  A warp has a quarter of each tile's
+// positions: it looks them up, a lane each, and copies them, as many lanes a position as
+// it has 16-byte pieces; so the warps exchange nothing but which positions count.
 template <int DP, int K>
 __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, Walk<DP>& w, int tid) {
   using G = Geo<DP>;
   using T = Traits<K>;
-  constexpr int BN = G::bn, PER = DP / 16 * BN / 128;  // 16-byte pieces of a thread
-  const int lane = tid & 31, row = tid * BN / 128, piece0 = (tid & (128 / BN - 1)) * PER;
-  const int pieces = a.head_dim / 16;
+  constexpr int BN = G::bn, MINE = BN / 4, PR = DP / 16, STEP = 32 / PR, PER = MINE / STEP;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int c = lane % PR, sub = lane / PR;  // the lane's piece, and its first position of the warp's
+  const bool on = c < a.head_dim / 16;
   RingPos load;
   uint32_t tiles = 0, groups = 0;
-  struct At {
-    int64_t off, soff;  // -1: not seen
-  };
+  int64_t off = -1;  // of the position that this lane looked up (-1: not seen)
+  float ks = 1.0f, vs = 1.0f;
   auto look_up = [&](int j) {  // tile j of the walk's piece
-    At at = {-1, 0};
-    const int pos = (w.ta + j) * BN + row;
-    if (pos >= w.tile.lo && pos < w.tile.hi) {
+    off = -1, ks = vs = 1.0f;
+    const int pos = (w.ta + j) * BN + warp * MINE + lane;
+    if (lane < MINE && pos >= w.tile.lo && pos < w.tile.hi) {
       int slot;
       const int page = page_of(a.q, w.at.seq, pos, slot), head = w.at.head;
+      if (page < 0) *reinterpret_cast<volatile int*>(&sm.holes) = 1;
       if (page >= 0) {
-        at.off = page * a.page_stride + slot * a.slot_stride + head * a.head_stride;
-        at.soff = page * a.scale_page_stride + slot * a.scale_slot_stride + head * a.scale_head_stride;
+        off = page * a.page_stride + slot * a.slot_stride + head * a.head_stride;
+        const int64_t s = page * a.scale_page_stride + slot * a.scale_slot_stride + head * a.scale_head_stride;
+        ks = a.k_scale[s], vs = a.v_scale[s];
       }
     }
-    return at;
   };
-  auto fetch = [&](uint4 (&b)[PER], const void* base, const float* scales, const At& at, float& scale) {
-    scale = 1.0f;  // a position that does not count: zeros
+  auto fetch = [&](uint4 (&b)[PER], const void* base) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) b[i] = make_uint4(0, 0, 0, 0);
-    if (at.off >= 0) {
-      scale = scales[at.soff];
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at.off) + piece0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (piece0 + i < pieces) b[i] = p[i];
+    for (int i = 0; i < PER; ++i) {
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, sub + STEP * i);
+      b[i] = make_uint4(0, 0, 0, 0);  // a position that does not count
+      if (o >= 0 && on) b[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + o + c * 16);
     }
   };
   auto store = [&](const uint4 (&b)[PER], float scale) {
     if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return false;
-    uint8_t* dst = ring + load.s * G::stage_bytes + row * 128;
-    Dequant<T::f16> dq;
-    dq.set(scale, scale);
+    uint8_t* dst = ring + load.s * G::stage_bytes + (c / 4) * (BN * 128);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
+      const int at = sub + STEP * i, row = warp * MINE + at;
+      const float s = __shfl_sync(0xFFFFFFFFu, scale, at);
+      Dequant<T::f16> dq;
+      dq.set(s, s);
       const uint32_t x[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
       uint32_t v[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[2 * k] = dq(bytes_of(x[k], 0, 0x1404)), v[2 * k + 1] = dq(bytes_of(x[k], 0, 0x3424));
-      const int p = 2 * (piece0 + i);
-      uint8_t* at = dst + (p / 8) * (BN * 128);
-      *reinterpret_cast<uint4*>(at + (((p & 7) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<uint4*>(at + ((((p + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+      // the second slab's lanes begin with their second half: its rows lie in the first one's banks
+      const int p = (2 * c) & 7, odd = c >> 2 & 1;
+      const uint4 v0 = make_uint4(v[0], v[1], v[2], v[3]), v1 = make_uint4(v[4], v[5], v[6], v[7]);
+      *reinterpret_cast<uint4*>(dst + row * 128 + (((p + odd) ^ (row & 7)) << 4)) = odd ? v1 : v0;
+      *reinterpret_cast<uint4*>(dst + row * 128 + (((p + 1 - odd) ^ (row & 7)) << 4)) = odd ? v0 : v1;
     }
     fence_async_smem();
     mbar_arrive(&sm.full[load.s]);
@@ -690,28 +722,28 @@ __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, 
   };
   if (!w.more()) return;
   uint4 kb[PER], vb[PER];
-  float ks, vs;
-  At at = look_up(0);
-  fetch(kb, a.k, a.k_scale, at, ks);
+  look_up(0);
+  fetch(kb, a.k);
   int j = 0, nt = w.tb - w.ta;
   for (;;) {
-    fetch(vb, a.v, a.v_scale, at, vs);
+    fetch(vb, a.v);
+    const float k_scale = ks, v_scale = vs;
     // which positions count, before the keys are handed over
-    uint32_t on = __ballot_sync(0xFFFFFFFFu, at.off >= 0);
-    if (BN == 64) {  // two threads a position
-      on &= 0x55555555u;
-      on = (on | on >> 1) & 0x33333333u, on = (on | on >> 2) & 0x0F0F0F0Fu, on = (on | on >> 4) & 0x00FF00FFu, on = (on | on >> 8) & 0xFFFFu;
-      if (lane == 0) reinterpret_cast<uint16_t*>(sm.bits[tiles & 7])[tid >> 5] = static_cast<uint16_t>(on);
-    } else if (lane == 0) {
-      sm.bits[tiles & 7][tid >> 5] = on;
+    const uint32_t seen = __ballot_sync(0xFFFFFFFFu, off >= 0);
+    if (lane == 0) {
+      if (MINE == 32) sm.bits[tiles & 7][warp] = seen;
+      else reinterpret_cast<uint16_t*>(sm.bits[tiles & 7])[warp] = static_cast<uint16_t>(seen);
     }
     ++tiles;
-    if (++j == nt) w.next(a), j = 0, nt = w.tb - w.ta;
+    if (++j == nt) {
+      w.next(a);
+      j = 0, nt = w.tb - w.ta;
+    }
     const bool more = j > 0 || w.more();
-    if (more) at = look_up(j);
-    if (!store(kb, ks)) return;
-    if (more) fetch(kb, a.k, a.k_scale, at, ks);
-    if (!store(vb, vs)) return;
+    if (more) look_up(j);
+    if (!store(kb, k_scale)) return;
+    if (more) fetch(kb, a.k);
+    if (!store(vb, v_scale)) return;
     if (!more) return;
   }
 }
@@ -755,6 +787,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
 #pragma unroll
         for (int k = 0; k < BN / 32; ++k)
           mma_ts(tm + G::o_col + (G::halves == 2 ? half * G::o_cols : 0), p0 + k * 8, v0 + k * 128, id_o, more || c > 0 || k > 0);
+        if (c == 0) mma_commit(smem_u32(&sm.half_done[buf]));
       }
     }
     return true;
@@ -834,33 +867,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
   uint8_t* ring = base + G::halves * G::q_bytes;
   const int tid = threadIdx.x, warp = tid >> 5;
   pdl_launch_dependents();
-  int ctas;
-  int64_t begin, end;
-  Place start;
-  const int64_t total = find_work<G::rows, G::bn, kThreads>(a, sm.plan, ctas, begin, end, start);
-  if (tid < 2) a.notes[2 * blockIdx.x + tid].count = 0;
-  if (begin == end) return;
-  if (tid == 0) {
+  if (warp == 12) tmem_alloc(smem_u32(&sm.tmem), 512);
+  if (tid == kThreads - 1) {
     for (int i = 0; i < G::stages; ++i) mbar_init(&sm.full[i], 128), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&sm.z_full[i], 1), mbar_init(&sm.p_half[i], kHalf), mbar_init(&sm.p_ready[i], kHalf), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.q_full[i], kHalf);
+      mbar_init(&sm.z_full[i], 1), mbar_init(&sm.half_done[i], 1), mbar_init(&sm.p_half[i], kHalf), mbar_init(&sm.p_ready[i], kHalf), mbar_init(&sm.o_full[i], 1),
+          mbar_init(&sm.q_full[i], kHalf);
     mbar_init(&sm.pv_done, 1);
-    sm.failed = 0;
+    sm.failed = sm.holes = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
   }
-  if (warp == 12) tmem_alloc(smem_u32(&sm.tmem), 512);
   tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  const Work work = find_work<G::rows, G::bn, kThreads>(a, sm.plan);
+  if (tid < 2) a.notes[2 * blockIdx.x + tid].count = 0;
+  tc_fence_after();  // find_work's barriers lie between
+  if (work.begin == work.end) {
+    if (warp == 12) tmem_dealloc(sm.tmem, 512);
+    return;
+  }
   {
     Walk<DP>& w = sm.walk[warp < 13 ? warp : 12];
-    if (warp < 13 && (tid & 31) == 0) w.begin(a, start, begin, end);
+    if (warp < 13 && (tid & 31) == 0) w.begin(a, work);
     __syncwarp();
     // registers: 2 x 128 x 184 + 128 x 96 + 128 x 48 = 512 x 128
     if (warp < 8) {
       reg_up<184>();
-      if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, sm.ahead[warp & 7], total, ctas, warp >> 2, tid & 127);
+      if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, sm.ahead[warp & 7], work, warp >> 2, tid & 127);
     } else if (warp < 12) {
       reg_down<96>();
       if constexpr (Traits<K>::e4m3) dequant_role<DP, K>(a, sm, ring, w, tid - 256);

@@ -630,7 +630,9 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
         if (all && maps.rows) {
           if (tid == 0) mbar_arrive_expect_tx(&sm.full[load.s], G::stage_bytes);
           else mbar_arrive(&sm.full[load.s]);
-          const int slab = static_cast<int>(divide(tid, maps.row_boxes)), row = (tid - slab * static_cast<int>(maps.row_boxes.d)) * maps.rows;
+          // lanes issue boxes one after the other, so the warps take turns
+          const int box = lane * 4 + warp, slab = static_cast<int>(divide(box, maps.row_boxes)),
+                    row = (box - slab * static_cast<int>(maps.row_boxes.d)) * maps.rows;
           if (slab < DP / 64) {
             const int2 at = sm.place[tiles & 3][row];
             load_box(dst + slab * (BN * 128) + row * 128, kv ? &maps.v : &maps.k, slab * 64, at.y, u.head, at.x, &sm.full[load.s]);

@@ -15,7 +15,9 @@
 // order, so each lane reads keys in whole 16-byte pieces and takes the query's
 // elements in the same order; the outputs' order is free likewise, so values are
 // read in 16-byte pieces of four positions and paired in registers.  e4m3 codes
-// become 16-bit values, scale included, between shared memory and the product.
+// become float16 values between shared memory and the product, a conversion for two;
+// the keys' scales are multiplied on z, the values' on the exponentials, in units of the
+// largest so far, which o follows as it follows m.
 //
 // Bound: reading the cache.
 #include <cuda_runtime.h>
@@ -40,6 +42,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;     // positions of a warp's step
 constexpr int kBn = kWarps * kStep;
+constexpr int kJoinRows = 4;  // of a unit that the warps join at once
 constexpr size_t kCtlBytes = 256;
 
 template <bool F16>
@@ -66,12 +69,15 @@ struct Shape {
   static constexpr int scale_bytes = T::e4m3 ? 2 * kStep * 4 : 0;
   static constexpr int stage_bytes = 2 * kStep * row_bytes + scale_bytes + 16;  // 16: which positions count
   static constexpr int ctas = DP <= 128 ? 2 : 1;            // on an SM
-  static constexpr int budget = (224 * 1024 / ctas - 6 * 1024) / kWarps;
+  static constexpr bool q_shared = DP > 128;                // the query's fragments lie in shared memory
+  static constexpr int join_bytes = kWarps * kJoinRows * DP * 4;
+  static constexpr int q_bytes = q_shared ? DP / 16 * 512 : 0;
+  static constexpr int budget = (224 * 1024 / ctas - 5 * 1024 - join_bytes - q_bytes) / kWarps;
   static constexpr int fit = budget / stage_bytes;
   static constexpr int stages = fit > 8 ? 8 : fit;
   static constexpr int ring_bytes = stages * stage_bytes;   // of a warp
+  static constexpr int smem = kWarps * ring_bytes + join_bytes + q_bytes;
   static_assert(stages >= 2, "ring");
-  static_assert(kWarps * ring_bytes >= kWarps * kRows * (DP + 2) * 4, "the join's buffers take the ring's place");
 };
 
 // Swizzles that spread a phase's lanes over the banks: keys are read in pieces
@@ -87,6 +93,12 @@ __device__ __forceinline__ uint32_t value_at(int row, int piece) {
 }
 
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// The codes in a word's low or high half as float16 values.
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, int high) {
+  const __half2 v(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(high ? w >> 16 : w), __NV_E4M3));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 // A lane's pieces of values of one group: positions 2t, 2t + 1, 2t + 8, 2t + 9.
 template <int DP, int K>
@@ -106,13 +118,13 @@ struct Values {
       }
     }
   }
-  // element j of the piece: the pairs of positions (2t, 2t + 1) and (2t + 8, 2t + 9)
-  template <class D>
-  __device__ __forceinline__ void pair(int j, const D& lo, const D& hi, uint32_t& b0, uint32_t& b1) const {
+  // element j of the piece: the pairs of positions (2t, 2t + 1) and (2t + 8, 2t + 9);
+  // of e4m3 codes the values without their scales
+  __device__ __forceinline__ void pair(int j, uint32_t& b0, uint32_t& b1) const {
     if constexpr (Traits<K>::e4m3) {
-      const uint32_t s = 0x4000u | ((4u + (j & 3)) << 12) | ((j & 3) << 4);
-      b0 = lo(bytes_of(w[0][j / 4], w[1][j / 4], s));
-      b1 = hi(bytes_of(w[2][j / 4], w[3][j / 4], s));
+      const uint32_t s = j & 2 ? 0x7362u : 0x5140u;  // elements j and j + 1 of both positions
+      b0 = two_codes(bytes_of(w[0][j / 4], w[1][j / 4], s), j & 1);
+      b1 = two_codes(bytes_of(w[2][j / 4], w[3][j / 4], s), j & 1);
     } else {
       const uint32_t s = j & 1 ? 0x7632u : 0x5410u;
       b0 = bytes_of(w[0][j / 2], w[1][j / 2], s);
@@ -121,124 +133,193 @@ struct Values {
   }
 };
 
+using RowWalk = Walk<kRows, kBn>;
+
 template <int DP, int K>
 __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_kernel(const AttnArgs a) {
   using S = Shape<DP, K>;
   using T = Traits<K>;
   constexpr int RB = S::row_bytes, KS = DP / 16, NB = DP / 8, EV = S::ev;
+  constexpr int half_type = T::f16 ? MOE_F16 : MOE_BF16;  // of the exponentials
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PlanSmem plan;
+  __shared__ RowWalk walks[2][kWarps];       // of the pieces that are worked on, and of those that are loaded
+  __shared__ float join_ml[kWarps][kRows][2];
+  float* join_o = reinterpret_cast<float*>(smem + kWarps * S::ring_bytes);                     // [warp][kJoinRows][DP]
+  uint4* q_frag = reinterpret_cast<uint4*>(smem + kWarps * S::ring_bytes + S::join_bytes);     // [KS][lane]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gi = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
 
   const Work work = find_work<kRows, kBn, kThreads>(a, plan);
   if (tid < 2) a.notes[2 * blockIdx.x + tid].count = 0;
   if (work.begin == work.end) return;
-  __syncthreads();
+  RowWalk &w = walks[0][warp], &lw = walks[1][warp];
+  if (lane < 2) walks[lane][warp].begin(a, work);
 
   uint8_t* ring = smem + warp * S::ring_bytes;
   const uint32_t ring_s = smem_u32(ring);
   const int pieces = a.head_dim * T::size / 16;
-  if (pieces < S::pieces) {  // elements past head_dim are zeros throughout
+  if (pieces < S::pieces)  // elements past head_dim are zeros throughout
     for (int i = lane; i < S::stages * S::stage_bytes / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
-    __syncwarp();
-  }
+  __syncwarp();
 
-  Place at = work.at;
-  Seq seq = work.seq;
-  const int end = work.end;
-  for (int x = work.begin; x < end;) {
-    const Tile tile = tile_of<kRows, kBn>(a, seq, at.tile);
-    const int ta = tile.t0 + at.at;
-    const int tb = min(tile.t1, ta + (end - x)), unit0 = x - at.at;
-    const int row0 = at.tile * kRows;
+  // The loading side runs stages ahead, into the next pieces.  Lane l copies for
+  // position (l & 15) of a step; its page is looked up a step before.
+  int l_pos = 0, l_left = 0, l_lo = 0, l_hi = 0, l_seq = 0, l_head = 0, page = -1, slot = 0;
+  auto open = [&] {
+    l_left = lw.more() ? lw.tb - lw.ta : 0;
+    l_pos = lw.ta * kBn + warp * kStep + (lane & 15);
+    l_lo = lw.tile.lo, l_hi = lw.tile.hi, l_seq = lw.at.seq, l_head = lw.at.head;
+  };
+  auto look_up = [&] { page = l_left > 0 && l_pos >= l_lo && l_pos < l_hi ? page_of(a.q, l_seq, l_pos, slot) : -1; };
+  auto issue = [&](int stage) {
+    if (l_left > 0) {
+      const uint32_t base = ring_s + stage * S::stage_bytes;
+      const bool on = page >= 0;
+      const int64_t off = on ? page * a.page_stride + slot * a.slot_stride + l_head * a.head_stride : -1;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on) & 0xFFFFu;
+      if constexpr (T::e4m3) {
+        const float* s = (lane < 16 ? a.k_scale : a.v_scale) + l_head * a.scale_head_stride;
+        cp_async4(base + 2 * kStep * RB + lane * 4,
+                  on ? s + page * a.scale_page_stride + slot * a.scale_slot_stride : static_cast<const void*>(a.query), on);
+      }
+      if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::stage_bytes + 2 * kStep * RB + S::scale_bytes) = mask;
+#pragma unroll
+      for (int i = 0; i < kStep * S::pieces / 32; ++i) {
+        const int n = lane + 32 * i, row = n / S::pieces, c = n % S::pieces;
+        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
+        if (c < pieces) {
+          // nothing is read for a position that does not count, but the address is one of memory
+          const void* ka = o < 0 ? a.query : static_cast<const uint8_t*>(a.k) + o + c * 16;
+          const void* va = o < 0 ? a.query : static_cast<const uint8_t*>(a.v) + o + c * 16;
+          cp_async16(base + key_at<RB>(row, c), ka, o >= 0);
+          cp_async16(base + kStep * RB + (S::ev == 8 && T::e4m3 ? row * RB + c * 16 : value_at<RB>(row, c)), va, o >= 0);
+        }
+      }
+      l_pos += kBn;
+      if (--l_left == 0) {
+        lw.next(a);
+        open();
+      }
+      look_up();
+    }
+    cp_commit();
+  };
+  open();
+  look_up();
+#pragma unroll 1
+  for (int i = 0; i < S::stages - 1; ++i) issue(i);
 
+  // A piece's query, in the order in which the keys are read.  For e4m3 caches
+  // it becomes float16, a row times a power of two (q_scale takes it back) that brings its
+  // largest magnitude to 2^13: exact but for elements below 2^-29 of that.
+  uint32_t qa[S::q_shared ? 1 : KS][4];
+  float q_scale[2] = {1.0f, 1.0f};
+  auto q_row = [&](int i) {  // this lane's row i (of rows gi and gi + 8), NULL if there is none
+    const int row0 = w.at.tile * kRows, r = gi + 8 * i;
+    if (r >= w.tile.rows) return static_cast<const uint16_t*>(nullptr);
+    const int token = static_cast<int>(divide(row0 + r, a.by_group)), g = row0 + r - token * a.group;
+    return static_cast<const uint16_t*>(a.query) + (w.seq.first + token) * a.ld_q +
+           static_cast<int64_t>(w.at.head * a.group + g) * a.head_dim;
+  };
+  auto q_at = [&](const uint16_t* q, int s) {
+    const int d = T::e4m3 ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 8 * (t + 4 * (s / 2)) + 4 * (s % 2);
+    return q && d < a.head_dim ? *reinterpret_cast<const uint2*>(q + d) : make_uint2(0, 0);
+  };
+  auto largest = [](uint32_t top, uint32_t u) {  // magnitudes' bits order them
+    u &= 0x7FFF7FFFu;
+    return max(top, max(u << 16, u & 0xFFFF0000u));
+  };
+  auto scale_of = [&](uint32_t top, float& back) {
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const int e = min(max(static_cast<int>(top >> 23) - 127, -100), 127) - 13;
+    back = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  };
+  auto scaled = [](uint32_t u, float f) { return pack2(bf16lo(u) * f, bf16hi(u) * f, MOE_F16); };
+  auto load_q = [&] {
+    if constexpr (!S::q_shared) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint16_t* q = q_row(i);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint2 u = q_at(q, s);
+          qa[s][i] = u.x, qa[s][2 + i] = u.y;
+        }
+      }
+    }
+  };
+  auto finish_q = [&] {
+    const bool narrow = T::e4m3 && a.type == MOE_BF16;
+    if constexpr (!S::q_shared) {
+      if (narrow) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) top = largest(largest(top, qa[s][i]), qa[s][2 + i]);
+          const float f = scale_of(top, q_scale[i]);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) qa[s][i] = scaled(qa[s][i], f), qa[s][2 + i] = scaled(qa[s][2 + i], f);
+        }
+      }
+    } else {  // registers are short: a warp brings a quarter of the fragments
+      const uint16_t* q[2] = {q_row(0), q_row(1)};
+      float f[2] = {1.0f, 1.0f};
+      if (narrow) {
+        uint32_t top[2] = {0, 0};
+#pragma unroll 4
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint2 u = q_at(q[i], s);
+            top[i] = largest(largest(top[i], u.x), u.y);
+          }
+        f[0] = scale_of(top[0], q_scale[0]), f[1] = scale_of(top[1], q_scale[1]);
+      }
+#pragma unroll 1
+      for (int s = warp; s < KS; s += kWarps) {
+        uint2 u0 = q_at(q[0], s), u1 = q_at(q[1], s);
+        if (narrow) u0 = make_uint2(scaled(u0.x, f[0]), scaled(u0.y, f[0])), u1 = make_uint2(scaled(u1.x, f[1]), scaled(u1.y, f[1]));
+        q_frag[s * 32 + lane] = make_uint4(u0.x, u1.x, u0.y, u1.y);
+      }
+    }
+  };
+  load_q();
+  finish_q();
+  if (S::q_shared) __syncthreads();
+
+  int stage = 0;
+  while (w.more()) {
+    const int row0 = w.at.tile * kRows, rows = w.tile.rows, ta = w.ta, steps = w.tb - w.ta;
     // the lane's two rows and what they see
     int lo[2], hi[2];
     int tight_lo, tight_hi;  // what all of the tile's rows see
     {
-      const int base = seq.len - seq.n;
+      const int base = w.seq.len - w.seq.n;
       const int p0 = base + static_cast<int>(divide(row0, a.by_group));
-      const int p1 = base + static_cast<int>(divide(row0 + tile.rows - 1, a.by_group));
-      tight_hi = sees_to(a, seq.len, p0), tight_lo = sees_from(a, p1);
+      const int p1 = base + static_cast<int>(divide(row0 + rows - 1, a.by_group));
+      tight_hi = sees_to(a, w.seq.len, p0), tight_lo = sees_from(a, p1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = gi + 8 * i;
-        const int p = base + static_cast<int>(divide(row0 + min(r, tile.rows - 1), a.by_group));
+        const int p = base + static_cast<int>(divide(row0 + min(r, rows - 1), a.by_group));
         lo[i] = sees_from(a, p);
-        hi[i] = r < tile.rows ? sees_to(a, seq.len, p) : 0;
+        hi[i] = r < rows ? sees_to(a, w.seq.len, p) : 0;
       }
     }
-
-    // the query, in the order in which the keys are read
-    uint32_t qa[KS][4];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d = T::e4m3 ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 8 * (t + 4 * (s / 2)) + 4 * (s % 2);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = gi + 8 * i;
-        uint2 u = make_uint2(0, 0);
-        if (r < tile.rows && d < a.head_dim) {
-          const int token = static_cast<int>(divide(row0 + r, a.by_group)), g = row0 + r - token * a.group;
-          u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.query) + (seq.first + token) * a.ld_q +
-                                              static_cast<int64_t>(at.head * a.group + g) * a.head_dim + d);
-        }
-        qa[s][i] = u.x, qa[s][2 + i] = u.y;
-      }
-    }
-
-    const uint8_t* kh = static_cast<const uint8_t*>(a.k) + at.head * a.head_stride;
-    const uint8_t* vh = static_cast<const uint8_t*>(a.v) + at.head * a.head_stride;
-    // lane l copies for position (l & 15) of a step; its page is looked up a step before
-    const int steps = tb - ta;
-    auto position = [&](int step) { return (ta + step) * kBn + warp * kStep + (lane & 15); };
-    auto look_up = [&](int step, int& slot) {
-      const int pos = position(step);
-      return step < steps && pos >= tile.lo && pos < tile.hi ? page_of(a.q, at.seq, pos, slot) : -1;
-    };
-    int slot = 0, page = look_up(0, slot);
-    auto issue = [&](int step, int stage) {
-      const uint32_t base = ring_s + stage * S::stage_bytes;
-      const bool on = page >= 0;
-      const int64_t off = on ? page * a.page_stride + slot * a.slot_stride : -1;
-      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on) & 0xFFFFu;
-      if (step < steps) {
-        if constexpr (T::e4m3) {
-          const float* s = (lane < 16 ? a.k_scale : a.v_scale) + at.head * a.scale_head_stride;
-          cp_async4(base + 2 * kStep * RB + lane * 4,
-                    on ? s + page * a.scale_page_stride + slot * a.scale_slot_stride : static_cast<const void*>(a.query), on);
-        }
-        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + stage * S::stage_bytes + 2 * kStep * RB + S::scale_bytes) = mask;
-#pragma unroll
-        for (int i = 0; i < kStep * S::pieces / 32; ++i) {
-          const int n = lane + 32 * i, row = n / S::pieces, c = n % S::pieces;
-          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row);
-          if (c < pieces) {
-            // nothing is read for a position that does not count, but the address is one of memory
-            const void* ka = o < 0 ? a.query : kh + o + c * 16;
-            const void* va = o < 0 ? a.query : vh + o + c * 16;
-            cp_async16(base + key_at<RB>(row, c), ka, o >= 0);
-            cp_async16(base + kStep * RB + (S::ev == 8 && T::e4m3 ? row * RB + c * 16 : value_at<RB>(row, c)), va, o >= 0);
-          }
-        }
-      }
-      cp_commit();
-      page = look_up(step + 1, slot);
-    };
-
     float o[NB][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float v_ref = 0.0f, v_inv = 0.0f;  // e4m3: o counts values in units of the largest scale so far
 #pragma unroll
     for (int j = 0; j < NB; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
 
 #pragma unroll 1
-    for (int i = 0; i < S::stages - 1; ++i) issue(i, i);
-    int stage = 0;
-#pragma unroll 1
     for (int step = 0; step < steps; ++step) {
       cp_wait<S::stages - 2>();
       __syncwarp();
-      issue(step + S::stages - 1, stage == 0 ? S::stages - 1 : stage - 1);
+      issue(stage == 0 ? S::stages - 1 : stage - 1);
       const uint8_t* ks = ring + stage * S::stage_bytes;
       const uint8_t* vs = ks + kStep * RB;
       const uint32_t mask = *reinterpret_cast<const uint32_t*>(ks + 2 * kStep * RB + S::scale_bytes);
@@ -249,26 +330,47 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
       // z: rows gi and gi + 8, positions 8 n + 2t and + 1
       float z[2][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
+      for (int n = 0; n < 2; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
+      auto query = [&](int s, uint32_t (&q)[4]) {
+        if (S::q_shared) {
+          const uint4 u = q_frag[s * 32 + lane];
+          q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
+        } else {
+          q[0] = qa[s][0], q[1] = qa[s][1], q[2] = qa[s][2], q[3] = qa[s][3];
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < S::pieces / 4; ++i) {
+        const uint4 u0 = lds128(ks + key_at<RB>(gi, t + 4 * i)), u1 = lds128(ks + key_at<RB>(8 + gi, t + 4 * i));
+        const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+        uint32_t q[4];
         if constexpr (T::e4m3) {
-          Dequant<T::f16> dq;
-          dq.set(sc[8 * n + gi], sc[8 * n + gi]);
 #pragma unroll
-          for (int i = 0; i < S::pieces / 4; ++i) {
-            const uint4 u = lds128(ks + key_at<RB>(8 * n + gi, t + 4 * i));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma16816<T::f16>(z[n], qa[4 * i + j], dq(bytes_of(w[j], 0, 0x1404)), dq(bytes_of(w[j], 0, 0x3424)));
+          for (int j = 0; j < 4; ++j) {
+            query(4 * i + j, q);
+            mma16816<true>(z[0], q, two_codes(w0[j], 0), two_codes(w0[j], 1));
+            mma16816<true>(z[1], q, two_codes(w1[j], 0), two_codes(w1[j], 1));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < S::pieces / 4; ++i) {
-            const uint4 u = lds128(ks + key_at<RB>(8 * n + gi, t + 4 * i));
-            mma16816<T::f16>(z[n], qa[2 * i], u.x, u.y);
-            mma16816<T::f16>(z[n], qa[2 * i + 1], u.z, u.w);
+          for (int j = 0; j < 2; ++j) {
+            query(2 * i + j, q);
+            mma16816<T::f16>(z[0], q, w0[2 * j], w0[2 * j + 1]);
+            mma16816<T::f16>(z[1], q, w1[2 * j], w1[2 * j + 1]);
           }
+        }
+      }
+      float vf[2][2];  // e4m3: the values' scales at positions 8 n + 2t and + 1
+      bool moved = false;
+      if constexpr (T::e4m3) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float2 k2 = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * t);
+          const float2 v2 = *reinterpret_cast<const float2*>(sc + kStep + 8 * n + 2 * t);
+          z[n][0] *= q_scale[0], z[n][1] *= q_scale[0], z[n][2] *= q_scale[1], z[n][3] *= q_scale[1];
+          z[n][0] *= k2.x, z[n][1] *= k2.y, z[n][2] *= k2.x, z[n][3] *= k2.y;
+          vf[n][0] = v2.x, vf[n][1] = v2.y;
+          moved |= fmaxf(v2.x, v2.y) > v_ref;
         }
       }
       const int first = (ta + step) * kBn + warp * kStep;
@@ -286,22 +388,36 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
           }
       }
       // the running maximum
-      float shrink[2];
-      bool moved = false;
+      float top[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x = fmaxf(fmaxf(z[0][2 * i], z[0][2 * i + 1]), fmaxf(z[1][2 * i], z[1][2 * i + 1]));
-        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-        x *= a.scale_log2;
-        shrink[i] = 1.0f;
-        if (x > m[i]) {
-          shrink[i] = exp2_approx(m[i] - x);  // 0 for the first
-          m[i] = x, moved = true;
-        }
+        top[i] = fmaxf(fmaxf(z[0][2 * i], z[0][2 * i + 1]), fmaxf(z[1][2 * i], z[1][2 * i + 1])) * a.scale_log2;
+        moved |= top[i] > m[i];
       }
       if (__any_sync(0xFFFFFFFFu, moved)) {
-        l[0] *= shrink[0], l[1] *= shrink[1];
+        float shrink[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = top[i];
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+          shrink[i] = 1.0f;
+          if (x > m[i]) {
+            shrink[i] = exp2_approx(m[i] - x);  // 0 for the first
+            m[i] = x;
+          }
+          l[i] *= shrink[i];
+        }
+        if constexpr (T::e4m3) {
+          float v = fmaxf(fmaxf(vf[0][0], vf[0][1]), fmaxf(vf[1][0], vf[1][1]));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+          if (v > v_ref) {
+            const float f = v_ref / v;
+            v_ref = v, v_inv = 1.0f / v;
+            shrink[0] *= f, shrink[1] *= f;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < NB; ++j) o[j][0] *= shrink[0], o[j][1] *= shrink[0], o[j][2] *= shrink[1], o[j][3] *= shrink[1];
       }
@@ -315,17 +431,19 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
           z[n][c] = exp2_approx(fmaf(z[n][c], a.scale_log2, -ref[c >> 1]));
           l[c >> 1] += z[n][c];
         }
-        pa[2 * n] = pack2(z[n][0], z[n][1], T::f16 ? MOE_F16 : MOE_BF16);
-        pa[2 * n + 1] = pack2(z[n][2], z[n][3], T::f16 ? MOE_F16 : MOE_BF16);
+        if constexpr (T::e4m3) {
+          vf[n][0] *= v_inv, vf[n][1] *= v_inv;
+          z[n][0] *= vf[n][0], z[n][1] *= vf[n][1], z[n][2] *= vf[n][0], z[n][3] *= vf[n][1];
+        }
+        pa[2 * n] = pack2(z[n][0], z[n][1], half_type);
+        pa[2 * n + 1] = pack2(z[n][2], z[n][3], half_type);
       }
 
-      Dequant<T::f16> dlo, dhi;
-      if constexpr (T::e4m3) {
-        dlo.set(sc[kStep + 2 * t], sc[kStep + 2 * t + 1]);
-        dhi.set(sc[kStep + 2 * t + 8], sc[kStep + 2 * t + 9]);
-      }
       bool odd = false;
       if (edge) {  // a value that some row must not see may be anything
+        if constexpr (T::e4m3)
+          odd = !(fmaxf(fmaxf(vf[0][0], vf[0][1]), fmaxf(vf[1][0], vf[1][1])) < INFINITY) || vf[0][0] != vf[0][0] ||
+                vf[0][1] != vf[0][1] || vf[1][0] != vf[1][0] || vf[1][1] != vf[1][1];
 #pragma unroll
         for (int h = 0; h < S::vgroups; ++h) {
           Values<DP, K> v;
@@ -333,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
 #pragma unroll
           for (int j = 0; j < EV; ++j) {
             uint32_t b0, b1;
-            v.pair(j, dlo, dhi, b0, b1);
+            v.pair(j, b0, b1);
             odd |= odd_value<T::f16>(b0) || odd_value<T::f16>(b1);
           }
         }
@@ -347,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
 #pragma unroll
           for (int j = 0; j < EV; ++j) {
             uint32_t b0, b1;
-            v.pair(j, dlo, dhi, b0, b1);
+            v.pair(j, b0, b1);
             mma16816<T::f16>(o[h * EV + j], pa, b0, b1);
           }
         }
@@ -372,12 +490,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
 #pragma unroll
             for (int j = 0; j < EV; ++j) {
               uint32_t b0, b1;
-              v.pair(j, dlo, dhi, b0, b1);
+              v.pair(j, b0, b1);
               const uint32_t b = k < 8 ? b0 : b1, bits = k & 1 ? b >> 16 : b & 0xFFFFu;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const float val = half_bits_to_f32(__shfl_sync(0xFFFFFFFFu, bits, ((2 * t + c) << 2) | ((k & 7) >> 1)),
-                                                   T::f16 ? MOE_F16 : MOE_BF16);
+                const float val = half_bits_to_f32(__shfl_sync(0xFFFFFFFFu, bits, ((2 * t + c) << 2) | ((k & 7) >> 1)), half_type);
                 if (who & 1) o[h * EV + j][c] += p[0] * val;
                 if (who & 4) o[h * EV + j][2 + c] += p[1] * val;
               }
@@ -386,85 +503,79 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
         }
       }
     }
-    cp_wait<0>();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+      if (t == 0) join_ml[warp][gi + 8 * i][0] = m[i], join_ml[warp][gi + 8 * i][1] = l[i];
     }
 
-    // the four warps' parts, through the ring's place
-    __syncthreads();
-    float* jo = reinterpret_cast<float*>(smem);            // [warp][row][DP]
-    float* jm = jo + kWarps * kRows * DP;                  // [warp][row][2]
-    // a lane has, of rows gi and gi + 8, the elements EV (n + 8 h) + j for n = 2t, 2t + 1
+    // The four warps' parts, a few rows at a time, while the next piece's query is
+    // on its way.
+    const bool whole = w.whole();
+    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (ta == w.tile.t0 ? 1 : 0);
+    const int seq_first = w.seq.first, kv_head = w.at.head, d4 = a.head_dim / 4;
+    if (!whole && tid == 0) w.note(a, work);
+    w.next(a);
+    const bool more = w.more();
+    if (more) load_q();
+    const float unit = T::e4m3 ? v_ref : 1.0f;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kJoinRows) {
+      // a lane has, of rows gi and gi + 8, the elements EV (n + 8 h) + j for n = 2t, 2t + 1
+      if (((gi ^ r0) & 4) == 0) {
+        const bool upper = r0 >= 8;
+        float* row = join_o + (warp * kJoinRows + (gi & 3)) * DP;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = gi + 8 * i;
-      if (r >= tile.rows) continue;
-      float* row = jo + (warp * kRows + r) * DP;
+        for (int h = 0; h < S::vgroups; ++h)
 #pragma unroll
-      for (int h = 0; h < S::vgroups; ++h)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int j = 0; j < EV; j += 4) {
-            const int b = h * EV + j;
-            *reinterpret_cast<float4*>(row + EV * (2 * t + c + 8 * h) + j) =
-                make_float4(o[b][2 * i + c], o[b + 1][2 * i + c], o[b + 2][2 * i + c], o[b + 3][2 * i + c]);
-          }
-      if (t == 0) jm[(warp * kRows + r) * 2] = m[i], jm[(warp * kRows + r) * 2 + 1] = l[i];
-    }
-    __syncthreads();
-    const bool whole = ta == tile.t0 && tb == tile.t1;
-    const int which = ta == tile.t0 ? 1 : 0;
-    const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + which;
-    const int d4 = a.head_dim / 4;
-    for (int i = tid; i < tile.rows * d4; i += kThreads) {
-      const int r = i / d4, d = (i - r * d4) * 4;
-      float mw[kWarps], top = -INFINITY, sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mw[w] = jm[(w * kRows + r) * 2], top = fmaxf(top, mw[w]);
-      const float ref = top == -INFINITY ? 0.0f : top;
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_approx(mw[w] - ref);
-        const float4 v = *reinterpret_cast<const float4*>(jo + (w * kRows + r) * DP + d);
-        sum += f * jm[(w * kRows + r) * 2 + 1];
-        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+            for (int j = 0; j < EV; j += 4) {
+              const int b = h * EV + j;
+              float4 v = make_float4(o[b][c], o[b + 1][c], o[b + 2][c], o[b + 3][c]);
+              if (upper) v = make_float4(o[b][2 + c], o[b + 1][2 + c], o[b + 2][2 + c], o[b + 3][2 + c]);
+              *reinterpret_cast<float4*>(row + EV * (2 * t + c + 8 * h) + j) =
+                  make_float4(v.x * unit, v.y * unit, v.z * unit, v.w * unit);
+            }
       }
-      if (whole) {
-        const int token = static_cast<int>(divide(row0 + r, a.by_group)), g = row0 + r - token * a.group;
-        const int64_t row = seq.first + token;
-        const int head = at.head * a.group + g;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint2 u;
-        u.x = pack2(acc.x * inv, acc.y * inv, T::f16 ? MOE_F16 : MOE_BF16);
-        u.y = pack2(acc.z * inv, acc.w * inv, T::f16 ? MOE_F16 : MOE_BF16);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d) = u;
-        if (d == 0 && a.lse)
-          a.lse[row * a.kv_heads * a.group + head] =
-              sum == 0.0f ? -INFINITY : (top + (log2f(sum) - exp_lift<T::f16>())) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + (part * kRows + r) * a.head_dim + d) = acc;
-        if (d == 0) a.part_ml[(part * kRows + r) * 2] = top, a.part_ml[(part * kRows + r) * 2 + 1] = sum;
+      __syncthreads();
+      if (r0 + kJoinRows >= rows && more) finish_q();  // all warps are past the old one
+#pragma unroll 1
+      for (int i = tid; i < min(kJoinRows, rows - r0) * d4; i += kThreads) {
+        const int rr = i / d4, d = (i - rr * d4) * 4, r = r0 + rr;
+        float mw[kWarps], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) mw[v] = join_ml[v][r][0], top = fmaxf(top, mw[v]);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          const float f = exp2_approx(mw[v] - ref);
+          const float4 x = *reinterpret_cast<const float4*>(join_o + (v * kJoinRows + rr) * DP + d);
+          sum += f * join_ml[v][r][1];
+          acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+        }
+        if (whole) {
+          const int token = static_cast<int>(divide(row0 + r, a.by_group)), g = row0 + r - token * a.group;
+          const int64_t row = seq_first + token;
+          const int head = kv_head * a.group + g;
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          uint2 u;
+          u.x = pack2(acc.x * inv, acc.y * inv, a.type), u.y = pack2(acc.z * inv, acc.w * inv, a.type);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d) = u;
+          if (d == 0 && a.lse)
+            a.lse[row * a.kv_heads * a.group + head] =
+                sum == 0.0f ? -INFINITY : (top + (log2f(sum) - exp_lift<T::f16>())) * kLn2;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (part * kRows + r) * a.head_dim + d) = acc;
+          if (d == 0) a.part_ml[(part * kRows + r) * 2] = top, a.part_ml[(part * kRows + r) * 2 + 1] = sum;
+        }
       }
+      __syncthreads();  // the buffers are free again, the next query is there
     }
-    if (!whole && tid == 0) {
-      Note n;
-      n.c0 = work.cta_of(unit0), n.count = work.cta_of(unit0 + tile.t1 - tile.t0 - 1) - n.c0 + 1;
-      n.row = row0, n.rows = tile.rows, n.first = seq.first, n.head = at.head;
-      a.notes[part] = n;
-    }
-    __syncthreads();  // the ring is free again
-    if (pieces < S::pieces) {
-      for (int i = lane; i < S::stages * S::stage_bytes / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
-      __syncwarp();
-    }
-    x += tb - ta;
-    next_unit<kRows>(a, at, seq);
   }
+  cp_wait<0>();
 }
 
 // ---- the join ---------------------------------------------------------------------
@@ -568,9 +679,9 @@ template <int DP, int K>
 cudaError_t launch_rows(const AttnArgs& a, int num_sms, cudaStream_t st) {
   using S = Shape<DP, K>;
   auto kernel = attention_rows_kernel<DP, K>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * S::ring_bytes);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
   if (e) return e;
-  kernel<<<num_sms * S::ctas, kThreads, kWarps * S::ring_bytes, st>>>(a);
+  kernel<<<num_sms * S::ctas, kThreads, S::smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -579,8 +690,7 @@ cudaError_t launch_rows(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st)
   switch (k) {
     case kBf16: return launch_rows<DP, kBf16>(a, num_sms, st);
     case kF16: return launch_rows<DP, kF16>(a, num_sms, st);
-    case kE4m3Bf16: return launch_rows<DP, kE4m3Bf16>(a, num_sms, st);
-    default: return launch_rows<DP, kE4m3F16>(a, num_sms, st);
+    default: return launch_rows<DP, kE4m3F16>(a, num_sms, st);  // for both types of q
   }
 }
 
@@ -678,7 +788,7 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   a.k = c.k, a.v = c.v, a.k_scale = c.k_scale, a.v_scale = c.v_scale;
   a.page_stride = c.page_stride * size, a.slot_stride = c.slot_stride * size, a.head_stride = c.head_stride * size;
   a.scale_page_stride = c.scale_page_stride, a.scale_slot_stride = c.scale_slot_stride, a.scale_head_stride = c.scale_head_stride;
-  a.head_dim = c.head_dim, a.kv_heads = c.kv_heads, a.group = group, a.causal = g.causal, a.window = g.window;
+  a.head_dim = c.head_dim, a.kv_heads = c.kv_heads, a.group = group, a.causal = g.causal, a.window = g.window, a.type = g.q_type;
   a.scale_log2 = g.scale * 1.4426950408889634f;
   a.by_group = divisor(static_cast<uint32_t>(group));
   const Kind kind = c.type == MOE_BF16 ? kBf16 : c.type == MOE_F16 ? kF16 : g.q_type == MOE_BF16 ? kE4m3Bf16 : kE4m3F16;
@@ -696,7 +806,7 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
       : c.head_dim <= 128  ? launch_rows<128>(a, kind, sms, st)
                            : launch_rows<256>(a, kind, sms, st);
   if (!e)
-    e = launch_join(a, grid, tile_rows, f16, many ? tiles_lift(f16) : f16 ? exp_lift<true>() : exp_lift<false>(), st);
+    e = launch_join(a, grid, tile_rows, f16, many ? tiles_lift(f16) : kind == kBf16 ? exp_lift<false>() : exp_lift<true>(), st);
   if (e) return reportf(MOE_ERR_CUDA, "moe_attention: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
   return MOE_OK;
 }

@@ -122,6 +122,7 @@ struct AttnArgs {
   int64_t page_stride, slot_stride, head_stride;                 // bytes
   int64_t scale_page_stride, scale_slot_stride, scale_head_stride;  // floats
   int head_dim, kv_heads, group, causal, window;
+  int type;           // of the query and the output
   float scale_log2;  // scale * log2(e)
   Divisor by_group;
   unsigned* ctl;    // [0] error bits
@@ -325,6 +326,58 @@ __device__ __forceinline__ Work find_work(const AttnArgs& a, PlanSmem& sm) {
   w.at = sm.at, w.seq = sm.seq;
   return w;
 }
+
+// One CTA's pieces of units, in order.  Each warp has one (or two) in shared memory,
+// which its first lane moves on: registers are short.
+template <int R, int BN>
+struct Walk {
+  Place at;
+  Seq seq;
+  Tile tile;
+  int x, end;  // tiles of the line: the piece's first, the CTA's last
+  int ta, tb;  // key tiles of this piece
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Work& work) {
+    at = work.at, seq = work.seq, x = work.begin, end = work.end;
+    cut(a);
+  }
+  __device__ __forceinline__ void cut(const AttnArgs& a) {
+    tile = tile_of<R, BN>(a, seq, at.tile);
+    ta = tile.t0 + at.at;
+    tb = min(tile.t1, ta + (end - x));
+  }
+  __device__ __forceinline__ bool more() const { return x < end; }
+  __device__ __forceinline__ bool whole() const { return ta == tile.t0 && tb == tile.t1; }
+  // all lanes of the warp
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) step(a);
+    __syncwarp();
+  }
+  // all lanes: a copy, and a copy one piece ahead
+  __device__ __forceinline__ void become(const Walk& o) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) *this = o;
+    __syncwarp();
+  }
+  __device__ __forceinline__ void follow(const AttnArgs& a, const Walk& o) {
+    become(o);
+    next(a);
+  }
+  __device__ __forceinline__ void step(const AttnArgs& a) {
+    if (x >= end) return;
+    x += tb - ta;
+    next_unit<R>(a, at, seq);
+    if (x < end) cut(a);
+  }
+  // Who shares a piece that is not whole, for the join.
+  __device__ __forceinline__ void note(const AttnArgs& a, const Work& work) const {
+    const int unit0 = x - at.at;
+    Note n;
+    n.c0 = work.cta_of(unit0), n.count = work.cta_of(unit0 + tile.t1 - tile.t0 - 1) - n.c0 + 1;
+    n.row = at.tile * R, n.rows = tile.rows, n.first = seq.first, n.head = at.head;
+    a.notes[2 * blockIdx.x + (ta == tile.t0 ? 1 : 0)] = n;
+  }
+};
 
 cudaError_t launch_tiles(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st);
 int tiles_rows(int head_dim);   // rows of launch_tiles' tiles

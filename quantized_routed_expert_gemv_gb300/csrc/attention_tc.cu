@@ -62,49 +62,8 @@ struct Geo {
   static constexpr int o_col = 256, o_cols = DP;
 };
 
-// One CTA's pieces of units, in order: the same for every role.  Each warp has
-// one in shared memory, which its first lane moves on: registers are short.
 template <int DP>
-struct Walk {
-  using G = Geo<DP>;
-  Place at;
-  Seq seq;
-  Tile tile;
-  int x, end;  // tiles of the line: the piece's first, the CTA's last
-  int ta, tb;  // key tiles of this piece
-  __device__ __forceinline__ void begin(const AttnArgs& a, const Work& work) {
-    at = work.at, seq = work.seq, x = work.begin, end = work.end;
-    cut(a);
-  }
-  __device__ __forceinline__ void cut(const AttnArgs& a) {
-    tile = tile_of<G::rows, G::bn>(a, seq, at.tile);
-    ta = tile.t0 + at.at;
-    tb = min(tile.t1, ta + (end - x));
-  }
-  __device__ __forceinline__ bool more() const { return x < end; }
-  // all lanes of the warp
-  __device__ __forceinline__ void next(const AttnArgs& a) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) step(a);
-    __syncwarp();
-  }
-  // all lanes: a copy, and a copy one piece ahead
-  __device__ __forceinline__ void become(const Walk& o) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) *this = o;
-    __syncwarp();
-  }
-  __device__ __forceinline__ void follow(const AttnArgs& a, const Walk& o) {
-    become(o);
-    next(a);
-  }
-  __device__ __forceinline__ void step(const AttnArgs& a) {
-    if (x >= end) return;
-    x += tb - ta;
-    next_unit<G::rows>(a, at, seq);
-    if (x < end) cut(a);
-  }
-};
+using TileWalk = Walk<Geo<DP>::rows, Geo<DP>::bn>;
 
 template <int DP>
 struct Shared {
@@ -119,7 +78,7 @@ struct Shared {
   uint32_t tmem;
   int failed;
   int holes;                             // a page was missing among those of a tile
-  Walk<DP> walk[13], ahead[8];           // of each warp; the softmax warps' next pieces
+  TileWalk<DP> walk[13], ahead[8];           // of each warp; the softmax warps' next pieces
   PlanSmem plan;
 };
 
@@ -301,7 +260,7 @@ __device__ __noinline__ bool odd_values(const AttnArgs& a, int seq, int head, in
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, Walk<DP>& w, Walk<DP>& nx, const Work& work,
+__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, TileWalk<DP>& w, TileWalk<DP>& nx, const Work& work,
                                              int half, int wtid) {
   using G = Geo<DP>;
   using T = Traits<K>;
@@ -312,7 +271,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
   uint32_t n_tile = 0, n_piece = 0, tiles = 0;  // this half's tiles and pieces; all tiles of the CTA
   // A piece's queries are on their way while the one before it ends: from its last
   // product with the old ones on their place is free.
-  auto load_q = [&](const Walk<DP>& u) {
+  auto load_q = [&](const TileWalk<DP>& u) {
     const int r = half * kHalf + wtid, row0 = u.at.tile * G::rows;
     const int token = static_cast<int>(divide(row0 + min(r, u.tile.rows - 1), a.by_group)), g = row0 + r - token * a.group;
     const uint16_t* q = static_cast<const uint16_t*>(a.query) + (u.seq.first + token) * a.ld_q +
@@ -330,7 +289,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
     fence_async_smem();
     mbar_arrive(&sm.q_full[half]);
   };
-  const auto here = [&](const Walk<DP>& u) { return u.more() && half * kHalf < u.tile.rows; };
+  const auto here = [&](const TileWalk<DP>& u) { return u.more() && half * kHalf < u.tile.rows; };
   if (here(w)) load_q(w);
   nx.follow(a, w);
   if (here(w)) hand_q();
@@ -471,7 +430,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       tc_fence_before();
       continue;
     }
-    const bool whole = w.ta == w.tile.t0 && w.tb == w.tile.t1;
+    const bool whole = w.whole();
     const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (w.ta == w.tile.t0 ? 1 : 0);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int head = w.at.head * a.group + (row0 + rc - token * a.group);
@@ -548,13 +507,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
         }
       }
     }
-    if (!whole && half == 0 && wtid == 0) {
-      Note n;
-      const int unit0 = w.x - w.at.at;
-      n.c0 = work.cta_of(unit0), n.count = work.cta_of(unit0 + w.tile.t1 - w.tile.t0 - 1) - n.c0 + 1;
-      n.row = row0, n.rows = w.tile.rows, n.first = w.seq.first, n.head = w.at.head;
-      a.notes[part] = n;
-    }
+    if (!whole && half == 0 && wtid == 0) w.note(a, work);
   }
 }
 
@@ -576,7 +529,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& maps, Shared<DP>& sm, uint8_t* ring, Walk<DP>& w, int tid) {
+__device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& maps, Shared<DP>& sm, uint8_t* ring, TileWalk<DP>& w, int tid) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn;
@@ -664,7 +617,7 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
 // positions: it looks them up, a lane each, and copies them, as many lanes a position as
 // it has 16-byte pieces; so the warps exchange nothing but which positions count.
 template <int DP, int K>
-__device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, Walk<DP>& w, int tid) {
+__device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, TileWalk<DP>& w, int tid) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn, MINE = BN / 4, PR = DP / 16, STEP = 32 / PR, PER = MINE / STEP;
@@ -751,7 +704,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, 
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint32_t qs, uint32_t ring, Walk<DP>& w) {
+__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint32_t qs, uint32_t ring, TileWalk<DP>& w) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn;
@@ -889,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
     return;
   }
   {
-    Walk<DP>& w = sm.walk[warp < 13 ? warp : 12];
+    TileWalk<DP>& w = sm.walk[warp < 13 ? warp : 12];
     if (warp < 13 && (tid & 31) == 0) w.begin(a, work);
     __syncwarp();
     // registers: 2 x 128 x 184 + 128 x 96 + 128 x 48 = 512 x 128

@@ -356,7 +356,9 @@ struct Walk {
   // all lanes: a copy, and a copy one piece ahead
   __device__ __forceinline__ void become(const Walk& o) {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) *this = o;
+    static_assert(sizeof(Walk) % 4 == 0 && sizeof(Walk) <= 128, "a word a lane");
+    if ((threadIdx.x & 31) < sizeof(Walk) / 4)
+      reinterpret_cast<int*>(this)[threadIdx.x & 31] = reinterpret_cast<const int*>(&o)[threadIdx.x & 31];
     __syncwarp();
   }
   __device__ __forceinline__ void follow(const AttnArgs& a, const Walk& o) {

@@ -19,7 +19,7 @@
 // Roles: eight warps (four with one half) take softmaxes, four bring keys and
 // values into a ring of tiles in 128-byte swizzled order (16-byte copies to places
 // looked up page by page, so that pages may have any size; e4m3 codes become 16-bit
-// values on the way), one issues the products.
+// values on the way), one issues the products, one goes from unit to unit ahead of all.
 //
 // What a row does not see but its tile does (the diagonal, a window's edge) gets
 // exponential 0, which an infinity or a NaN among the values would turn into
@@ -69,7 +69,7 @@ template <int DP>
 struct Shared {
   using G = Geo<DP>;
   uint64_t full[G::stages], empty[G::stages];
-  uint64_t z_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], q_full[2], pv_done;
+  uint64_t z_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], q_full[2], pv_done, tail;
   // Of the tiles under way.  A slow producer thread may be at tile t - 1 while a
   // fast one writes tile t + 1; softmaxes may be three tiles behind.
   int64_t off[4][G::bn];                 // byte offsets of a tile's positions, -1: not seen
@@ -78,7 +78,8 @@ struct Shared {
   uint32_t tmem;
   int failed;
   int holes;                             // a page was missing among those of a tile
-  TileWalk<DP> walk[13], ahead[8];           // of each warp; the softmax warps' next pieces
+  TileWalk<DP> walk, pieces[4];          // one warp goes from piece to piece, the others take them from a ring
+  uint64_t piece_full[4], piece_empty[4];
   PlanSmem plan;
 };
 
@@ -171,6 +172,40 @@ __device__ __forceinline__ bool wait(S& sm, const AttnArgs& a, uint64_t* bar, ui
   return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_long(a.ctl, &sm.failed, bar, parity);
 }
 
+// A warp's place in the ring of pieces.  The last one has no tiles.
+template <int DP>
+struct Pieces {
+  Shared<DP>& sm;
+  const AttnArgs& a;
+  int i = 0;
+  __device__ __forceinline__ Pieces(Shared<DP>& s, const AttnArgs& args) : sm(s), a(args) {}
+  __device__ __forceinline__ bool ready(int ahead) const {
+    return wait(sm, a, &sm.piece_full[(i + ahead) & 3], ((i + ahead) >> 2) & 1);
+  }
+  __device__ __forceinline__ const TileWalk<DP>& at(int ahead) const { return sm.pieces[(i + ahead) & 3]; }
+  __device__ __forceinline__ void done() {  // all lanes
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.piece_empty[i & 3]);
+    ++i;
+  }
+};
+
+// The warp that goes from piece to piece (all lanes).
+template <int DP>
+__device__ __forceinline__ void walk_role(const AttnArgs& a, Shared<DP>& sm, const Work& work) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) sm.walk.begin(a, work);
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0;; ++i) {
+    if (i >= 4 && !wait(sm, a, &sm.piece_empty[i & 3], ((i >> 2) - 1) & 1)) return;
+    sm.pieces[i & 3].become(sm.walk);
+    if (lane == 0) mbar_arrive(&sm.piece_full[i & 3]);
+    if (!sm.walk.more()) return;
+    sm.walk.next(a);
+  }
+}
+
 // A cached 16-byte piece's eight 16-bit values as the products see them.
 template <int K>
 __device__ __forceinline__ uint4 values_at(const void* base, int64_t off, int d, float scale) {
@@ -260,7 +295,7 @@ __device__ __noinline__ bool odd_values(const AttnArgs& a, int seq, int head, in
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, TileWalk<DP>& w, TileWalk<DP>& nx, const Work& work,
+__device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* qs, const Work& work,
                                              int half, int wtid) {
   using G = Geo<DP>;
   using T = Traits<K>;
@@ -290,13 +325,19 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
     mbar_arrive(&sm.q_full[half]);
   };
   const auto here = [&](const TileWalk<DP>& u) { return u.more() && half * kHalf < u.tile.rows; };
-  if (here(w)) load_q(w);
-  nx.follow(a, w);
-  if (here(w)) hand_q();
-  for (; w.more(); w.become(nx), nx.next(a)) {
+  Pieces<DP> pieces(sm, a);
+  if (!pieces.ready(0)) return;
+  if (here(pieces.at(0))) {
+    load_q(pieces.at(0));
+    hand_q();
+  }
+#pragma unroll 1
+  for (; pieces.at(0).more(); pieces.done()) {
+    const TileWalk<DP>&w = pieces.at(0), &nx = pieces.at(1);
     const int nt = w.tb - w.ta;
     if (!here(w)) {
       tiles += nt;
+      if (!pieces.ready(1)) return;
       if (here(nx)) {
         load_q(nx);
         hand_q();
@@ -310,6 +351,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
     const int lo = sees_from(a, pos), hi = sees_to(a, w.seq.len, pos);
     const bool some = half * kHalf + warp * 32 < w.tile.rows;  // the warp has rows
     const int all_lo = __reduce_max_sync(0xFFFFFFFFu, lo), all_hi = __reduce_min_sync(0xFFFFFFFFu, hi);
+    const int ta = w.ta;
     float m = -INFINITY, l = 0.0f;  // m: the reference, scaled
 #pragma unroll 1
     for (int j = 0; j < nt; ++j, ++n_tile, ++tiles) {
@@ -317,10 +359,13 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       const uint32_t zaddr = tm + buf * G::z_cols;
       if (!wait(sm, a, &sm.z_full[buf], (G::halves == 2 ? n_tile : n_tile >> 1) & 1)) return;
       tc_fence_after();
-      if (j == nt - 1 && here(nx)) load_q(nx);
+      if (j == nt - 1) {
+        if (!pieces.ready(1)) return;
+        if (here(nx)) load_q(nx);
+      }
       if (some) {
         constexpr int HB = BN / 2;
-        const int first = (w.ta + j) * BN;
+        const int first = (ta + j) * BN;
         // Pages may be missing, which is rare: asked for here, looked at when the first
         // exponentials are there, as shared memory answers late beside the products.
         const int holes = *reinterpret_cast<volatile int*>(&sm.holes);
@@ -330,11 +375,11 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
           tmem_ld32(zaddr + c, z);
           if (masked) {
             tmem_wait();
-            const int from = lo - first - c, to = hi - first - c;
-            const uint32_t bits = sm.bits[tiles & 7][c / 32];
+            // positions from `from` up to `to`, as bits
+            const int from = min(max(lo - first - c, 0), 32), to = min(max(hi - first - c, 0), 32);
+            const uint32_t see = sm.bits[tiles & 7][c / 32] & (from < 32 ? ~0u << from : 0u) & (to > 0 ? ~0u >> (32 - to) : 0u);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k < from || k >= to || !(bits >> k & 1)) z[k] = -INFINITY;
+            for (int k = 0; k < 32; ++k) z[k] = see & (1u << k) ? z[k] : -INFINITY;
           }
         };
         // One half of the positions after the other, in the same few instructions: code
@@ -529,7 +574,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& maps, Shared<DP>& sm, uint8_t* ring, TileWalk<DP>& w, int tid) {
+__device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& maps, Shared<DP>& sm, uint8_t* ring, int tid) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn;
@@ -539,23 +584,27 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
   const int pieces = a.head_dim * T::size / 16;
   const uint32_t ring_s = smem_u32(ring);
   RingPos load;
-  uint32_t tiles = 0, groups = 0;
+  uint32_t tiles = 0, groups = 0, tails = 0;
   // thread t looks up position t of the next tile
   int page = -1, slot = 0, head = 0;
   bool seen = false;
   struct View {
     int first, nt, lo, hi, seq, head, len;
   };
-  auto view = [&] { return View{w.ta * BN, w.tb - w.ta, w.tile.lo, w.tile.hi, w.at.seq, w.at.head, w.seq.len}; };
+  Pieces<DP> ps(sm, a);
+  auto view = [&] {
+    const TileWalk<DP>& w = ps.at(0);
+    return View{w.ta * BN, w.more() ? w.tb - w.ta : 0, w.tile.lo, w.tile.hi, w.at.seq, w.at.head, w.seq.len};
+  };
   auto look_up = [&](const View& u, int j) {
-    page = -1, head = u.head;
+    page = -1, slot = 0, head = u.head;
     const int pos = u.first + j * BN + tid;
     if (tid < BN && pos < u.len) page = page_of(a.q, u.seq, pos, slot);
     const bool counts = tid < BN && pos >= u.lo && pos < u.hi;
     seen = page >= 0 && counts;
     if (counts && page < 0) *reinterpret_cast<volatile int*>(&sm.holes) = 1;
   };
-  // The looked-up tile, for all producers; whether all of its positions exist.
+  // The looked-up tile, for all producers.
   auto post = [&] {
     if (tid < BN) {
       const uint32_t on = __ballot_sync(0xFFFFFFFFu, seen);
@@ -563,35 +612,53 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
       sm.place[tiles & 3][tid] = make_int2(page, slot);
       if (lane == 0) sm.bits[tiles & 7][warp] = on;
     }
-    return !named_bar_or(1, 128, tid < BN && page < 0);
+    named_bar(1, 128);
   };
-  look_up(view(), 0);
-  while (w.more()) {
-    const View u = view();
+  if (!ps.ready(0)) return;
+  View u = view();
+  look_up(u, 0);
+  while (u.nt > 0) {
     const int nt = u.nt;
-    w.next(a);
+    ps.done();
+    if (!ps.ready(0)) return;
+    const View after = view();
 #pragma unroll 1
     for (int j = 0; j < nt; ++j, ++tiles) {
-      const bool all = post();
+      post();
       if (j + 1 < nt) look_up(u, j + 1);
-      else if (w.more()) look_up(view(), 0);
+      else if (after.nt > 0) look_up(after, 0);
       const int64_t* offs = sm.off[tiles & 3];
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++groups) {
         if (groups >= G::stages && !wait(sm, a, &sm.empty[load.s], load.ph ^ 1)) return;
         const uint32_t dst = ring_s + load.s * G::stage_bytes;
-        if (all && maps.rows) {
-          if (tid == 0) mbar_arrive_expect_tx(&sm.full[load.s], G::stage_bytes);
-          else mbar_arrive(&sm.full[load.s]);
+        if (maps.rows) {
+          // The slots behind the sequence's end may hold anything: the values there become
+          // zeros before the products see them.  What has no page is out of the tensor's bounds: zeros.
+          const int held = u.len - (u.first + j * BN);
+          uint64_t* bar = kv && held < BN ? &sm.tail : &sm.full[load.s];
+          if (tid == 0) mbar_arrive_expect_tx(bar, G::stage_bytes);
+          else if (bar != &sm.tail) mbar_arrive(bar);
           // lanes issue boxes one after the other, so the warps take turns
           const int box = lane * 4 + warp, slab = static_cast<int>(divide(box, maps.row_boxes)),
                     row = (box - slab * static_cast<int>(maps.row_boxes.d)) * maps.rows;
           if (slab < DP / 64) {
             const int2 at = sm.place[tiles & 3][row];
-            load_box(dst + slab * (BN * 128) + row * 128, kv ? &maps.v : &maps.k, slab * 64, at.y, u.head, at.x, &sm.full[load.s]);
+            load_box(dst + slab * (BN * 128) + row * 128, kv ? &maps.v : &maps.k, slab * 64, at.y, u.head,
+                     at.x < 0 ? a.q.n_pages : at.x, bar);
+          }
+          if (bar == &sm.tail) {
+            if (!wait(sm, a, bar, tails++ & 1)) return;
+            if (tid < BN && tid >= held)
+#pragma unroll 4
+              for (int c = 0; c < DP / 8; ++c)
+                *reinterpret_cast<uint4*>(ring + load.s * G::stage_bytes + (c / 8) * (BN * 128) + tid * 128 + (c & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            mbar_arrive(&sm.full[load.s]);
           }
         } else {
-          // a tile that the sequence ends in, or whose pages are small: what does not count is zeros
+          // pages that no box of 8 positions divides: what does not count is zeros
           const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k);
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
@@ -609,6 +676,7 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
         load.next(G::stages);
       }
     }
+    u = after;
   }
 }
 
@@ -617,7 +685,7 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, const Maps& map
 // positions: it looks them up, a lane each, and copies them, as many lanes a position as
 // it has 16-byte pieces; so the warps exchange nothing but which positions count.
 template <int DP, int K>
-__device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, TileWalk<DP>& w, int tid) {
+__device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, int tid) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn, MINE = BN / 4, PR = DP / 16, STEP = 32 / PR, PER = MINE / STEP;
@@ -628,7 +696,9 @@ __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, 
   uint32_t tiles = 0, groups = 0;
   int64_t off = -1;  // of the position that this lane looked up (-1: not seen)
   float ks = 1.0f, vs = 1.0f;
-  auto look_up = [&](int j) {  // tile j of the walk's piece
+  Pieces<DP> ps(sm, a);
+  auto look_up = [&](int j) {  // tile j of the piece
+    const TileWalk<DP>& w = ps.at(0);
     off = -1, ks = vs = 1.0f;
     const int pos = (w.ta + j) * BN + warp * MINE + lane;
     if (lane < MINE && pos >= w.tile.lo && pos < w.tile.hi) {
@@ -675,11 +745,12 @@ __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, 
     ++groups;
     return true;
   };
-  if (!w.more()) return;
+  auto tiles_of = [&] { return ps.at(0).more() ? ps.at(0).tb - ps.at(0).ta : 0; };
   uint4 kb[PER], vb[PER];
+  if (!ps.ready(0)) return;
   look_up(0);
   fetch(kb, a.k);
-  int j = 0, nt = w.tb - w.ta;
+  int j = 0, nt = tiles_of();
   for (;;) {
     fetch(vb, a.v);
     const float k_scale = ks, v_scale = vs;
@@ -691,10 +762,11 @@ __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, 
     }
     ++tiles;
     if (++j == nt) {
-      w.next(a);
-      j = 0, nt = w.tb - w.ta;
+      ps.done();
+      if (!ps.ready(0)) return;
+      j = 0, nt = tiles_of();
     }
-    const bool more = j > 0 || w.more();
+    const bool more = nt > 0;
     if (more) look_up(j);
     if (!store(kb, k_scale)) return;
     if (more) fetch(kb, a.k);
@@ -704,7 +776,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, 
 }
 
 template <int DP, int K>
-__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint32_t qs, uint32_t ring, TileWalk<DP>& w) {
+__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint32_t qs, uint32_t ring) {
   using G = Geo<DP>;
   using T = Traits<K>;
   constexpr int BN = G::bn;
@@ -756,10 +828,13 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared<DP>& sm, uint
     r.next(G::stages);
     return s;
   };
-  for (; w.more(); w.next(a)) {
-    const int nt = w.tb - w.ta;
+  Pieces<DP> ps(sm, a);
+#pragma unroll 1
+  for (;; ps.done()) {
+    if (!ps.ready(0) || !ps.at(0).more()) return;
+    const int nt = ps.at(0).tb - ps.at(0).ta;
     if constexpr (G::halves == 2) {
-      const int halves = w.tile.rows > kHalf ? 2 : 1;
+      const int halves = ps.at(0).tile.rows > kHalf ? 2 : 1;
       int ks = take(p);
       if (ks < 0) return;
       for (int h = 0; h < halves; ++h) {
@@ -828,7 +903,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
     for (int i = 0; i < 2; ++i)
       mbar_init(&sm.z_full[i], 1), mbar_init(&sm.half_done[i], 1), mbar_init(&sm.p_half[i], kHalf), mbar_init(&sm.p_ready[i], kHalf), mbar_init(&sm.o_full[i], 1),
           mbar_init(&sm.q_full[i], kHalf);
-    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.pv_done, 1), mbar_init(&sm.tail, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.piece_full[i], 1), mbar_init(&sm.piece_empty[i], 4 * G::halves + 4 + 1);
     sm.failed = sm.holes = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
@@ -842,20 +918,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const Attn
     return;
   }
   {
-    TileWalk<DP>& w = sm.walk[warp < 13 ? warp : 12];
-    if (warp < 13 && (tid & 31) == 0) w.begin(a, work);
-    __syncwarp();
-    // registers: 2 x 128 x 184 + 128 x 96 + 128 x 48 = 512 x 128
+    // registers of the roles' 128 threads: 2 x 184 + 96 + 48 or 2 x 168 + 128 + 48 = 4 x 128
+    constexpr bool e4m3 = Traits<K>::e4m3;
     if (warp < 8) {
-      reg_up<184>();
-      if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, w, sm.ahead[warp & 7], work, warp >> 2, tid & 127);
+      reg_up<e4m3 ? 168 : 184>();
+      if (warp < 4 * G::halves) softmax_role<DP, K>(a, sm, base, work, warp >> 2, tid & 127);
     } else if (warp < 12) {
-      reg_down<96>();
-      if constexpr (Traits<K>::e4m3) dequant_role<DP, K>(a, sm, ring, w, tid - 256);
-      else producer_role<DP, K>(a, maps, sm, ring, w, tid - 256);
+      reg_down<e4m3 ? 128 : 96>();
+      if constexpr (Traits<K>::e4m3) dequant_role<DP, K>(a, sm, ring, tid - 256);
+      else producer_role<DP, K>(a, maps, sm, ring, tid - 256);
     } else {
       reg_down<48>();
-      if (warp == 12) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring), w);
+      if (warp == 12) mma_role<DP, K>(a, sm, smem_u32(base), smem_u32(ring));
+      else if (warp == 13) walk_role<DP>(a, sm, work);
     }
   }
   if (tid == 384 && *reinterpret_cast<volatile int*>(&sm.failed)) {

@@ -68,7 +68,9 @@ struct Shape {
   static constexpr int vgroups = DP / (8 * ev);
   static constexpr int scale_bytes = T::e4m3 ? 2 * kStep * 4 : 0;
   static constexpr int stage_bytes = 2 * kStep * row_bytes + scale_bytes + 16;  // 16: which positions count
-  static constexpr int ctas = DP <= 128 ? 2 : 1;            // on an SM
+  // on an SM: as many warps as their registers allow, while two stages of each fit (64
+  // ragged e4m3 sequences with heads of 128: two CTAs 183 us, three 1xx)
+  static constexpr int ctas = DP <= 64 ? 3 : DP <= 128 ? 2 : 1;
   static constexpr bool q_shared = DP > 128;                // the query's fragments lie in shared memory
   static constexpr int join_bytes = kWarps * kJoinRows * DP * 4;
   static constexpr int q_bytes = q_shared ? DP / 16 * 512 : 0;
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 constexpr int kFewRows = 48;
 
 // CTAs of the widest grid that a workspace serves, on an SM.
-constexpr int kMaxCtas = 2;
+constexpr int kMaxCtas = 3;
 
 struct Parts {
   size_t notes, ml, o, bytes;
@@ -765,7 +767,7 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
     return reportf(MOE_ERR_ARG, "moe_attention: %d rows of %d query heads a key head are more than 2^30", seqs->rows, group);
   // key tiles of 64 positions, row tiles of 16 rows, at the worst
   const int64_t row_tiles = (static_cast<int64_t>(seqs->rows) * group / kRows + seqs->n_seqs) * c.kv_heads;
-  if (row_tiles * (a.q.cap / kBn + 1) > 0x7FFFFFFF)
+  if (row_tiles * (a.q.cap / kBn + 1 + kUnitCost) > 0x7FFFFFFF)
     return reportf(MOE_ERR_UNSUPPORTED, "moe_attention: %d rows in %d sequences of up to %d positions are more than 2^31 tiles of work",
                    seqs->rows, seqs->n_seqs, a.q.cap);
   if (!g.q || !g.out || !workspace) return reportf(MOE_ERR_ARG, "moe_attention: q, out or workspace is NULL");
@@ -796,7 +798,8 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const bool many = static_cast<int64_t>(seqs->max_rows) * group > kFewRows;
-  const int grid = many ? sms : sms * (c.head_dim <= 128 ? 2 : 1), tile_rows = many ? tiles_rows(c.head_dim) : kRows;
+  const int per_sm = c.head_dim > 128 ? 1 : c.head_dim > 64 ? 2 : 3;  // as Shape has them
+  const int grid = many ? sms : sms * per_sm, tile_rows = many ? tiles_rows(c.head_dim) : kRows;
   const Parts p = parts_of(grid, tile_rows, c.head_dim);
   a.ctl = reinterpret_cast<unsigned*>(base);
   a.notes = reinterpret_cast<Note*>(base + p.notes);

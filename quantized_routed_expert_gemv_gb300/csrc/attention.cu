@@ -37,7 +37,7 @@ __host__ __device__ constexpr float exp_lift() {
   return F16 ? 15.0f : 0.0f;
 }
 
-constexpr int kRows = 16;     // rows of a tile
+constexpr int kRows = 16;     // rows of the larger tile
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;     // positions of a warp's step
@@ -59,7 +59,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DP, int K>
+template <int DP, int K, int R>
 struct Shape {
   using T = Traits<K>;
   static constexpr int row_bytes = DP * T::size;            // of one position in shared memory
@@ -68,12 +68,12 @@ struct Shape {
   static constexpr int vgroups = DP / (8 * ev);
   static constexpr int scale_bytes = T::e4m3 ? 2 * kStep * 4 : 0;
   static constexpr int stage_bytes = 2 * kStep * row_bytes + scale_bytes + 16;  // 16: which positions count
-  // on an SM: as many warps as their registers allow, while two stages of each fit (64
-  // ragged e4m3 sequences with heads of 128: two CTAs 183 us, three 1xx)
-  static constexpr int ctas = DP <= 64 ? 3 : DP <= 128 ? 2 : 1;
-  static constexpr bool q_shared = DP > 128;                // the query's fragments lie in shared memory
+  // On an SM: as many warps as registers and two stages of each allow.  64 ragged e4m3
+  // sequences with 8 rows of 128: two CTAs 140 us, three 123.
+  static constexpr int ctas = DP <= 64 || (row_bytes <= 128 && R == 8) ? 3 : DP <= 128 ? 2 : 1;
+  static constexpr bool q_shared = DP > 128 && R > 8;       // the query's fragments lie in shared memory
   static constexpr int join_bytes = kWarps * kJoinRows * DP * 4;
-  static constexpr int q_bytes = q_shared ? DP / 16 * 512 : 0;
+  static constexpr int q_bytes = q_shared ? DP / 16 * (R / 8) * 256 : 0;
   static constexpr int budget = (224 * 1024 / ctas - 5 * 1024 - join_bytes - q_bytes) / kWarps;
   static constexpr int fit = budget / stage_bytes;
   static constexpr int stages = fit > 8 ? 8 : fit;
@@ -102,10 +102,17 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t w, int high) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// An 8 x 8 matrix of 16-bit values, two of row gi a lane, turned over.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
 // A lane's pieces of values of one group: positions 2t, 2t + 1, 2t + 8, 2t + 9.
-template <int DP, int K>
+template <int DP, int K, int R>
 struct Values {
-  using S = Shape<DP, K>;
+  using S = Shape<DP, K, R>;
   uint32_t w[4][S::ev == 16 || !Traits<K>::e4m3 ? 4 : 2];
   __device__ __forceinline__ void load(const uint8_t* v, int t, int gi, int h) {
 #pragma unroll
@@ -135,24 +142,23 @@ struct Values {
   }
 };
 
-using RowWalk = Walk<kRows, kBn>;
-
-template <int DP, int K>
-__global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_kernel(const AttnArgs a) {
-  using S = Shape<DP, K>;
+template <int DP, int K, int R>
+__global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_rows_kernel(const AttnArgs a) {
+  using S = Shape<DP, K, R>;
+  using RowWalk = Walk<R, kBn>;
   using T = Traits<K>;
-  constexpr int RB = S::row_bytes, KS = DP / 16, NB = DP / 8, EV = S::ev;
+  constexpr int RB = S::row_bytes, KS = DP / 16, MB = DP / 16, NB = R / 8, EV = S::ev;
   constexpr int half_type = T::f16 ? MOE_F16 : MOE_BF16;  // of the exponentials
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PlanSmem plan;
   __shared__ RowWalk walks[2][kWarps];       // of the pieces that are worked on, and of those that are loaded
-  __shared__ float join_ml[kWarps][kRows][2];
+  __shared__ float join_ml[kWarps][R][2];
   float* join_o = reinterpret_cast<float*>(smem + kWarps * S::ring_bytes);                     // [warp][kJoinRows][DP]
-  uint4* q_frag = reinterpret_cast<uint4*>(smem + kWarps * S::ring_bytes + S::join_bytes);     // [KS][lane]
+  uint2* q_frag = reinterpret_cast<uint2*>(smem + kWarps * S::ring_bytes + S::join_bytes);     // [KS][NB][lane]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gi = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
 
-  const Work work = find_work<kRows, kBn, kThreads>(a, plan);
+  const Work work = find_work<R, kBn, kThreads>(a, plan);
   if (tid < 2) a.notes[2 * blockIdx.x + tid].count = 0;
   if (work.begin == work.end) return;
   RowWalk &w = walks[0][warp], &lw = walks[1][warp];
@@ -215,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
   // A piece's query, in the order in which the keys are read.  For e4m3 caches
   // it becomes float16, a row times a power of two (q_scale takes it back) that brings its
   // largest magnitude to 2^13: exact but for elements below 2^-29 of that.
-  uint32_t qa[S::q_shared ? 1 : KS][4];
-  float q_scale[2] = {1.0f, 1.0f};
-  auto q_row = [&](int i) {  // this lane's row i (of rows gi and gi + 8), NULL if there is none
-    const int row0 = w.at.tile * kRows, r = gi + 8 * i;
+  uint32_t qb[S::q_shared ? 1 : KS][NB][2];
+  float q_scale[NB][2];  // of rows 8 n + 2t and + 1
+  auto q_row = [&](int n) {  // row 8 n + gi, NULL if there is none
+    const int row0 = w.at.tile * R, r = gi + 8 * n;
     if (r >= w.tile.rows) return static_cast<const uint16_t*>(nullptr);
     const int token = static_cast<int>(divide(row0 + r, a.by_group)), g = row0 + r - token * a.group;
     return static_cast<const uint16_t*>(a.query) + (w.seq.first + token) * a.ld_q +
@@ -240,53 +246,55 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
     return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   };
   auto scaled = [](uint32_t u, float f) { return pack2(bf16lo(u) * f, bf16hi(u) * f, MOE_F16); };
+  auto spread = [&](int n, float back) {  // from the lanes that read a row to those that have it in z
+    q_scale[n][0] = __shfl_sync(0xFFFFFFFFu, back, (2 * t) << 2), q_scale[n][1] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + 1) << 2);
+  };
   auto load_q = [&] {
     if constexpr (!S::q_shared) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint16_t* q = q_row(i);
+      for (int n = 0; n < NB; ++n) {
+        const uint16_t* q = q_row(n);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           const uint2 u = q_at(q, s);
-          qa[s][i] = u.x, qa[s][2 + i] = u.y;
+          qb[s][n][0] = u.x, qb[s][n][1] = u.y;
         }
       }
     }
   };
   auto finish_q = [&] {
     const bool narrow = T::e4m3 && a.type == MOE_BF16;
-    if constexpr (!S::q_shared) {
-      if (narrow) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+    for (int n = 0; n < NB; ++n) {
+      float f = 1.0f, back = 1.0f;
+      if constexpr (!S::q_shared) {
+        if (narrow) {
           uint32_t top = 0;
 #pragma unroll
-          for (int s = 0; s < KS; ++s) top = largest(largest(top, qa[s][i]), qa[s][2 + i]);
-          const float f = scale_of(top, q_scale[i]);
+          for (int s = 0; s < KS; ++s) top = largest(largest(top, qb[s][n][0]), qb[s][n][1]);
+          f = scale_of(top, back);
 #pragma unroll
-          for (int s = 0; s < KS; ++s) qa[s][i] = scaled(qa[s][i], f), qa[s][2 + i] = scaled(qa[s][2 + i], f);
+          for (int s = 0; s < KS; ++s) qb[s][n][0] = scaled(qb[s][n][0], f), qb[s][n][1] = scaled(qb[s][n][1], f);
+        }
+      } else {  // registers are short: a warp brings a quarter of the fragments
+        const uint16_t* q = q_row(n);
+        if (narrow) {
+          uint32_t top = 0;
+#pragma unroll 4
+          for (int s = 0; s < KS; ++s) {
+            const uint2 u = q_at(q, s);
+            top = largest(largest(top, u.x), u.y);
+          }
+          f = scale_of(top, back);
+        }
+#pragma unroll 1
+        for (int s = warp; s < KS; s += kWarps) {
+          uint2 u = q_at(q, s);
+          if (narrow) u = make_uint2(scaled(u.x, f), scaled(u.y, f));
+          q_frag[(s * NB + n) * 32 + lane] = u;
         }
       }
-    } else {  // registers are short: a warp brings a quarter of the fragments
-      const uint16_t* q[2] = {q_row(0), q_row(1)};
-      float f[2] = {1.0f, 1.0f};
-      if (narrow) {
-        uint32_t top[2] = {0, 0};
-#pragma unroll 4
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint2 u = q_at(q[i], s);
-            top[i] = largest(largest(top[i], u.x), u.y);
-          }
-        f[0] = scale_of(top[0], q_scale[0]), f[1] = scale_of(top[1], q_scale[1]);
-      }
-#pragma unroll 1
-      for (int s = warp; s < KS; s += kWarps) {
-        uint2 u0 = q_at(q[0], s), u1 = q_at(q[1], s);
-        if (narrow) u0 = make_uint2(scaled(u0.x, f[0]), scaled(u0.y, f[0])), u1 = make_uint2(scaled(u1.x, f[1]), scaled(u1.y, f[1]));
-        q_frag[s * 32 + lane] = make_uint4(u0.x, u1.x, u0.y, u1.y);
-      }
+      if (T::e4m3) spread(n, back);
     }
   };
   load_q();
@@ -295,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
 
   int stage = 0;
   while (w.more()) {
-    const int row0 = w.at.tile * kRows, rows = w.tile.rows, ta = w.ta, steps = w.tb - w.ta;
-    // the lane's two rows and what they see
-    int lo[2], hi[2];
+    const int row0 = w.at.tile * R, rows = w.tile.rows, ta = w.ta, steps = w.tb - w.ta;
+    // what the lane's rows 8 n + 2t and + 1 see
+    int lo[NB][2], hi[NB][2];
     int tight_lo, tight_hi;  // what all of the tile's rows see
     {
       const int base = w.seq.len - w.seq.n;
@@ -305,17 +313,23 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
       const int p1 = base + static_cast<int>(divide(row0 + rows - 1, a.by_group));
       tight_hi = sees_to(a, w.seq.len, p0), tight_lo = sees_from(a, p1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = gi + 8 * i;
-        const int p = base + static_cast<int>(divide(row0 + min(r, rows - 1), a.by_group));
-        lo[i] = sees_from(a, p);
-        hi[i] = r < rows ? sees_to(a, w.seq.len, p) : 0;
-      }
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = 8 * n + 2 * t + c;
+          const int p = base + static_cast<int>(divide(row0 + min(r, rows - 1), a.by_group));
+          lo[n][c] = sees_from(a, p);
+          hi[n][c] = r < rows ? sees_to(a, w.seq.len, p) : 0;
+        }
     }
-    float o[NB][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float o[MB][NB][4], m[NB][2], l[NB][2];
     float v_ref = 0.0f, v_inv = 0.0f;  // e4m3: o counts values in units of the largest scale so far
 #pragma unroll
-    for (int j = 0; j < NB; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    for (int n = 0; n < NB; ++n) {
+      m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < MB; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
+    }
 
 #pragma unroll 1
     for (int step = 0; step < steps; ++step) {
@@ -329,50 +343,44 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
       if (++stage == S::stages) stage = 0;
       if (mask == 0) continue;
 
-      // z: rows gi and gi + 8, positions 8 n + 2t and + 1
-      float z[2][4];
+      // z: positions gi (values 0 and 1) and gi + 8, rows 8 n + 2t and + 1
+      float z[NB][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
-      auto query = [&](int s, uint32_t (&q)[4]) {
-        if (S::q_shared) {
-          const uint4 u = q_frag[s * 32 + lane];
-          q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
-        } else {
-          q[0] = qa[s][0], q[1] = qa[s][1], q[2] = qa[s][2], q[3] = qa[s][3];
+      for (int n = 0; n < NB; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
+      auto product = [&](int s, const uint32_t (&k)[4]) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          if constexpr (S::q_shared) {
+            const uint2 u = q_frag[(s * NB + n) * 32 + lane];
+            mma16816<T::f16>(z[n], k, u.x, u.y);
+          } else {
+            mma16816<T::f16>(z[n], k, qb[s][n][0], qb[s][n][1]);
+          }
         }
       };
 #pragma unroll
       for (int i = 0; i < S::pieces / 4; ++i) {
         const uint4 u0 = lds128(ks + key_at<RB>(gi, t + 4 * i)), u1 = lds128(ks + key_at<RB>(8 + gi, t + 4 * i));
         const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-        uint32_t q[4];
         if constexpr (T::e4m3) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            query(4 * i + j, q);
-            mma16816<true>(z[0], q, two_codes(w0[j], 0), two_codes(w0[j], 1));
-            mma16816<true>(z[1], q, two_codes(w1[j], 0), two_codes(w1[j], 1));
-          }
+          for (int j = 0; j < 4; ++j)
+            product(4 * i + j, {two_codes(w0[j], 0), two_codes(w1[j], 0), two_codes(w0[j], 1), two_codes(w1[j], 1)});
         } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            query(2 * i + j, q);
-            mma16816<T::f16>(z[0], q, w0[2 * j], w0[2 * j + 1]);
-            mma16816<T::f16>(z[1], q, w1[2 * j], w1[2 * j + 1]);
-          }
+          for (int j = 0; j < 2; ++j) product(2 * i + j, {w0[2 * j], w1[2 * j], w0[2 * j + 1], w1[2 * j + 1]});
         }
       }
-      float vf[2][2];  // e4m3: the values' scales at positions 8 n + 2t and + 1
+      float vf[2];  // e4m3: the values' scales at positions gi and gi + 8
       bool moved = false;
       if constexpr (T::e4m3) {
+        const float k0 = sc[gi], k1 = sc[gi + 8];
+        vf[0] = sc[kStep + gi], vf[1] = sc[kStep + gi + 8];
+        moved = fmaxf(vf[0], vf[1]) > v_ref;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float2 k2 = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * t);
-          const float2 v2 = *reinterpret_cast<const float2*>(sc + kStep + 8 * n + 2 * t);
-          z[n][0] *= q_scale[0], z[n][1] *= q_scale[0], z[n][2] *= q_scale[1], z[n][3] *= q_scale[1];
-          z[n][0] *= k2.x, z[n][1] *= k2.y, z[n][2] *= k2.x, z[n][3] *= k2.y;
-          vf[n][0] = v2.x, vf[n][1] = v2.y;
-          moved |= fmaxf(v2.x, v2.y) > v_ref;
+        for (int n = 0; n < NB; ++n) {
+          z[n][0] *= q_scale[n][0], z[n][1] *= q_scale[n][1], z[n][2] *= q_scale[n][0], z[n][3] *= q_scale[n][1];
+          z[n][0] *= k0, z[n][1] *= k0, z[n][2] *= k1, z[n][3] *= k1;
         }
       }
       const int first = (ta + step) * kBn + warp * kStep;
@@ -380,75 +388,78 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
       uint32_t seen = 0;  // bit 4 n + c: value c of block n is seen
       if (edge) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int k = 8 * n + 2 * t + (c & 1), pos = first + k;
-            const bool see = (mask >> k & 1) && pos >= lo[c >> 1] && pos < hi[c >> 1];
+            const int k = gi + 8 * (c >> 1), pos = first + k;
+            const bool see = (mask >> k & 1) && pos >= lo[n][c & 1] && pos < hi[n][c & 1];
             if (see) seen |= 1u << (4 * n + c);
             else z[n][c] = -INFINITY;
           }
       }
       // the running maximum
-      float top[2];
+      float top[NB][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(fmaxf(z[0][2 * i], z[0][2 * i + 1]), fmaxf(z[1][2 * i], z[1][2 * i + 1])) * a.scale_log2;
-        moved |= top[i] > m[i];
-      }
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[n][c] = fmaxf(z[n][c], z[n][2 + c]) * a.scale_log2;
+          moved |= top[n][c] > m[n][c];
+        }
       if (__any_sync(0xFFFFFFFFu, moved)) {
-        float shrink[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x = top[i];
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-          shrink[i] = 1.0f;
-          if (x > m[i]) {
-            shrink[i] = exp2_approx(m[i] - x);  // 0 for the first
-            m[i] = x;
-          }
-          l[i] *= shrink[i];
-        }
+        float f = 1.0f;
         if constexpr (T::e4m3) {
-          float v = fmaxf(fmaxf(vf[0][0], vf[0][1]), fmaxf(vf[1][0], vf[1][1]));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+          float v = fmaxf(vf[0], vf[1]);
+#pragma unroll
+          for (int i = 4; i < 32; i *= 2) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, i));
           if (v > v_ref) {
-            const float f = v_ref / v;
+            f = v_ref / v;
             v_ref = v, v_inv = 1.0f / v;
-            shrink[0] *= f, shrink[1] *= f;
           }
         }
 #pragma unroll
-        for (int j = 0; j < NB; ++j) o[j][0] *= shrink[0], o[j][1] *= shrink[0], o[j][2] *= shrink[1], o[j][3] *= shrink[1];
-      }
-      const float ref[2] = {(m[0] == -INFINITY ? 0.0f : m[0]) - exp_lift<T::f16>(),
-                            (m[1] == -INFINITY ? 0.0f : m[1]) - exp_lift<T::f16>()};
-      uint32_t pa[4];
+        for (int n = 0; n < NB; ++n) {
+          float shrink[2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+          for (int c = 0; c < 2; ++c) {
+            float x = top[n][c];
+#pragma unroll
+            for (int i = 4; i < 32; i *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, i));
+            shrink[c] = 1.0f;
+            if (x > m[n][c]) {
+              shrink[c] = exp2_approx(m[n][c] - x);  // 0 for the first
+              m[n][c] = x;
+            }
+            l[n][c] *= shrink[c];
+            shrink[c] *= f;
+          }
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+            o[j][n][0] *= shrink[0], o[j][n][1] *= shrink[1], o[j][n][2] *= shrink[0], o[j][n][3] *= shrink[1];
+        }
+      }
+      if constexpr (T::e4m3) vf[0] *= v_inv, vf[1] *= v_inv;
+      uint32_t pb[NB][2];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          z[n][c] = exp2_approx(fmaf(z[n][c], a.scale_log2, -ref[c >> 1]));
-          l[c >> 1] += z[n][c];
+          const float ref = (m[n][c & 1] == -INFINITY ? 0.0f : m[n][c & 1]) - exp_lift<T::f16>();
+          z[n][c] = exp2_approx(fmaf(z[n][c], a.scale_log2, -ref));
+          l[n][c & 1] += z[n][c];
+          if constexpr (T::e4m3) z[n][c] *= vf[c >> 1];
         }
-        if constexpr (T::e4m3) {
-          vf[n][0] *= v_inv, vf[n][1] *= v_inv;
-          z[n][0] *= vf[n][0], z[n][1] *= vf[n][1], z[n][2] *= vf[n][0], z[n][3] *= vf[n][1];
-        }
-        pa[2 * n] = pack2(z[n][0], z[n][1], half_type);
-        pa[2 * n + 1] = pack2(z[n][2], z[n][3], half_type);
+        // position by position for the next product's operand
+        pb[n][0] = transposed(pack2(z[n][0], z[n][1], half_type));
+        pb[n][1] = transposed(pack2(z[n][2], z[n][3], half_type));
       }
 
       bool odd = false;
       if (edge) {  // a value that some row must not see may be anything
-        if constexpr (T::e4m3)
-          odd = !(fmaxf(fmaxf(vf[0][0], vf[0][1]), fmaxf(vf[1][0], vf[1][1])) < INFINITY) || vf[0][0] != vf[0][0] ||
-                vf[0][1] != vf[0][1] || vf[1][0] != vf[1][0] || vf[1][1] != vf[1][1];
+        if constexpr (T::e4m3) odd = !(vf[0] < INFINITY) || !(vf[1] < INFINITY);
 #pragma unroll
         for (int h = 0; h < S::vgroups; ++h) {
-          Values<DP, K> v;
+          Values<DP, K, R> v;
           v.load(vs, t, gi, h);
 #pragma unroll
           for (int j = 0; j < EV; ++j) {
@@ -462,55 +473,57 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
       if (!odd) {
 #pragma unroll
         for (int h = 0; h < S::vgroups; ++h) {
-          Values<DP, K> v;
+          Values<DP, K, R> v;
           v.load(vs, t, gi, h);
 #pragma unroll
-          for (int j = 0; j < EV; ++j) {
-            uint32_t b0, b1;
-            v.pair(j, b0, b1);
-            mma16816<T::f16>(o[h * EV + j], pa, b0, b1);
+          for (int j = 0; j < EV; j += 2) {
+            uint32_t va[4];
+            v.pair(j, va[0], va[2]);
+            v.pair(j + 1, va[1], va[3]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma16816<T::f16>(o[(h * EV + j) / 2][n], va, pb[n][0], pb[n][1]);
           }
         }
       } else {
         // One position at a time, into the rows that see it: its values are in the
-        // lanes of its pair, column n of theirs in group n's lane.
+        // lanes of its pair, its exponentials in the lanes of its place in z.
 #pragma unroll 1
         for (int k = 0; k < kStep; ++k) {
-          const int from = (gi << 2) | ((k & 7) >> 1);
-          const uint32_t who = __shfl_sync(0xFFFFFFFFu, seen, from) >> (4 * (k >> 3) + (k & 1));
-          float p[2];
+          const int from = ((k & 7) << 2) | t;
+          const uint32_t who = __shfl_sync(0xFFFFFFFFu, seen, from) >> (2 * (k >> 3));
+          float p[NB][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float lo8 = __shfl_sync(0xFFFFFFFFu, k & 1 ? z[0][2 * i + 1] : z[0][2 * i], from);
-            const float hi8 = __shfl_sync(0xFFFFFFFFu, k & 1 ? z[1][2 * i + 1] : z[1][2 * i], from);
-            p[i] = k < 8 ? lo8 : hi8;
-          }
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) p[n][c] = __shfl_sync(0xFFFFFFFFu, k < 8 ? z[n][c] : z[n][2 + c], from);
 #pragma unroll
           for (int h = 0; h < S::vgroups; ++h) {
-            Values<DP, K> v;
+            Values<DP, K, R> v;
             v.load(vs, t, gi, h);
 #pragma unroll
             for (int j = 0; j < EV; ++j) {
               uint32_t b0, b1;
               v.pair(j, b0, b1);
               const uint32_t b = k < 8 ? b0 : b1, bits = k & 1 ? b >> 16 : b & 0xFFFFu;
+              const float val = half_bits_to_f32(__shfl_sync(0xFFFFFFFFu, bits, (gi << 2) | ((k & 7) >> 1)), half_type);
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const float val = half_bits_to_f32(__shfl_sync(0xFFFFFFFFu, bits, ((2 * t + c) << 2) | ((k & 7) >> 1)), half_type);
-                if (who & 1) o[h * EV + j][c] += p[0] * val;
-                if (who & 4) o[h * EV + j][2 + c] += p[1] * val;
-              }
+              for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  if (who >> (4 * n + c) & 1) o[(h * EV + j) / 2][n][(j & 1) * 2 + c] += p[n][c] * val;
             }
           }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-      if (t == 0) join_ml[warp][gi + 8 * i][0] = m[i], join_ml[warp][gi + 8 * i][1] = l[i];
-    }
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int i = 4; i < 32; i *= 2) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], i);
+        if (gi == 0) join_ml[warp][8 * n + 2 * t + c][0] = m[n][c], join_ml[warp][8 * n + 2 * t + c][1] = l[n][c];
+      }
 
     // The four warps' parts, a few rows at a time, while the next piece's query is
     // on its way.
@@ -524,22 +537,21 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
     const float unit = T::e4m3 ? v_ref : 1.0f;
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += kJoinRows) {
-      // a lane has, of rows gi and gi + 8, the elements EV (n + 8 h) + j for n = 2t, 2t + 1
-      if (((gi ^ r0) & 4) == 0) {
-        const bool upper = r0 >= 8;
-        float* row = join_o + (warp * kJoinRows + (gi & 3)) * DP;
+      // a lane has, of rows 8 n + 2t and + 1, the elements EV (gi + 8 h) + j
+      if (((2 * t ^ r0) & 4) == 0) {
 #pragma unroll
-        for (int h = 0; h < S::vgroups; ++h)
+        for (int c = 0; c < 2; ++c) {
+          float* row = join_o + (warp * kJoinRows + ((2 * t + c) & 3)) * DP;
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int h = 0; h < S::vgroups; ++h)
 #pragma unroll
             for (int j = 0; j < EV; j += 4) {
-              const int b = h * EV + j;
-              float4 v = make_float4(o[b][c], o[b + 1][c], o[b + 2][c], o[b + 3][c]);
-              if (upper) v = make_float4(o[b][2 + c], o[b + 1][2 + c], o[b + 2][2 + c], o[b + 3][2 + c]);
-              *reinterpret_cast<float4*>(row + EV * (2 * t + c + 8 * h) + j) =
-                  make_float4(v.x * unit, v.y * unit, v.z * unit, v.w * unit);
+              const int b = (h * EV + j) / 2;
+              float4 v = make_float4(o[b][0][c], o[b][0][2 + c], o[b + 1][0][c], o[b + 1][0][2 + c]);
+              if (NB > 1 && r0 >= 8) v = make_float4(o[b][NB - 1][c], o[b][NB - 1][2 + c], o[b + 1][NB - 1][c], o[b + 1][NB - 1][2 + c]);
+              *reinterpret_cast<float4*>(row + EV * (gi + 8 * h) + j) = make_float4(v.x * unit, v.y * unit, v.z * unit, v.w * unit);
             }
+        }
       }
       __syncthreads();
       if (r0 + kJoinRows >= rows && more) finish_q();  // all warps are past the old one
@@ -570,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K>::ctas) attention_rows_k
             a.lse[row * a.kv_heads * a.group + head] =
                 sum == 0.0f ? -INFINITY : (top + (log2f(sum) - exp_lift<T::f16>())) * kLn2;
         } else {
-          *reinterpret_cast<float4*>(a.part_o + (part * kRows + r) * a.head_dim + d) = acc;
-          if (d == 0) a.part_ml[(part * kRows + r) * 2] = top, a.part_ml[(part * kRows + r) * 2 + 1] = sum;
+          *reinterpret_cast<float4*>(a.part_o + (part * R + r) * a.head_dim + d) = acc;
+          if (d == 0) a.part_ml[(part * R + r) * 2] = top, a.part_ml[(part * R + r) * 2 + 1] = sum;
         }
       }
       __syncthreads();  // the buffers are free again, the next query is there
@@ -677,23 +689,32 @@ Parts parts_of(int grid, int tile_rows, int head_dim) {
   return p;
 }
 
-template <int DP, int K>
-cudaError_t launch_rows(const AttnArgs& a, int num_sms, cudaStream_t st) {
-  using S = Shape<DP, K>;
-  auto kernel = attention_rows_kernel<DP, K>;
+template <int DP, int K, int R>
+cudaError_t launch_rows(const AttnArgs& a, int num_sms, int* grid, cudaStream_t st) {
+  using S = Shape<DP, K, R>;
+  static_assert(S::ctas <= kMaxCtas, "workspace");
+  auto kernel = attention_rows_kernel<DP, K, R>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
   if (e) return e;
-  kernel<<<num_sms * S::ctas, kThreads, S::smem, st>>>(a);
+  *grid = num_sms * S::ctas;
+  kernel<<<*grid, kThreads, S::smem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <int DP>
-cudaError_t launch_rows(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st) {
+template <int DP, int R>
+cudaError_t launch_rows(const AttnArgs& a, Kind k, int num_sms, int* grid, cudaStream_t st) {
   switch (k) {
-    case kBf16: return launch_rows<DP, kBf16>(a, num_sms, st);
-    case kF16: return launch_rows<DP, kF16>(a, num_sms, st);
-    default: return launch_rows<DP, kE4m3F16>(a, num_sms, st);  // for both types of q
+    case kBf16: return launch_rows<DP, kBf16, R>(a, num_sms, grid, st);
+    case kF16: return launch_rows<DP, kF16, R>(a, num_sms, grid, st);
+    default: return launch_rows<DP, kE4m3F16, R>(a, num_sms, grid, st);  // for both types of q
   }
+}
+
+template <int R>
+cudaError_t launch_rows(const AttnArgs& a, Kind k, int num_sms, int* grid, cudaStream_t st) {
+  return a.head_dim <= 64    ? launch_rows<64, R>(a, k, num_sms, grid, st)
+         : a.head_dim <= 128 ? launch_rows<128, R>(a, k, num_sms, grid, st)
+                             : launch_rows<256, R>(a, k, num_sms, grid, st);
 }
 
 bool heads_ok(int32_t q_heads, int32_t kv_heads) {
@@ -797,17 +818,17 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   const bool f16 = g.q_type == MOE_F16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  const bool many = static_cast<int64_t>(seqs->max_rows) * group > kFewRows;
-  const int per_sm = c.head_dim > 128 ? 1 : c.head_dim > 64 ? 2 : 3;  // as Shape has them
-  const int grid = many ? sms : sms * per_sm, tile_rows = many ? tiles_rows(c.head_dim) : kRows;
-  const Parts p = parts_of(grid, tile_rows, c.head_dim);
+  const int64_t most = static_cast<int64_t>(seqs->max_rows) * group;
+  const bool many = most > kFewRows;
+  const int tile_rows = many ? tiles_rows(c.head_dim) : most > 8 ? 16 : 8;
+  const Parts p = parts_of(many ? sms : sms * kMaxCtas, tile_rows, c.head_dim);
   a.ctl = reinterpret_cast<unsigned*>(base);
   a.notes = reinterpret_cast<Note*>(base + p.notes);
   a.part_ml = reinterpret_cast<float*>(base + p.ml), a.part_o = reinterpret_cast<float*>(base + p.o);
-  e = many                 ? launch_tiles(a, kind, sms, st)
-      : c.head_dim <= 64   ? launch_rows<64>(a, kind, sms, st)
-      : c.head_dim <= 128  ? launch_rows<128>(a, kind, sms, st)
-                           : launch_rows<256>(a, kind, sms, st);
+  int grid = sms;
+  e = many              ? launch_tiles(a, kind, sms, st)
+      : tile_rows == 16 ? launch_rows<16>(a, kind, sms, &grid, st)
+                        : launch_rows<8>(a, kind, sms, &grid, st);
   if (!e)
     e = launch_join(a, grid, tile_rows, f16, many ? tiles_lift(f16) : kind == kBf16 ? exp_lift<false>() : exp_lift<true>(), st);
   if (e) return reportf(MOE_ERR_CUDA, "moe_attention: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));

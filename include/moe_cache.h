@@ -106,13 +106,19 @@ int moe_cache_read(const moe_kv_cache *cache, const moe_sequences *seqs, void *k
  *           them; rows times query heads a key head is at most 2^30.
  *   scale:  > 0 and finite.   causal: 0 or 1.   window: >= 0, 0 for none.
  *
- * Products run on the tensor cores with fp32 sums; z, its running maximum, the
- * sums of exponentials and out are kept in fp32.  The exponentials are rounded
- * to q_type for the second product (at most half a step each, so that a
- * result moves by less than half a step of q_type of the mean |v|), and out
- * once, when it is stored.  A cache's e4m3 values are read in q_type: exactly
- * for MOE_BF16 (but below 2^-126); as float16 for MOE_F16, exactly if the head's largest
- * magnitude lies in [2^-7, 57344], and infinite from 65520 on. */
+ * Products run on the tensor cores with fp32 sums; z, the sums of exponentials
+ * and out are kept in fp32.  The exponentials are rounded to q_type (float16 for few
+ * rows of an e4m3 cache) for the second product, at most half a step each, so that
+ * a result moves by less than half a step of the mean |v|; out is rounded once, when
+ * it is stored.  The order of sums goes by the sequences and the GPU's number of
+ * SMs alone.  Few rows (max_rows times query heads a key head up to 16, of
+ * an e4m3 cache 32) take e4m3 values as they are; more of them read them in q_type:
+ * exactly for MOE_BF16 (but below 2^-126), as float16 for MOE_F16, which is exact if the head's
+ * largest magnitude lies in [2^-7, 57344], and infinite from 65520 on.
+ *
+ * Keys and values in pages of a multiple of 16 slots are read fastest; pages of
+ * an odd number of slots, or of 2 or 4 times one, take about twice as long where
+ * many rows attend. */
 typedef struct moe_attention_args {
     const void *q;
     void *out;

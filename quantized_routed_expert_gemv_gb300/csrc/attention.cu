@@ -6,18 +6,21 @@
 // two: scale * log2(e) q . k); when m grows, l and o shrink by 2^(old - new).
 // Parts of the positions, of one warp, one CTA or several, join the same way.
 //
-// Layout: a unit's tile has 16 rows (attention.cuh).  A CTA of four warps takes 64
+// Layout: a unit's tile has 8 or 16 rows (attention.cuh).  A CTA of four warps takes 64
 // positions at a time, each warp 16 of its own, with its own m, l and o, so
 // that warps never wait for one another until the unit ends.  Each warp copies its
 // positions' keys and values to a ring of stages in shared memory (cp.async, 16
-// bytes a lane), several steps ahead.  Products are m16n8k16 tensor-core
-// instructions with the 16 rows as M: the sum over a head's elements may run in any
-// order, so each lane reads keys in whole 16-byte pieces and takes the query's
-// elements in the same order; the outputs' order is free likewise, so values are
-// read in 16-byte pieces of four positions and paired in registers.  e4m3 codes
-// become float16 values between shared memory and the product, a conversion for two;
-// the keys' scales are multiplied on z, the values' on the exponentials, in units of the
-// largest so far, which o follows as it follows m.
+// bytes a lane), several steps and units ahead.  Products are m16n8k16 tensor-core
+// instructions with positions, then a head's elements, as M and rows as N, so that no
+// half of them is empty for 8 rows (heads of few rows leave tcgen05's 128 idle, and the
+// cache's bytes bound them).  The sum over a head's elements may run in any order, so
+// each lane reads keys in whole 16-byte pieces and takes the query's elements in
+// the same order; the outputs' order is free likewise, so values are read in 16-byte
+// pieces of four positions and paired in registers.  Exponentials are turned over
+// (movmatrix) between the products.  e4m3 codes become float16 values between shared
+// memory and the product, a conversion for two; the keys' scales are multiplied on
+// z, the values' on the exponentials, in units of the largest so far, which o
+// follows as it follows m.
 //
 // Bound: reading the cache.
 #include <cuda_runtime.h>
@@ -297,8 +300,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
       if (T::e4m3) spread(n, back);
     }
   };
-  load_q();
-  finish_q();
+  if (w.more()) {  // for all warps alike: a CTA's places may be a unit's beginning alone
+    load_q();
+    finish_q();
+  }
   if (S::q_shared) __syncthreads();
 
   int stage = 0;
@@ -669,9 +674,17 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 
 // ---- host --------------------------------------------------------------------------
 
-// Rows of a sequence times query heads of a key head up to which tiles of 16
-// rows are taken.
-constexpr int kFewRows = 48;
+// Rows of a sequence times query heads of a key head up to which tiles of 8 or 16
+// rows are taken; more of them read the cache several times over, the tiles of 256 of
+// attention_tc.cu once.  16 sequences of 8192 positions, 8 key heads of 128, in a graph:
+//   rows            8      16     24     32     48
+//   bf16, 8         92.8   177    259    341    451 us
+//   bf16, 16        93.2   95.7   178    180    263
+//   bf16, 256       106    106    107    108    109
+//   e4m3, 8         64.2   116    166    213    308
+//   e4m3, 16        78.6   83.6   145    148    214
+//   e4m3, 256       189    190    191    191    193
+constexpr int few_rows(int type) { return type == MOE_E4M3 ? 32 : 16; }
 
 // CTAs of the widest grid that a workspace serves, on an SM.
 constexpr int kMaxCtas = 3;
@@ -819,7 +832,7 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const int64_t most = static_cast<int64_t>(seqs->max_rows) * group;
-  const bool many = most > kFewRows;
+  const bool many = most > few_rows(c.type);
   const int tile_rows = many ? tiles_rows(c.head_dim) : most > 8 ? 16 : 8;
   const Parts p = parts_of(many ? sms : sms * kMaxCtas, tile_rows, c.head_dim);
   a.ctl = reinterpret_cast<unsigned*>(base);

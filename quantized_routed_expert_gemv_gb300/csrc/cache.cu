@@ -6,8 +6,8 @@
 // nearest even: the division is exact, so is code * s.
 //
 // Bound: memory; each value is read once and written once.  A unit is one head
-// of one row's keys and values, worked on by the fewest threads (a power of two)
-// that hold 16 of each, so an e4m3 unit is stored in whole 16-byte pieces and
+// of one row's keys or values, worked on by the fewest threads (a power of two)
+// that hold 16 of them, so an e4m3 unit is stored in whole 16-byte pieces and
 // its largest magnitude is a few shuffles away.  Which sequence a row belongs to
 // is found by the warp: 32 starts are compared at a time.
 #include <cuda_runtime.h>
@@ -196,50 +196,44 @@ struct Sixteen {
   }
 };
 
-// A thread has 16 keys and the 16 values beside them: they share the way to
-// their slot, which takes three reads one after the other, and are read meanwhile
-// (8192 rows of 8 heads of 128, bf16 to e4m3: 16.4 -> 10.2 us).
+// blockIdx.y: 0 keys, 1 values.  What is written is read while the way to its
+// slot is found, which takes three reads one after the other.
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const MoveArgs a) {
+  const bool values = blockIdx.y != 0;
   const uint32_t unit = (blockIdx.x * kThreads + threadIdx.x) >> a.tpu_log2;
   const int row = static_cast<int>(divide(unit, a.heads)), head = static_cast<int>(unit - row * a.heads.d);
   const int d = static_cast<int>(threadIdx.x & ((1u << a.tpu_log2) - 1)) * 16;
-  Sixteen v[2];
+  Sixteen s;
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[kv].x[i] = 0.0f;
-    if (row < a.q.rows && d < a.c.head_dim) v[kv].load(a, kv ? a.v : a.k, row_at(a, row, head, d, kv ? a.ld_v : a.ld_k));
-  }
+  for (int i = 0; i < 16; ++i) s.x[i] = 0.0f;
+  if (row < a.q.rows && d < a.c.head_dim) s.load(a, values ? a.v : a.k, row_at(a, row, head, d, values ? a.ld_v : a.ld_k));
   const Place p = place_of(a);
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const Sixteen& s = v[kv];
-    void* dst = kv ? a.c.v : a.c.k;
-    if (a.c.type != MOE_E4M3) {
-      if (p.held) {
-        const int64_t at = cache_at(a.c, p);
-        s.store_half(dst, a.c.type, at, 0);
-        s.store_half(dst, a.c.type, at + 8, 8);
-      }
-      continue;
+  void* dst = values ? a.c.v : a.c.k;
+  if (a.c.type != MOE_E4M3) {
+    if (p.held) {
+      const int64_t at = cache_at(a.c, p);
+      s.store_half(dst, a.c.type, at, 0);
+      s.store_half(dst, a.c.type, at + 8, 8);
     }
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(s.x[i]) & 0x7FFFFFFFu);
-    for (int o = (1 << a.tpu_log2) >> 1; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (!p.held) continue;
-    float inv;
-    const float scale = block_scale(m, inv);
-    uint4 w = make_uint4(e4m3x4(s.x[0] * inv, s.x[1] * inv, s.x[2] * inv, s.x[3] * inv),
-                         e4m3x4(s.x[4] * inv, s.x[5] * inv, s.x[6] * inv, s.x[7] * inv),
-                         e4m3x4(s.x[8] * inv, s.x[9] * inv, s.x[10] * inv, s.x[11] * inv),
-                         e4m3x4(s.x[12] * inv, s.x[13] * inv, s.x[14] * inv, s.x[15] * inv));
-    if (inv == 0.0f) w = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + cache_at(a.c, p)) = w;
-    if (p.d == 0) (kv ? a.c.v_scale : a.c.k_scale)[scale_at(a.c, p)] = scale;
+    return;
   }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(s.x[i]) & 0x7FFFFFFFu);
+  for (int o = (1 << a.tpu_log2) >> 1; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (!p.held) return;
+  float inv;
+  const float scale = block_scale(m, inv);
+  uint4 w = make_uint4(e4m3x4(s.x[0] * inv, s.x[1] * inv, s.x[2] * inv, s.x[3] * inv),
+                       e4m3x4(s.x[4] * inv, s.x[5] * inv, s.x[6] * inv, s.x[7] * inv),
+                       e4m3x4(s.x[8] * inv, s.x[9] * inv, s.x[10] * inv, s.x[11] * inv),
+                       e4m3x4(s.x[12] * inv, s.x[13] * inv, s.x[14] * inv, s.x[15] * inv));
+  if (inv == 0.0f) w = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + cache_at(a.c, p)) = w;
+  if (p.d == 0) (values ? a.c.v_scale : a.c.k_scale)[scale_at(a.c, p)] = scale;
 }
 
+// A thread has 16 keys and the 16 values beside them, which share the way to their slot.
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const MoveArgs a) {
   const Place p = place_of(a);
   if (!p.in) return;
@@ -315,7 +309,7 @@ int move(const char* name, bool write, const moe_kv_cache* cache, const moe_sequ
   const unsigned grid = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (write)
-    cache_write_kernel<<<grid, kThreads, 0, st>>>(a);
+    cache_write_kernel<<<dim3(grid, 2), kThreads, 0, st>>>(a);
   else
     cache_read_kernel<<<grid, kThreads, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();

@@ -1,6 +1,7 @@
 """Refusals of the paged cache and of attention over it (include/moe_cache.h) and
 of their tensor wrappers: arguments are checked on the host before any launch,
 so these need no GPU."""
+import contextlib
 import ctypes
 
 import pytest
@@ -112,6 +113,39 @@ def test_attention_refuses(L, kw, rc):
     many = seqs_of(rows=1 << 24)
     wide = attn_args(q_heads=256, ld_q=256 * 64, ld_out=256 * 64)
     assert L.moe_attention(ctypes.byref(wide), ctypes.byref(cache_of()), ctypes.byref(many), P, 1 << 30, None) == ARG
+
+
+def test_more_work_than_counts_is_refused(L):
+    c = cache_of(page_size=1 << 20)
+    s = seqs_of(n_seqs=65536, rows=65536, table_width=1024, ld_table=1024)
+    assert L.moe_attention(ctypes.byref(attn_args()), ctypes.byref(c), ctypes.byref(s), P, 1 << 30, None) == UNSUPPORTED
+
+
+def test_calls_on_another_stream(calls, monkeypatch):
+    """What a call on another stream uses is recorded on it, and what it allocates is its own."""
+    used, asked = [], []
+
+    class Other:
+        def __init__(self, raw):
+            self.raw = raw
+
+    monkeypatch.setattr(device, "_other", lambda dev, st: None if st in (None, 0) else Other(st))
+    monkeypatch.setattr(device, "_empty", lambda dev, other, dtype, *shape: asked.append(other) or torch.empty(*shape, dtype=dtype))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, st: used.append(st.raw))
+    monkeypatch.setattr(torch.cuda, "stream", lambda st: contextlib.nullcontext())
+    c, s = a_cache(torch.float8_e4m3fn), some_seqs()
+    att = device.PagedAttention(4, 2, 64, device=_Cpu(), stream=5)
+    assert asked[-1].raw == 5
+    q, k = Z(3, 4, 64, dtype=BF), Z(3, 2, 64, dtype=BF)
+    for call, own in ((lambda st: c.write(k, k, s, stream=st), 7), (lambda st: c.read(s, rows=3, stream=st), 7),
+                      (lambda st: att(q, c, s, stream=st), 8)):
+        del used[:], asked[:]
+        call(9)
+        assert used == [9] * own and all(o.raw == 9 for o in asked)
+        assert calls[-1][1][-1] == 9
+        del used[:], asked[:]
+        call(None)
+        assert used == [] and all(o is None for o in asked)
 
 
 def test_workspaces_refuse(L):

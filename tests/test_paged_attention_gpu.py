@@ -71,6 +71,44 @@ def test_many_sequences(n):
     run(b, queries(b, 4, BF))
 
 
+@pytest.mark.parametrize("n", [500, 513, 1100])
+def test_many_sequences_in_large_tiles(n):
+    """The hint takes the kernel of many rows, which looks at 512 sequences at a time."""
+    g = torch.Generator().manual_seed(n)
+    seqs = [(int(torch.randint(0, 4, (), generator=g)), int(torch.randint(0, 150, (), generator=g))) for _ in range(n)]
+    b = Batch(seqs, 2, 64, 16, max_rows=1000)
+    run(b, queries(b, 4, BF))
+
+
+@pytest.mark.parametrize("max_rows", [1, 1000])
+@pytest.mark.parametrize("q_type,powers", [(BF, (-120, -40, 0, 6, 9, 60)), (F16, (-14, -3, 0, 4, 5))])
+def test_scales_far_from_one(max_rows, q_type, powers):
+    """Heads of an e4m3 cache whose magnitudes differ by powers of two, keys and
+    values alike, and queries that bring z back to about one."""
+    b = Batch([(3, 300), (2, 40)], 1, 64, 16, E4M3, max_rows=max_rows)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    for kp in powers[:2] + powers[-2:]:
+        for s, (_, length) in enumerate(b.seqs):
+            pos = torch.arange(length, device=DEV)
+            pick = torch.tensor(powers, device=DEV, dtype=torch.float64)[torch.randint(0, len(powers), (length, 1, 1), generator=g, device=DEV)]
+            k, v = (torch.randn(length, 1, 64, generator=g, device=DEV).double().clamp(-3, 3) for _ in range(2))
+            b.held[s] = [b.put(s, "k", pos, k * 2.0 ** kp), b.put(s, "v", pos, v * torch.exp2(pick))]
+        q = queries(b, 4, q_type)
+        run(b, q, scale=0.125 * 2.0 ** -kp)
+
+
+@pytest.mark.parametrize("max_rows", [1, 1000])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** 90])
+def test_queries_far_from_one(max_rows, size):
+    """bfloat16 queries beyond float16's range over an e4m3 cache; a row of
+    zeros, and rows whose elements differ by many powers of two."""
+    b = Batch([(3, 200), (1, 77)], 2, 80, 16, E4M3, max_rows=max_rows)
+    q = queries(b, 8, BF, size=size)
+    q[1, 3] = 0.0
+    q[0, 2] *= torch.exp2(-torch.arange(80, device=DEV) // 4.0).to(BF)
+    run(b, q, scale=0.1 / size)
+
+
 @pytest.mark.parametrize("seqs,heads,group", [
     ([(1, 50000)], 1, 8), ([(1, 30000), (1, 10), (1, 7000)], 2, 4), ([(2, 9000)] * 3, 4, 8), ([(40, 6000)], 1, 2)])
 def test_keys_split_over_the_gpu(seqs, heads, group):
@@ -161,6 +199,29 @@ def test_missing_pages_are_seen_by_no_token():
         b.held[s] = [x[keep] for x in b.held[s]]
         b.seqs[s] = (b.seqs[s][0], int(keep.sum()))
     check(b, q, (out, lse), causal=False)
+
+
+@pytest.mark.parametrize("max_rows", [1, 1000])
+@pytest.mark.parametrize("cache_type", [BF, E4M3])
+def test_a_cache_without_pages(max_rows, cache_type):
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    q = torch.ones(5, 4, 64, dtype=BF, device=DEV)
+    att, cache = PagedAttention(4, 2, 64), PagedCache.empty(0, 16, 2, 64, cache_type)
+    none = torch.empty(2, 0, dtype=torch.int32, device=DEV)
+    for table in (i32(0, 1, 2, 3).view(2, 2), none):
+        out, lse = torch.full_like(q, 7.0), torch.full((5, 4), 7.0, device=DEV)
+        att(q, cache, Sequences(i32(0, 2, 5), i32(20, 3), table, max_rows=max_rows), out=out, lse=lse)
+        torch.cuda.synchronize()
+        assert (out == 0).all() and torch.isneginf(lse).all() and att.check() == 0
+
+
+@pytest.mark.parametrize("max_rows", [1, 2, 1000])
+@pytest.mark.parametrize("seqs", [[(1, 1)], [(1, 3)] * 5, [(0, 9), (1, 1), (0, 2), (2, 70), (0, 0)], [(1, 1), (1, 400), (0, 5)]])
+def test_fewer_tiles_than_ctas(max_rows, seqs):
+    """Parts of the work that hold no key tile, at the last sequence's end too;
+    the tables and queries end where the last row does."""
+    b = Batch(seqs, 2, 64, 16, max_rows=max_rows)
+    run(b, queries(b, 4, BF))
 
 
 def test_sequences_that_share_pages():

@@ -112,17 +112,30 @@ __device__ __forceinline__ Place place_of(const MoveArgs& a) {
   p.head = static_cast<int>(unit - p.row * a.heads.d);
   p.d = static_cast<int>(threadIdx.x & (tpu - 1)) * 16;
   const int warp_unit = (blockIdx.x * kThreads + (threadIdx.x & ~31u)) >> a.tpu_log2;
-  const int s0 = find_seq(a.q, static_cast<int>(divide(warp_unit, a.heads)));
+  const int first_row = static_cast<int>(divide(warp_unit, a.heads)), lane = threadIdx.x & 31;
   p.in = p.held = false, p.page = -1, p.slot = 0;
-  if (p.row < a.q.rows) {
-    const int s = next_seq(a.q, s0, p.row);
-    const Seq q = load_seq(a.q, s);
-    if (p.row >= q.first && p.row < q.first + q.n) {
-      p.in = true;
-      const int pos = q.len - q.n + (p.row - q.first);
-      if (pos >= 0) p.page = page_of(a.q, s, pos, p.slot);
-      p.held = p.page >= 0;
+  Seq q = {0, 0, 0};
+  int s = 0;
+  if (a.q.n <= 32 && __all_sync(0xFFFFFFFFu, p.row == first_row)) {
+    // few sequences, one row: a lane has a sequence, so one read instead of three in turn
+    // (8192 rows of 8 heads of 128 17.0 -> 16.4 us, 32614 read back 41 -> 39)
+    const Seq mine = lane < a.q.n ? load_seq(a.q, lane) : Seq{0x7FFFFFFF, 0, 0};
+    const int start = lane < a.q.n ? a.q.starts[lane] : 0x7FFFFFFF;
+    s = max(__popc(__ballot_sync(0xFFFFFFFFu, start <= p.row)) - 1, 0);
+    q.first = __shfl_sync(0xFFFFFFFFu, mine.first, s), q.n = __shfl_sync(0xFFFFFFFFu, mine.n, s);
+    q.len = __shfl_sync(0xFFFFFFFFu, mine.len, s);
+  } else {
+    const int s0 = find_seq(a.q, first_row);
+    if (p.row < a.q.rows) {
+      s = next_seq(a.q, s0, p.row);
+      q = load_seq(a.q, s);
     }
+  }
+  if (p.row < a.q.rows && p.row >= q.first && p.row < q.first + q.n) {
+    p.in = true;
+    const int pos = q.len - q.n + (p.row - q.first);
+    if (pos >= 0) p.page = page_of(a.q, s, pos, p.slot);
+    p.held = p.page >= 0;
   }
   if (p.d >= a.c.head_dim) p.in = p.held = false;
   return p;

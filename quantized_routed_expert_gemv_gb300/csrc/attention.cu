@@ -23,6 +23,8 @@
 // follows as it follows m.
 //
 // Bound: reading the cache.
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
@@ -707,7 +709,8 @@ cudaError_t launch_rows(const AttnArgs& a, int num_sms, int* grid, cudaStream_t 
   using S = Shape<DP, K, R>;
   static_assert(S::ctas <= kMaxCtas, "workspace");
   auto kernel = attention_rows_kernel<DP, K, R>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
+  static std::atomic<uint64_t> allowed{0};  // devices
+  const cudaError_t e = allow_smem(allowed, kernel, S::smem);
   if (e) return e;
   *grid = num_sms * S::ctas;
   kernel<<<*grid, kThreads, S::smem, st>>>(a);
@@ -735,11 +738,20 @@ bool heads_ok(int32_t q_heads, int32_t kv_heads) {
          q_heads / kv_heads <= 128;
 }
 
-int sm_count(int* sms) {
+// The current device's SMs, asked for once a device.
+cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (!e && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return e;
   if (!e) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (!e && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
   return e;
+}
+
+size_t workspace_bytes_for(int sms, int head_dim) {
+  const size_t few = parts_of(sms * kMaxCtas, kRows, head_dim).bytes, many = parts_of(sms, tiles_rows(head_dim), head_dim).bytes;
+  return few > many ? few : many;
 }
 
 }  // namespace
@@ -760,8 +772,7 @@ extern "C" size_t moe_attention_workspace_bytes(int32_t q_heads, int32_t kv_head
   using namespace moe;
   int sms = 0;
   if (!heads_ok(q_heads, kv_heads) || head_dim < 16 || head_dim > 256 || head_dim % 16 || sm_count(&sms)) return 0;
-  const size_t few = parts_of(sms * kMaxCtas, kRows, head_dim).bytes, many = parts_of(sms, tiles_rows(head_dim), head_dim).bytes;
-  return few > many ? few : many;
+  return workspace_bytes_for(sms, head_dim);
 }
 
 extern "C" int moe_attention_workspace_init(void* workspace, size_t workspace_bytes, void* stream) {
@@ -813,9 +824,9 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
       reinterpret_cast<uintptr_t>(workspace) % 256)
     return reportf(MOE_ERR_ALIGN, "moe_attention: q or out is not 16-byte aligned, lse not 4, or workspace not 256");
   int sms = 0;
-  cudaError_t e = static_cast<cudaError_t>(sm_count(&sms));
+  cudaError_t e = sm_count(&sms);
   if (e) return reportf(MOE_ERR_CUDA, "moe_attention: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
-  const size_t need = moe_attention_workspace_bytes(g.q_heads, c.kv_heads, c.head_dim);
+  const size_t need = workspace_bytes_for(sms, c.head_dim);
   if (workspace_bytes < need)
     return reportf(MOE_ERR_ARG, "moe_attention: these heads need %zu bytes of workspace, got %zu", need, workspace_bytes);
 

@@ -19,6 +19,7 @@
 // CTA's block there does an equal share of the unit's outputs.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -390,6 +391,18 @@ struct Walk {
     a.notes[2 * blockIdx.x + (ta == tile.t0 ? 1 : 0)] = n;
   }
 };
+
+// Lets a kernel have `bytes` of dynamic shared memory, once a device (`allowed`: a
+// bit each; a second thread may do it again, with the same value).
+template <class F>
+cudaError_t allow_smem(std::atomic<uint64_t>& allowed, F* kernel, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e || (dev < 64 && allowed.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (!e && dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 cudaError_t launch_tiles(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st);
 int tiles_rows(int head_dim);   // rows of launch_tiles' tiles

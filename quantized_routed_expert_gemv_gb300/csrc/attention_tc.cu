@@ -988,7 +988,8 @@ bool encode(CUtensorMap* map, const void* base, const AttnArgs& a, int rows, boo
 template <int DP, int K>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t st) {
   auto kernel = attention_tiles_kernel<DP, K>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<DP>::smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(allowed, kernel, Geo<DP>::smem);
   if (e) return e;
   Maps maps = {};
   maps.row_boxes = divisor(1);

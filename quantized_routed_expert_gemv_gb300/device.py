@@ -8,6 +8,7 @@ pointers to ``moe_decode`` / ``moe_prefill_chunk``.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import numpy as np
 import torch
@@ -267,12 +268,19 @@ class Fp8Linear:
 def _heads(t: torch.Tensor, rows, heads: int, dim: int, where: str, name: str) -> int:
     """Leading dimension of a [rows][heads][dim] tensor whose heads follow each
     other (rows None: any)."""
-    if t.dim() != 3 or t.shape[1:] != (heads, dim) or rows is not None and t.shape[0] != rows:
-        _refuse(where, f"{name} has the shape {tuple(t.shape)}, not [{'rows' if rows is None else rows}][{heads}][{dim}]")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or shape[1] != heads or rows is not None and shape[0] != rows:
+        _refuse(where, f"{name} has the shape {tuple(shape)}, not [{'rows' if rows is None else rows}][{heads}][{dim}]")
     ld, head, step = t.stride()
-    if step != 1 or heads > 1 and head != dim:
+    if step != 1 or head != dim and heads > 1:
         _refuse(where, f"{name}'s rows must be contiguous")
-    return ld if t.shape[0] > 1 else -(-max(ld, heads * dim) // 8) * 8
+    return ld if shape[0] > 1 else -(-max(ld, heads * dim) // 8) * 8
+
+
+def _current_device() -> int:
+    """torch.cuda.current_device() without its check that CUDA is initialised: a
+    tensor on a GPU shows that, and the check takes a tenth of a call."""
+    return torch._C._cuda_getDevice()
 
 
 class Sequences:
@@ -303,15 +311,15 @@ class Sequences:
                         _ld(page_table, n, width, me) if width else 0, n)
         self._width, self._args = width, {}
 
-    def args(self, rows: int) -> moe.moe_sequences:
-        """The call's argument for tensors of `rows` rows (one object for each
+    def args(self, rows: int):
+        """The call's argument (a reference to a moe_sequences) for tensors of `rows` rows (one object for each
         number of rows, never changed: two threads may hold it)."""
         a = self._args.get(rows)
         if a is None:
             if len(self._args) >= 64:
                 self._args = {}
             most = rows if self.max_rows is None else min(rows, self.max_rows)
-            a = self._args[rows] = moe.moe_sequences(*self._fields, rows, most, self._width)
+            a = self._args[rows] = ctypes.byref(moe.moe_sequences(*self._fields, rows, most, self._width))
         return a
 
 
@@ -350,6 +358,7 @@ class PagedCache:
         self.args = moe.moe_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if quant else None,
                                      v_scale.data_ptr() if quant else None, *strides[:3], *scales,
                                      moe.MOE_E4M3 if quant else _ELEM_TYPE[k.dtype], *k.shape)
+        self._ref = ctypes.byref(self.args)
 
     @staticmethod
     def _strides(t: torch.Tensor) -> tuple:
@@ -364,18 +373,22 @@ class PagedCache:
         return cls(new(*shape, head_dim), new(*shape, head_dim), *scales)
 
     def _move(self, me, fn, seqs, k, v, stream):
-        rows = k.shape[0]
-        ld_k, ld_v = (_heads(t, rows, self.kv_heads, self.head_dim, me, n) for t, n in ((k, "k"), (v, "v")))
-        if k.dtype != v.dtype:
-            _refuse(me, f"k is of type {k.dtype}, v of {v.dtype}")
-        if not k.get_device() == v.get_device() == seqs.index == self.index or self.index != torch.cuda.current_device():
-            _on_gpu(me, self.index, k, v, *seqs.tensors)
-        other = None if stream is None else _other(self.device, stream)
-        if other is not None:
-            for t in self.tensors + seqs.tensors:
-                t.record_stream(other)
-        fn(self.args, seqs.args(rows), k.data_ptr(), ld_k, v.data_ptr(), ld_v, _type(k.dtype, me),
-           _stream(self.device, stream))
+        rows, index = k.shape[0], self.index
+        ld_k = _heads(k, None, self.kv_heads, self.head_dim, me, "k")
+        ld_v = _heads(v, rows, self.kv_heads, self.head_dim, me, "v")
+        dtype = k.dtype
+        if dtype != v.dtype:
+            _refuse(me, f"k is of type {dtype}, v of {v.dtype}")
+        if not k.get_device() == v.get_device() == seqs.index == index or index != _current_device():
+            _on_gpu(me, index, k, v, *seqs.tensors)
+        if stream is None:
+            stream = _stream(self.device, None)
+        else:
+            other = _other(self.device, stream)
+            if other is not None:
+                for t in self.tensors + seqs.tensors:
+                    t.record_stream(other)
+        fn(self._ref, seqs.args(rows), k.data_ptr(), ld_k, v.data_ptr(), ld_v, _type(dtype, me), stream)
 
     def write(self, k: torch.Tensor, v: torch.Tensor, seqs: Sequences, stream=None) -> None:
         """moe_cache_write of k and v [rows][kv_heads][head_dim]."""
@@ -428,7 +441,7 @@ class PagedAttention:
         ld_q = _heads(q, None, self.q_heads, self.head_dim, me, "q")
         rows = q.shape[0]
         index = self.index
-        if not q.get_device() == cache.index == seqs.index == index or index != torch.cuda.current_device():
+        if not q.get_device() == cache.index == seqs.index == index or index != _current_device():
             _on_gpu(me, index, q, *cache.tensors, *seqs.tensors)
         other = None if stream is None else _other(self.device, stream)
         if other is not None:
@@ -449,7 +462,7 @@ class PagedAttention:
             lse_ptr = lse.data_ptr()
         a = moe.moe_attention_args(q.data_ptr(), out.data_ptr(), lse_ptr, ld_q, ld_out, _type(q.dtype, me), self.q_heads,
                                    int(causal), window, self.head_dim ** -0.5 if scale is None else scale)
-        moe.moe_attention(a, cache.args, seqs.args(rows), self.ws_ptr, self.ws_bytes, _stream(self.device, stream))
+        moe.moe_attention(a, cache._ref, seqs.args(rows), self.ws_ptr, self.ws_bytes, _stream(self.device, stream))
         return out
 
     def check(self, stream=None) -> int:

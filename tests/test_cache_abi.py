@@ -165,6 +165,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(device, "_on_gpu", lambda *a: None)
     monkeypatch.setattr(device, "_other", lambda *a: None)
     monkeypatch.setattr(device, "_stream", lambda dev, st: 0 if st is None else st)
+    monkeypatch.setattr(device, "_current_device", lambda: -1)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     for name, value in (("moe_cache_write", None), ("moe_cache_read", None), ("moe_attention", None),
                         ("moe_attention_workspace_bytes", 1024), ("moe_attention_workspace_init", None)):
@@ -227,7 +228,7 @@ def test_moves_refuse_tensors(calls):
     k, v = c.read(s, rows=7)
     assert k.shape == v.shape == (7, 2, 64) and k.dtype == BF
     assert [n for n, _ in calls] == ["moe_cache_write", "moe_cache_read"]
-    assert calls[0][1][1].rows == 3 and calls[1][1][1].rows == 7
+    assert calls[0][1][1]._obj.rows == 3 and calls[1][1][1]._obj.rows == 7
 
 
 def test_attention_refuses_tensors(calls):
@@ -245,7 +246,7 @@ def test_attention_refuses_tensors(calls):
     out = att(q, c, s, lse=Z(3, 4))
     assert out.shape == q.shape and out.dtype == BF
     name, (a, cache, seqs, ws, ws_bytes, st) = calls[0]
-    assert name == "moe_attention" and a.ld_q == a.ld_out == 256 and a.scale == 0.125 and seqs.max_rows == 2 and seqs.rows == 3
+    assert name == "moe_attention" and a.ld_q == a.ld_out == 256 and a.scale == 0.125 and seqs._obj.max_rows == 2 and seqs._obj.rows == 3
 
 
 class _Cpu:

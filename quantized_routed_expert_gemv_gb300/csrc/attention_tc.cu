@@ -27,9 +27,10 @@
 // NaN: rows whose output is not finite are looked at again one by one.
 //
 // Bound: the way from a product to its exponentials and back, which the other half's
-// product hides in part.  4096 rows behind 12288 of 64 heads of 128: 1400 us, 1370
-// TFLOP/s, 70% of the measured bf16 rate; a tile of 128 positions and 256 rows takes 3390
-// clocks, of which its products, by themselves 1055 to 1090 for 16, are 2130.
+// product hides in part.  4096 rows behind 12288 of 64 heads of 128: 1400 to 1456 us
+// by GPU, 1320 to 1370 TFLOP/s, 67 to 70% of the measured bf16 rate; a tile of 128
+// positions and 256 rows takes 3390 clocks, of which its products, by themselves 1055
+// to 1090 for 16, are 2130.
 // Code that runs once a unit or tile waits for its own instructions, so loops are
 // rolled where they can be: of products 1596 -> 1454 us, with exponentials 1454 -> 1400.
 #include <cuda.h>

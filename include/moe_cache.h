@@ -111,8 +111,8 @@ int moe_cache_read(const moe_kv_cache *cache, const moe_sequences *seqs, void *k
  * rows of an e4m3 cache) for the second product, at most half a step each, so that
  * a result moves by less than half a step of the mean |v|; out is rounded once, when
  * it is stored.  The order of sums goes by the sequences and the GPU's number of
- * SMs alone.  Few rows (max_rows times query heads a key head up to 16, of
- * an e4m3 cache 32) take e4m3 values as they are; more of them read them in q_type:
+ * SMs alone.  Few rows (max_rows times query heads a key head up to 16)
+ * take e4m3 values as they are; more of them read them in q_type:
  * exactly for MOE_BF16 (but below 2^-126), as float16 for MOE_F16, which is exact if the head's
  * largest magnitude lies in [2^-7, 57344], and infinite from 65520 on.
  *

@@ -682,11 +682,13 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 //   rows            8      16     24     32     48
 //   bf16, 8         92.8   177    259    341    451 us
 //   bf16, 16        93.2   95.7   178    180    263
-//   bf16, 256       106    106    107    108    109
-//   e4m3, 8         64.2   116    166    213    308
-//   e4m3, 16        78.6   83.6   145    148    214
-//   e4m3, 256       189    190    191    191    193
-constexpr int few_rows(int type) { return type == MOE_E4M3 ? 32 : 16; }
+//   bf16, 256       106    106    107    107    109
+//   e4m3, 8         63.7   116    166    211    306
+//   e4m3, 16        78.3   83.4   145    148    212
+//   e4m3, 256       133    134    135    135    136
+// At 24 and 32 rows of e4m3 caches heads of 64 would gain from tiles of 16 (92 and 95
+// us against 108), heads of 256 lose (208 and 214 against 134 and 136).
+constexpr int kFewRows = 16;
 
 // CTAs of the widest grid that a workspace serves, on an SM.
 constexpr int kMaxCtas = 3;
@@ -843,7 +845,7 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const int64_t most = static_cast<int64_t>(seqs->max_rows) * group;
-  const bool many = most > few_rows(c.type);
+  const bool many = most > kFewRows;
   const int tile_rows = many ? tiles_rows(c.head_dim) : most > 8 ? 16 : 8;
   const Parts p = parts_of(many ? sms : sms * kMaxCtas, tile_rows, c.head_dim);
   a.ctl = reinterpret_cast<unsigned*>(base);

@@ -58,7 +58,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // The bytes s of {a, b} (0..3 of a, 4..7 of b), lowest first.
 __device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 
-// What turns a head's e4m3 codes into 16-bit values of its scale.
+// What turns a head's e4m3 codes into 16-bit values: made by each lane of a warp
+// from a scale of its own, taken from lane to lane by of().  `twice`: some lane's scale
+// needs a second product.
+template <bool B>
+struct Bool {
+  static constexpr bool value = B;
+};
+
 template <bool F16>
 struct Dequant;
 
@@ -69,19 +76,31 @@ template <>
 struct Dequant<false> {
   __nv_bfloat162 m, more;
   bool twice;
-  __device__ __forceinline__ void set(float s0, float s1) {
-    twice = __any_sync(0xFFFFFFFFu, s0 > 128.0f || s1 > 128.0f);
-    const float a0 = twice ? 1.329227995784916e36f : s0 * 1.329227995784916e36f;  // 2^120
-    const float a1 = twice ? 1.329227995784916e36f : s1 * 1.329227995784916e36f;
-    m = __floats2bfloat162_rn(a0, a1);
-    more = __floats2bfloat162_rn(s0, s1);
+  Dequant() = default;
+  __device__ __forceinline__ explicit Dequant(float s) {
+    twice = __any_sync(0xFFFFFFFFu, s > 128.0f);
+    m = __float2bfloat162_rn(twice ? 1.329227995784916e36f : s * 1.329227995784916e36f);  // 2^120
+    more = __float2bfloat162_rn(s);
   }
-  // codes in the high bytes of x's halves
-  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
-    const uint32_t bits = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
-    __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), m);
-    if (twice) v = __hmul2(v, more);
-    return *reinterpret_cast<const uint32_t*>(&v);
+  template <bool TWICE>
+  __device__ __forceinline__ Dequant of(int lane, Bool<TWICE>) const {
+    Dequant d;
+    d.m = __shfl_sync(0xFFFFFFFFu, m, lane);
+    if (TWICE) d.more = __shfl_sync(0xFFFFFFFFu, more, lane);
+    return d;
+  }
+  // four codes to four values
+  template <bool TWICE>
+  __device__ __forceinline__ void operator()(uint32_t x, uint32_t* out, Bool<TWICE>) const {
+    // the values' high bytes (sign, upper bits of the exponent) and low bytes, then both in turn
+    const uint32_t high = ((x >> 4) & 0x07070707u) | (x & 0x80808080u), low = (x << 4) & 0xF0F0F0F0u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t bits = bytes_of(low, high, i ? 0x7362 : 0x5140);
+      __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), m);
+      if (TWICE) v = __hmul2(v, more);
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
   }
 };
 
@@ -92,17 +111,29 @@ template <>
 struct Dequant<true> {
   __half2 m, more;
   bool twice;
-  __device__ __forceinline__ void set(float s0, float s1) {
-    twice = __any_sync(0xFFFFFFFFu, fmaxf(s0, s1) > 32768.0f || fminf(s0, s1) < 6.103515625e-05f);
-    const float c0 = fminf(fmaxf(s0, 6.103515625e-05f), 32768.0f), c1 = fminf(fmaxf(s1, 6.103515625e-05f), 32768.0f);
-    m = __floats2half2_rn(s0 == s0 ? c0 : s0, s1 == s1 ? c1 : s1);
-    more = __floats2half2_rn(fminf(s0 / c0, 32768.0f), fminf(s1 / c1, 32768.0f));
+  Dequant() = default;
+  __device__ __forceinline__ explicit Dequant(float s) {
+    twice = __any_sync(0xFFFFFFFFu, s > 32768.0f || s < 6.103515625e-05f);
+    const float c = fminf(fmaxf(s, 6.103515625e-05f), 32768.0f);
+    m = __float2half2_rn(s == s ? c : s);
+    more = __float2half2_rn(fminf(s / c, 32768.0f));
   }
-  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
-    const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(bytes_of(x, 0, 0x31));
-    __half2 v = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)), m);
-    if (twice) v = __hmul2(v, more);
-    return *reinterpret_cast<const uint32_t*>(&v);
+  template <bool TWICE>
+  __device__ __forceinline__ Dequant of(int lane, Bool<TWICE>) const {
+    Dequant d;
+    d.m = __shfl_sync(0xFFFFFFFFu, m, lane);
+    if (TWICE) d.more = __shfl_sync(0xFFFFFFFFu, more, lane);
+    return d;
+  }
+  template <bool TWICE>
+  __device__ __forceinline__ void operator()(uint32_t x, uint32_t* out, Bool<TWICE>) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(x >> 16 * i);
+      __half2 v = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)), m);
+      if (TWICE) v = __hmul2(v, more);
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
   }
 };
 

@@ -58,7 +58,9 @@ typedef struct moe_kv_cache {
  * other memory: starts are taken as if cut to [0, rows] and kv_lens to
  * [0, table_width * page_size] (and to 2^30), and a page outside [0, n_pages) is one that
  * is missing. A missing page, or a position below 0, is not written, is read
- * as zeros, and is seen by no token. */
+ * as zeros, and is seen by no token.  Where starts, cut so, fall, moe_attention
+ * writes nothing and moe_attention_check reports it; moe_cache_write and
+ * moe_cache_read take a row as one of the sequences that it lies in, or of none. */
 typedef struct moe_sequences {
     const int32_t *starts, *kv_lens, *page_table;
     int64_t ld_table;
@@ -143,8 +145,9 @@ int moe_attention(const moe_attention_args *args, const moe_kv_cache *cache, con
                   size_t workspace_bytes, void *stream);
 
 /* Synchronises `stream` and reads the error word that device code latches in
- * the workspace: MOE_OK or MOE_ERR_TIMEOUT (a bounded wait ran out; outputs of
- * the calls since the last check are undefined).  Clears it after an error. */
+ * the workspace: MOE_OK, MOE_ERR_TIMEOUT (a bounded wait ran out; outputs of
+ * the calls since the last check are undefined) or MOE_ERR_ARG (the starts of a call
+ * fell; it wrote nothing).  Clears it after an error. */
 int moe_attention_check(void *workspace, void *stream);
 
 #ifdef __cplusplus

@@ -873,6 +873,7 @@ extern "C" int moe_attention_check(void* workspace, void* stream) {
     if (!e) e = cudaStreamSynchronize(st);
   }
   if (e) return reportf(MOE_ERR_CUDA, "moe_attention_check: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
-  if (bits) return reportf(MOE_ERR_TIMEOUT, "moe_attention_check: a bounded device-side wait ran out (bits 0x%x)", bits);
+  if (bits & kErrTimeout) return reportf(MOE_ERR_TIMEOUT, "moe_attention_check: a bounded device-side wait ran out (bits 0x%x)", bits);
+  if (bits) return reportf(MOE_ERR_ARG, "moe_attention_check: the starts of a call fell (bits 0x%x)", bits);
   return MOE_OK;
 }

@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include "cache.cuh"
+#include "common.cuh"
 
 namespace moe {
 
@@ -290,6 +291,8 @@ __device__ __forceinline__ void next_unit(const AttnArgs& a, Place& p, Seq& s) {
 }
 
 // All of a CTA's threads (THREADS, a multiple of 128) find its part of the line.
+// Starts that fall would let sequences share rows, so that their tiles have no
+// bound that the host could have checked: no CTA has a part then.
 // It runs once a CTA, from instructions that come from afar, so its time goes by
 // its length: few and narrow operations (with 64-bit ones and divisions for
 // every cut it took 6500 clocks instead of 4000 in front of 128 rows over 32768).
@@ -302,15 +305,16 @@ __device__ __forceinline__ Work find_work(const AttnArgs& a, PlanSmem& sm) {
   int cost, incl;  // tiles of a head of this thread's sequence, and of the chunk's sequences up to it
   Seq mine;
   int ch = 0, before = 0;
-  bool again = false;
+  bool again = false, falls = false;
 #pragma unroll 1
   for (;;) {
     mine = {0, 0, 0};
-    if (ch * THREADS + tid < a.q.n) mine = load_seq(a.q, ch * THREADS + tid);
+    bool fall = false;
+    if (ch * THREADS + tid < a.q.n) mine = load_seq(a.q, ch * THREADS + tid, fall);
     cost = head_cost<R, BN>(a, mine);
     incl = warp_scan(cost * a.kv_heads);
     if (lane == 31) sm.tiles[warp] = incl;
-    __syncthreads();
+    falls |= __syncthreads_or(fall) != 0;
     const int v = lane < THREADS / 32 ? sm.tiles[lane] : 0;
     const int all = __reduce_add_sync(0xFFFFFFFFu, v);
     incl += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? v : 0);
@@ -322,6 +326,10 @@ __device__ __forceinline__ Work find_work(const AttnArgs& a, PlanSmem& sm) {
     // its first and last tile
     const int grid = gridDim.x, ctas = grid < w.total ? grid : w.total, c = blockIdx.x;
     w.begin = w.end = 0;
+    if (falls) {
+      if (c == 0 && tid == 0) latch_error(a.ctl, kErrRange);
+      return w;
+    }
     if (c >= ctas) return w;
     w.each = static_cast<uint32_t>(w.total) / static_cast<uint32_t>(ctas), w.more = w.total - w.each * ctas;
     w.begin = w.cut(c), w.end = w.cut(c + 1);

@@ -45,12 +45,19 @@ struct Seq {
   int first, n, len;
 };
 
-__device__ __forceinline__ Seq load_seq(const Seqs& q, int s) {
+// `falls`: the sequence ends before it starts, which leaves it without rows.
+__device__ __forceinline__ Seq load_seq(const Seqs& q, int s, bool& falls) {
   Seq r;
   r.first = min(max(q.starts[s], 0), q.rows);
-  r.n = min(max(q.starts[s + 1], r.first), q.rows) - r.first;
+  const int end = min(max(q.starts[s + 1], 0), q.rows);
+  falls = end < r.first;
+  r.n = max(end - r.first, 0);
   r.len = min(max(q.kv_lens[s], 0), q.cap);
   return r;
+}
+__device__ __forceinline__ Seq load_seq(const Seqs& q, int s) {
+  bool falls;
+  return load_seq(q, s, falls);
 }
 
 // The page of a position in [0, cap) and the slot in it; -1 for a missing page.

@@ -361,5 +361,5 @@ def moe_attention(args: moe_attention_args, cache: moe_kv_cache, seqs: moe_seque
 
 
 def moe_attention_check(ws: int, stream: int = 0) -> int:
-    """Returns the device-latched status code (MOE_OK or MOE_ERR_TIMEOUT)."""
+    """Returns the device-latched status code (MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_ARG)."""
     return int(lib().moe_attention_check(ws, stream))

@@ -1,0 +1,74 @@
+"""Attention over the paged cache at the edges of its contract: device values
+outside it, magnitudes far from one, layouts and pages in both kernels."""
+import math
+
+import pytest
+import torch
+
+from paged import BF, DEV, E4M3, F16, F32, Batch, attend, check, queries, reference
+from quantized_routed_expert_gemv_gb300 import moe
+from quantized_routed_expert_gemv_gb300.device import PagedAttention, PagedCache, Sequences
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [(BF, BF), (F16, F16), (BF, E4M3), (F16, E4M3)]
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("max_rows", [1, 2, 1000])
+@pytest.mark.parametrize("starts", [(0, 12, 0, 12), (12, 0, 3, 5), (0, 5, 4, 12), (3, 5, 9, -4), (1 << 30, 0, 12, 12)])
+def test_starts_that_fall(max_rows, starts):
+    """Nothing is written, and the check says so, once."""
+    b = Batch([(4, 300), (4, 20), (4, 700)], 2, 64, 16, max_rows=max_rows)
+    q, out, lse = queries(b, 8, BF), torch.full((12, 8, 64), 7.0, dtype=BF, device=DEV), torch.full((12, 8), 7.0, device=DEV)
+    good = b.starts.clone()
+    att, cache, seqs = PagedAttention(8, 2, 64), b.cache(), b.sequences()
+    b.starts.copy_(i32(*starts))
+    att(q, cache, seqs, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    assert att.check() == moe.MOE_ERR_ARG and att.check() == moe.MOE_OK
+    b.starts.copy_(good)
+    att(q, cache, seqs, out=out, lse=lse)
+    torch.cuda.synchronize()
+    check(b, q, (out, lse))
+    assert att.check() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("max_rows", [1, 1000])
+@pytest.mark.parametrize("n", [129, 600, 65536])
+def test_many_starts_that_fall(max_rows, n):
+    """Sequences that would have far more tiles together than 32 bits count; and
+    one fall among many starts, wherever it is."""
+    rows, heads, table = 1024, 8, torch.zeros(n, 256, dtype=torch.int32, device=DEV)
+    cache, att = PagedCache.empty(2, 16, heads, 64, BF), PagedAttention(64, heads, 64)
+    q = torch.zeros(rows, 64, 64, dtype=BF, device=DEV)
+    out = torch.full_like(q, 7.0)
+    lens = torch.full((n,), 4096, dtype=torch.int32, device=DEV)
+    starts = torch.arange(n + 1, dtype=torch.int32, device=DEV) % 2 * rows
+    seqs = Sequences(starts, lens, table, max_rows=max_rows)
+    for fall in (None, 1, n // 2, n):
+        if fall is not None:
+            starts[:fall], starts[fall:] = rows, rows - 1
+        att(q, cache, seqs, out=out)
+        torch.cuda.synchronize()
+        assert (out == 7.0).all() and att.check() == moe.MOE_ERR_ARG
+
+
+def test_moves_with_starts_that_fall():
+    """Rows are taken as some sequence's or none's; nothing else is touched."""
+    b = Batch([(4, 8), (4, 8), (4, 8)], 2, 64, 4, BF)
+    used = sorted(set(b.table.flatten().tolist()))
+    other = [p for p in range(b.n_pages) if p not in used]
+    before = b.k[other].clone().view(torch.int16)
+    b.starts.copy_(i32(0, 12, 2, 9))
+    x = torch.ones(12, 2, 64, dtype=BF, device=DEV)
+    k, v = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    cache = b.cache()
+    cache.write(x, x, b.sequences())
+    cache.read(b.sequences(), k_out=k, v_out=v)
+    torch.cuda.synchronize()
+    assert torch.equal(b.k[other].view(torch.int16), before)

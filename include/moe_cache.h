@@ -107,6 +107,10 @@ int moe_cache_read(const moe_kv_cache *cache, const moe_sequences *seqs, void *k
  *   q_heads: a multiple of kv_heads, at most 4096, and at most 128 for each of
  *           them; rows times query heads a key head is at most 2^30.
  *   scale:  > 0 and finite.   causal: 0 or 1.   window: >= 0, 0 for none.
+ * Calls that might be 2^31 places of work are MOE_ERR_UNSUPPORTED:
+ *     (rows * q_heads / kv_heads / R + n_seqs) * kv_heads * (positions / B + 4)
+ * with R = 256 and B = 128 for heads of up to 128, R = 128 and B = 64 for larger ones, and
+ * positions = table_width * page_size (at most 2^30).
  *
  * Products run on the tensor cores with fp32 sums; z, the sums of exponentials
  * and out are kept in fp32.  The exponentials are rounded to q_type (float16 for few

@@ -740,6 +740,14 @@ bool heads_ok(int32_t q_heads, int32_t kv_heads) {
          q_heads / kv_heads <= 128;
 }
 
+// Whether 32 bits count the places of a line of such tiles, whatever the device values are
+// (attention.cuh): all rows in as many row tiles as sequences can make of them, each as
+// long as the page table.
+bool counts(const moe_sequences& s, int32_t cap, int32_t kv_heads, int group, int tile_rows, int tile_keys) {
+  const int64_t units = (static_cast<int64_t>(s.rows) * group / tile_rows + s.n_seqs) * kv_heads;
+  return units * (cap / tile_keys + 1 + kUnitCost) <= 0x7FFFFFFF;
+}
+
 // The current device's SMs, asked for once a device.
 cudaError_t sm_count(int* sms) {
   static std::atomic<int> known[64];
@@ -812,11 +820,14 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   const int group = g.q_heads / c.kv_heads;
   if (static_cast<int64_t>(seqs->rows) * group > (1 << 30))
     return reportf(MOE_ERR_ARG, "moe_attention: %d rows of %d query heads a key head are more than 2^30", seqs->rows, group);
-  // key tiles of 64 positions, row tiles of 16 rows, at the worst
-  const int64_t row_tiles = (static_cast<int64_t>(seqs->rows) * group / kRows + seqs->n_seqs) * c.kv_heads;
-  if (row_tiles * (a.q.cap / kBn + 1 + kUnitCost) > 0x7FFFFFFF)
-    return reportf(MOE_ERR_UNSUPPORTED, "moe_attention: %d rows in %d sequences of up to %d positions are more than 2^31 tiles of work",
-                   seqs->rows, seqs->n_seqs, a.q.cap);
+  const int64_t most = static_cast<int64_t>(seqs->max_rows) * group;
+  const int few_rows = most > 8 ? 16 : 8;
+  const bool many = most > kFewRows || !counts(*seqs, a.q.cap, c.kv_heads, group, few_rows, kBn);
+  const int tile_rows = many ? tiles_rows(c.head_dim) : few_rows;
+  if (many && !counts(*seqs, a.q.cap, c.kv_heads, group, tile_rows, tiles_keys(c.head_dim)))
+    return reportf(MOE_ERR_UNSUPPORTED,
+                   "moe_attention: %d rows of %d heads in %d sequences of up to %d positions are 2^31 places of work or more", seqs->rows,
+                   g.q_heads, seqs->n_seqs, a.q.cap);
   if (!g.q || !g.out || !workspace) return reportf(MOE_ERR_ARG, "moe_attention: q, out or workspace is NULL");
   const int64_t width = static_cast<int64_t>(g.q_heads) * c.head_dim;
   if (g.ld_q < width || g.ld_out < width || g.ld_q % 8 || g.ld_out % 8)
@@ -844,9 +855,6 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   const bool f16 = g.q_type == MOE_F16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  const int64_t most = static_cast<int64_t>(seqs->max_rows) * group;
-  const bool many = most > kFewRows;
-  const int tile_rows = many ? tiles_rows(c.head_dim) : most > 8 ? 16 : 8;
   const Parts p = parts_of(many ? sms : sms * kMaxCtas, tile_rows, c.head_dim);
   a.ctl = reinterpret_cast<unsigned*>(base);
   a.notes = reinterpret_cast<Note*>(base + p.notes);

@@ -445,6 +445,7 @@ cudaError_t allow_smem(std::atomic<uint64_t>& allowed, F* kernel, int bytes) {
 
 cudaError_t launch_tiles(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st);
 int tiles_rows(int head_dim);   // rows of launch_tiles' tiles
+int tiles_keys(int head_dim);   // their positions
 float tiles_lift(bool f16);     // its exponentials' factor, in powers of two
 cudaError_t launch_join(const AttnArgs& a, int grid, int tile_rows, bool f16, float lift, cudaStream_t st);
 

@@ -1050,6 +1050,7 @@ cudaError_t launch(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st) {
 }  // namespace
 
 int tiles_rows(int head_dim) { return head_dim <= 64 ? Geo<64>::rows : head_dim <= 128 ? Geo<128>::rows : Geo<256>::rows; }
+int tiles_keys(int head_dim) { return head_dim <= 64 ? Geo<64>::bn : head_dim <= 128 ? Geo<128>::bn : Geo<256>::bn; }
 float tiles_lift(bool f16) { return f16 ? tile_lift<true>() : tile_lift<false>(); }
 
 cudaError_t launch_tiles(const AttnArgs& a, Kind k, int num_sms, cudaStream_t st) {

@@ -121,6 +121,29 @@ def test_more_work_than_counts_is_refused(L):
     assert L.moe_attention(ctypes.byref(attn_args()), ctypes.byref(c), ctypes.byref(s), P, 1 << 30, None) == UNSUPPORTED
 
 
+# rows, sequences, table width (of pages of 16), heads, head size, max_rows: a workspace of 0 bytes is
+# refused after the count of the work, so nothing is launched
+@pytest.mark.parametrize("rows,n,width,heads,dim,max_rows,fits", [
+    # one prompt of 262144: 2^31 tiles of 16 rows and 64 positions, 1/32 of that in tiles of 256 and 128
+    (262144, 1, 16384, (64, 8), 128, 262144, True),
+    # the hint of single tokens is wrong: tiles of 8 rows would be too many, larger ones are not
+    (131072, 1, 8192, (64, 8), 128, 1, True), (1 << 20, 1, 8192, (64, 8), 128, 1, True),
+    # both sides of the limit: (2^15 * 4 / 128 + n) * 1 * (2^24 / 64 + 4) <= 2^31 - 1
+    (1 << 15, 7167, 1 << 20, (4, 1), 256, 1000, True), (1 << 15, 7168, 1 << 20, (4, 1), 256, 1000, False),
+    (1 << 15, 7168, 1 << 20, (4, 1), 256, 1, False),
+    # and of the larger tiles: (2^20 * 4 / 256 + n) * 1 * (2^24 / 128 + 4)
+    (1 << 20, 0, 1 << 20, (4, 1), 64, 9, True), (1 << 15, 15871, 1 << 20, (4, 1), 64, 1, True),
+    (1 << 15, 15872, 1 << 20, (4, 1), 64, 1, False)])
+def test_the_work_that_counts(L, rows, n, width, heads, dim, max_rows, fits):
+    if fits and n:
+        assert (rows * heads[0] // heads[1] // (256 if dim <= 128 else 128) + n) * heads[1] * (width * 16 // (128 if dim <= 128 else 64) + 4) < 2 ** 31
+    c = cache_of(kv_heads=heads[1], head_dim=dim, head_stride=16 * dim, slot_stride=dim, page_stride=16 * dim * heads[1])
+    a = attn_args(q_heads=heads[0], ld_q=heads[0] * dim, ld_out=heads[0] * dim)
+    s = seqs_of(n_seqs=n, rows=rows, table_width=width, ld_table=width, max_rows=max_rows)
+    rc = L.moe_attention(ctypes.byref(a), ctypes.byref(c), ctypes.byref(s), P, 0, None)
+    assert (rc != UNSUPPORTED) == fits and (rc != OK or n == 0)
+
+
 def test_calls_on_another_stream(calls, monkeypatch):
     """What a call on another stream uses is recorded on it, and what it allocates is its own."""
     used, asked = [], []

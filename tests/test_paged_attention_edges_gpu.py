@@ -72,3 +72,19 @@ def test_moves_with_starts_that_fall():
     cache.read(b.sequences(), k_out=k, v_out=v)
     torch.cuda.synchronize()
     assert torch.equal(b.k[other].view(torch.int16), before)
+
+
+def test_a_hint_of_single_tokens_for_a_long_prompt():
+    """2^31 places of work in tiles of 8 rows: larger ones are taken.  Keys of zeros
+    weigh all values alike."""
+    n, heads, group, dim = 131072, 8, 8, 16
+    cache, att = PagedCache.empty(n // 256, 256, heads, dim, BF), PagedAttention(heads * group, heads, dim)
+    cache.tensors[0].zero_(), cache.tensors[1].fill_(0.0)
+    cache.tensors[1][:, ::2] = 2.0                               # every second position
+    table = torch.arange(n // 256, dtype=torch.int32, device=DEV).view(1, -1)
+    q = torch.ones(n, heads * group, dim, dtype=BF, device=DEV)
+    out, lse = torch.full_like(q, 7.0), torch.empty(n, heads * group, device=DEV)
+    att(q, cache, Sequences(i32(0, n), i32(n), table, max_rows=1), causal=False, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert att.check() == 0 and (out == 1.0).all()
+    assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -18  # fp32 sums of ones, log2 and a product of 12: 2^-20 each

@@ -70,37 +70,29 @@ struct Bool {
 template <bool F16>
 struct Dequant;
 
-// bf16: a code's exponent and mantissa are bits 4 to 10 of a bf16 that is 2^-120
-// times the value; a scale of up to 2^7 is multiplied on with 2^120, a larger
-// one in a second product.  Both are powers of two: exact.
+// bf16: the hardware's conversion to float16 (a NaN's code becomes a NaN), then the
+// scale in fp32: exact, as a code has 4 significant bits.
 template <>
 struct Dequant<false> {
-  __nv_bfloat162 m, more;
-  bool twice;
+  float s;
+  static constexpr bool twice = false;
   Dequant() = default;
-  __device__ __forceinline__ explicit Dequant(float s) {
-    twice = __any_sync(0xFFFFFFFFu, s > 128.0f);
-    m = __float2bfloat162_rn(twice ? 1.329227995784916e36f : s * 1.329227995784916e36f);  // 2^120
-    more = __float2bfloat162_rn(s);
-  }
+  __device__ __forceinline__ explicit Dequant(float scale) : s(scale) {}
   template <bool TWICE>
   __device__ __forceinline__ Dequant of(int lane, Bool<TWICE>) const {
-    Dequant d;
-    d.m = __shfl_sync(0xFFFFFFFFu, m, lane);
-    if (TWICE) d.more = __shfl_sync(0xFFFFFFFFu, more, lane);
-    return d;
+    return Dequant(__shfl_sync(0xFFFFFFFFu, s, lane));
   }
   // four codes to four values
   template <bool TWICE>
   __device__ __forceinline__ void operator()(uint32_t x, uint32_t* out, Bool<TWICE>) const {
-    // the values' high bytes (sign, upper bits of the exponent) and low bytes, then both in turn
-    const uint32_t high = ((x >> 4) & 0x07070707u) | (x & 0x80808080u), low = (x << 4) & 0xF0F0F0F0u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t bits = bytes_of(low, high, i ? 0x7362 : 0x5140);
-      __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), m);
-      if (TWICE) v = __hmul2(v, more);
-      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+      const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(x >> 16 * i);
+      float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+      asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+          : "+f"(f.x), "+f"(f.y)
+          : "f"(s));
+      out[i] = pack2(f.x, f.y, MOE_BF16);
     }
   }
 };

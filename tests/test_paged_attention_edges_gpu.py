@@ -88,3 +88,44 @@ def test_a_hint_of_single_tokens_for_a_long_prompt():
     torch.cuda.synchronize()
     assert att.check() == 0 and (out == 1.0).all()
     assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -18  # fp32 sums of ones, log2 and a product of 12: 2^-20 each
+
+
+@pytest.mark.parametrize("code", [0x7F, 0xFF])
+@pytest.mark.parametrize("q_type", [BF, F16])
+@pytest.mark.parametrize("dim,max_rows", [(64, 1), (64, 1000), (128, 1), (128, 1000), (256, 1000), (80, 1000)])
+@pytest.mark.parametrize("scale_up", [0, 12])
+def test_codes_that_are_nan_with_finite_scales(code, q_type, dim, max_rows, scale_up):
+    """As a cast that does not saturate leaves them.  A key's makes the rows that see it
+    NaN, a value's one element of them; the cache read back holds the same."""
+    b = Batch([(3, 260)], 2, dim, 16, E4M3, max_rows=max_rows)
+    if scale_up:  # scales beyond 2^7, which take the second product
+        for s in (b.k_scale, b.v_scale):
+            s[torch.isfinite(s)] *= 2.0 ** scale_up
+        b.held = [[x * 2.0 ** scale_up for x in h] for h in b.held]
+    q, scale = queries(b, 4, q_type), dim ** -0.5 * 2.0 ** -scale_up
+    clean, _ = attend(b, q, 2, scale=scale)
+    check(b, q, attend(b, q, 2, scale=scale), scale=scale)
+    element = dim - 3
+    for which in "kv":
+        for place in (0, 70, 131, 258):
+            page, slot = b.table[0, place // 16].item(), place % 16
+            at = getattr(b, which).view(torch.uint8)[page, slot, 1]
+            kept = at[element].item()
+            at[element] = code
+            out, lse = attend(b, q, 2, scale=scale)
+            ko, vo = b.cache().read(Sequences(i32(0, 260), i32(260), b.table), rows=260, out_type=F32)
+            torch.cuda.synchronize()
+            assert torch.isnan((ko if which == "k" else vo)[place, 1, element])
+            sees = torch.arange(257, 260, device=DEV) >= place
+            odd = torch.zeros(3, 4, dim, dtype=torch.bool, device=DEV)
+            if which == "k":
+                odd[sees, 2:] = True
+                assert torch.equal(torch.isnan(lse), odd[..., 0])
+            else:
+                odd[sees, 2:, element] = True
+                assert torch.isfinite(lse).all()
+            assert torch.equal(torch.isnan(out), odd)
+            d = (out.float() - clean.float()).abs()[~odd]
+            # tiles may be taken one position at a time
+            assert (d <= 2.0 ** -6 * (2.0 ** scale_up + clean.float().abs()[~odd])).all()
+            at[element] = kept

@@ -2,8 +2,10 @@
 // that several CTAs share, and the entry points (include/moe_cache.h).
 //
 // Mathematics: a row's softmax over its positions is taken in one pass with a
-// running maximum m, sum l of 2^(z - m) and output o, all fp32 (z in powers of
-// two: scale * log2(e) q . k); when m grows, l and o shrink by 2^(old - new).
+// running maximum m of z = q . k, sum l of 2^(c (z - m)) with c = scale * log2(e),
+// and output o, all fp32; when m grows, l and o shrink by 2^(c (old - new)).  m is subtracted
+// before the scale is multiplied on: exact near the maximum, however large z is (c z
+// rounded before the subtraction is off by 2 from 2^25 on, by 128 from 2^31 on).
 // Parts of the positions, of one warp, one CTA or several, join the same way.
 //
 // Layout: a unit's tile has 8 or 16 rows (attention.cuh).  A CTA of four warps takes 64
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          top[n][c] = fmaxf(z[n][c], z[n][2 + c]) * a.scale_log2;
+          top[n][c] = fmaxf(z[n][c], z[n][2 + c]);
           moved |= top[n][c] > m[n][c];
         }
       if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
             for (int i = 4; i < 32; i *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, i));
             shrink[c] = 1.0f;
             if (x > m[n][c]) {
-              shrink[c] = exp2_approx(m[n][c] - x);  // 0 for the first
+              shrink[c] = exp2_approx((m[n][c] - x) * a.scale_log2);  // 0 for the first
               m[n][c] = x;
             }
             l[n][c] *= shrink[c];
@@ -451,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float ref = (m[n][c & 1] == -INFINITY ? 0.0f : m[n][c & 1]) - exp_lift<T::f16>();
-          z[n][c] = exp2_approx(fmaf(z[n][c], a.scale_log2, -ref));
+          const float ref = m[n][c & 1] == -INFINITY ? 0.0f : m[n][c & 1];
+          z[n][c] = exp2_approx(fmaf(z[n][c] - ref, a.scale_log2, exp_lift<T::f16>()));
           l[n][c & 1] += z[n][c];
           if constexpr (T::e4m3) z[n][c] *= vf[c >> 1];
         }
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) {
-          const float f = exp2_approx(mw[v] - ref);
+          const float f = exp2_approx((mw[v] - ref) * a.scale_log2);
           const float4 x = *reinterpret_cast<const float4*>(join_o + (v * kJoinRows + rr) * DP + d);
           sum += f * join_ml[v][r][1];
           acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d) = u;
           if (d == 0 && a.lse)
             a.lse[row * a.kv_heads * a.group + head] =
-                sum == 0.0f ? -INFINITY : (top + (log2f(sum) - exp_lift<T::f16>())) * kLn2;
+                sum == 0.0f ? -INFINITY : fmaf(top, a.scale, (log2f(sum) - exp_lift<T::f16>()) * kLn2);
         } else {
           *reinterpret_cast<float4*>(a.part_o + (part * R + r) * a.head_dim + d) = acc;
           if (d == 0) a.part_ml[(part * R + r) * 2] = top, a.part_ml[(part * R + r) * 2 + 1] = sum;
@@ -607,9 +609,9 @@ constexpr int kJoinThreads = 256;
 struct Part {
   float m, l;
   float4 o;
-  __device__ __forceinline__ void add(float m2, float l2, float4 o2) {
+  __device__ __forceinline__ void add(float m2, float l2, float4 o2, float scale_log2) {
     const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
-    const float f = exp2_approx(m - ref), f2 = exp2_approx(m2 - ref);
+    const float f = exp2_approx((m - ref) * scale_log2), f2 = exp2_approx((m2 - ref) * scale_log2);
     m = top, l = l * f + l2 * f2;
     o = make_float4(o.x * f + o2.x * f2, o.y * f + o2.y * f2, o.z * f + o2.z * f2, o.w * f + o2.w * f2);
   }
@@ -651,13 +653,13 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
           }
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) p.add(ml[b].x, ml[b].y, o[b]);
+        for (int b = 0; b < kBatch; ++b) p.add(ml[b].x, ml[b].y, o[b], a.scale_log2);
       }
       for (int s = per_warp; s < 32; s <<= 1) {
         const float m2 = __shfl_xor_sync(0xFFFFFFFFu, p.m, s), l2 = __shfl_xor_sync(0xFFFFFFFFu, p.l, s);
         const float4 o2 = make_float4(__shfl_xor_sync(0xFFFFFFFFu, p.o.x, s), __shfl_xor_sync(0xFFFFFFFFu, p.o.y, s),
                                       __shfl_xor_sync(0xFFFFFFFFu, p.o.z, s), __shfl_xor_sync(0xFFFFFFFFu, p.o.w, s));
-        p.add(m2, l2, o2);
+        p.add(m2, l2, o2, a.scale_log2);
       }
       if (on && first == 0) {
         const int token = static_cast<int>(divide(n.row + r, a.by_group)), g = n.row + r - token * a.group;
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         u.x = pack2(p.o.x * inv, p.o.y * inv, type), u.y = pack2(p.o.z * inv, p.o.w * inv, type);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d) = u;
         if (d == 0 && a.lse)
-          a.lse[row * a.kv_heads * a.group + head] = p.l == 0.0f ? -INFINITY : (p.m + (log2f(p.l) - lift)) * kLn2;
+          a.lse[row * a.kv_heads * a.group + head] = p.l == 0.0f ? -INFINITY : fmaf(p.m, a.scale, (log2f(p.l) - lift) * kLn2);
       }
     }
   }
@@ -849,7 +851,7 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
   a.page_stride = c.page_stride * size, a.slot_stride = c.slot_stride * size, a.head_stride = c.head_stride * size;
   a.scale_page_stride = c.scale_page_stride, a.scale_slot_stride = c.scale_slot_stride, a.scale_head_stride = c.scale_head_stride;
   a.head_dim = c.head_dim, a.kv_heads = c.kv_heads, a.group = group, a.causal = g.causal, a.window = g.window, a.type = g.q_type;
-  a.scale_log2 = g.scale * 1.4426950408889634f;
+  a.scale = g.scale, a.scale_log2 = g.scale * 1.4426950408889634f;
   a.by_group = divisor(static_cast<uint32_t>(group));
   const Kind kind = c.type == MOE_BF16 ? kBf16 : c.type == MOE_F16 ? kF16 : g.q_type == MOE_BF16 ? kE4m3Bf16 : kE4m3F16;
   const bool f16 = g.q_type == MOE_F16;

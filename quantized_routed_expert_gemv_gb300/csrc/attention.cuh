@@ -149,11 +149,11 @@ struct AttnArgs {
   int64_t scale_page_stride, scale_slot_stride, scale_head_stride;  // floats
   int head_dim, kv_heads, group, causal, window;
   int type;           // of the query and the output
-  float scale_log2;  // scale * log2(e)
+  float scale, scale_log2;  // scale, and scale * log2(e)
   Divisor by_group;
   unsigned* ctl;    // [0] error bits
   struct Note* notes;  // [G][2]
-  float* part_ml;   // [G][2][tile_rows][2]
+  float* part_ml;   // [G][2][tile_rows][2]: maximum of q . k, sum
   float* part_o;    // [G][2][tile_rows][head_dim]
 };
 

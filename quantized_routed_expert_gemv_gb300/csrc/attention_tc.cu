@@ -50,6 +50,11 @@ constexpr int kHalf = 128;         // rows of a half
 // row's reference is moved: what the largest float16 leaves room for (65504).
 constexpr float kMost = 49152.0f;
 
+// From where on the reference is subtracted from z before the scale is multiplied on, which is
+// exact near it.  Below, its rounding (2^-17) shifts a row's exponentials by 2^-17 together; far
+// above, it would pass float16's range.  For every tile: prompts 2 to 3% slower.
+constexpr float kLarge = 256.0f;
+
 template <bool F16>
 __host__ __device__ constexpr float tile_lift() {
   return F16 ? 7.0f : 0.0f;
@@ -234,7 +239,7 @@ __device__ __forceinline__ uint4 values_at(const void* base, int64_t off, int d,
 }
 
 // What positions [k0, k1) add to a row's output, taken one position at a time, with
-// exponentials relative to `ref` (all lanes, one row): lane l returns the sums of
+// exponentials relative to z = `ref` (all lanes, one row): lane l returns the sums of
 // elements 4 l + 128 i to 4 l + 3 + 128 i.
 template <int DP, int K>
 __device__ __noinline__ void row_again(const AttnArgs& a, int seq, int head, const uint16_t* q, int k0, int k1, float ref,
@@ -261,7 +266,8 @@ __device__ __noinline__ void row_again(const AttnArgs& a, int seq, int head, con
 #pragma unroll
         for (int i = 0; i < 8; ++i) z = fmaf(x[i], y[i], z);
       }
-      p = half_bits_to_f32(f32_to_half_bits(exp2_approx(fmaf(z, a.scale_log2, -ref)), type), type);
+      // z may differ from the tensor cores' in the last bits: no further above than kMost
+      p = half_bits_to_f32(f32_to_half_bits(exp2_approx(fminf(fmaf(z - ref, a.scale_log2, tile_lift<T::f16>()), 15.5f)), type), type);
     }
     for (uint32_t m = __ballot_sync(0xFFFFFFFFu, page >= 0); m; m &= m - 1) {
       const int l = __ffs(m) - 1;
@@ -359,7 +365,11 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
     const bool some = half * kHalf + warp * 32 < w.tile.rows;  // the warp has rows
     const int all_lo = __reduce_max_sync(0xFFFFFFFFu, lo), all_hi = __reduce_min_sync(0xFFFFFFFFu, hi);
     const int ta = w.ta;
-    float m = -INFINITY, l = 0.0f;  // m: the reference, scaled
+    float m = -INFINITY, l = 0.0f;  // m: the reference
+    // Exponentials are 2^(scale z + ref) with the reference in ref, or, where that would be
+    // rounded too far, 2^(scale (z - base) + ref); large: some row of the warp has a base.
+    float base = 0.0f, ref = 0.0f;
+    bool large = false;
 #pragma unroll 1
     for (int j = 0; j < nt; ++j, ++n_tile, ++tiles) {
       const int buf = G::halves == 2 ? half : n_tile & 1;
@@ -376,8 +386,8 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
         // Pages may be missing, which is rare: asked for here, looked at when the first
         // exponentials are there, as shared memory answers late beside the products.
         const int holes = *reinterpret_cast<volatile int*>(&sm.holes);
-        bool masked = first < all_lo || first + BN > all_hi;
-        // z of 32 positions, -inf where the row does not see
+        bool masked = first < all_lo || first + BN > all_hi || large;
+        // z (less the base) of 32 positions, -inf where the row does not see
         auto load = [&](int c, float (&z)[32]) {
           tmem_ld32(zaddr + c, z);
           if (masked) {
@@ -386,7 +396,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
             const int from = min(max(lo - first - c, 0), 32), to = min(max(hi - first - c, 0), 32);
             const uint32_t see = sm.bits[tiles & 7][c / 32] & (from < 32 ? ~0u << from : 0u) & (to > 0 ? ~0u >> (32 - to) : 0u);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) z[k] = see & (1u << k) ? z[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) z[k] = see & (1u << k) ? z[k] - base : -INFINITY;
           }
         };
         // One half of the positions after the other, in the same few instructions: code
@@ -406,6 +416,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
               if (hb > 0 && !wait(sm, a, &sm.half_done[buf], (G::halves == 2 ? n_tile : n_tile >> 1) & 1)) return;
               if (G::halves == 1 && hb == 0 && j > 0 && !wait(sm, a, &sm.pv_done, (n_tile - 1) & 1)) return;
               float top = -INFINITY;
+              base = 0.0f;
 #pragma unroll 1
               for (int c = hb * HB; c < BN; c += 32) {
                 float z[32];
@@ -414,10 +425,14 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) top = fmaxf(fmaxf(top, z[k]), z[k + 1]);
               }
-              top *= a.scale_log2;
-              const float f = far && top > m ? exp2_approx(m - top) : 1.0f;
+              const float f = far && top > m ? exp2_approx((m - top) * a.scale_log2) : 1.0f;
               if (far && top > m) m = top;
               l *= f;
+              const float scaled = m == -INFINITY ? 0.0f : m * a.scale_log2;
+              const bool mine = !(fabsf(scaled) <= kLarge);
+              base = mine ? m : 0.0f, ref = mine ? tile_lift<T::f16>() : tile_lift<T::f16>() - scaled;
+              large = __any_sync(0xFFFFFFFFu, mine);
+              masked |= large;
               if (scale_o) {
                 tc_fence_after();
 #pragma unroll 1
@@ -434,7 +449,6 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
               }
             }
             // exponentials, as 16-bit values in p, and their sum
-            const float ref = tile_lift<T::f16>() - (m == -INFINITY ? 0.0f : m);
             float z[HB / 32][32], s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < HB / 32; ++c) load(hb * HB + 32 * c, z[c]);
@@ -529,7 +543,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
         float* ml = a.part_ml + (part * G::rows + r) * 2;
         ml[0] = m, ml[1] = l;
       } else if (a.lse) {
-        a.lse[row * a.kv_heads * a.group + head] = l == 0.0f ? -INFINITY : (m + (log2f(l) - tile_lift<T::f16>())) * kLn2;
+        a.lse[row * a.kv_heads * a.group + head] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, (log2f(l) - tile_lift<T::f16>()) * kLn2);
       }
     }
     // rows that an unseen value of the tiles may have spoilt
@@ -547,7 +561,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared<DP>& sm, 
       uint16_t* orow = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(out), src));
       float* prow = reinterpret_cast<float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(po), src));
       float o[(DP + 127) / 128][4];
-      row_again<DP, K>(a, w.at.seq, w.at.head, qr, b0, b1, (mr == -INFINITY ? 0.0f : mr) - tile_lift<T::f16>(), o);
+      row_again<DP, K>(a, w.at.seq, w.at.head, qr, b0, b1, mr == -INFINITY ? 0.0f : mr, o);
 #pragma unroll
       for (int i = 0; i < (DP + 127) / 128; ++i) {
         const int d = 4 * lane + 128 * i;

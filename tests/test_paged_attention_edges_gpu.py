@@ -129,3 +129,36 @@ def test_codes_that_are_nan_with_finite_scales(code, q_type, dim, max_rows, scal
             # tiles may be taken one position at a time
             assert (d <= 2.0 ** -6 * (2.0 ** scale_up + clean.float().abs()[~odd])).all()
             at[element] = kept
+
+
+@pytest.mark.parametrize("q_type,cache,power", [
+    (BF, BF, 4), (BF, BF, 25), (BF, BF, 33), (BF, BF, 60), (F16, F16, 4), (F16, F16, 25), (F16, F16, 29), (BF, E4M3, 25), (BF, E4M3, 40),
+    (F16, E4M3, 25), (F16, E4M3, 29)])
+@pytest.mark.parametrize("rows,max_rows,dim", [(1, 1, 64), (3, 2, 128), (3, 1000, 64), (300, 300, 128), (40, 40, 256)])
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+def test_large_products(q_type, cache, power, rows, max_rows, dim, scale):
+    """z of 2^power and a few steps of fp32 below: exact, so the weights are too, but
+    for the product with the scale (2^-22 of up to 2^7 steps' logarithm), the
+    exponentials (2^-22) and the sum, beside their rounding to 16 bits."""
+    length = 700
+    b = Batch([(rows, length)], 1, dim, 16, cache, max_rows=max_rows)
+    step = max(1.0, 2.0 ** (power - 23))                       # z's steps: below 2^power of half of this
+    a, k0 = 2.0 ** (power // 2), 2.0 ** (power - power // 2)
+    pos = torch.arange(length, device=DEV)
+    drop = ((pos * 7) % 5).double()
+    k, v = torch.zeros(length, 1, dim, device=DEV, dtype=torch.float64), b.held[0][1].abs() + 0.5
+    # z = a k0 - step drop: the second element in units that an e4m3 head of this scale holds
+    unit = k0 * 2.0 ** -10
+    k[:, 0, 0], k[:, 0, 1] = k0, -drop * unit
+    b.held[0] = [b.put(0, "k", pos, k.float() if cache == E4M3 else k), b.put(0, "v", pos, v.float())]
+    assert torch.equal(b.held[0][0], k)
+    q = torch.zeros(rows, 4, dim, device=DEV)
+    q[..., 0], q[..., 1] = a, step / unit
+    assert torch.equal(q.to(q_type).float(), q)
+    out, lse = attend(b, q.to(q_type), 1, scale=scale, causal=False)
+    z = (2.0 ** power - step * drop) * scale
+    p = torch.exp(z - z.max())
+    want = (p[:, None] * b.held[0][1][:, 0]).sum(0) / p.sum()
+    half = 2.0 ** -9 if q_type == BF else 2.0 ** -12
+    assert ((out.double() - want).abs() <= want.abs() * (2 * half + 2.0 ** -13)).all()
+    assert ((lse.double() - (z.max() + torch.log(p.sum()))).abs() <= 2.0 ** -22 * z.max().abs() + 2.0 ** -13).all()

@@ -113,10 +113,13 @@ int moe_cache_read(const moe_kv_cache *cache, const moe_sequences *seqs, void *k
  * positions = table_width * page_size (at most 2^30).
  *
  * Products run on the tensor cores with fp32 sums; z, the sums of exponentials
- * and out are kept in fp32.  The exponentials are rounded to q_type (float16 for few
- * rows of an e4m3 cache) for the second product, at most half a step each, so that
- * a result moves by less than half a step of the mean |v|; out is rounded once, when
- * it is stored.  The order of sums goes by the sequences and the GPU's number of
+ * and out are kept in fp32.  The exponentials are rounded to q_type for the second
+ * product (few rows of an e4m3 cache: exponentials times the values' scales, to float16),
+ * at most half a step each, so that a result moves by less than half a step of the
+ * mean |v|.  float16 has no steps below 2^-39 (many rows: 2^-31) of a row's largest
+ * exponential or, in few rows of an e4m3 cache, 2^-33 of its largest exponential times
+ * scale; exponentials below 2^-126 of the largest are 0; sums need |v| times positions
+ * below 2^118.  out is rounded once, when it is stored.  The order of sums goes by the sequences and the GPU's number of
  * SMs alone.  Few rows (max_rows times query heads a key head up to 16)
  * take e4m3 values as they are; more of them read them in q_type:
  * exactly for MOE_BF16 (but below 2^-126), as float16 for MOE_F16, which is exact if the head's

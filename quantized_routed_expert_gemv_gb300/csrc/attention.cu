@@ -21,8 +21,9 @@
 // pieces of four positions and paired in registers.  Exponentials are turned over
 // (movmatrix) between the products.  e4m3 codes become float16 values between shared
 // memory and the product, a conversion for two; the keys' scales are multiplied on
-// z, the values' on the exponentials, in units of the largest so far, which o
-// follows as it follows m.
+// z, the values' on the exponentials, which makes a row's weights.  A weight is rounded to
+// float16 in the row's own unit, a power of two that its largest weight so far has set and
+// o follows: positions that a row does not see, or that weigh nothing, have no part in it.
 //
 // Bound: reading the cache.
 #include <atomic>
@@ -39,10 +40,16 @@ namespace {
 
 // log2 of the factor that all exponentials carry: float16 holds fewer small
 // values than large ones, so the largest exponential is 2^15 there.
-template <bool F16>
+// Weights of an e4m3 cache have units instead.
+template <int K>
 __host__ __device__ constexpr float exp_lift() {
-  return F16 ? 15.0f : 0.0f;
+  return K == kF16 ? 15.0f : 0.0f;
 }
+// The largest weight moves a row's unit so that it is 2^kUnitTop at most; smaller
+// ones are rounded to 11 bits down to 2^-(14 + kUnitTop) of it, then to multiples of 2^-(24 + kUnitTop).
+// The unit stays until a weight passes 2^kUnitMost, so that it seldom moves.
+constexpr int kUnitTop = 10, kUnitMost = 14;
+constexpr float kLowest = -3.402823466e38f;  // the maximum of no positions
 
 constexpr int kRows = 16;     // rows of the larger tile
 constexpr int kWarps = 4;
@@ -332,10 +339,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
         }
     }
     float o[MB][NB][4], m[NB][2], l[NB][2];
-    float v_ref = 0.0f, v_inv = 0.0f;  // e4m3: o counts values in units of the largest scale so far
+    float unit[NB][2];  // e4m3: o counts weights in units of 2^unit, a whole number in [-126, 126]
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+      m[n][0] = m[n][1] = kLowest, l[n][0] = l[n][1] = 0.0f;
+      unit[n][0] = unit[n][1] = -126.0f;
 #pragma unroll
       for (int j = 0; j < MB; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
     }
@@ -381,11 +389,9 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
         }
       }
       float vf[2];  // e4m3: the values' scales at positions gi and gi + 8
-      bool moved = false;
       if constexpr (T::e4m3) {
         const float k0 = sc[gi], k1 = sc[gi + 8];
         vf[0] = sc[kStep + gi], vf[1] = sc[kStep + gi + 8];
-        moved = fmaxf(vf[0], vf[1]) > v_ref;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           z[n][0] *= q_scale[n][0], z[n][1] *= q_scale[n][1], z[n][2] *= q_scale[n][0], z[n][3] *= q_scale[n][1];
@@ -406,58 +412,100 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
             else z[n][c] = -INFINITY;
           }
       }
-      // the running maximum
-      float top[NB][2];
+      // the running maximum, and what l and o shrink by when it grows
+      auto largest_z = [&](int n, int c) {
+        float x = fmaxf(z[n][c], z[n][2 + c]);
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+        for (int i = 4; i < 32; i *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, i));
+        return x;
+      };
+      auto shrink_o = [&](int n, float f0, float f1) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          top[n][c] = fmaxf(z[n][c], z[n][2 + c]);
-          moved |= top[n][c] > m[n][c];
-        }
-      if (__any_sync(0xFFFFFFFFu, moved)) {
-        float f = 1.0f;
-        if constexpr (T::e4m3) {
-          float v = fmaxf(vf[0], vf[1]);
+        for (int j = 0; j < MB; ++j) o[j][n][0] *= f0, o[j][n][1] *= f1, o[j][n][2] *= f0, o[j][n][3] *= f1;
+      };
+      bool moved = false;
+      if constexpr (!T::e4m3) {
 #pragma unroll
-          for (int i = 4; i < 32; i *= 2) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, i));
-          if (v > v_ref) {
-            f = v_ref / v;
-            v_ref = v, v_inv = 1.0f / v;
-          }
-        }
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          float shrink[2];
+          for (int c = 0; c < 2; ++c) moved |= fmaxf(z[n][c], z[n][2 + c]) > m[n][c];
+        if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = top[n][c];
+          for (int n = 0; n < NB; ++n) {
+            float shrink[2];
 #pragma unroll
-            for (int i = 4; i < 32; i *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, i));
-            shrink[c] = 1.0f;
-            if (x > m[n][c]) {
-              shrink[c] = exp2_approx((m[n][c] - x) * a.scale_log2);  // 0 for the first
-              m[n][c] = x;
+            for (int c = 0; c < 2; ++c) {
+              const float x = largest_z(n, c);
+              shrink[c] = 1.0f;
+              if (x > m[n][c]) {
+                shrink[c] = exp2_approx((m[n][c] - x) * a.scale_log2);
+                m[n][c] = x;
+              }
+              l[n][c] *= shrink[c];
             }
-            l[n][c] *= shrink[c];
-            shrink[c] *= f;
+            shrink_o(n, shrink[0], shrink[1]);
           }
-#pragma unroll
-          for (int j = 0; j < MB; ++j)
-            o[j][n][0] *= shrink[0], o[j][n][1] *= shrink[1], o[j][n][2] *= shrink[0], o[j][n][3] *= shrink[1];
         }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            z[n][c] = exp2_approx(fmaf(z[n][c] - m[n][c & 1], a.scale_log2, exp_lift<K>()));
+            l[n][c & 1] += z[n][c];
+          }
+      } else {
+        // exponentials and weights as powers of two
+        const float v_log2[2] = {log2_approx(vf[0]), log2_approx(vf[1])};
+        float d[NB][4], w[NB][4];
+        auto relate = [&] {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              d[n][c] = (z[n][c] - m[n][c & 1]) * a.scale_log2;
+              w[n][c] = d[n][c] + (v_log2[c >> 1] - unit[n][c & 1]);
+            }
+        };
+        relate();
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) moved |= d[n][c] > 0.0f || w[n][c] > static_cast<float>(kUnitMost);
+        if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            float shrink[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float x = largest_z(n, c);
+              float grown = 0.0f;  // m's growth in powers of two, of which the unit follows whole ones
+              if (x > m[n][c]) {
+                grown = fminf((x - m[n][c]) * a.scale_log2, 4096.0f);
+                m[n][c] = x;
+              }
+              l[n][c] *= exp2_approx(-grown);
+              float top = fmaxf((z[n][c] - m[n][c]) * a.scale_log2 + v_log2[0], (z[n][2 + c] - m[n][c]) * a.scale_log2 + v_log2[1]);
+#pragma unroll
+              for (int i = 4; i < 32; i *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+              const float was = unit[n][c] - floorf(grown), to = top > was + kUnitMost ? ceilf(top) - kUnitTop : was;
+              unit[n][c] = fminf(fmaxf(to, -126.0f), 126.0f);
+              shrink[c] = exp2_approx(floorf(grown) - grown) * exp2_approx(was - unit[n][c]);
+            }
+            shrink_o(n, shrink[0], shrink[1]);
+          }
+          relate();
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            l[n][c & 1] += exp2_approx(d[n][c]);
+            z[n][c] = exp2_approx(w[n][c]);
+          }
       }
-      if constexpr (T::e4m3) vf[0] *= v_inv, vf[1] *= v_inv;
       uint32_t pb[NB][2];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float ref = m[n][c & 1] == -INFINITY ? 0.0f : m[n][c & 1];
-          z[n][c] = exp2_approx(fmaf(z[n][c] - ref, a.scale_log2, exp_lift<T::f16>()));
-          l[n][c & 1] += z[n][c];
-          if constexpr (T::e4m3) z[n][c] *= vf[c >> 1];
-        }
         // position by position for the next product's operand
         pb[n][0] = transposed(pack2(z[n][0], z[n][1], half_type));
         pb[n][1] = transposed(pack2(z[n][2], z[n][3], half_type));
@@ -543,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
     w.next(a);
     const bool more = w.more();
     if (more) load_q();
-    const float unit = T::e4m3 ? v_ref : 1.0f;
+    // of e4m3 caches a row's weights' unit, 1 otherwise
+    auto unit_of = [&](int n, int c) { return T::e4m3 ? __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(unit[n][c])) << 23) : 1.0f; };
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += kJoinRows) {
       // a lane has, of rows 8 n + 2t and + 1, the elements EV (gi + 8 h) + j
@@ -551,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float* row = join_o + (warp * kJoinRows + ((2 * t + c) & 3)) * DP;
+          const float u = NB > 1 && r0 >= 8 ? unit_of(NB - 1, c) : unit_of(0, c);
 #pragma unroll
           for (int h = 0; h < S::vgroups; ++h)
 #pragma unroll
@@ -558,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
               const int b = (h * EV + j) / 2;
               float4 v = make_float4(o[b][0][c], o[b][0][2 + c], o[b + 1][0][c], o[b + 1][0][2 + c]);
               if (NB > 1 && r0 >= 8) v = make_float4(o[b][NB - 1][c], o[b][NB - 1][2 + c], o[b + 1][NB - 1][c], o[b + 1][NB - 1][2 + c]);
-              *reinterpret_cast<float4*>(row + EV * (gi + 8 * h) + j) = make_float4(v.x * unit, v.y * unit, v.z * unit, v.w * unit);
+              *reinterpret_cast<float4*>(row + EV * (gi + 8 * h) + j) = make_float4(v.x * u, v.y * u, v.z * u, v.w * u);
             }
         }
       }
@@ -589,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d) = u;
           if (d == 0 && a.lse)
             a.lse[row * a.kv_heads * a.group + head] =
-                sum == 0.0f ? -INFINITY : fmaf(top, a.scale, (log2f(sum) - exp_lift<T::f16>()) * kLn2);
+                sum == 0.0f ? -INFINITY : fmaf(top, a.scale, (log2f(sum) - exp_lift<K>()) * kLn2);
         } else {
           *reinterpret_cast<float4*>(a.part_o + (part * R + r) * a.head_dim + d) = acc;
           if (d == 0) a.part_ml[(part * R + r) * 2] = top, a.part_ml[(part * R + r) * 2 + 1] = sum;
@@ -866,7 +916,7 @@ extern "C" int moe_attention(const moe_attention_args* args, const moe_kv_cache*
       : tile_rows == 16 ? launch_rows<16>(a, kind, sms, &grid, st)
                         : launch_rows<8>(a, kind, sms, &grid, st);
   if (!e)
-    e = launch_join(a, grid, tile_rows, f16, many ? tiles_lift(f16) : kind == kBf16 ? exp_lift<false>() : exp_lift<true>(), st);
+    e = launch_join(a, grid, tile_rows, f16, many ? tiles_lift(f16) : kind == kF16 ? exp_lift<kF16>() : 0.0f, st);
   if (e) return reportf(MOE_ERR_CUDA, "moe_attention: %s (%s)", cudaGetErrorString(e), cudaGetErrorName(e));
   return MOE_OK;
 }

@@ -56,6 +56,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The bytes s of {a, b} (0..3 of a, 4..7 of b), lowest first.
 __device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 

@@ -14,6 +14,12 @@ pytestmark = pytest.mark.gpu
 KINDS = [(BF, BF), (F16, F16), (BF, E4M3), (F16, E4M3)]
 
 
+# The hint is cut to the rows of the call's tensors: rows of no sequence behind the others
+# take calls of few rows to the kernel of many.
+def behind(max_rows):
+    return 300 if max_rows == 1000 else 0
+
+
 def i32(*v):
     return torch.tensor(v, dtype=torch.int32, device=DEV)
 
@@ -97,13 +103,13 @@ def test_a_hint_of_single_tokens_for_a_long_prompt():
 def test_codes_that_are_nan_with_finite_scales(code, q_type, dim, max_rows, scale_up):
     """As a cast that does not saturate leaves them.  A key's makes the rows that see it
     NaN, a value's one element of them; the cache read back holds the same."""
-    b = Batch([(3, 260)], 2, dim, 16, E4M3, max_rows=max_rows)
+    b = Batch([(3, 260)], 2, dim, 16, E4M3, max_rows=max_rows, behind=behind(max_rows))
     if scale_up:  # scales beyond 2^7, which take the second product
         for s in (b.k_scale, b.v_scale):
             s[torch.isfinite(s)] *= 2.0 ** scale_up
         b.held = [[x * 2.0 ** scale_up for x in h] for h in b.held]
     q, scale = queries(b, 4, q_type), dim ** -0.5 * 2.0 ** -scale_up
-    clean, _ = attend(b, q, 2, scale=scale)
+    clean = attend(b, q, 2, scale=scale)[0][:3]
     check(b, q, attend(b, q, 2, scale=scale), scale=scale)
     element = dim - 3
     for which in "kv":
@@ -112,7 +118,7 @@ def test_codes_that_are_nan_with_finite_scales(code, q_type, dim, max_rows, scal
             at = getattr(b, which).view(torch.uint8)[page, slot, 1]
             kept = at[element].item()
             at[element] = code
-            out, lse = attend(b, q, 2, scale=scale)
+            out, lse = (t[:3] for t in attend(b, q, 2, scale=scale))
             ko, vo = b.cache().read(Sequences(i32(0, 260), i32(260), b.table), rows=260, out_type=F32)
             torch.cuda.synchronize()
             assert torch.isnan((ko if which == "k" else vo)[place, 1, element])
@@ -141,24 +147,66 @@ def test_large_products(q_type, cache, power, rows, max_rows, dim, scale):
     for the product with the scale (2^-22 of up to 2^7 steps' logarithm), the
     exponentials (2^-22) and the sum, beside their rounding to 16 bits."""
     length = 700
-    b = Batch([(rows, length)], 1, dim, 16, cache, max_rows=max_rows)
+    b = Batch([(rows, length)], 1, dim, 16, cache, max_rows=max_rows, behind=behind(max_rows))
     step = max(1.0, 2.0 ** (power - 23))                       # z's steps: below 2^power of half of this
     a, k0 = 2.0 ** (power // 2), 2.0 ** (power - power // 2)
     pos = torch.arange(length, device=DEV)
-    drop = ((pos * 7) % 5).double()
+    drop = (1 + (pos * 7) % 5).double()
     k, v = torch.zeros(length, 1, dim, device=DEV, dtype=torch.float64), b.held[0][1].abs() + 0.5
     # z = a k0 - step drop: the second element in units that an e4m3 head of this scale holds
     unit = k0 * 2.0 ** -10
     k[:, 0, 0], k[:, 0, 1] = k0, -drop * unit
     b.held[0] = [b.put(0, "k", pos, k.float() if cache == E4M3 else k), b.put(0, "v", pos, v.float())]
     assert torch.equal(b.held[0][0], k)
-    q = torch.zeros(rows, 4, dim, device=DEV)
+    q = torch.zeros(b.rows, 4, dim, device=DEV)
     q[..., 0], q[..., 1] = a, step / unit
     assert torch.equal(q.to(q_type).float(), q)
-    out, lse = attend(b, q.to(q_type), 1, scale=scale, causal=False)
+    out, lse = (t[:rows] for t in attend(b, q.to(q_type), 1, scale=scale, causal=False))
     z = (2.0 ** power - step * drop) * scale
     p = torch.exp(z - z.max())
     want = (p[:, None] * b.held[0][1][:, 0]).sum(0) / p.sum()
     half = 2.0 ** -9 if q_type == BF else 2.0 ** -12
     assert ((out.double() - want).abs() <= want.abs() * (2 * half + 2.0 ** -13)).all()
     assert ((lse.double() - (z.max() + torch.log(p.sum()))).abs() <= 2.0 ** -22 * z.max().abs() + 2.0 ** -13).all()
+
+
+@pytest.mark.parametrize("q_type,max_rows", [(BF, 1), (F16, 1), (BF, 1000)])
+@pytest.mark.parametrize("dim,group", [(64, 1), (128, 4), (80, 8), (256, 2)])
+@pytest.mark.parametrize("power", [-60, -20, 20, 40, 100])
+@pytest.mark.parametrize("which", ["newest", "newest two", "behind the window", "without weight", "with a small weight", "every other"])
+def test_values_of_other_magnitudes(q_type, max_rows, dim, group, power, which):
+    """An e4m3 cache, values of some positions 2^power times the others': rows that do
+    not see them, or give them (nearly) no weight, are as exact as without them."""
+    length, rows, window = 150, 2, 0
+    b = Batch([(rows, length), (rows, 40)], 1, dim, 16, E4M3, max_rows=max_rows, behind=behind(max_rows))
+    q = queries(b, group, q_type, size=0.5)
+    for s, (_, n) in enumerate(b.seqs):
+        pos = torch.arange(n, device=DEV)
+        k, v = (x.float().clamp(-3, 3) for x in b.held[s])
+        k[..., 0] = 0.0
+        far = {"newest": pos == n - 1, "newest two": pos >= n - 2, "every other": pos % 2 == 1}.get(which, pos % 16 == 5)
+        if which == "behind the window":
+            window, far = 21, pos < n - 22
+        if which in ("without weight", "with a small weight"):
+            # the row's logit is 90 or 30 below: e^-90 < 2^-129, e^-30 about 2^-43
+            k[far] = 0.0
+            k[far, :, 0] = -90.0 if which == "without weight" else -30.0
+            q[..., 0] = 1.0
+        v[far] *= 2.0 ** power
+        b.held[s] = [b.put(s, "k", pos, k), b.put(s, "v", pos, v)]
+    scale = 1.0 if which.startswith("with") and "window" not in which else dim ** -0.5
+    # weights of 2^-126 and less of the largest count as nothing: their share of what check() allows
+    # for is in its bound only while the values are below 2^70 or so
+    if which == "without weight" and power == 100:
+        for h in b.held:
+            far = torch.arange(len(h[1]), device=DEV) % 16 == 5
+            h[1] = torch.where(far[:, None, None], torch.zeros_like(h[1]), h[1])
+    out, lse = attend(b, q, 1, scale=scale, window=window)
+    out, lse, ref, rlse, d, dl = (t[:2 * rows] for t in (out, lse, *reference(b, q, scale, True, window)))
+    # float16 holds magnitudes below 65520; larger ones are infinite
+    inside, outside = ref.abs() + d < 65504, ref.abs() - d >= 65520
+    if q_type == BF:
+        inside, outside = torch.ones_like(inside), torch.zeros_like(outside)
+    far = (out.double() - ref).abs() - d
+    assert (far[inside] <= 0).all(), f"{far[inside].max().item()} over its bound"
+    assert torch.isinf(out[outside]).all() and ((lse.double() - rlse).abs() <= dl).all()

@@ -454,6 +454,8 @@ class PagedAttention:
             ld_out = _heads(out, rows, self.q_heads, self.head_dim, me, "out")
             if out.dtype != q.dtype or out.get_device() != index:
                 _refuse(me, f"out is of type {out.dtype} on {out.device}, q of {q.dtype} on {q.device}")
+        if not 0 <= window <= 0x7FFFFFFF:  # ctypes would cut it to 32 bits
+            _refuse(me, f"window={window} must be in [0, 2^31)")
         lse_ptr = None
         if lse is not None:
             _matrix(lse, (rows, self.q_heads), me, "lse")

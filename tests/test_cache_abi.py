@@ -272,6 +272,17 @@ def test_attention_refuses_tensors(calls):
     assert name == "moe_attention" and a.ld_q == a.ld_out == 256 and a.scale == 0.125 and seqs._obj.max_rows == 2 and seqs._obj.rows == 3
 
 
+@pytest.mark.parametrize("window", [-1, 1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 32) + 5])
+def test_windows_that_32_bits_do_not_hold(calls, window):
+    att = device.PagedAttention(4, 2, 64, device=_Cpu())
+    del calls[:]
+    q = Z(3, 4, 64, dtype=BF)
+    refused("window", att, q, a_cache(), some_seqs(), window=window)
+    assert not calls
+    att(q, a_cache(), some_seqs(), window=0x7FFFFFFF)
+    assert calls[0][1][0].window == 0x7FFFFFFF
+
+
 class _Cpu:
     """Stands for a GPU: torch.device of the CPU with the index of its tensors."""
 

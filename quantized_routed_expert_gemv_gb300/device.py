@@ -373,8 +373,8 @@ class PagedCache:
         return cls(new(*shape, head_dim), new(*shape, head_dim), *scales)
 
     def _move(self, me, fn, seqs, k, v, stream):
-        rows, index = k.shape[0], self.index
         ld_k = _heads(k, None, self.kv_heads, self.head_dim, me, "k")
+        rows, index = k.shape[0], self.index
         ld_v = _heads(v, rows, self.kv_heads, self.head_dim, me, "v")
         dtype = k.dtype
         if dtype != v.dtype:

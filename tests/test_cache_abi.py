@@ -272,6 +272,12 @@ def test_attention_refuses_tensors(calls):
     assert name == "moe_attention" and a.ld_q == a.ld_out == 256 and a.scale == 0.125 and seqs._obj.max_rows == 2 and seqs._obj.rows == 3
 
 
+def test_moves_refuse_a_tensor_without_dimensions(calls):
+    refused("shape", a_cache().write, Z(()), Z(3, 2, 64), some_seqs())
+    refused("shape", a_cache().read, some_seqs(), k_out=Z(()), v_out=Z(()))
+    assert not calls
+
+
 @pytest.mark.parametrize("window", [-1, 1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 32) + 5])
 def test_windows_that_32_bits_do_not_hold(calls, window):
     att = device.PagedAttention(4, 2, 64, device=_Cpu())

@@ -116,6 +116,13 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t w, int high) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// x, or the largest finite value for more; NaN stays.
+__device__ __forceinline__ float finite(float x) {
+  float y;
+  asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // An 8 x 8 matrix of 16-bit values, two of row gi a lane, turned over.
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   uint32_t d;
@@ -394,8 +401,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, K, R>::ctas) attention_row
         vf[0] = sc[kStep + gi], vf[1] = sc[kStep + gi + 8];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          z[n][0] *= q_scale[n][0], z[n][1] *= q_scale[n][1], z[n][2] *= q_scale[n][0], z[n][3] *= q_scale[n][1];
-          z[n][0] *= k0, z[n][1] *= k0, z[n][2] *= k1, z[n][3] *= k1;
+          // both factors at once: one of them alone may send z out of range; their product does only
+          // where z is out of range too, or 0
+          z[n][0] *= finite(q_scale[n][0] * k0), z[n][1] *= finite(q_scale[n][1] * k0);
+          z[n][2] *= finite(q_scale[n][0] * k1), z[n][3] *= finite(q_scale[n][1] * k1);
         }
       }
       const int first = (ta + step) * kBn + warp * kStep;

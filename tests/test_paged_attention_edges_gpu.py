@@ -210,3 +210,18 @@ def test_values_of_other_magnitudes(q_type, max_rows, dim, group, power, which):
     far = (out.double() - ref).abs() - d
     assert (far[inside] <= 0).all(), f"{far[inside].max().item()} over its bound"
     assert torch.isinf(out[outside]).all() and ((lse.double() - rlse).abs() <= dl).all()
+
+
+@pytest.mark.parametrize("max_rows", [1, 1000])
+@pytest.mark.parametrize("power", [-124, -110, -60, 60, 110])
+def test_keys_and_queries_far_apart(max_rows, power):
+    """Keys of an e4m3 cache of about 2^power, queries of 2^-power: neither scale may be
+    multiplied on z by itself.  One position has a key of zeros."""
+    b = Batch([(3, 200), (1, 77)], 2, 128, 16, E4M3, max_rows=max_rows, behind=behind(max_rows))
+    for s, (_, n) in enumerate(b.seqs):
+        pos = torch.arange(n, device=DEV)
+        k = torch.randn(n, 2, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(s)).double().clamp(-3, 3) * 2.0 ** power
+        k[7] = 0.0
+        b.held[s][0] = b.put(s, "k", pos, k)
+    q = (queries(b, 8, F32).double().clamp(-3, 3) * 2.0 ** -power).to(BF)
+    check(b, q, attend(b, q, 2))

@@ -49,9 +49,9 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const Seqs& q, int s, bool& falls) {
   Seq r;
   r.first = min(max(q.starts[s], 0), q.rows);
-  const int end = min(max(q.starts[s + 1], 0), q.rows);
-  falls = end < r.first;
-  r.n = max(end - r.first, 0);
+  const int end = q.starts[s + 1];
+  falls = end < r.first && r.first > 0;  // cut to [0, rows] too
+  r.n = min(max(end, r.first), q.rows) - r.first;
   r.len = min(max(q.kv_lens[s], 0), q.cap);
   return r;
 }

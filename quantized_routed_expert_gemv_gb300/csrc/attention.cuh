@@ -94,11 +94,8 @@ struct Dequant<false> {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(x >> 16 * i);
-      float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
-      asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-          : "+f"(f.x), "+f"(f.y)
-          : "f"(s));
-      out[i] = pack2(f.x, f.y, MOE_BF16);
+      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+      out[i] = pack2(f.x * s, f.y * s, MOE_BF16);
     }
   }
 };

@@ -52,7 +52,8 @@ typedef struct moe_kv_cache {
  *   rows:       rows of the call's tensors, in [0, 2^24].  Rows of no sequence
  *               are neither read nor written.
  *   max_rows:   the most rows of one sequence, or more: a hint that chooses
- *               between kernels, never what they compute.
+ *               between kernels.  They compute the same, with the roundings and
+ *               the range of float16 values that moe_attention states for each.
  * All of it is read by the kernels only, so a captured call follows what the
  * buffers hold when it is replayed.  Device values outside the contract touch no
  * other memory: starts are taken as if cut to [0, rows] and kv_lens to
@@ -75,7 +76,9 @@ typedef struct moe_sequences {
  * MOE_E4M3 gets, per token and head, the smallest power of two s >= 2^-126
  * with max |x| <= 448 s (1 for zeros) and the codes x / s rounded to nearest
  * even; a head that holds a NaN or an infinity gets a NaN scale and NaN codes.
- * No two rows of a call may share a slot. */
+ * No two rows of a call may share a slot.
+ * Calls of rows * kv_heads * t > 2^31 - 256, where t is head_dim / 16 rounded up to
+ * a power of two, are MOE_ERR_ARG, here and in moe_cache_read. */
 int moe_cache_write(const moe_kv_cache *cache, const moe_sequences *seqs, const void *k, int64_t ld_k, const void *v,
                     int64_t ld_v, int32_t type, void *stream);
 
@@ -119,15 +122,17 @@ int moe_cache_read(const moe_kv_cache *cache, const moe_sequences *seqs, void *k
  * mean |v|.  float16 has no steps below 2^-39 (many rows: 2^-31) of a row's largest
  * exponential or, in few rows of an e4m3 cache, 2^-33 of its largest exponential times
  * scale; exponentials below 2^-126 of the largest are 0; sums need |v| times positions
- * below 2^118.  out is rounded once, when it is stored.  The order of sums goes by the sequences and the GPU's number of
- * SMs alone.  Few rows (max_rows times query heads a key head up to 16)
- * take e4m3 values as they are; more of them read them in q_type:
- * exactly for MOE_BF16 (but below 2^-126), as float16 for MOE_F16, which is exact if the head's
- * largest magnitude lies in [2^-7, 57344], and infinite from 65520 on.
+ * below 2^118.  out is rounded once, when it is stored.  The order of sums goes by the
+ * sequences, max_rows (as the kernel goes by it) and the GPU's number of SMs alone.
+ * Few rows (max_rows times query heads a key head up to 16) take e4m3 values as they
+ * are; more of them read them in q_type: exactly for MOE_BF16 (but below 2^-126), as float16
+ * for MOE_F16, which is exact if the head's largest magnitude lies in [2^-7, 57344], and
+ * infinite from 65520 on.  So float16 queries over an e4m3 cache of such magnitudes get
+ * other results where some sequence has many rows: bf16 ones do not.
  *
  * Keys and values in pages of a multiple of 16 slots are read fastest; pages of
- * an odd number of slots, or of 2 or 4 times one, take about twice as long where
- * many rows attend. */
+ * an odd number of slots, or of 2 or 4 times one, and 16-bit caches with a stride of 0 or
+ * of 2^40 bytes or more, take about twice as long where many rows attend. */
 typedef struct moe_attention_args {
     const void *q;
     void *out;

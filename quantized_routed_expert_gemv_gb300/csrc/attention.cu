@@ -31,7 +31,6 @@
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
-#include "common.cuh"
 
 namespace moe {
 int reportf(int code, const char* fmt, ...);
@@ -83,7 +82,7 @@ struct Shape {
   static constexpr int scale_bytes = T::e4m3 ? 2 * kStep * 4 : 0;
   static constexpr int stage_bytes = 2 * kStep * row_bytes + scale_bytes + 16;  // 16: which positions count
   // On an SM: as many warps as registers and two stages of each allow.  64 ragged e4m3
-  // sequences with 8 rows of 128: two CTAs 140 us, three 123.
+  // sequences with 8 rows of 128: two CTAs 138 us, three 123.
   static constexpr int ctas = DP <= 64 || (row_bytes <= 128 && R == 8) ? 3 : DP <= 128 ? 2 : 1;
   static constexpr bool q_shared = DP > 128 && R > 8;       // the query's fragments lie in shared memory
   static constexpr int join_bytes = kWarps * kJoinRows * DP * 4;
@@ -741,14 +740,16 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 // rows are taken; more of them read the cache several times over, the tiles of 256 of
 // attention_tc.cu once.  16 sequences of 8192 positions, 8 key heads of 128, in a graph:
 //   rows            8      16     24     32     48
-//   bf16, 8         92.8   177    259    341    451 us
-//   bf16, 16        93.2   95.7   178    180    263
+//   bf16, 8         94.7   180    263    343    460 us
+//   bf16, 16        94.9   97.1   182    183    265
 //   bf16, 256       106    106    107    107    109
-//   e4m3, 8         63.7   116    166    211    306
-//   e4m3, 16        78.3   83.4   145    148    212
-//   e4m3, 256       133    134    135    135    136
-// At 24 and 32 rows of e4m3 caches heads of 64 would gain from tiles of 16 (92 and 95
-// us against 108), heads of 256 lose (208 and 214 against 134 and 136).
+//   e4m3, 8         65.5   118    170    216    315
+//   e4m3, 16        82.0   88.2   152    156    224
+//   e4m3, 256       135    135    137    137    138
+// At 24 and 32 rows of e4m3 caches heads of 64 gain and lose with tiles of 16: 102 and 106
+// us against 107 there, 14.4 and 14.8 against 17.4 and 18.1 over one sequence of 4000, but
+// 118 and 122 against 109 over 64 of 2048, 40 and 42 against 37 over 64 of 300.  Heads of 256
+// lose (212 and 218 against 146).
 constexpr int kFewRows = 16;
 
 // CTAs of the widest grid that a workspace serves, on an SM.

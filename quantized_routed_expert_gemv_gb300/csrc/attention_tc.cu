@@ -27,8 +27,8 @@
 // NaN: rows whose output is not finite are looked at again one by one.
 //
 // Bound: the way from a product to its exponentials and back, which the other half's
-// product hides in part.  4096 rows behind 12288 of 64 heads of 128: 1400 to 1456 us
-// by GPU, 1320 to 1370 TFLOP/s, 67 to 70% of the measured bf16 rate; a tile of 128
+// product hides in part.  4096 rows behind 12288 of 64 heads of 128: 1395 to 1460 us
+// by GPU, 1320 to 1380 TFLOP/s, 67 to 70% of the measured bf16 rate; a tile of 128
 // positions and 256 rows takes 3390 clocks, of which its products, by themselves 1055
 // to 1090 for 16, are 2130.
 // Code that runs once a unit or tile waits for its own instructions, so loops are
@@ -37,7 +37,6 @@
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
-#include "common.cuh"
 #include "tcgen05.cuh"
 
 namespace moe {
@@ -133,13 +132,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 32 bytes at a 32-byte boundary: a whole sector for each lane, as lanes have rows of their own.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-               "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 template <int N>
@@ -711,8 +703,9 @@ __device__ const uint4 zeros[16] = {};
 // Bound by these warps' own instructions, so what can be done once a position or tile
 // is: scales and addresses are made by the lane that looked a position up, one of
 // zeros stands for what does not count, pages are asked for half a tile before
-// their use.  2048 rows over 4096 positions of 8 heads of 128, bf16 queries of 64:
-// 289 -> 259 -> 243 (four codes turned at once) -> 218 us (addresses); 16-bit caches 195.
+// their use.  2048 rows over 4096 positions of 8 heads of 128, queries of 64, in a graph:
+// bf16 221 us, float16 206, 16-bit caches 190 and 194.  (bf16 codes turned bit by bit, which
+// takes a NaN's code for 480, 213; with a look for such codes 237.)
 template <int DP, int K>
 __device__ __forceinline__ void dequant_role(const AttnArgs& a, Shared<DP>& sm, uint8_t* ring, int tid) {
   using G = Geo<DP>;
@@ -1013,7 +1006,8 @@ EncodeFn encoder() {
 }
 
 // The tensor (elements, slots, heads, pages) of keys or values of a 16-bit
-// cache.  False if the driver refuses it.
+// cache.  False if the driver refuses it, or strides that it would refuse: tiles are
+// then copied in pieces, as for pages that no box of 8 positions divides.
 bool encode(CUtensorMap* map, const void* base, const AttnArgs& a, int rows, bool f16) {
   const EncodeFn fn = encoder();
   if (!fn) return false;

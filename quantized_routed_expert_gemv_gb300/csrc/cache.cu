@@ -153,18 +153,6 @@ __device__ __forceinline__ int64_t row_at(const MoveArgs& a, int row, int head, 
   return row * ld + static_cast<int64_t>(head) * a.c.head_dim + d;
 }
 
-// 32 bytes at a 32-byte boundary.
-__device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
-  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p));
-}
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-               "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 struct Sixteen {
   float x[16];
   __device__ __forceinline__ void load(const MoveArgs& a, const void* src, int64_t at) {
@@ -313,7 +301,7 @@ int move(const char* name, bool write, const moe_kv_cache* cache, const moe_sequ
                            static_cast<uintptr_t>(ld_v * size);
   a.vec = places % 32 == 0 ? 2 : places % 16 == 0 ? 1 : 0;
   a.heads = divisor(static_cast<uint32_t>(cache->kv_heads));
-  // row ranges of at most 2^31 threads; one range for up to 2^24 rows of 8 heads of 256
+  // threads are counted in 32 bits: up to 2^24 rows of 7 heads of 256, fewer than 2^17 of 1024
   const int64_t threads_row = static_cast<int64_t>(cache->kv_heads) << a.tpu_log2;
   const int64_t threads = threads_row * seqs->rows;
   if (threads > 0x7FFFFF00)

@@ -93,6 +93,18 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t i, const float
   }
 }
 
+// 32 bytes at a 32-byte boundary: a whole sector for a lane.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // The scale of a block whose largest |x| has these bits: the smallest power
 // of two s >= 2^-126 with max <= 448 s (448 = 1.75 * 2^8), 1 for zeros, NaN
 // if there is an infinity or a NaN.  `inv` is 1 / s (0 for NaN).

@@ -327,7 +327,9 @@ class PagedCache:
     """The paged keys and values of one layer (moe_kv_cache): k and v
     [n_pages][page_size][kv_heads][head_dim] in bfloat16, float16 or
     float8_e4m3fn, each head's elements contiguous, other strides free; for float8
-    also k_scale and v_scale, float32 [n_pages][page_size][kv_heads]."""
+    also k_scale and v_scale, float32 [n_pages][page_size][kv_heads], powers of two
+    (NaN for a head that is not finite) as write() makes them: with others a value is
+    rounded where many bfloat16 rows attend."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):

@@ -258,8 +258,9 @@ __device__ __noinline__ void row_again(const AttnArgs& a, int seq, int head, con
 #pragma unroll
         for (int i = 0; i < 8; ++i) z = fmaf(x[i], y[i], z);
       }
-      // z may differ from the tensor cores' in the last bits: no further above than kMost
-      p = half_bits_to_f32(f32_to_half_bits(exp2_approx(fminf(fmaf(z - ref, a.scale_log2, tile_lift<T::f16>()), 15.5f)), type), type);
+      // z may differ from the tensor cores' in the last bits: no further above than kMost; NaN stays
+      const float e = fmaf(z - ref, a.scale_log2, tile_lift<T::f16>());
+      p = half_bits_to_f32(f32_to_half_bits(exp2_approx(e > 15.5f ? 15.5f : e), type), type);
     }
     for (uint32_t m = __ballot_sync(0xFFFFFFFFu, page >= 0); m; m &= m - 1) {
       const int l = __ffs(m) - 1;

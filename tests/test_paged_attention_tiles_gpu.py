@@ -117,3 +117,29 @@ def test_what_a_row_does_not_see_may_be_anything(q_type, cache, dim, rows, windo
                 assert not torch.isfinite(out[odd]).any() and torch.equal(lse, clean_lse)
             elif place != 130:
                 assert torch.isnan(lse[odd]).all()
+
+
+@pytest.mark.parametrize("q_type,cache", KINDS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("length", [460, 20000])
+def test_a_key_that_is_seen_beside_a_value_that_is_not(q_type, cache, dim, length):
+    """Rows that see a NaN key are NaN, also where a value behind them has their rows
+    taken again; the rows before it are not."""
+    rows = 200
+    b = Batch([(rows, length)], 1, dim, 16, cache)
+    q = queries(b, 2, q_type)
+    clean = attend(b, q, 1)
+    check(b, q, clean)
+    key, value = length - 100, length - 10
+    for name, pos in (("k", key), ("v", value)):
+        page, slot = b.table[0, pos // 16].item(), pos % 16
+        if cache == E4M3:
+            getattr(b, name).view(torch.uint8)[page, slot, 0] = 0x7F
+        else:
+            getattr(b, name)[page, slot, 0] = math.nan
+    out, lse = attend(b, q, 1)
+    sees = torch.arange(length - rows, length, device=DEV) >= key
+    assert torch.isnan(out[sees]).all() and torch.isnan(lse[sees]).all()
+    assert torch.equal(lse[~sees], clean[1][~sees])
+    d = (out.float() - clean[0].float()).abs()[~sees]
+    assert (d <= 2.0 ** -6 * (1 + clean[0].float().abs()[~sees])).all()
